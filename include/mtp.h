@@ -342,6 +342,116 @@ MTP_API int mtp_set_debug(mtp_handle *h, int32_t skip_arrival_cta, int64_t spin_
  * UNSUPPORTED_SHAPE. */
 MTP_API int mtp_set_path(mtp_handle *h, int32_t path);
 
+/* ---------------------------------------------------------------- paged key cache
+ *
+ * Serving programs hold the target's K (and V) in pages of P tokens; the pages of the framework
+ * describe the shared K only as one tensor per attention type, so these entry points are the
+ * library's own. The key of sequence b at position t lies in physical page
+ * block_table[b * table_stride + t / P] at offset t % P: element (page, t % P, kv_head, i) is
+ * k[page * stride_page + (t % P) * stride_t + kv_head * stride_h + i], so token-major
+ * ([n_pages][P][n_kv][d]) and head-major ([n_pages][n_kv][P][d]) caches, and K and V in one
+ * allocation, are strides. A slot is page * P + offset.
+ * Limits: dtype bf16 or fp32; head_dim <= 512, a multiple of 16 bytes; page_size a power of two
+ * <= 256; n_pages * page_size and max_pages * page_size <= 2^30 (element offsets are 64-bit);
+ * 16-byte aligned pointers; strides >= head_dim and multiples of 16 bytes. A block_table entry
+ * outside [0, n_pages) is no page: its keys are left out (and never read). ctx_len is clamped to
+ * [0, max_pages * page_size] on the device. Rows of a page at or past ctx_len are never used,
+ * whatever they hold.
+ * These calls keep no state, need no handle and use the current device; scratch is the caller's
+ * `workspace` (16-byte aligned, not shared by calls that may overlap), sized by the
+ * *_workspace call with the same arguments. They may be captured into CUDA graphs. */
+typedef struct mtp_paged_kv {
+  void *k;                    /* device, model dtype */
+  void *v;                    /* device, the layout of k, or NULL (V = K) */
+  const int32_t *block_table; /* device [B][table_stride] (not read by mtp_page_append) */
+  const int32_t *ctx_len;     /* device [B]: valid keys (not read by mtp_page_append) */
+  int8_t *codes;              /* device [n_pages][n_kv][head_dim] page summaries, or NULL */
+  float *scales;              /* device [n_pages][n_kv], or NULL (with codes) */
+  int64_t stride_page, stride_t, stride_h; /* elements */
+  int64_t table_stride;       /* entries between sequences (>= max_pages) */
+  int32_t n_pages;            /* physical pages */
+  int32_t page_size;          /* P */
+  int32_t max_pages;          /* logical pages of a sequence (columns of block_table used) */
+  int32_t n_kv_head, head_dim;
+  int32_t dtype;              /* enum mtp_dtype */
+} mtp_paged_kv;
+
+/* Block tables and slot maps from request lengths. Sequence b holds old_len[b] tokens in
+ * ceil(old_len[b] / P) pages and shall hold new_len[b]:
+ *   growers   (new > old) take ceil(new / P) - ceil(old / P) pages from the head of the ring of
+ *             free pages, in batch order, appended to their block_table rows. A grower is granted
+ *             while the sums of pages and of new tokens over the growers up to it fit ring_state's
+ *             count and max_tokens; the first that does not fit and every later grower are denied
+ *             and keep their length;
+ *   shrinkers (new < old; 0 ends a sequence) return the pages behind ceil(new / P) to the ring's
+ *             tail; these can be taken from the next call on;
+ *   a new_len outside [0, max_pages * P] is denied.
+ * Entries of block_table behind a sequence's pages are left as they were.
+ *   old_len, new_len device [B] int32;  block_table device [B][table_stride], updated in place
+ *   free_ring   device [n_pages] int32, updated in place: the free pages are
+ *               free_ring[(head + i) % n_pages], i < count
+ *   ring_state  device [2] int32: head, count
+ *   len_out     device [B] int32: length after the call
+ *   slot_map    device [max_tokens] int32: the slots of the new tokens, sequence after sequence;
+ *               -1 behind the last (NULL only when max_tokens == 0); 16-byte aligned
+ *   cu_new      device [B + 1] int32: sequence b's new tokens are [cu_new[b], cu_new[b + 1])
+ *   state_out   device [2] int32: the ring's head and count after the call
+ *   status      device [4] int32: new tokens, pages taken, pages returned, denied sequences
+ * len_out and state_out must not be old_len / new_len and ring_state (the inputs stay readable,
+ * so the call can be repeated). B <= 8192. Errors: INVALID_ARG, UNSUPPORTED_SHAPE, CUDA. */
+MTP_API int mtp_page_plan(const int32_t *old_len, const int32_t *new_len, int32_t B, int32_t *block_table,
+                          int64_t table_stride, int32_t max_pages, int32_t *free_ring, int32_t n_pages,
+                          const int32_t *ring_state, int32_t page_size, int32_t max_tokens, int32_t *len_out,
+                          int32_t *slot_map, int32_t *cu_new, int32_t *state_out, int32_t *status, void *stream);
+
+/* Writes T rows into their slots: row t of k_new (and of v_new when the cache has a V) to slot
+ * slot_map[t]; rows whose slot is outside [0, n_pages * P) are skipped. When the cache has
+ * summaries, every page whose last slot is written gets its summary from all P rows it then
+ * holds: per KV head m = the mean key rounded to fp32, scale = fl32(max |m| * fl32(1 / 127)),
+ * codes = rint(fl32(m / scale)); a mean that is not finite gives scale NaN and codes 0. A slot
+ * may occur once in slot_map.
+ *   k_new, v_new device rows of [n_kv][head_dim], model dtype, row_stride_k / row_stride_v
+ *                elements apart (>= n_kv * head_dim, multiples of 16 bytes)
+ *   slot_map     device [T] int32
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, CUDA. */
+MTP_API int mtp_page_append(const mtp_paged_kv *kv, const void *k_new, const void *v_new, int64_t row_stride_k,
+                            int64_t row_stride_v, const int32_t *slot_map, int32_t T, void *stream);
+
+/* Attention of one new token per sequence over the paged cache, split over the cache's length
+ * and joined: out[b][h] = sum_j p_j v_j, p = softmax(scale q[b][h] . k_j) over the attended
+ * positions: [0, L), the last `window` of them when window > 0, and with `pages` only those in
+ * the listed logical pages of the head's KV head (entries outside the sequence's pages are
+ * skipped; a page listed twice counts twice). fp32 arithmetic; bf16 keys enter exactly. A
+ * sequence with nothing to attend gets out 0 and lse -inf. Query head h reads KV head
+ * h / (n_head / n_kv_head).
+ *   q         device [B][n_head][head_dim] fp32
+ *   pages     device [B][n_kv_head][n_list] int32 or NULL
+ *   scale     softmax scale, 0 -> 1 / sqrt(head_dim)
+ *   out       device [B][n_head][head_dim] fp32
+ *   lse       device [B][n_head] fp32 log of the sum of exponentials, or NULL
+ * Errors: INVALID_ARG (workspace too small included), UNSUPPORTED_SHAPE, CUDA. */
+MTP_API int mtp_paged_attention(const mtp_paged_kv *kv, const float *q, int32_t B, int32_t n_head, int32_t window,
+                                float scale, const int32_t *pages, int32_t n_list, float *out, float *lse,
+                                void *workspace, int64_t workspace_bytes, void *stream);
+MTP_API int mtp_paged_attention_workspace(const mtp_paged_kv *kv, int32_t B, int32_t n_head, int32_t n_list,
+                                          int64_t *bytes);
+
+/* Pages a query attends, by a cheap score of each page: per query head the step
+ * s = fl32(max |q| * fl32(1 / 127)) and codes c = rint(fl32(q / s)) (all 0 when q is not
+ * finite), the page's score per KV head = max over its query heads of
+ * fl32(fl32((c . codes) * s) * scale) with the integer dot product. The first keep_first and the
+ * last keep_last pages of a sequence score +inf, as does a page of scale NaN; a block_table entry
+ * that is no page scores -inf. sel[b][g] lists the n_select pages of the highest scores (ties:
+ * lower page) in increasing order, -1 behind them when the sequence has fewer. Only complete
+ * pages need a summary when keep_last >= 1.
+ *   q    device [B][n_head][head_dim] fp32;  sel device [B][n_kv_head][n_select] int32
+ * Errors: INVALID_ARG (keep_first < 0, keep_last < 1, n_select < keep_first + keep_last, no
+ * summaries, workspace too small), UNSUPPORTED_SHAPE, CUDA. */
+MTP_API int mtp_page_select(const mtp_paged_kv *kv, const float *q, int32_t B, int32_t n_head, int32_t n_select,
+                            int32_t keep_first, int32_t keep_last, int32_t *sel, void *workspace,
+                            int64_t workspace_bytes, void *stream);
+MTP_API int mtp_page_select_workspace(const mtp_paged_kv *kv, int32_t B, int64_t *bytes);
+
 /* Free the workspace and the handle (synchronises). NULL is ignored. */
 MTP_API void mtp_destroy(mtp_handle *h);
 

@@ -11,4 +11,7 @@ def __getattr__(name):
     if name in ("Drafter", "verify_greedy", "verify_sample", "make_config", "make_kv"):
         from . import drafter
         return getattr(drafter, name)
+    if name in ("PagedKV", "page_plan", "page_append", "page_select", "paged_attention"):
+        from . import paged
+        return getattr(paged, name)
     raise AttributeError(name)

@@ -19,7 +19,8 @@ MTP_LAYER_SLIDING, MTP_LAYER_FULL = 0, 1
 # Every symbol include/mtp.h declares.
 EXPORTS = ("mtp_init_weights", "mtp_draft_block", "mtp_centroid_head", "mtp_verify_greedy", "mtp_get_status",
            "mtp_set_path", "mtp_destroy", "mtp_last_error", "mtp_centroid_head_noalloc", "mtp_set_logit_mask",
-           "mtp_verify_sample", "mtp_set_sparse_head", "mtp_set_debug")
+           "mtp_verify_sample", "mtp_set_sparse_head", "mtp_set_debug", "mtp_page_plan", "mtp_page_append",
+           "mtp_page_select", "mtp_page_select_workspace", "mtp_paged_attention", "mtp_paged_attention_workspace")
 MASK_NEG_1E30, MASK_MIN_MINUS_ONE = 0, 1  # enum mtp_logit_mask
 HEAD_AUTO, HEAD_PER_SEQUENCE, HEAD_CLUSTER_MAJOR = 0, 1, 2  # enum mtp_sparse_head
 
@@ -56,6 +57,12 @@ class mtp_kv(ctypes.Structure):
                 ("stride_b", ctypes.c_int64), ("stride_t", ctypes.c_int64), ("max_ctx", ctypes.c_int32)]
 
 
+class mtp_paged_kv(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "block_table", "ctx_len", "codes", "scales")] + [
+        (n, ctypes.c_int64) for n in ("stride_page", "stride_t", "stride_h", "table_stride")] + [
+        (n, ctypes.c_int32) for n in ("n_pages", "page_size", "max_pages", "n_kv_head", "head_dim", "dtype")]
+
+
 _lib = None
 
 
@@ -82,13 +89,22 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mtp_set_logit_mask.argtypes = [vp, i32]
     lib.mtp_set_sparse_head.argtypes = [vp, i32]
     lib.mtp_set_debug.argtypes = [vp, i32, ctypes.c_int64]
+    i64, f32, pkv = ctypes.c_int64, ctypes.c_float, ctypes.POINTER(mtp_paged_kv)
+    lib.mtp_page_plan.argtypes = [vp, vp, i32, vp, i64, i32, vp, i32, vp, i32, i32, vp, vp, vp, vp, vp, vp]
+    lib.mtp_page_append.argtypes = [pkv, vp, vp, i64, i64, vp, i32, vp]
+    lib.mtp_paged_attention.argtypes = [pkv, vp, i32, i32, i32, f32, vp, i32, vp, vp, vp, i64, vp]
+    lib.mtp_paged_attention_workspace.argtypes = [pkv, i32, i32, i32, ctypes.POINTER(i64)]
+    lib.mtp_page_select.argtypes = [pkv, vp, i32, i32, i32, i32, i32, vp, vp, i64, vp]
+    lib.mtp_page_select_workspace.argtypes = [pkv, i32, ctypes.POINTER(i64)]
     lib.mtp_destroy.argtypes = [vp]
     lib.mtp_destroy.restype = None
     lib.mtp_last_error.argtypes = []
     lib.mtp_last_error.restype = ctypes.c_char_p
     for name in ("mtp_init_weights", "mtp_draft_block", "mtp_centroid_head", "mtp_verify_greedy",
                  "mtp_get_status", "mtp_set_path", "mtp_centroid_head_noalloc", "mtp_set_logit_mask",
-                 "mtp_verify_sample", "mtp_set_sparse_head", "mtp_set_debug"):
+                 "mtp_verify_sample", "mtp_set_sparse_head", "mtp_set_debug", "mtp_page_plan", "mtp_page_append",
+                 "mtp_page_select", "mtp_page_select_workspace", "mtp_paged_attention",
+                 "mtp_paged_attention_workspace"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -167,6 +183,47 @@ def mtp_set_sparse_head(handle: int, mode: int) -> None:
 
 def mtp_set_debug(handle: int, skip_arrival_cta: int, spin_limit_cycles: int) -> None:
     _check(load_library().mtp_set_debug(handle, skip_arrival_cta, spin_limit_cycles), "mtp_set_debug")
+
+
+def mtp_page_plan(old_len: int, new_len: int, B: int, block_table: int, table_stride: int, max_pages: int,
+                  free_ring: int, n_pages: int, ring_state: int, page_size: int, max_tokens: int, len_out: int,
+                  slot_map: int, cu_new: int, state_out: int, status: int, stream: int = 0) -> None:
+    _check(load_library().mtp_page_plan(old_len, new_len, B, block_table, table_stride, max_pages, free_ring, n_pages,
+                                        ring_state, page_size, max_tokens, len_out, slot_map or None, cu_new,
+                                        state_out, status, stream or None), "mtp_page_plan")
+
+
+def mtp_page_append(kv: mtp_paged_kv, k_new: int, v_new: int, row_stride_k: int, row_stride_v: int, slot_map: int,
+                    T: int, stream: int = 0) -> None:
+    _check(load_library().mtp_page_append(kv, k_new or None, v_new or None, row_stride_k, row_stride_v,
+                                          slot_map or None, T, stream or None), "mtp_page_append")
+
+
+def mtp_paged_attention_workspace(kv: mtp_paged_kv, B: int, n_head: int, n_list: int) -> int:
+    n = ctypes.c_int64()
+    _check(load_library().mtp_paged_attention_workspace(kv, B, n_head, n_list, ctypes.byref(n)),
+           "mtp_paged_attention_workspace")
+    return n.value
+
+
+def mtp_paged_attention(kv: mtp_paged_kv, q: int, B: int, n_head: int, window: int, scale: float, pages: int,
+                        n_list: int, out: int, lse: int, workspace: int, workspace_bytes: int,
+                        stream: int = 0) -> None:
+    _check(load_library().mtp_paged_attention(kv, q, B, n_head, window, scale, pages or None, n_list, out,
+                                              lse or None, workspace or None, workspace_bytes, stream or None),
+           "mtp_paged_attention")
+
+
+def mtp_page_select_workspace(kv: mtp_paged_kv, B: int) -> int:
+    n = ctypes.c_int64()
+    _check(load_library().mtp_page_select_workspace(kv, B, ctypes.byref(n)), "mtp_page_select_workspace")
+    return n.value
+
+
+def mtp_page_select(kv: mtp_paged_kv, q: int, B: int, n_head: int, n_select: int, keep_first: int, keep_last: int,
+                    sel: int, workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _check(load_library().mtp_page_select(kv, q, B, n_head, n_select, keep_first, keep_last, sel, workspace or None,
+                                          workspace_bytes, stream or None), "mtp_page_select")
 
 
 def mtp_destroy(handle: int) -> None:

@@ -1,0 +1,68 @@
+// The paged key cache shared by the paged operators (plan, append, select, attention): layout,
+// argument block and the internal entry points. A page holds P = 2^pshift tokens; the key of
+// sequence b at position t lies in physical page block_table[b][t / P] at offset t % P.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "mtp.h"
+
+namespace mtp {
+namespace pg {
+
+constexpr int kMaxSms = 160;  // grids and workspaces are sized for at most this many SMs
+
+// A validated mtp_paged_kv, in the form the kernels take.
+struct Cache {
+  void* k;
+  void* v;                  // null: V = K
+  const int* table;         // [B][table_stride]
+  const int* ctx_len;       // [B]
+  signed char* codes;       // page summaries, or null
+  float* scales;
+  long long sp, st, sh;     // elements between pages, tokens, KV heads
+  long long table_stride;
+  int n_pages, pshift, max_pages, nkv, d, f32;
+};
+
+// Attended range of one sequence: keys [lo, hi) of its positions.
+__device__ __forceinline__ void key_range(const Cache& c, int b, int window, int& lo, int& hi) {
+  const int cap = c.max_pages << c.pshift;
+  hi = min(max(c.ctx_len[b], 0), cap);
+  lo = window > 0 ? max(0, hi - window) : 0;
+}
+// Physical page of logical page lp of sequence b, or -1 when the table's entry is no page.
+__device__ __forceinline__ int phys_page(const Cache& c, int b, int lp) {
+  const int page = __ldg(c.table + static_cast<size_t>(b) * c.table_stride + lp);
+  return static_cast<unsigned>(page) < static_cast<unsigned>(c.n_pages) ? page : -1;
+}
+
+struct AttArgs {
+  Cache c;
+  const float* q;           // [B][nh][d]
+  const int* list;          // [B][nkv][n_list] logical pages, or null (every page)
+  float* out;               // [B][nh][d]
+  float* lse;               // [B][nh] or null
+  float* ws_acc;            // partial sums of the splits
+  float* ws_ml;             // their (max, exp-sum)
+  float scale_log2;         // softmax scale * log2(e)
+  int B, nh, n_list, window, nsplit;
+};
+
+}  // namespace pg
+
+// Workspace bytes and launch of the one-token attention.
+long long paged_att_workspace(const pg::Cache& c, int B, int nh, int n_list);
+long long page_select_workspace(const pg::Cache& c, int B);
+int run_paged_att(pg::AttArgs a, void* ws, int num_sms, cudaStream_t st);
+
+int run_page_plan(const int* old_len, const int* new_len, int B, int* table, long long table_stride, int max_pages,
+                  int* ring, int n_pages, const int* state, int pshift, int max_tokens, int* len_out, int* slots,
+                  int* cu_new, int* state_out, int* status, int num_sms, cudaStream_t st);
+int run_page_append(const pg::Cache& c, const void* k_new, const void* v_new, long long row_k, long long row_v,
+                    const int* slots, int T, int num_sms, cudaStream_t st);
+int run_page_select(const pg::Cache& c, const float* q, int B, int nh, int n_select, int keep_first, int keep_last,
+                    int* sel, void* ws, int num_sms, cudaStream_t st);
+
+}  // namespace mtp

@@ -1,0 +1,291 @@
+// Attention of one new token over a paged key cache, split over the cache's length and joined:
+// out_h = sum_j p_j v_j with p = softmax(scale q_h . k_j) over the attended positions j of the
+// sequence, read through the block table (all pages, the last `window` keys, or a list of
+// selected pages per KV head).
+//
+// This file: the CUDA-core kernel for every dtype and head dim, and the join of the splits.
+// One CTA of 4 warps per (sequence, KV head, group of heads, split). LPK lanes hold one key row
+// (16-byte vectors), 32 / LPK rows side by side in a warp, U row blocks in flight; every lane
+// keeps its vectors of GP queries and GP running sums in registers, so a key row is read once
+// for all heads of the group. Scores, maxima, sums and outputs are fp32.
+#include "mtp_common.cuh"
+#include "mtp_launch.h"
+#include "mtp_paged.cuh"
+
+namespace mtp {
+namespace pg {
+
+constexpr int kAttWarps = 4;
+
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& u, float* out);
+template <>
+__device__ __forceinline__ void unpack<__nv_bfloat16>(const uint4& u, float* out) {
+  const unsigned w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    out[2 * i] = __uint_as_float(w[i] << 16);
+    out[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+template <>
+__device__ __forceinline__ void unpack<float>(const uint4& u, float* out) {
+  out[0] = __uint_as_float(u.x);
+  out[1] = __uint_as_float(u.y);
+  out[2] = __uint_as_float(u.z);
+  out[3] = __uint_as_float(u.w);
+}
+
+// exp2 of x - m with a row that has no key yet (m = -inf) giving 0
+__device__ __forceinline__ float pexp(float x, float m) { return m == -INFINITY ? 0.f : exp2f(x - m); }
+
+template <typename T, int LPK, int NV, int GP>
+__global__ void __launch_bounds__(kAttWarps * 32) k_paged_att(const __grid_constant__ AttArgs a) {
+  pdl_enter();
+  constexpr int VE = Elem<T>::kVec, U = NV >= 4 ? 1 : 4 / NV, KPW = 32 / LPK;
+  extern __shared__ __align__(16) float sm_att[];  // [warps][GP][d] sums, then [warps][GP] m, l
+  const Cache& c = a.c;
+  const int d = c.d, nvec = d / VE, G = a.nh / c.nkv, ngrp = (G + GP - 1) / GP;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, li = lane % LPK, sub = lane / LPK;
+  int it = blockIdx.x;
+  const int sp = it % a.nsplit;
+  it /= a.nsplit;
+  const int hg = it % ngrp;
+  it /= ngrp;
+  const int g = it % c.nkv, b = it / c.nkv;
+  const int h0 = g * G + hg * GP, nh = min(GP, G - hg * GP);
+  int lo, hi;
+  key_range(c, b, a.window, lo, hi);
+  // keys are numbered by position (dense), or by (list entry, offset)
+  const int P = 1 << c.pshift;
+  const int i0 = a.list ? 0 : lo, i1 = a.list ? a.n_list << c.pshift : hi;
+  const int step = KPW * U * kAttWarps;
+  const int chunk = ((max(i1 - i0, 0) + a.nsplit - 1) / a.nsplit + step - 1) / step * step;
+  const int j0 = i0 + sp * chunk, j1 = min(i1, j0 + chunk);
+  const int* list = a.list ? a.list + (static_cast<size_t>(b) * c.nkv + g) * a.n_list : nullptr;
+
+  float q[GP][NV * VE], acc[GP][NV * VE], m[GP], l[GP];
+#pragma unroll
+  for (int h = 0; h < GP; ++h) {
+    m[h] = -INFINITY;
+    l[h] = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int v = li + LPK * j;
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        acc[h][j * VE + e] = 0.f;
+        q[h][j * VE + e] = (h < nh && v < nvec) ? a.q[(static_cast<size_t>(b) * a.nh + h0 + h) * d + v * VE + e] : 0.f;
+      }
+    }
+  }
+  for (int base = j0 + warp * KPW * U; base < j1; base += step) {
+    uint4 kv[U][NV], vv[U][NV];
+    bool on[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = base + u * KPW + sub;
+      int pos = i, lp = i >> c.pshift;
+      on[u] = i < j1;
+      if (on[u] && list) {
+        lp = list[i >> c.pshift];
+        pos = (lp << c.pshift) + (i & (P - 1));
+        on[u] = lp >= 0 && lp < c.max_pages && pos >= lo && pos < hi;
+      }
+      const int page = on[u] ? phys_page(c, b, lp) : -1;
+      on[u] = page >= 0;
+      const size_t at = on[u] ? static_cast<size_t>(page) * c.sp + static_cast<size_t>(pos & (P - 1)) * c.st +
+                                    static_cast<size_t>(g) * c.sh
+                              : 0;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int v = li + LPK * j;
+        const bool rd = on[u] && v < nvec;
+        kv[u][j] = rd ? __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(c.k) + at + v * VE))
+                      : make_uint4(0, 0, 0, 0);
+        if (c.v)
+          vv[u][j] = rd ? __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(c.v) + at + v * VE))
+                        : make_uint4(0, 0, 0, 0);
+      }
+    }
+    float s[U][GP];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float x[NV * VE];
+#pragma unroll
+      for (int j = 0; j < NV; ++j) unpack<T>(kv[u][j], x + j * VE);
+#pragma unroll
+      for (int h = 0; h < GP; ++h) {
+        float t = 0.f;
+#pragma unroll
+        for (int e = 0; e < NV * VE; ++e) t = fmaf(q[h][e], x[e], t);
+#pragma unroll
+        for (int o = LPK / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+        s[u][h] = on[u] ? t * a.scale_log2 : -INFINITY;
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < GP; ++h) {
+      float mn = m[h];
+#pragma unroll
+      for (int u = 0; u < U; ++u) mn = fmaxf(mn, s[u][h]);
+      const float corr = pexp(m[h], mn);
+      m[h] = mn;
+      l[h] *= corr;
+#pragma unroll
+      for (int e = 0; e < NV * VE; ++e) acc[h][e] *= corr;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        s[u][h] = pexp(s[u][h], mn);
+        l[h] += s[u][h];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float x[NV * VE];
+#pragma unroll
+      for (int j = 0; j < NV; ++j) unpack<T>(c.v ? vv[u][j] : kv[u][j], x + j * VE);
+#pragma unroll
+      for (int h = 0; h < GP; ++h)
+#pragma unroll
+        for (int e = 0; e < NV * VE; ++e) acc[h][e] = fmaf(s[u][h], x[e], acc[h][e]);
+    }
+  }
+  // join the rows held side by side in the warp, then the warps
+  float* ml = sm_att + kAttWarps * GP * d;
+#pragma unroll
+  for (int h = 0; h < GP; ++h) {
+    float mn = m[h];
+#pragma unroll
+    for (int o = LPK; o < 32; o <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    const float corr = pexp(m[h], mn);
+    l[h] *= corr;
+#pragma unroll
+    for (int o = LPK; o < 32; o <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
+#pragma unroll
+    for (int e = 0; e < NV * VE; ++e) {
+      float t = acc[h][e] * corr;
+#pragma unroll
+      for (int o = LPK; o < 32; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      const int v = li + LPK * (e / VE);
+      if (sub == 0 && v < nvec) sm_att[(warp * GP + h) * d + v * VE + e % VE] = t;
+    }
+    if (lane == 0) {
+      ml[warp * GP + h] = mn;
+      ml[(kAttWarps + warp) * GP + h] = l[h];
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < nh * d; i += kAttWarps * 32) {
+    const int h = i / d, e = i % d;
+    float M = -INFINITY, num = 0.f, den = 0.f;
+#pragma unroll
+    for (int w = 0; w < kAttWarps; ++w) M = fmaxf(M, ml[w * GP + h]);
+#pragma unroll
+    for (int w = 0; w < kAttWarps; ++w) {
+      const float f = pexp(ml[w * GP + h], M);
+      num = fmaf(f, sm_att[(w * GP + h) * d + e], num);
+      den = fmaf(f, ml[(kAttWarps + w) * GP + h], den);
+    }
+    const size_t row = static_cast<size_t>(b) * a.nh + h0 + h;
+    if (a.nsplit == 1) {
+      a.out[row * d + e] = M == -INFINITY ? 0.f : num / den;
+      if (a.lse && e == 0) a.lse[row] = M == -INFINITY ? -INFINITY : (M + log2f(den)) * 0.6931471805599453f;
+    } else {
+      a.ws_acc[(row * a.nsplit + sp) * d + e] = num;
+      if (e == 0) {
+        a.ws_ml[(row * a.nsplit + sp) * 2] = M;
+        a.ws_ml[(row * a.nsplit + sp) * 2 + 1] = den;
+      }
+    }
+  }
+}
+
+// Joins the splits of one (sequence, head) per CTA.
+__global__ void __launch_bounds__(128) k_paged_join(const __grid_constant__ AttArgs a) {
+  pdl_enter();
+  const size_t row = blockIdx.x;
+  const int d = a.c.d, n = a.nsplit;
+  const float* ml = a.ws_ml + row * n * 2;
+  float M = -INFINITY;
+  for (int s = 0; s < n; ++s) M = fmaxf(M, ml[2 * s]);
+  float den = 0.f;
+  for (int s = 0; s < n; ++s) den += pexp(ml[2 * s], M) * ml[2 * s + 1];
+  for (int e = threadIdx.x; e < d; e += 128) {
+    float num = 0.f;
+    for (int s = 0; s < n; ++s) num = fmaf(pexp(ml[2 * s], M), a.ws_acc[(row * n + s) * d + e], num);
+    a.out[row * d + e] = M == -INFINITY ? 0.f : num / den;
+  }
+  if (a.lse && threadIdx.x == 0) a.lse[row] = M == -INFINITY ? -INFINITY : (M + log2f(den)) * 0.6931471805599453f;
+}
+
+template <typename T, int LPK, int NV, int GP>
+int launch_att(const AttArgs& a, cudaStream_t st) {
+  const int G = a.nh / a.c.nkv, ngrp = (G + GP - 1) / GP;
+  const long long grid = static_cast<long long>(a.B) * a.c.nkv * ngrp * a.nsplit;
+  const int smem = kAttWarps * GP * (a.c.d + 2) * 4;
+  k_paged_att<T, LPK, NV, GP><<<static_cast<unsigned>(grid), kAttWarps * 32, smem, st>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) {
+    set_error("paged attention launch: %s", cudaGetErrorString(e));
+    return MTP_ERR_CUDA;
+  }
+  return MTP_OK;
+}
+
+// Heads per CTA: the queries and sums of GP heads have to stay in registers (GP * NV * VE <= 64).
+template <typename T, int LPK, int NV>
+int launch_group(const AttArgs& a, cudaStream_t st) {
+  const int G = a.nh / a.c.nkv;
+  constexpr int kMost = NV * Elem<T>::kVec >= 16 ? 4 : 8;
+  if (G == 1) return launch_att<T, LPK, NV, 1>(a, st);
+  if (G == 2) return launch_att<T, LPK, NV, 2>(a, st);
+  if (G <= 4 || kMost == 4) return launch_att<T, LPK, NV, 4>(a, st);
+  return launch_att<T, LPK, NV, kMost>(a, st);
+}
+
+template <typename T>
+int launch_type(const AttArgs& a, cudaStream_t st) {
+  const int nvec = a.c.d / Elem<T>::kVec;
+  if (nvec <= 8) return launch_group<T, 8, 1>(a, st);
+  if (nvec <= 16) return launch_group<T, 16, 1>(a, st);
+  if (nvec <= 32) return launch_group<T, 32, 1>(a, st);
+  if (nvec <= 64) return launch_group<T, 32, 2>(a, st);
+  return launch_group<T, 32, 4>(a, st);
+}
+
+// Splits of a sequence's keys: about 8 CTAs per SM over the batch, at least 64 keys each.
+int choose_splits(const Cache& c, int B, int nh, int n_list, int window, int num_sms) {
+  const long long units = static_cast<long long>(B) * nh;
+  long long keys = static_cast<long long>(n_list > 0 ? n_list : c.max_pages) << c.pshift;
+  if (window > 0 && window < keys) keys = window;
+  long long n = 8LL * num_sms * (nh / c.nkv) / units;
+  if (n > keys / 64) n = keys / 64;
+  if (n > 256) n = 256;
+  return n < 1 ? 1 : static_cast<int>(n);
+}
+
+}  // namespace pg
+
+long long paged_att_workspace(const pg::Cache& c, int B, int nh, int n_list) {
+  // a window only shortens the key range and fewer SMs take fewer splits, so this is a bound
+  const long long n = pg::choose_splits(c, B, nh, n_list, 0, pg::kMaxSms);
+  return n > 1 ? static_cast<long long>(B) * nh * n * (c.d + 2) * 4 : 0;
+}
+
+int run_paged_att(pg::AttArgs a, void* ws, int num_sms, cudaStream_t st) {
+  a.nsplit = pg::choose_splits(a.c, a.B, a.nh, a.list ? a.n_list : 0, a.window, num_sms);
+  a.ws_acc = static_cast<float*>(ws);
+  a.ws_ml = a.ws_acc + static_cast<size_t>(a.B) * a.nh * a.nsplit * a.c.d;
+  int rc = a.c.f32 ? pg::launch_type<float>(a, st) : pg::launch_type<__nv_bfloat16>(a, st);
+  if (rc || a.nsplit == 1) return rc;
+  pg::k_paged_join<<<a.B * a.nh, 128, 0, st>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) {
+    set_error("paged attention join launch: %s", cudaGetErrorString(e));
+    return MTP_ERR_CUDA;
+  }
+  return MTP_OK;
+}
+
+}  // namespace mtp

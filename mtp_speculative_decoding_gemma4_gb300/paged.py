@@ -1,0 +1,217 @@
+"""Torch-facing layer over the paged-cache entry points of the C ABI: the cache's descriptor,
+argument checks and output allocation. Marshalling only; every operator runs in libmtp.so.
+
+Outputs and workspaces come from torch's allocator on the stream that the call uses: by default
+torch's current stream of the tensors' device, else the cudaStream_t passed as `stream`.
+"""
+from __future__ import annotations
+
+from typing import Optional
+
+import torch
+
+from . import binding as B
+
+_DT = {torch.bfloat16: B.MTP_DTYPE_BF16, torch.float32: B.MTP_DTYPE_F32}
+
+
+def _need(t, name: str, dtype, ndim: int, device=None) -> torch.Tensor:
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.dim() == ndim):
+        raise ValueError(f"{name} must be a {ndim}-dimensional CUDA tensor of {dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return t
+
+
+def _need_flat(t, name: str, dtype, shape, device=None) -> torch.Tensor:
+    _need(t, name, dtype, len(shape), device)
+    if not t.is_contiguous() or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name} must be contiguous of shape {list(shape)} (got {list(t.shape)})")
+    return t
+
+
+class _On:
+    """The device and stream of a call: makes the tensors' device current and, for a stream
+    other than torch's current one, allocates on that stream."""
+
+    __slots__ = ("stream", "_dev", "_ctx")
+
+    def __init__(self, device: torch.device, stream: Optional[int]):
+        self._dev = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        self._ctx = None
+        current = torch.cuda.current_stream(device).cuda_stream
+        if stream is None:
+            stream = current
+        elif stream != current:
+            self._ctx = torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if stream else
+                                          torch.cuda.default_stream(device))
+        self.stream = stream
+
+    def __enter__(self):
+        if self._dev is not None:
+            self._dev.__enter__()
+        if self._ctx is not None:
+            self._ctx.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+        if self._dev is not None:
+            self._dev.__exit__(*exc)
+
+
+class PagedKV:
+    """A key cache in pages: k [n_pages][P][n_kv][d] (bf16 or fp32, last dimension contiguous;
+    other strides free, so a head-major cache is passed as its transposed view), v of the same
+    strides or None (V = K), block_table int32 [B][max_pages], ctx_len int32 [B]; codes int8
+    [n_pages][n_kv][d] and scales fp32 [n_pages][n_kv] hold page summaries (page_append writes
+    them, page_select scores them). block_table and ctx_len may be None for page_append alone.
+    Holds the tensors; the descriptor is made once and the buffers may change their contents."""
+
+    def __init__(self, k: torch.Tensor, block_table: Optional[torch.Tensor] = None,
+                 ctx_len: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None,
+                 codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None):
+        if not (isinstance(k, torch.Tensor) and k.is_cuda and k.dtype in _DT and k.dim() == 4):
+            raise ValueError("k must be a 4-dimensional CUDA tensor [n_pages][P][n_kv][d] of bf16 or fp32")
+        dev = k.device
+        n_pages, P, n_kv, d = k.shape
+        if v is not None:
+            _need(v, "v", k.dtype, 4, dev)
+            if v.shape != k.shape or v.stride() != k.stride():
+                raise ValueError("v must have the shape and strides of k")
+        if k.stride(3) != 1:
+            raise ValueError("the last dimension of k must be contiguous")
+        c = self.c = B.mtp_paged_kv()
+        if block_table is not None:
+            _need(block_table, "block_table", torch.int32, 2, dev)
+            if block_table.shape[1] > 1 and block_table.stride(1) != 1:
+                raise ValueError("the last dimension of block_table must be contiguous")
+            if ctx_len is None:
+                raise ValueError("block_table needs ctx_len")
+            _need_flat(ctx_len, "ctx_len", torch.int32, (block_table.shape[0],), dev)
+            c.block_table, c.ctx_len = block_table.data_ptr(), ctx_len.data_ptr()
+            c.max_pages = block_table.shape[1]
+            c.table_stride = block_table.stride(0) if block_table.shape[0] > 1 else block_table.shape[1]
+        if codes is not None or scales is not None:
+            _need_flat(codes, "codes", torch.int8, (n_pages, n_kv, d), dev)
+            _need_flat(scales, "scales", torch.float32, (n_pages, n_kv), dev)
+            c.codes, c.scales = codes.data_ptr(), scales.data_ptr()
+        c.k, c.v = k.data_ptr(), 0 if v is None else v.data_ptr()
+        # the stride of a dimension of size one is never used: any legal value
+        c.stride_page = k.stride(0) if n_pages > 1 else max(k.stride(0), P * n_kv * d)
+        c.stride_t = k.stride(1) if P > 1 else max(k.stride(1), n_kv * d)
+        c.stride_h = k.stride(2) if n_kv > 1 else d
+        c.n_pages, c.page_size, c.n_kv_head, c.head_dim, c.dtype = n_pages, P, n_kv, d, _DT[k.dtype]
+        self.k, self.v, self.block_table, self.ctx_len, self.codes, self.scales = k, v, block_table, ctx_len, codes, scales
+        self.device, self.batch = dev, 0 if block_table is None else block_table.shape[0]
+
+
+def page_plan(old_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.Tensor, free_ring: torch.Tensor,
+              ring_state: torch.Tensor, page_size: int, max_tokens: int, stream: Optional[int] = None):
+    """Takes and returns pages so that sequence b holds new_len[b] instead of old_len[b] tokens
+    (int32 [B]): updates block_table [B][max_pages] and the ring of free pages free_ring
+    [n_pages] (ring_state: head and count) in place and returns (len_out [B], slot_map
+    [max_tokens], cu_new [B + 1], state_out [2], status [4]), as mtp_page_plan describes."""
+    dev = getattr(old_len, "device", None)
+    _need_flat(old_len, "old_len", torch.int32, (None,))
+    Bn = old_len.shape[0]
+    _need_flat(new_len, "new_len", torch.int32, (Bn,), dev)
+    _need(block_table, "block_table", torch.int32, 2, dev)
+    _need_flat(free_ring, "free_ring", torch.int32, (None,), dev)
+    _need_flat(ring_state, "ring_state", torch.int32, (2,), dev)
+    if block_table.shape[0] != Bn or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError(f"block_table must be [{Bn}][max_pages] with a contiguous last dimension")
+    if max_tokens < 0:
+        raise ValueError("max_tokens must be >= 0")
+    with _On(dev, stream) as st:
+        # one allocation: slot_map (16-byte aligned), then the small outputs
+        head = (max_tokens + 3) // 4 * 4
+        buf = torch.empty(head + 2 * Bn + 7, dtype=torch.int32, device=dev)
+        slots, len_out = buf[:max_tokens], buf[head:head + Bn]
+        cu, tail = buf[head + Bn:head + 2 * Bn + 1], head + 2 * Bn + 1
+        state, status = buf[tail:tail + 2], buf[tail + 2:tail + 6]
+        base = buf.data_ptr()
+        B.mtp_page_plan(old_len.data_ptr(), new_len.data_ptr(), Bn, block_table.data_ptr(),
+                        block_table.stride(0) if Bn > 1 else block_table.shape[1], block_table.shape[1],
+                        free_ring.data_ptr(), free_ring.shape[0], ring_state.data_ptr(), page_size, max_tokens,
+                        base + 4 * head, base, base + 4 * (head + Bn), base + 4 * tail, base + 4 * (tail + 2), st)
+    return len_out, slots, cu, state, status
+
+
+def page_append(kv: PagedKV, k_new: torch.Tensor, slot_map: torch.Tensor, v_new: Optional[torch.Tensor] = None,
+                stream: Optional[int] = None) -> None:
+    """Writes row t of k_new [T][n_kv][d] (and v_new, for a cache with a V) into slot slot_map[t]
+    (int32 [T]; slots outside the cache are skipped) and, for a cache with summaries, refreshes
+    the summary of every page whose last slot is written. Rows may be strided (the last two
+    dimensions contiguous)."""
+    n_kv, d = kv.k.shape[2:]
+    for t, name in ((k_new, "k_new"), (v_new, "v_new")):
+        if t is None:
+            continue
+        _need(t, name, kv.k.dtype, 3, kv.device)
+        if t.shape[1:] != kv.k.shape[2:] or t.shape[0] != k_new.shape[0] or t.numel() and (t.stride(2) != 1 or
+                n_kv > 1 and t.stride(1) != d):
+            raise ValueError(f"{name} must be [T][{n_kv}][{d}] with contiguous rows")
+    T = k_new.shape[0]
+    _need_flat(slot_map, "slot_map", torch.int32, (T,), kv.device)
+    row = lambda t: n_kv * d if t is None or T < 2 else t.stride(0)  # noqa: E731
+    with _On(kv.device, stream) as st:
+        B.mtp_page_append(kv.c, k_new.data_ptr(), 0 if v_new is None else v_new.data_ptr(), row(k_new), row(v_new),
+                          slot_map.data_ptr(), T, st)
+
+
+def _queries(q, kv: PagedKV):
+    _need_flat(q, "q", torch.float32, (kv.batch, None, kv.c.head_dim), kv.device)
+    if kv.block_table is None:
+        raise ValueError("the cache has no block_table")
+    return q.shape[0], q.shape[1]
+
+
+def paged_attention(q: torch.Tensor, kv: PagedKV, window: int = 0, scale: float = 0.0,
+                    pages: Optional[torch.Tensor] = None, want_lse: bool = False, out: Optional[torch.Tensor] = None,
+                    stream: Optional[int] = None):
+    """Attention of one new token per sequence, q fp32 [B][n_head][d], over the paged cache: all
+    ctx_len[b] keys, the last `window` (> 0), or those of the logical pages listed in `pages`
+    (int32 [B][n_kv][n], -1: none). Returns out fp32 [B][n_head][d], with want_lse (out, lse
+    [B][n_head])."""
+    Bn, nh = _queries(q, kv)
+    n_list = 0
+    if pages is not None:
+        _need_flat(pages, "pages", torch.int32, (Bn, kv.c.n_kv_head, None), kv.device)
+        n_list = pages.shape[2]
+        if n_list < 1:
+            raise ValueError("pages must list at least one entry per KV head")
+    if out is not None:
+        _need_flat(out, "out", torch.float32, tuple(q.shape), kv.device)
+    with _On(kv.device, stream) as st:
+        if out is None:
+            out = torch.empty_like(q)
+        lse = torch.empty((Bn, nh), dtype=torch.float32, device=kv.device) if want_lse else None
+        n = B.mtp_paged_attention_workspace(kv.c, Bn, nh, n_list)
+        ws = torch.empty(n, dtype=torch.uint8, device=kv.device) if n else None
+        B.mtp_paged_attention(kv.c, q.data_ptr(), Bn, nh, window, scale, pages.data_ptr() if n_list else 0, n_list,
+                              out.data_ptr(), lse.data_ptr() if want_lse else 0, ws.data_ptr() if n else 0, n, st)
+    return (out, lse) if want_lse else out
+
+
+def page_select(q: torch.Tensor, kv: PagedKV, n_select: int, keep_first: int = 1, keep_last: int = 1,
+                out: Optional[torch.Tensor] = None, stream: Optional[int] = None) -> torch.Tensor:
+    """The n_select logical pages of the highest scores per sequence and KV head, in increasing
+    order (int32 [B][n_kv][n_select], -1 behind them): the first keep_first and last keep_last
+    pages, then those whose summaries' dot product with q is largest. A list for
+    paged_attention(pages=...)."""
+    Bn, nh = _queries(q, kv)
+    shape = (Bn, kv.c.n_kv_head, n_select)
+    if out is not None:
+        _need_flat(out, "out", torch.int32, shape, kv.device)
+    elif n_select < 1:
+        raise ValueError("n_select must be >= 1")
+    with _On(kv.device, stream) as st:
+        if out is None:
+            out = torch.empty(shape, dtype=torch.int32, device=kv.device)
+        n = B.mtp_page_select_workspace(kv.c, Bn)
+        ws = torch.empty(n, dtype=torch.uint8, device=kv.device)
+        B.mtp_page_select(kv.c, q.data_ptr(), Bn, nh, n_select, keep_first, keep_last, out.data_ptr(), ws.data_ptr(), n,
+                          st)
+    return out
