@@ -57,6 +57,11 @@ long long paged_att_workspace(const pg::Cache& c, int B, int nh, int n_list);
 long long page_select_workspace(const pg::Cache& c, int B);
 int run_paged_att(pg::AttArgs a, void* ws, int num_sms, cudaStream_t st);
 
+// Its tensor-core form (mtp_paged_tc.cu), which run_paged_att takes where it serves the shape.
+bool paged_tc_supported(const pg::Cache& c);
+long long paged_tc_workspace(const pg::Cache& c);
+int run_paged_tc(const pg::AttArgs& a, void* ws, int num_sms, cudaStream_t st);
+
 int run_page_plan(const int* old_len, const int* new_len, int B, int* table, long long table_stride, int max_pages,
                   int* ring, int n_pages, const int* state, int pshift, int max_tokens, int* len_out, int* slots,
                   int* cu_new, int* state_out, int* status, int num_sms, cudaStream_t st);

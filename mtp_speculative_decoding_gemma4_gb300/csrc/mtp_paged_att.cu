@@ -36,8 +36,8 @@ __device__ __forceinline__ void unpack<float>(const uint4& u, float* out) {
   out[3] = __uint_as_float(u.w);
 }
 
-// exp2 of x - m with a row that has no key yet (m = -inf) giving 0
-__device__ __forceinline__ float pexp(float x, float m) { return m == -INFINITY ? 0.f : exp2f(x - m); }
+// exp2 of x - m; with no key yet (m = -inf, x = -inf) 0
+__device__ __forceinline__ float pexp(float x, float m) { return exp2f(x - (m == -INFINITY ? 0.f : m)); }
 
 template <typename T, int LPK, int NV, int GP>
 __global__ void __launch_bounds__(kAttWarps * 32) k_paged_att(const __grid_constant__ AttArgs a) {
@@ -189,8 +189,8 @@ __global__ void __launch_bounds__(kAttWarps * 32) k_paged_att(const __grid_const
     }
     const size_t row = static_cast<size_t>(b) * a.nh + h0 + h;
     if (a.nsplit == 1) {
-      a.out[row * d + e] = M == -INFINITY ? 0.f : num / den;
-      if (a.lse && e == 0) a.lse[row] = M == -INFINITY ? -INFINITY : (M + log2f(den)) * 0.6931471805599453f;
+      a.out[row * d + e] = den == 0.f ? 0.f : num / den;  // 0: nothing attended
+      if (a.lse && e == 0) a.lse[row] = den == 0.f ? -INFINITY : (M + log2f(den)) * 0.6931471805599453f;
     } else {
       a.ws_acc[(row * a.nsplit + sp) * d + e] = num;
       if (e == 0) {
@@ -214,9 +214,9 @@ __global__ void __launch_bounds__(128) k_paged_join(const __grid_constant__ AttA
   for (int e = threadIdx.x; e < d; e += 128) {
     float num = 0.f;
     for (int s = 0; s < n; ++s) num = fmaf(pexp(ml[2 * s], M), a.ws_acc[(row * n + s) * d + e], num);
-    a.out[row * d + e] = M == -INFINITY ? 0.f : num / den;
+    a.out[row * d + e] = den == 0.f ? 0.f : num / den;  // 0: nothing attended
   }
-  if (a.lse && threadIdx.x == 0) a.lse[row] = M == -INFINITY ? -INFINITY : (M + log2f(den)) * 0.6931471805599453f;
+  if (a.lse && threadIdx.x == 0) a.lse[row] = den == 0.f ? -INFINITY : (M + log2f(den)) * 0.6931471805599453f;
 }
 
 template <typename T, int LPK, int NV, int GP>
@@ -268,12 +268,14 @@ int choose_splits(const Cache& c, int B, int nh, int n_list, int window, int num
 }  // namespace pg
 
 long long paged_att_workspace(const pg::Cache& c, int B, int nh, int n_list) {
+  if (paged_tc_supported(c)) return paged_tc_workspace(c);
   // a window only shortens the key range and fewer SMs take fewer splits, so this is a bound
   const long long n = pg::choose_splits(c, B, nh, n_list, 0, pg::kMaxSms);
   return n > 1 ? static_cast<long long>(B) * nh * n * (c.d + 2) * 4 : 0;
 }
 
 int run_paged_att(pg::AttArgs a, void* ws, int num_sms, cudaStream_t st) {
+  if (paged_tc_supported(a.c)) return run_paged_tc(a, ws, num_sms, st);
   a.nsplit = pg::choose_splits(a.c, a.B, a.nh, a.list ? a.n_list : 0, a.window, num_sms);
   a.ws_acc = static_cast<float*>(ws);
   a.ws_ml = a.ws_acc + static_cast<size_t>(a.B) * a.nh * a.nsplit * a.c.d;
