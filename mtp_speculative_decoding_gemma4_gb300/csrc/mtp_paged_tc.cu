@@ -18,12 +18,13 @@
 // numbered through and dealt evenly over one CTA per SM, whatever the lengths. A unit that crosses
 // CTAs leaves unnormalised sums, (max, exp-sum) per part; k_paged_tc_join adds them in CTA order.
 //
-// One CTA: warp 4 loads (pages found through the block table; pairs of [128 keys][64 dims] boxes,
-// 128-byte swizzle, a ring of 6 pairs = 192 KB, about 64-160 KB in flight), one thread of warp 5
-// issues the MMAs (whichever of the next score pair and the next sum is ready), warps 0..3 own
-// one key per thread for the softmax and one dim per thread and 128-dim block for the sums. The
-// softmax reference is the first tile's maximum and moves only when a score exceeds it by 2^8
-// (one barrier per tile agrees on that), so running sums are rarely rescaled.
+// One CTA: warp 8 loads (pages found through the block table; slots of [KT keys][128 dims] in two
+// 128-byte-swizzled boxes, a ring of 192 KB), one thread of warp 9 issues the MMAs (whichever of
+// the next score slot and the next sum is ready), and two warpgroups take the tiles in turn, each
+// with a softmax reference and sums of its own (one thread per key, then one per dim of each
+// 128-dim block); they are joined at the end of a segment. The reference is a maximum that moves
+// only when a score exceeds it by 2^8 (one barrier per tile agrees on that), so running sums are
+// rarely rescaled.
 // Rows that hold no attended key but lie in an attended page are set to zero before the sums
 // (0 * NaN would not vanish). Waits are bounded; a CTA that gives up writes NaN.
 #include <cudaTypedefs.h>
@@ -38,18 +39,15 @@ namespace pgt {
 using pg::AttArgs;
 using pg::Cache;
 
-constexpr int kTile = 128;                 // keys per tile (tcgen05 M)
-constexpr int kBox = kTile * 128;          // one box: 128 keys x 64 dims of bf16
-constexpr int kPair = 2 * kBox;            // 128 dims
-constexpr int kRing = 6;                   // pairs in the ring
-constexpr int kThreadsTc = 192;
+constexpr int kRingBytes = 192 * 1024;     // loaded keys
+constexpr int kThreadsTc = 320;            // two warpgroups for the softmax, a load and an MMA warp
 constexpr int kInfo = 8;                   // tiles whose row positions are kept
 constexpr long long kSpin = 4000000000LL;  // about 2 s
 
 struct Args {
   AttArgs a;
   int granule;   // keys dealt as a whole
-  int rows;      // keys per TMA box (min(P, 128))
+  int rows;      // keys per TMA box (min(P, keys per tile))
   int grid;      // CTAs that share the granules
   int ngrp;      // head groups per KV head
   int* meta;     // [grid][4]: first output row, heads, last CTA of the unit a CTA starts and does not end
@@ -105,16 +103,26 @@ __device__ __forceinline__ void tma_4d(unsigned dst, const CUtensorMap* map, int
       : "memory");
 }
 // Shared-memory descriptors, 128-byte swizzle: 8-row groups are 1024 bytes apart; in the MN-major
-// form (rows = K index, 64 MN elements per row) `lead` is the distance of the next 64.
-__device__ __forceinline__ unsigned long long desc(unsigned addr, unsigned lead) {
-  return static_cast<unsigned long long>((addr & 0x3FFFFu) >> 4) | (static_cast<unsigned long long>(lead >> 4) << 16) |
-         (static_cast<unsigned long long>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// form (rows = K index, 64 MN elements per row) `lead` is the distance of the next 64. The low
+// word holds the address, so a step is one 32-bit addition.
+__device__ __forceinline__ constexpr unsigned desc_lo(unsigned addr, unsigned lead) {
+  return ((addr & 0x3FFFFu) >> 4) | ((lead >> 4) << 16);
 }
-__device__ __forceinline__ void mma(unsigned d, unsigned long long a, unsigned long long b, unsigned idesc, bool acc) {
+constexpr unsigned kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+// One elected thread issues (its caller's branch is made by elect.sync, which keeps the operands
+// in uniform registers: 36 cycles per instruction instead of 53, measured; any other choice of
+// the thread makes the compiler guard every instruction).
+__device__ __forceinline__ void mma(unsigned d, unsigned a, unsigned b, unsigned idesc, bool acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+      "{\n .reg .pred p;\n .reg .b64 da, db;\n mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(kDescHi)
       : "memory");
+}
+__device__ __forceinline__ bool elect() {
+  unsigned e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(e));
+  return e != 0;
 }
 __device__ __forceinline__ void commit(unsigned bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
@@ -160,16 +168,23 @@ __device__ __forceinline__ void split3(float v, __nv_bfloat16& hi, __nv_bfloat16
 template <int D, int NH>
 struct Lay {
   static constexpr int N = NH == 4 ? 16 : 32;           // MMA columns (3 NH used, the rest ignored)
-  static constexpr int NP = D / 128;                    // pairs per tile and operand
+  static constexpr int NP = D / 128;                    // 128-dim slots per tile and operand
+  // keys per tile: 64 where a tile of 128 keys would leave too little of the ring for loads in
+  // flight (d = 512) or the query buffers no room; the MMA's other 64 rows are then not used
+  static constexpr int KT = D == 512 || (D == 256 && NH == 8) ? 64 : 128;
+  static constexpr int box = KT * 128;                  // KT keys x 64 dims
+  static constexpr int slot = 2 * box;
+  static constexpr int ring = kRingBytes / slot;        // 6 or 12 slots
   static constexpr int RB = NH == 4 ? 2048 : 3072;      // bytes of one 64-element block of the N side
-  static constexpr int PB = D == 512 && NH == 8 ? 1 : 2;  // probability buffers
-  static constexpr int q = kRing * kPair;
-  static constexpr int p = q + (D / 64) * RB;
-  static constexpr int bars = p + PB * 2 * RB;
-  static constexpr int nbars = 2 * kRing + 2 * 5 + 2 + kInfo;
+  static constexpr int QB = D == 512 ? 1 : 2;           // query buffers
+  static constexpr int PBY = KT / 64 * RB;              // bytes of one probability buffer
+  static constexpr int q = kRingBytes;
+  static constexpr int p = q + QB * (D / 64) * RB;
+  static constexpr int bars = p + 2 * PBY;
+  static constexpr int nbars = 2 * ring + 2 * 6 + 1 + kInfo;
   static constexpr int info = bars + nbars * 8;          // [kInfo][16] first position of each row group, or -1
-  static constexpr int red = info + kInfo * 16 * 4;      // [4][8] + [4][8] floats
-  static constexpr int misc = red + 2 * 4 * 8 * 4;       // tensor-memory address, dead word, scan words
+  static constexpr int red = info + kInfo * 16 * 4;      // per warpgroup [4][8] maxima, [4][8] sums, [8] references
+  static constexpr int misc = red + 2 * 72 * 4;          // tensor-memory address, dead word, scan words
   static constexpr int total = misc + 64 * 4 + 1024;     // + alignment
   static constexpr int cols = 4 * NP * N;                // 2 score and 2 sum regions of NP * N columns
 };
@@ -216,6 +231,10 @@ struct Walk {
     off = s.e;
     return true;
   }
+  // one past the last key number of a segment (its first is s.a * granule)
+  __device__ __forceinline__ int end(const Args& g, const Seg& s) const {
+    return min(g.a.list ? g.a.n_list << g.a.c.pshift : s.hi - s.base, s.e * g.granule);
+  }
 };
 
 template <int D, int NH>
@@ -223,18 +242,17 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     k_paged_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
                const __grid_constant__ Args g) {
   using LY = Lay<D, NH>;
-  constexpr int N = LY::N, NP = LY::NP, RB = LY::RB, PB = LY::PB;
+  constexpr int N = LY::N, NP = LY::NP, RB = LY::RB, KT = LY::KT, kRing = LY::ring, QB = LY::QB;
   extern __shared__ __align__(1024) char sm_raw[];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   char* sm = sm_raw + ((1024u - (sa(sm_raw) & 1023u)) & 1023u);
   const unsigned base = sa(sm);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const unsigned full0 = base + LY::bars, empty0 = full0 + 8 * kRing, sfull0 = empty0 + 8 * kRing, sfree0 = sfull0 + 16,
-                 pfull0 = sfree0 + 16, ofull0 = pfull0 + 16, ofree0 = ofull0 + 16, qfull = ofree0 + 16, drain = qfull + 8,
-                 ifull0 = drain + 8;
+                 pfull0 = sfree0 + 16, ofull0 = pfull0 + 16, ofree0 = ofull0 + 16, qfull0 = ofree0 + 16,
+                 drain = qfull0 + 16, ifull0 = drain + 8;
   int* info = reinterpret_cast<int*>(sm + LY::info);
-  float* red = reinterpret_cast<float*>(sm + LY::red);
-  int* misc = reinterpret_cast<int*>(sm + LY::misc);  // 0: tensor memory, 1: dead, 2..4: b, sub, off, 8..: scan
+  int* misc = reinterpret_cast<int*>(sm + LY::misc);  // 0: tensor memory, 1: dead, 2..5: b, sub, off, per, 8..: scan
   volatile int* dead = misc + 1;
   const AttArgs& a = g.a;
   const Cache& c = a.c;
@@ -252,8 +270,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       mbar_init(pfull0 + 8 * i, 4);
       mbar_init(ofull0 + 8 * i, 1);
       mbar_init(ofree0 + 8 * i, 4);
+      mbar_init(qfull0 + 8 * i, 4);
     }
-    mbar_init(qfull, 4);
     mbar_init(drain, 1);
     for (int i = 0; i < kInfo; ++i) mbar_init(ifull0 + 8 * i, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -263,9 +281,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sa(misc)), "r"(LY::cols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  // the query and probability blocks' unused rows
-  for (int i = tid; i < (LY::bars - LY::q) / 16; i += kThreadsTc)
-    reinterpret_cast<uint4*>(sm + LY::q)[i] = make_uint4(0, 0, 0, 0);
   fence_before();
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
@@ -306,16 +321,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       }
     }
     if (tid == 0) misc[5] = per;
-    // sequences with nothing to attend have no granule: out 0, lse -inf
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-      if (Walk::count(g, b, lo, hi, bs) == 0) {
-        for (int i = tid; i < a.nh * D; i += kThreadsTc) a.out[static_cast<size_t>(b) * a.nh * D + i] = 0.f;
-        if (a.lse)
-          for (int i = tid; i < a.nh; i += kThreadsTc) a.lse[static_cast<size_t>(b) * a.nh + i] = -INFINITY;
-      }
-    }
   }
-  fence_async();
+  // a unit that starts here and goes on in the next CTAs
+  int* meta = g.meta + 4 * blockIdx.x;
+  if (tid == 0) meta[1] = 0;
   __syncthreads();
   fence_after();
   const unsigned tmem = *reinterpret_cast<volatile unsigned*>(misc);
@@ -327,21 +336,18 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     w.off = misc[4];
     w.load(g);
   }
-  // a unit that starts here and goes on in the next CTAs
-  int* meta = g.meta + 4 * blockIdx.x;
-  if (tid == 0) meta[1] = 0;
 
-  if (work && warp == 4) {
+  if (warp == 8) {
     // ---------------- loads
-    const int R = g.rows, ng = kTile / R, P = 1 << c.pshift;
-    int pc = 0, tt = 0;
+    const int R = g.rows, ng = KT / R, P = 1 << c.pshift;
+    int pc = 0, tt = 0, slot = 0;  // slots and tiles so far, the next slot and the ring's phase there
+    unsigned phase = 0;
     bool ok = true;
     Walk::Seg s;
     while (ok && w.next(g, subs, s)) {
-      const int kvh = s.sub / g.ngrp, e1 = a.list ? a.n_list << c.pshift : s.hi - s.base;
+      const int kvh = s.sub / g.ngrp, i1 = w.end(g, s);
       const int* list = a.list ? a.list + (static_cast<size_t>(s.b) * c.nkv + kvh) * a.n_list : nullptr;
-      const int i1 = min(e1, s.e * g.granule);
-      for (int i0 = s.a * g.granule; i0 < i1 && ok; i0 += kTile, ++tt) {
+      for (int i0 = s.a * g.granule; i0 < i1 && ok; i0 += KT, ++tt) {
         // lane l < ng: row group l of the tile, its physical page and first position
         int page = -1, pos = -1, off = 0;
         const int i = i0 + lane * R;
@@ -359,28 +365,32 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             if (page >= 0) pos = (lp << c.pshift) + off;
           }
         }
-        for (int j = 0; j < PT; ++j, ++pc) {
-          const int slot = pc % kRing;
+        for (int j = 0; j < PT; ++j) {
           const unsigned bar = full0 + 8 * slot;
           if (pc >= kRing) {
-            if (lane == 0) ok = wait_bar(empty0 + 8 * slot, ((pc / kRing) - 1) & 1, dead);
+            if (lane == 0) ok = wait_bar(empty0 + 8 * slot, phase ^ 1, dead);
             ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
             if (!ok) break;
           }
           if (j == 0) {
-            // the info slot's tile is long summed: its last pair was freed kRing pairs ago
+            // the info slot's tile is long summed: its last slot was freed a ring ago
             if (lane < ng) info[(tt % kInfo) * 16 + lane] = pos;
             __syncwarp();
             if (lane == 0) mbar_arrive(ifull0 + 8 * (tt % kInfo));
           }
-          if (lane == 0) mbar_expect_tx(bar, kPair);
+          if (lane == 0) mbar_expect_tx(bar, LY::slot);
           __syncwarp();
           if (lane < ng) {
             const int x = (j % NP) * 128;
-            const unsigned dst = base + slot * kPair + lane * R * 128;
+            const unsigned dst = base + slot * LY::slot + lane * R * 128;
             const CUtensorMap* map = j < NP ? &mapK : &mapV;
             tma_4d(dst, map, x, off, kvh, page, bar);
-            tma_4d(dst + kBox, map, x + 64, off, kvh, page, bar);
+            tma_4d(dst + LY::box, map, x + 64, off, kvh, page, bar);
+          }
+          ++pc;
+          if (++slot == kRing) {
+            slot = 0;
+            phase ^= 1;
           }
         }
       }
@@ -392,66 +402,88 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       while (!try_wait(full0 + 8 * (i % kRing), (i / kRing) & 1) && clock64() - t0 < kSpin) {
       }
     }
-  } else if (work && warp == 5) {
-    if (lane == 0) {
-      // ---------------- MMA issue
+  } else if (warp == 9) {
+    if (elect()) {
+      // ---------------- MMA issue: the next score tile or the next sum tile, whichever is ready.
+      // A tile's slots of one operand are NP neighbours (the ring is a multiple of NP).
       const unsigned idS = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<unsigned>(N >> 3) << 17) | (8u << 24);
       const unsigned idO = idS | (1u << 15);
       const unsigned tS = tmem, tO = tmem + 2 * NP * N;
-      int tq = 0, iq = 0, tp = 0, left = 0, nseg = 0;  // next score tile and pair, next sum tile
-      bool more = true;
+      const unsigned kd = desc_lo(base, 16), vd = desc_lo(base, LY::box), qd = desc_lo(base + LY::q, 16),
+                     pd = desc_lo(base + LY::p, 16);
+      // tiles whose scores / sums are issued, their first slots and the ring's phases there
+      int tq = 0, tp = 0, left = 0, nseg = 0, wq = 0, nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;
+      int sq = 0, sp = own_v ? NP : 0;
+      unsigned fq = 0, fp = 0, owner = 0;  // owner bit i: the warpgroup of tile tp + i
+      bool more = work;
       long long t0 = clock64();
       while (more || tp < tq) {
         bool did = false;
-        if (more && tq <= tp + 1) {
-          bool ready = true;
-          if (left == 0) {
-            Walk::Seg s;
-            more = w.next(g, subs, s);
-            if (more) {
-              const int e1 = a.list ? a.n_list << c.pshift : s.hi - s.base;
-              left = (min(e1, s.e * g.granule) - s.a * g.granule + kTile - 1) / kTile;
-              ++nseg;
-            }
-            continue;
+        if (more && left == 0) {
+          Walk::Seg s;
+          more = w.next(g, subs, s);
+          if (more) {
+            left = (w.end(g, s) - s.a * g.granule + KT - 1) / KT;
+            wq = 0;
+            ++nseg;
           }
-          const int pc = tq * PT + iq, slot = pc % kRing;
-          if (iq == 0)
-            ready = test_wait(qfull, (nseg - 1) & 1) && (tq < 2 || test_wait(sfree0 + 8 * (tq & 1), ((tq >> 1) - 1) & 1));
-          if (ready && test_wait(full0 + 8 * slot, (pc / kRing) & 1)) {
-            fence_after();
-            const unsigned kp = base + slot * kPair, qp = base + LY::q + 2 * iq * RB;
-            const unsigned d = tS + ((tq & 1) * NP + iq) * N;
+          continue;
+        }
+        if (more && tq < tp + 3) {
+          const int use = wq ? nq1 : nq0, qb = (nseg - 1) % QB;
+          bool ready = test_wait(qfull0 + 8 * qb, ((nseg - 1) / QB) & 1) &&
+                       (use == 0 || test_wait(sfree0 + 8 * wq, (use - 1) & 1));
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-              mma(d, desc(kp + (x >> 2) * kBox + (x & 3) * 32, 16), desc(qp + (x >> 2) * RB + (x & 3) * 32, 16), idS, x > 0);
-            if (own_v) commit(empty0 + 8 * slot);
-            if (++iq == NP) {
-              commit(sfull0 + 8 * (tq & 1));
-              iq = 0;
-              ++tq;
-              --left;
+          for (int i = 0; i < NP; ++i) ready = ready && test_wait(full0 + 8 * (sq + i), fq);
+          if (ready) {
+            fence_after();
+            const unsigned k0 = kd + sq * (LY::slot >> 4), q0 = qd + qb * ((D / 64) * RB >> 4), d = tS + wq * NP * N;
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+#pragma unroll
+              for (int x = 0; x < 8; ++x)
+                mma(d + i * N, k0 + ((i * LY::slot + (x >> 2) * LY::box + (x & 3) * 32) >> 4),
+                    q0 + (((2 * i + (x >> 2)) * RB + (x & 3) * 32) >> 4), idS, x > 0);
+            }
+            if (own_v) {
+#pragma unroll
+              for (int i = 0; i < NP; ++i) commit(empty0 + 8 * (sq + i));
+            }
+            commit(sfull0 + 8 * wq);
+            owner = (owner & ~(1u << (tq - tp))) | (static_cast<unsigned>(wq) << (tq - tp));
+            ++tq;
+            --left;
+            if (wq) ++nq1; else ++nq0;
+            wq ^= 1;
+            if ((sq += PT) >= kRing) {
+              sq -= kRing;
+              fq ^= 1;
             }
             did = true;
           }
         }
         if (!did && tp < tq) {
-          const unsigned pb = tp % PB, pph = (tp / PB) & 1;
-          if (test_wait(pfull0 + 8 * pb, pph) && (tp < 2 || test_wait(ofree0 + 8 * (tp & 1), ((tp >> 1) - 1) & 1))) {
+          const int wp = owner & 1, use = wp ? np1 : np0;
+          if (test_wait(pfull0 + 8 * wp, use & 1) && (use == 0 || test_wait(ofree0 + 8 * wp, (use - 1) & 1))) {
+            if (own_v)
+              for (int i = 0; i < NP; ++i) wait_bar(full0 + 8 * (sp + i), fp, dead);
             fence_after();
-            for (int m = 0; m < NP; ++m) {
-              const int pc = tp * PT + (own_v ? NP : 0) + m, slot = pc % kRing;
-              if (own_v && !wait_bar(full0 + 8 * slot, (pc / kRing) & 1, dead)) break;
-              fence_after();
-              const unsigned vp = base + slot * kPair, pp = base + LY::p + pb * 2 * RB;
-              const unsigned d = tO + ((tp & 1) * NP + m) * N;
+            const unsigned v0 = vd + sp * (LY::slot >> 4), p0 = pd + wp * (LY::PBY >> 4), d = tO + wp * NP * N;
 #pragma unroll
-              for (int x = 0; x < 8; ++x)
-                mma(d, desc(vp + x * 2048, kBox), desc(pp + (x >> 2) * RB + (x & 3) * 32, 16), idO, x > 0);
-              commit(empty0 + 8 * slot);
+            for (int i = 0; i < NP; ++i) {
+#pragma unroll
+              for (int x = 0; x < KT / 16; ++x)
+                mma(d + i * N, v0 + ((i * LY::slot + x * 2048) >> 4), p0 + (((x >> 2) * RB + (x & 3) * 32) >> 4), idO, x > 0);
+              commit(empty0 + 8 * (sp + i));
             }
-            commit(ofull0 + 8 * (tp & 1));
+            commit(ofull0 + 8 * wp);
+            owner >>= 1;
             ++tp;
+            if (wp) ++np1; else ++np0;
+            if ((sp += PT) >= kRing) {
+              sp -= kRing;
+              fp ^= 1;
+            }
             did = true;
           }
         }
@@ -472,16 +504,22 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       }
     }
     __syncwarp();
-  } else if (work) {
-    // ---------------- softmax, sums, outputs: thread = key of a tile, dim of a 128-dim block
-    const unsigned tw = tmem + (static_cast<unsigned>(32 * warp) << 16);
-    const unsigned tS = tw, tO = tw + 2 * NP * N;
-    auto bar128 = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
-    Walk::Seg s, sn;
+  } else {
+    // ---------------- softmax, sums, outputs. A warpgroup takes every other tile of a segment
+    // with a reference, sums and outputs of its own: thread = key of a tile, and dim of each
+    // 128-dim block of the sums. The two are joined at the segment's end.
+    const int wg = warp >> 2, wt = tid & 127, ww = warp & 3;
+    float* red = reinterpret_cast<float*>(sm + LY::red) + 72 * wg;
+    const float* red0 = reinterpret_cast<const float*>(sm + LY::red);
+    const unsigned tw = tmem + (static_cast<unsigned>(32 * ww) << 16);
+    const unsigned tS = tw + wg * NP * N, tO = tw + (2 + wg) * NP * N;
+    char* const pbuf = sm + LY::p + wg * LY::PBY;
+    auto bar_wg = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); };
+    auto bar_all = [] { asm volatile("bar.sync 3, 256;" ::: "memory"); };
     // the queries of a unit as three bf16 terms per value: row term * NH + head
-    auto put_q = [&](const Walk::Seg& u) {
+    auto put_q = [&](const Walk::Seg& u, int buf) {
       const int kvh = u.sub / g.ngrp, h0 = kvh * G + (u.sub % g.ngrp) * NH, nh = min(NH, G - (u.sub % g.ngrp) * NH);
-      for (int i = tid; i < NH * (D / 8); i += 128) {
+      for (int i = wt; i < NH * (D / 8); i += 128) {
         const int h = i / (D / 8), ch = i % (D / 8);
         float v[8];
         if (h < nh) {
@@ -498,19 +536,24 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 #pragma unroll
         for (int term = 0; term < 3; ++term) {
           const int r = term * NH + h;
-          *reinterpret_cast<uint4*>(sm + LY::q + (ch >> 3) * RB + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) =
+          *reinterpret_cast<uint4*>(sm + LY::q + (buf * (D / 64) + (ch >> 3)) * RB + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) =
               *reinterpret_cast<const uint4*>(t[term]);
         }
       }
       fence_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(qfull);
+      if (lane == 0) mbar_arrive(qfull0 + 8 * buf);
     };
-    bool have = w.next(g, subs, s);
-    put_q(s);
-    int tt = 0;  // tiles so far in this CTA
     const int R = g.rows;
+    Walk::Seg s, sn;
+    bool have = work && w.next(g, subs, s);
+    if (have && wg == 0) put_q(s, 0);
+    int tt = 0, own = 0, seg = 0;  // tiles of the CTA before this segment, tiles of this warpgroup, segments
     while (have) {
+      const bool more = w.next(g, subs, sn);
+      // with two query buffers the next unit's queries are ready before its first tile; the
+      // buffer's last products ended with the segment before this one
+      if (QB == 2 && more && wg == 1) put_q(sn, (seg + 1) & 1);
       float acc[NP][NH], m[NH], l[NH];
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
@@ -519,46 +562,47 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 #pragma unroll
         for (int b = 0; b < NP; ++b) acc[b][h] = 0.f;
       }
-      auto take_o = [&](int t) {  // the sums of tile t
-        wait_bar(ofull0 + 8 * (t & 1), (t >> 1) & 1, dead);
+      auto take_o = [&](int use) {  // the sums of this warpgroup's tile `use`
+        wait_bar(ofull0 + 8 * wg, use & 1, dead);
         __syncwarp();
         fence_after();
 #pragma unroll
         for (int b = 0; b < NP; ++b) {
           float v[3 * NH];
-          ld_terms<NH>(tO + ((t & 1) * NP + b) * N, v);
+          ld_terms<NH>(tO + b * N, v);
           ld_wait();
 #pragma unroll
           for (int h = 0; h < NH; ++h) acc[b][h] += (v[2 * NH + h] + v[NH + h]) + v[h];
         }
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(ofree0 + 8 * (t & 1));
+        if (lane == 0) mbar_arrive(ofree0 + 8 * wg);
       };
-      const int e1 = a.list ? a.n_list << c.pshift : s.hi - s.base;
-      const int nt = (min(e1, s.e * g.granule) - s.a * g.granule + kTile - 1) / kTile;
-      for (int t = 0; t < nt; ++t, ++tt) {
-        bool pending = t > 0;  // the sums of tile tt - 1 are not in acc yet
-        wait_bar(ifull0 + 8 * (tt % kInfo), (tt / kInfo) & 1, dead);
-        const int pb = info[(tt % kInfo) * 16 + tid / R], pos = pb + (tid & (R - 1));
+      const int nt = (w.end(g, s) - s.a * g.granule + KT - 1) / KT;
+      for (int t = wg; t < nt; t += 2, ++own) {
+        const int at = tt + t;
+        wait_bar(ifull0 + 8 * (at % kInfo), (at / kInfo) & 1, dead);
+        const int pb = wt < KT ? info[(at % kInfo) * 16 + wt / R] : -1, pos = pb + (wt & (R - 1));
         const bool on = pb >= 0 && pos >= s.lo && pos < s.hi;
-        wait_bar(sfull0 + 8 * (tt & 1), (tt >> 1) & 1, dead);
+        wait_bar(sfull0 + 8 * wg, own & 1, dead);
         __syncwarp();
         fence_after();
         float sc[NH];
 #pragma unroll
         for (int h = 0; h < NH; ++h) sc[h] = 0.f;
+        if (KT == 128 || ww < KT / 32) {
 #pragma unroll
-        for (int b = 0; b < NP; ++b) {
-          float v[3 * NH];
-          ld_terms<NH>(tS + ((tt & 1) * NP + b) * N, v);
-          ld_wait();
+          for (int b = 0; b < NP; ++b) {
+            float v[3 * NH];
+            ld_terms<NH>(tS + b * N, v);
+            ld_wait();
 #pragma unroll
-          for (int h = 0; h < NH; ++h) sc[h] += (v[2 * NH + h] + v[NH + h]) + v[h];
+            for (int h = 0; h < NH; ++h) sc[h] += (v[2 * NH + h] + v[NH + h]) + v[h];
+          }
         }
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(sfree0 + 8 * (tt & 1));
+        if (lane == 0) mbar_arrive(sfree0 + 8 * wg);
         bool up = false;
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
@@ -566,21 +610,19 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           up = up || (on && !(sc[h] <= m[h] + 8.f));  // NaN counts
         }
         int any;
-        asm volatile("{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n bar.red.or.pred q, 1, 128, p;\n selp.s32 %0, 1, 0, q;\n}"
+        asm volatile("{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n bar.red.or.pred q, %2, 128, p;\n selp.s32 %0, 1, 0, q;\n}"
                      : "=r"(any)
-                     : "r"(up ? 1 : 0)
+                     : "r"(up ? 1 : 0), "r"(1 + wg)
                      : "memory");
+        // the sums of this warpgroup's last tile: its probability buffer is free after them
+        if (t > wg) take_o(own - 1);
         if (any) {  // a new reference: the maximum so far of every head
-          if (pending) {
-            take_o(tt - 1);
-            pending = false;
-          }
 #pragma unroll
           for (int h = 0; h < NH; ++h) {
             const float x = warp_max(sc[h]);
-            if (lane == 0) red[warp * 8 + h] = x;
+            if (lane == 0) red[ww * 8 + h] = x;
           }
-          bar128();
+          bar_wg();
 #pragma unroll
           for (int h = 0; h < NH; ++h) {
             const float mn = fmaxf(fmaxf(fmaxf(red[h], red[8 + h]), fmaxf(red[16 + h], red[24 + h])), m[h]);
@@ -590,83 +632,126 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 #pragma unroll
             for (int b = 0; b < NP; ++b) acc[b][h] *= corr;
           }
-          bar128();
+          bar_wg();
         }
-        if (PB == 1 && pending) {  // the one probability buffer is free once the last sums are done
-          take_o(tt - 1);
-          pending = false;
-        }
-        char* pt = sm + LY::p + (tt % PB) * 2 * RB + (tid >> 6) * RB + (tid & 7) * 2;
-        const int ch = (tid & 63) >> 3;
+        if (KT == 128 || wt < KT) {
+          char* pt = pbuf + (wt >> 6) * RB + (wt & 7) * 2;
+          const int ch = (wt & 63) >> 3;
 #pragma unroll
-        for (int h = 0; h < NH; ++h) {
-          const float p = exp2f(sc[h] - (m[h] == -INFINITY ? 0.f : m[h]));
-          l[h] += p;
-          __nv_bfloat16 x[3];
-          split3(p, x[0], x[1], x[2]);
+          for (int h = 0; h < NH; ++h) {
+            const float p = exp2f(sc[h] - (m[h] == -INFINITY ? 0.f : m[h]));
+            l[h] += p;
+            __nv_bfloat16 x[3];
+            split3(p, x[0], x[1], x[2]);
 #pragma unroll
-          for (int term = 0; term < 3; ++term) {
-            const int r = term * NH + h;
-            *reinterpret_cast<__nv_bfloat16*>(pt + r * 128 + ((ch ^ (r & 7)) << 4)) = x[term];
+            for (int term = 0; term < 3; ++term) {
+              const int r = term * NH + h;
+              *reinterpret_cast<__nv_bfloat16*>(pt + r * 128 + ((ch ^ (r & 7)) << 4)) = x[term];
+            }
           }
-        }
-        if (pb >= 0 && !on) {  // a stale row of an attended page
-          for (int j = 0; j < NP; ++j) {
-            const int pc = tt * PT + (own_v ? NP : 0) + j, slot = pc % kRing;
-            if (own_v && !wait_bar(full0 + 8 * slot, (pc / kRing) & 1, dead)) break;
+          if (pb >= 0 && !on) {  // a stale row of an attended page
+            for (int j = 0; j < NP; ++j) {
+              const int pc = at * PT + (own_v ? NP : 0) + j, slot = pc % kRing;
+              if (own_v && !wait_bar(full0 + 8 * slot, (pc / kRing) & 1, dead)) break;
 #pragma unroll
-            for (int x = 0; x < 16; ++x)
-              *reinterpret_cast<uint4*>(sm + slot * kPair + (x >> 3) * kBox + tid * 128 + (x & 7) * 16) =
-                  make_uint4(0, 0, 0, 0);
+              for (int x = 0; x < 16; ++x)
+                *reinterpret_cast<uint4*>(sm + slot * LY::slot + (x >> 3) * LY::box + wt * 128 + (x & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+            }
           }
+          fence_async();
         }
-        fence_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(pfull0 + 8 * (tt % PB));
-        if (pending) take_o(tt - 1);
+        if (lane == 0) mbar_arrive(pfull0 + 8 * wg);
       }
-      have = w.next(g, subs, sn);
-      if (have) put_q(sn);  // every score product of this unit is done
-      if (nt > 0) take_o(tt - 1);
-      // ---- normalise or leave the part for the join
+      // one query buffer: it is free once the last tile's scores are done
+      if (QB == 1 && more && wg == ((nt - 1) & 1)) put_q(sn, 0);
+      if (nt > wg) take_o(own - 1);
+      // ---- join the warpgroups; normalise, or leave the part for k_paged_tc_join
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
         const float x = warp_sum(l[h]);
-        if (lane == 0) red[32 + warp * 8 + h] = x;
+        if (lane == 0) red[32 + ww * 8 + h] = x;
+        if (wt == 0) red[64 + h] = m[h];
       }
-      bar128();
-      const int kvh = s.sub / g.ngrp, h0 = kvh * G + (s.sub % g.ngrp) * NH, nh = min(NH, G - (s.sub % g.ngrp) * NH);
-      const size_t row0 = static_cast<size_t>(s.b) * a.nh + h0;
-      const bool whole = s.a == 0 && s.e == s.n;
-      const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + (s.a == 0 ? 1 : 0)) * NH;
+      bar_all();
+      float den[NH];
       const float bad = *dead ? NAN : 0.f;
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
-        if (h >= nh) break;
-        const float den = (red[32 + h] + red[40 + h]) + (red[48 + h] + red[56 + h]) + bad;
-        if (whole) {
-          const float inv = den == 0.f ? 0.f : 1.f / den;  // 0: nothing attended
+        const float m0 = red0[64 + h], m1 = red0[72 + 64 + h], M = fmaxf(m0, m1), ref = M == -INFINITY ? 0.f : M;
+        const float f0 = exp2f(m0 - ref), f1 = exp2f(m1 - ref);
+        const float* r0 = red0 + 32 + h;
+        const float* r1 = red0 + 72 + 32 + h;
+        den[h] = f0 * ((r0[0] + r0[8]) + (r0[16] + r0[24])) + f1 * ((r1[0] + r1[8]) + (r1[16] + r1[24])) + bad;
+        m[h] = M;
 #pragma unroll
-          for (int b = 0; b < NP; ++b) a.out[(row0 + h) * D + b * 128 + tid] = acc[b][h] * inv;
-          if (a.lse && tid == 0) a.lse[row0 + h] = den == 0.f ? -INFINITY : (m[h] + log2f(den)) * 0.6931471805599453f;
-        } else {
+        for (int b = 0; b < NP; ++b) acc[b][h] *= wg == 0 ? f0 : f1;
+      }
+      if (nt > 1) {
+        // warpgroup 1's sums through the idle probability buffers, XV values per thread at a time
+        constexpr int XV = 2 * LY::PBY / 512;
+        float* x = reinterpret_cast<float*>(sm + LY::p);
 #pragma unroll
-          for (int b = 0; b < NP; ++b) a.ws_acc[(part + h) * D + b * 128 + tid] = acc[b][h];
-          if (tid == 0) {
-            a.ws_ml[(part + h) * 2] = m[h];
-            a.ws_ml[(part + h) * 2 + 1] = den;
+        for (int i0 = 0; i0 < NP * NH; i0 += XV) {
+          if (wg == 1) {
+#pragma unroll
+            for (int i = i0; i < i0 + XV && i < NP * NH; ++i) x[(i - i0) * 128 + wt] = acc[i / NH][i % NH];
+          }
+          bar_all();
+          if (wg == 0) {
+#pragma unroll
+            for (int i = i0; i < i0 + XV && i < NP * NH; ++i) acc[i / NH][i % NH] += x[(i - i0) * 128 + wt];
+          }
+          bar_all();
+        }
+      } else {
+        bar_all();
+      }
+      const int kvh = s.sub / g.ngrp, h0 = kvh * G + (s.sub % g.ngrp) * NH, nh = min(NH, G - (s.sub % g.ngrp) * NH);
+      const size_t row0 = static_cast<size_t>(s.b) * a.nh + h0;
+      const bool whole = s.a == 0 && s.e == s.n;
+      if (wg == 0) {
+        const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + (s.a == 0 ? 1 : 0)) * NH;
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          if (h >= nh) break;
+          if (whole) {
+            const float inv = den[h] == 0.f ? 0.f : 1.f / den[h];  // 0: nothing attended
+#pragma unroll
+            for (int b = 0; b < NP; ++b) a.out[(row0 + h) * D + b * 128 + wt] = acc[b][h] * inv;
+            if (a.lse && wt == 0)
+              a.lse[row0 + h] = den[h] == 0.f ? -INFINITY : (m[h] + log2f(den[h])) * 0.6931471805599453f;
+          } else {
+#pragma unroll
+            for (int b = 0; b < NP; ++b) a.ws_acc[(part + h) * D + b * 128 + wt] = acc[b][h];
+            if (wt == 0) {
+              a.ws_ml[(part + h) * 2] = m[h];
+              a.ws_ml[(part + h) * 2 + 1] = den[h];
+            }
           }
         }
+        if (!whole && s.a == 0 && wt == 0) {
+          // a unit that goes on in the next CTA ends this CTA's granules
+          const int first = static_cast<int>(blockIdx.x) * per + (per - (s.e - s.a));
+          meta[0] = static_cast<int>(row0);
+          meta[1] = nh;
+          meta[2] = (first + s.n - 1) / per;
+        }
       }
-      if (!whole && s.a == 0 && tid == 0) {
-        // the unit's granules start at this segment's first, so its last lies in this CTA
-        const int first = static_cast<int>(blockIdx.x) * per + (per - (s.e - s.a));
-        meta[0] = static_cast<int>(row0);
-        meta[1] = nh;
-        meta[2] = (first + s.n - 1) / per;
-      }
-      bar128();  // red is free again
+      tt += nt;
+      ++seg;
       s = sn;
+      have = more;
+    }
+    // sequences with nothing to attend have no granule: out 0, lse -inf
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+      int lo, hi, bs;
+      if (Walk::count(g, b, lo, hi, bs) == 0) {
+        for (int i = tid; i < a.nh * D; i += 256) a.out[static_cast<size_t>(b) * a.nh * D + i] = 0.f;
+        if (a.lse)
+          for (int i = tid; i < a.nh; i += 256) a.lse[static_cast<size_t>(b) * a.nh + i] = -INFINITY;
+      }
     }
     fence_before();
   }
@@ -770,6 +855,7 @@ template <int D, int NH>
 int launch(const Args& g, cudaStream_t st) {
   using LY = Lay<D, NH>;
   static_assert(LY::total <= 232448, "shared memory of one CTA");
+  static_assert(LY::KT == 64 || LY::KT == 128, "keys per tile");
   static_assert(LY::cols <= 512 && (LY::cols & (LY::cols - 1)) == 0, "tensor memory columns");
   CUtensorMap mk, mv;
   int rc = make_map(&mk, g.a.c, g.a.c.k, g.rows);
@@ -821,13 +907,14 @@ int run_paged_tc(const pg::AttArgs& a, void* ws, int num_sms, cudaStream_t st) {
   memset(&g, 0, sizeof(g));
   g.a = a;
   const int P = 1 << a.c.pshift, G = a.nh / a.c.nkv, NH = G <= 4 ? 4 : 8;
-  g.rows = P < kTile ? P : kTile;
+  const int tile = a.c.d == 512 || (a.c.d == 256 && NH == 8) ? 64 : 128;  // Lay::KT
+  g.rows = P < tile ? P : tile;
   g.ngrp = (G + NH - 1) / NH;
   // the most keys a unit can have; with few of them, smaller granules spread them over the SMs
   long long keys = static_cast<long long>(a.list ? a.n_list : a.c.max_pages) * P;
   if (!a.list && a.window > 0 && a.window + g.rows < keys) keys = a.window + g.rows;
   const long long units = static_cast<long long>(a.B) * a.c.nkv * g.ngrp;
-  g.granule = kTile;
+  g.granule = 128;
   while (g.granule > 32 && g.granule > g.rows && units * ((keys + g.granule - 1) / g.granule) < num_sms) g.granule /= 2;
   const long long most = units * ((keys + g.granule - 1) / g.granule);
   if (most > INT32_MAX) {
