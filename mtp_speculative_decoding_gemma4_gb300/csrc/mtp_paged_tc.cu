@@ -18,8 +18,8 @@
 // numbered through and dealt evenly over one CTA per SM, whatever the lengths. A unit that crosses
 // CTAs leaves unnormalised sums, (max, exp-sum) per part; k_paged_tc_join adds them in CTA order.
 //
-// One CTA: warp 8 loads (pages found through the block table; slots of [KT keys][128 dims] in two
-// 128-byte-swizzled boxes, a ring of 192 KB), one thread of warp 9 issues the MMAs (whichever of
+// One CTA: warp 10 finds the tiles' pages through the block table,
+// warp 8 loads them (slots of [KT keys][128 dims] in two 128-byte-swizzled boxes, a ring of 192 KB), one thread of warp 9 issues the MMAs (whichever of
 // the next score slot and the next sum is ready), and two warpgroups take the tiles in turn, each
 // with a softmax reference and sums of its own (one thread per key, then one per dim of each
 // 128-dim block); they are joined at the end of a segment. The reference is a maximum that moves
@@ -40,13 +40,14 @@ using pg::AttArgs;
 using pg::Cache;
 
 constexpr int kRingBytes = 192 * 1024;     // loaded keys
-constexpr int kThreadsTc = 320;            // two warpgroups for the softmax, a load and an MMA warp
-constexpr int kInfo = 8;                   // tiles whose row positions are kept
+constexpr int kThreadsTc = 352;            // two warpgroups for the softmax; load, MMA and find warps
+constexpr int kAhead = 8;                  // tiles that the find warp runs ahead of the load warp
+constexpr int kInfo = 2 * kAhead;          // tiles whose pages and positions are kept
 constexpr long long kSpin = 4000000000LL;  // about 2 s
 
 struct Args {
   AttArgs a;
-  int granule;   // keys dealt as a whole
+  int gshift;    // log2 of the keys of a granule, which are dealt as a whole
   int rows;      // keys per TMA box (min(P, keys per tile))
   int grid;      // CTAs that share the granules
   int ngrp;      // head groups per KV head
@@ -143,6 +144,12 @@ __device__ __forceinline__ void ld4(unsigned t, float* v) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(t));
 }
+__device__ __forceinline__ void st4(unsigned t, const float* v) {
+  const unsigned* r = reinterpret_cast<const unsigned*>(v);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(t), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3])
+               : "memory");
+}
 __device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // The three term columns of NH heads at tensor-memory address t: v[3 * NH].
@@ -170,7 +177,7 @@ struct Lay {
   static constexpr int N = NH == 4 ? 16 : 32;           // MMA columns (3 NH used, the rest ignored)
   static constexpr int NP = D / 128;                    // 128-dim slots per tile and operand
   // keys per tile: 64 where a tile of 128 keys would leave too little of the ring for loads in
-  // flight (d = 512) or the query buffers no room; the MMA's other 64 rows are then not used
+  // flight (d = 512) or the query buffers no room
   static constexpr int KT = D == 512 || (D == 256 && NH == 8) ? 64 : 128;
   static constexpr int box = KT * 128;                  // KT keys x 64 dims
   static constexpr int slot = 2 * box;
@@ -182,10 +189,11 @@ struct Lay {
   static constexpr int p = q + QB * (D / 64) * RB;
   static constexpr int bars = p + 2 * PBY;
   static constexpr int nbars = 2 * ring + 2 * 6 + 1 + kInfo;
-  static constexpr int info = bars + nbars * 8;          // [kInfo][16] first position of each row group, or -1
-  static constexpr int red = info + kInfo * 16 * 4;      // per warpgroup [4][8] maxima, [4][8] sums, [8] references
-  static constexpr int misc = red + 2 * 72 * 4;          // tensor-memory address, dead word, scan words
-  static constexpr int total = misc + 64 * 4 + 1024;     // + alignment
+  // per tile: first position of each row group (-1: none), its physical page, the KV head
+  static constexpr int info = bars + nbars * 8;
+  static constexpr int red = info + kInfo * 33 * 4;      // per warpgroup [4][8] maxima, [4][8] sums, [8] references
+  static constexpr int misc = red + 2 * 72 * 4;          // tensor-memory address, dead word, tiles begun
+  static constexpr int total = misc + 16 + 1024;     // + alignment
   static constexpr int cols = 4 * NP * N;                // 2 score and 2 sum regions of NP * N columns
 };
 
@@ -203,9 +211,51 @@ struct Walk {
       base = lo & ~(g.rows - 1);
       keys = hi - base;
     }
-    return (keys + g.granule - 1) / g.granule;
+    return (keys + (1 << g.gshift) - 1) >> g.gshift;
   }
   __device__ __forceinline__ void load(const Args& g) { n = count(g, b, lo, hi, base); }
+  // This CTA's granules and the unit they begin in: the whole warp, a lane for 1/32 of the
+  // sequences. Returns the granules per CTA.
+  __device__ __forceinline__ int locate(const Args& g, int subs) {
+    const int lane = threadIdx.x & 31, per_b = (g.a.B + 31) >> 5, b0 = min(g.a.B, lane * per_b), b1 = min(g.a.B, b0 + per_b);
+    int mine = 0;
+#pragma unroll 4
+    for (int i = b0; i < b1; ++i) mine += count(g, i, lo, hi, base);
+    mine *= subs;
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const int total = __shfl_sync(0xffffffffu, incl, 31), per = (total + g.grid - 1) / g.grid;
+    r = min(total, static_cast<int>(blockIdx.x) * per);
+    r1 = min(total, r + per);
+    b = sub = off = n = 0;
+    if (r >= r1) return per;
+    const int f = __ffs(__ballot_sync(0xffffffffu, incl > r)) - 1;
+    if (lane == f) {
+      int at = r - (incl - mine);
+      for (b = b0;; ++b) {
+        n = count(g, b, lo, hi, base);
+        if (at < n * subs) break;
+        at -= n * subs;
+      }
+      if (subs > 1) {
+        sub = at / n;
+        at -= sub * n;
+      }
+      off = at;
+    }
+    b = __shfl_sync(0xffffffffu, b, f);
+    sub = __shfl_sync(0xffffffffu, sub, f);
+    off = __shfl_sync(0xffffffffu, off, f);
+    n = __shfl_sync(0xffffffffu, n, f);
+    lo = __shfl_sync(0xffffffffu, lo, f);
+    hi = __shfl_sync(0xffffffffu, hi, f);
+    base = __shfl_sync(0xffffffffu, base, f);
+    return per;
+  }
   struct Seg {
     int b, sub, a, e, n, lo, hi, base;
   };
@@ -233,7 +283,7 @@ struct Walk {
   }
   // one past the last key number of a segment (its first is s.a * granule)
   __device__ __forceinline__ int end(const Args& g, const Seg& s) const {
-    return min(g.a.list ? g.a.n_list << g.a.c.pshift : s.hi - s.base, s.e * g.granule);
+    return min(g.a.list ? g.a.n_list << g.a.c.pshift : s.hi - s.base, s.e << g.gshift);
   }
 };
 
@@ -252,8 +302,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                  pfull0 = sfree0 + 16, ofull0 = pfull0 + 16, ofree0 = ofull0 + 16, qfull0 = ofree0 + 16,
                  drain = qfull0 + 16, ifull0 = drain + 8;
   int* info = reinterpret_cast<int*>(sm + LY::info);
-  int* misc = reinterpret_cast<int*>(sm + LY::misc);  // 0: tensor memory, 1: dead, 2..5: b, sub, off, per, 8..: scan
-  volatile int* dead = misc + 1;
+  int* misc = reinterpret_cast<int*>(sm + LY::misc);  // 0: tensor memory, 1: dead, 2: begun
+  volatile int *dead = misc + 1, *begun = misc + 2;  // begun: tiles that the load warp has begun
   const AttArgs& a = g.a;
   const Cache& c = a.c;
   const bool own_v = c.v != nullptr;
@@ -275,84 +325,41 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     mbar_init(drain, 1);
     for (int i = 0; i < kInfo; ++i) mbar_init(ifull0 + 8 * i, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    misc[1] = 0;
+    misc[1] = misc[2] = 0;
   }
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sa(misc)), "r"(LY::cols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   fence_before();
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-
-  // ---- this CTA's share: granules [r0, r1) of all units
-  Walk w;
-  {
-    const int per_b = (a.B + kThreadsTc - 1) / kThreadsTc, b0 = min(a.B, tid * per_b), b1 = min(a.B, b0 + per_b);
-    int lo, hi, bs, mine = 0;
-    for (int b = b0; b < b1; ++b) mine += Walk::count(g, b, lo, hi, bs) * subs;
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 31) misc[8 + warp] = incl;
-    __syncthreads();
-    int before = incl - mine, total = 0;
-#pragma unroll
-    for (int i = 0; i < kThreadsTc / 32; ++i) {
-      if (i < warp) before += misc[8 + i];
-      total += misc[8 + i];
-    }
-    const int per = (total + g.grid - 1) / g.grid;
-    w.r = min(total, static_cast<int>(blockIdx.x) * per);
-    w.r1 = min(total, w.r + per);
-    if (w.r < w.r1 && w.r >= before && w.r < before + mine) {
-      int at = before;
-      for (int b = b0; b < b1; ++b) {
-        const int n = Walk::count(g, b, lo, hi, bs);
-        if (w.r < at + n * subs) {
-          misc[2] = b;
-          misc[3] = (w.r - at) / n;
-          misc[4] = (w.r - at) % n;
-          break;
-        }
-        at += n * subs;
-      }
-    }
-    if (tid == 0) misc[5] = per;
-  }
-  // a unit that starts here and goes on in the next CTAs
-  int* meta = g.meta + 4 * blockIdx.x;
-  if (tid == 0) meta[1] = 0;
   __syncthreads();
   fence_after();
   const unsigned tmem = *reinterpret_cast<volatile unsigned*>(misc);
-  const bool work = w.r < w.r1;
-  const int per = misc[5];
-  if (work) {
-    w.b = misc[2];
-    w.sub = misc[3];
-    w.off = misc[4];
-    w.load(g);
-  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  if (warp == 8) {
-    // ---------------- loads
-    const int R = g.rows, ng = KT / R, P = 1 << c.pshift;
-    int pc = 0, tt = 0, slot = 0;  // slots and tiles so far, the next slot and the ring's phase there
-    unsigned phase = 0;
+  // ---- this CTA's share: granules [r, r1) of all units (every warp for itself: no exchange)
+  Walk w;
+  const int per = w.locate(g, subs);
+  const bool work = w.r < w.r1;
+  // a unit that starts here and goes on in the next CTAs
+  int* meta = g.meta + 4 * blockIdx.x;
+  if (tid == 0) meta[1] = 0;
+
+  if (warp == 10) {
+    // ---------------- pages: looks up the tiles' pages up to kAhead tiles before they are loaded
+    // (a lane per row group, several tiles at once)
+    const int R = g.rows, ng = KT / R, P = 1 << c.pshift, nb = min(32 / ng, kAhead);
+    int tt = 0;
     bool ok = true;
     Walk::Seg s;
     while (ok && w.next(g, subs, s)) {
       const int kvh = s.sub / g.ngrp, i1 = w.end(g, s);
       const int* list = a.list ? a.list + (static_cast<size_t>(s.b) * c.nkv + kvh) * a.n_list : nullptr;
-      for (int i0 = s.a * g.granule; i0 < i1 && ok; i0 += KT, ++tt) {
-        // lane l < ng: row group l of the tile, its physical page and first position
-        int page = -1, pos = -1, off = 0;
-        const int i = i0 + lane * R;
-        if (lane < ng && i < i1) {
-          int lp;
+      for (int i0 = (s.a << g.gshift); i0 < i1 && ok; i0 += nb * KT) {
+        int page = -1, pos = -1;
+        const int i = i0 + lane * R;  // the tiles' row groups follow one another
+        if (lane < nb * ng && i < i1) {
+          int lp, off;
           if (list) {
             lp = list[i >> c.pshift];
             off = i & (P - 1);
@@ -365,25 +372,67 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             if (page >= 0) pos = (lp << c.pshift) + off;
           }
         }
-        for (int j = 0; j < PT; ++j) {
-          const unsigned bar = full0 + 8 * slot;
-          if (pc >= kRing) {
-            if (lane == 0) ok = wait_bar(empty0 + 8 * slot, phase ^ 1, dead);
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        for (int j = 0; j < nb && i0 + j * KT < i1; ++j, ++tt) {
+          // the load warp has begun tile tt - kAhead, so tile tt - kInfo is done with
+          if (tt >= kAhead) {
+            const long long t0 = clock64();
+            while (*begun < tt - kAhead + 1 && ok) {
+              if (*dead || clock64() - t0 > kSpin) {
+                *dead = 1;
+                ok = false;
+              }
+            }
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
           }
-          if (j == 0) {
-            // the info slot's tile is long summed: its last slot was freed a ring ago
-            if (lane < ng) info[(tt % kInfo) * 16 + lane] = pos;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(ifull0 + 8 * (tt % kInfo));
+          int* in = info + (tt % kInfo) * 33;
+          if (lane / ng == j) {
+            in[lane - j * ng] = pos;
+            in[16 + lane - j * ng] = page;
           }
-          if (lane == 0) mbar_expect_tx(bar, LY::slot);
+          if (lane == 0) in[32] = kvh;
           __syncwarp();
-          if (lane < ng) {
-            const int x = (j % NP) * 128;
-            const unsigned dst = base + slot * LY::slot + lane * R * 128;
-            const CUtensorMap* map = j < NP ? &mapK : &mapV;
+          if (lane == 0) mbar_arrive(ifull0 + 8 * (tt % kInfo));
+        }
+      }
+    }
+    if (ok) {  // the end
+      if (tt >= kAhead) {
+        const long long t0 = clock64();
+        while (*begun < tt - kAhead + 1 && !*dead && clock64() - t0 < kSpin) {
+        }
+      }
+      __syncwarp();
+      if (lane == 0) {
+        info[(tt % kInfo) * 33 + 32] = -1;
+        mbar_arrive(ifull0 + 8 * (tt % kInfo));
+      }
+    }
+  } else if (warp == 8) {
+    // ---------------- loads
+    if (elect()) {
+      const int R = g.rows, ng = KT / R, P = 1 << c.pshift;
+      int pc = 0, slot = 0;  // slots so far, the next slot and the ring's phase there
+      unsigned phase = 0;
+      bool ok = true;
+      for (int tt = 0; ok; ++tt) {
+        if (!wait_bar(ifull0 + 8 * (tt % kInfo), (tt / kInfo) & 1, dead)) break;
+        const int* in = info + (tt % kInfo) * 33;
+        const int kvh = in[32];
+        if (kvh < 0) break;
+        for (int j = 0; j < PT; ++j) {
+          const unsigned bar = full0 + 8 * slot;
+          if (pc >= kRing && !wait_bar(empty0 + 8 * slot, phase ^ 1, dead)) {
+            ok = false;
+            break;
+          }
+          if (j == 0) *begun = tt + 1;
+          mbar_expect_tx(bar, LY::slot);
+          const int x = (j < NP ? j : j - NP) * 128;
+          const CUtensorMap* map = j < NP ? &mapK : &mapV;
+          unsigned dst = base + slot * LY::slot;
+          for (int r = 0; r < ng; ++r, dst += R * 128) {
+            const int pos = in[r], off = pos < 0 ? 0 : pos & (P - 1), page = in[16 + r];  // page -1: zeros
             tma_4d(dst, map, x, off, kvh, page, bar);
             tma_4d(dst + LY::box, map, x + 64, off, kvh, page, bar);
           }
@@ -394,20 +443,21 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           }
         }
       }
-    }
-    // no copy may be in flight when the CTA ends
-    __syncwarp();
-    for (int i = max(0, pc - kRing); i < pc; ++i) {
-      const long long t0 = clock64();
-      while (!try_wait(full0 + 8 * (i % kRing), (i / kRing) & 1) && clock64() - t0 < kSpin) {
+      // no copy may be in flight when the CTA ends
+      for (int i = max(0, pc - kRing); i < pc; ++i) {
+        const long long t0 = clock64();
+        while (!try_wait(full0 + 8 * (i % kRing), (i / kRing) & 1) && clock64() - t0 < kSpin) {
+        }
       }
     }
+    __syncwarp();
   } else if (warp == 9) {
     if (elect()) {
       // ---------------- MMA issue: the next score tile or the next sum tile, whichever is ready.
       // A tile's slots of one operand are NP neighbours (the ring is a multiple of NP).
-      const unsigned idS = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<unsigned>(N >> 3) << 17) | (8u << 24);
-      const unsigned idO = idS | (1u << 15);
+      // fp32 += bf16 x bf16, N columns, M = KT (scores) or 128 with A MN-major (sums)
+      const unsigned id = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<unsigned>(N >> 3) << 17);
+      const unsigned idS = id | (static_cast<unsigned>(KT >> 4) << 24), idO = id | (1u << 15) | (8u << 24);
       const unsigned tS = tmem, tO = tmem + 2 * NP * N;
       const unsigned kd = desc_lo(base, 16), vd = desc_lo(base, LY::box), qd = desc_lo(base + LY::q, 16),
                      pd = desc_lo(base + LY::p, 16);
@@ -423,13 +473,38 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           Walk::Seg s;
           more = w.next(g, subs, s);
           if (more) {
-            left = (w.end(g, s) - s.a * g.granule + KT - 1) / KT;
+            left = (w.end(g, s) - (s.a << g.gshift) + KT - 1) / KT;
             wq = 0;
             ++nseg;
           }
           continue;
         }
-        if (more && tq < tp + 3) {
+        if (tp < tq) {
+          const int wp = owner & 1, use = wp ? np1 : np0;
+          if (test_wait(pfull0 + 8 * wp, use & 1) && (use == 0 || test_wait(ofree0 + 8 * wp, (use - 1) & 1))) {
+            if (own_v)
+              for (int i = 0; i < NP; ++i) wait_bar(full0 + 8 * (sp + i), fp, dead);
+            fence_after();
+            const unsigned v0 = vd + sp * (LY::slot >> 4), p0 = pd + wp * (LY::PBY >> 4), d = tO + wp * NP * N;
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+#pragma unroll
+              for (int x = 0; x < KT / 16; ++x)
+                mma(d + i * N, v0 + ((i * LY::slot + x * 2048) >> 4), p0 + (((x >> 2) * RB + (x & 3) * 32) >> 4), idO, x > 0);
+              commit(empty0 + 8 * (sp + i));
+            }
+            commit(ofull0 + 8 * wp);
+            owner >>= 1;
+            ++tp;
+            if (wp) ++np1; else ++np0;
+            if ((sp += PT) >= kRing) {
+              sp -= kRing;
+              fp ^= 1;
+            }
+            did = true;
+          }
+        }
+        if (!did && more && tq < tp + 3) {
           const int use = wq ? nq1 : nq0, qb = (nseg - 1) % QB;
           bool ready = test_wait(qfull0 + 8 * qb, ((nseg - 1) / QB) & 1) &&
                        (use == 0 || test_wait(sfree0 + 8 * wq, (use - 1) & 1));
@@ -462,31 +537,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             did = true;
           }
         }
-        if (!did && tp < tq) {
-          const int wp = owner & 1, use = wp ? np1 : np0;
-          if (test_wait(pfull0 + 8 * wp, use & 1) && (use == 0 || test_wait(ofree0 + 8 * wp, (use - 1) & 1))) {
-            if (own_v)
-              for (int i = 0; i < NP; ++i) wait_bar(full0 + 8 * (sp + i), fp, dead);
-            fence_after();
-            const unsigned v0 = vd + sp * (LY::slot >> 4), p0 = pd + wp * (LY::PBY >> 4), d = tO + wp * NP * N;
-#pragma unroll
-            for (int i = 0; i < NP; ++i) {
-#pragma unroll
-              for (int x = 0; x < KT / 16; ++x)
-                mma(d + i * N, v0 + ((i * LY::slot + x * 2048) >> 4), p0 + (((x >> 2) * RB + (x & 3) * 32) >> 4), idO, x > 0);
-              commit(empty0 + 8 * (sp + i));
-            }
-            commit(ofull0 + 8 * wp);
-            owner >>= 1;
-            ++tp;
-            if (wp) ++np1; else ++np0;
-            if ((sp += PT) >= kRing) {
-              sp -= kRing;
-              fp ^= 1;
-            }
-            did = true;
-          }
-        }
         if (did) {
           t0 = clock64();
         } else if (*dead) {
@@ -514,8 +564,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     const unsigned tw = tmem + (static_cast<unsigned>(32 * ww) << 16);
     const unsigned tS = tw + wg * NP * N, tO = tw + (2 + wg) * NP * N;
     char* const pbuf = sm + LY::p + wg * LY::PBY;
+    // this thread's key of a tile: the accumulator row of its tensor-memory lane (M = 64 fills
+    // the lower half of each warp's lanes)
+    const int key = KT == 128 ? wt : 16 * ww + lane;
+    const bool has = KT == 128 || lane < 16;
     auto bar_wg = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); };
-    auto bar_all = [] { asm volatile("bar.sync 3, 256;" ::: "memory"); };
     // the queries of a unit as three bf16 terms per value: row term * NH + head
     auto put_q = [&](const Walk::Seg& u, int buf) {
       const int kvh = u.sub / g.ngrp, h0 = kvh * G + (u.sub % g.ngrp) * NH, nh = min(NH, G - (u.sub % g.ngrp) * NH);
@@ -578,11 +631,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(ofree0 + 8 * wg);
       };
-      const int nt = (w.end(g, s) - s.a * g.granule + KT - 1) / KT;
+      const int nt = (w.end(g, s) - (s.a << g.gshift) + KT - 1) / KT;
       for (int t = wg; t < nt; t += 2, ++own) {
         const int at = tt + t;
         wait_bar(ifull0 + 8 * (at % kInfo), (at / kInfo) & 1, dead);
-        const int pb = wt < KT ? info[(at % kInfo) * 16 + wt / R] : -1, pos = pb + (wt & (R - 1));
+        const int pb = has ? info[(at % kInfo) * 33 + key / R] : -1, pos = pb + (key & (R - 1));
         const bool on = pb >= 0 && pos >= s.lo && pos < s.hi;
         wait_bar(sfull0 + 8 * wg, own & 1, dead);
         __syncwarp();
@@ -590,15 +643,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         float sc[NH];
 #pragma unroll
         for (int h = 0; h < NH; ++h) sc[h] = 0.f;
-        if (KT == 128 || ww < KT / 32) {
 #pragma unroll
-          for (int b = 0; b < NP; ++b) {
-            float v[3 * NH];
-            ld_terms<NH>(tS + b * N, v);
-            ld_wait();
+        for (int b = 0; b < NP; ++b) {
+          float v[3 * NH];
+          ld_terms<NH>(tS + b * N, v);
+          ld_wait();
 #pragma unroll
-            for (int h = 0; h < NH; ++h) sc[h] += (v[2 * NH + h] + v[NH + h]) + v[h];
-          }
+          for (int h = 0; h < NH; ++h) sc[h] += (v[2 * NH + h] + v[NH + h]) + v[h];
         }
         fence_before();
         __syncwarp();
@@ -634,9 +685,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           }
           bar_wg();
         }
-        if (KT == 128 || wt < KT) {
-          char* pt = pbuf + (wt >> 6) * RB + (wt & 7) * 2;
-          const int ch = (wt & 63) >> 3;
+        if (has) {
+          char* pt = pbuf + (key >> 6) * RB + (key & 7) * 2;
+          const int ch = (key & 63) >> 3;
 #pragma unroll
           for (int h = 0; h < NH; ++h) {
             const float p = exp2f(sc[h] - (m[h] == -INFINITY ? 0.f : m[h]));
@@ -655,7 +706,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
               if (own_v && !wait_bar(full0 + 8 * slot, (pc / kRing) & 1, dead)) break;
 #pragma unroll
               for (int x = 0; x < 16; ++x)
-                *reinterpret_cast<uint4*>(sm + slot * LY::slot + (x >> 3) * LY::box + wt * 128 + (x & 7) * 16) =
+                *reinterpret_cast<uint4*>(sm + slot * LY::slot + (x >> 3) * LY::box + key * 128 + (x & 7) * 16) =
                     make_uint4(0, 0, 0, 0);
             }
           }
@@ -667,51 +718,64 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       // one query buffer: it is free once the last tile's scores are done
       if (QB == 1 && more && wg == ((nt - 1) & 1)) put_q(sn, 0);
       if (nt > wg) take_o(own - 1);
-      // ---- join the warpgroups; normalise, or leave the part for k_paged_tc_join
+      // ---- warpgroup 0 joins the two (the other's sums come through tensor memory, where both
+      // have the same lanes) and normalises, or leaves the part for k_paged_tc_join
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
         const float x = warp_sum(l[h]);
         if (lane == 0) red[32 + ww * 8 + h] = x;
         if (wt == 0) red[64 + h] = m[h];
       }
-      bar_all();
-      float den[NH];
+      if (wg == 1) {
+        if (nt > 1) {
+#pragma unroll
+          for (int b = 0; b < NP; ++b)
+#pragma unroll
+            for (int h = 0; h < NH; h += 4) st4(tO + b * NH + h, acc[b] + h);
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        }
+        fence_before();
+        asm volatile("bar.arrive 3, 256;" ::: "memory");
+        asm volatile("bar.sync 4, 256;" ::: "memory");  // warpgroup 0 has read them
+        tt += nt;
+        ++seg;
+        s = sn;
+        have = more;
+        continue;
+      }
+      asm volatile("bar.sync 3, 256;" ::: "memory");
+      fence_after();
+      float den[NH], f1[NH];
       const float bad = *dead ? NAN : 0.f;
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
-        const float m0 = red0[64 + h], m1 = red0[72 + 64 + h], M = fmaxf(m0, m1), ref = M == -INFINITY ? 0.f : M;
-        const float f0 = exp2f(m0 - ref), f1 = exp2f(m1 - ref);
+        const float m1 = red0[72 + 64 + h], M = fmaxf(m[h], m1), ref = M == -INFINITY ? 0.f : M;
+        const float f0 = exp2f(m[h] - ref);
+        f1[h] = exp2f(m1 - ref);
         const float* r0 = red0 + 32 + h;
         const float* r1 = red0 + 72 + 32 + h;
-        den[h] = f0 * ((r0[0] + r0[8]) + (r0[16] + r0[24])) + f1 * ((r1[0] + r1[8]) + (r1[16] + r1[24])) + bad;
+        den[h] = f0 * ((r0[0] + r0[8]) + (r0[16] + r0[24])) + f1[h] * ((r1[0] + r1[8]) + (r1[16] + r1[24])) + bad;
         m[h] = M;
 #pragma unroll
-        for (int b = 0; b < NP; ++b) acc[b][h] *= wg == 0 ? f0 : f1;
+        for (int b = 0; b < NP; ++b) acc[b][h] *= f0;
       }
       if (nt > 1) {
-        // warpgroup 1's sums through the idle probability buffers, XV values per thread at a time
-        constexpr int XV = 2 * LY::PBY / 512;
-        float* x = reinterpret_cast<float*>(sm + LY::p);
 #pragma unroll
-        for (int i0 = 0; i0 < NP * NH; i0 += XV) {
-          if (wg == 1) {
+        for (int b = 0; b < NP; ++b) {
+          float v[NH];
 #pragma unroll
-            for (int i = i0; i < i0 + XV && i < NP * NH; ++i) x[(i - i0) * 128 + wt] = acc[i / NH][i % NH];
-          }
-          bar_all();
-          if (wg == 0) {
+          for (int h = 0; h < NH; h += 4) ld4(tO + NP * N + b * NH + h, v + h);
+          ld_wait();
 #pragma unroll
-            for (int i = i0; i < i0 + XV && i < NP * NH; ++i) acc[i / NH][i % NH] += x[(i - i0) * 128 + wt];
-          }
-          bar_all();
+          for (int h = 0; h < NH; ++h) acc[b][h] = fmaf(f1[h], v[h], acc[b][h]);
         }
-      } else {
-        bar_all();
+        fence_before();
       }
+      asm volatile("bar.arrive 4, 256;" ::: "memory");
       const int kvh = s.sub / g.ngrp, h0 = kvh * G + (s.sub % g.ngrp) * NH, nh = min(NH, G - (s.sub % g.ngrp) * NH);
       const size_t row0 = static_cast<size_t>(s.b) * a.nh + h0;
       const bool whole = s.a == 0 && s.e == s.n;
-      if (wg == 0) {
+      {
         const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + (s.a == 0 ? 1 : 0)) * NH;
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
@@ -914,9 +978,10 @@ int run_paged_tc(const pg::AttArgs& a, void* ws, int num_sms, cudaStream_t st) {
   long long keys = static_cast<long long>(a.list ? a.n_list : a.c.max_pages) * P;
   if (!a.list && a.window > 0 && a.window + g.rows < keys) keys = a.window + g.rows;
   const long long units = static_cast<long long>(a.B) * a.c.nkv * g.ngrp;
-  g.granule = 128;
-  while (g.granule > 32 && g.granule > g.rows && units * ((keys + g.granule - 1) / g.granule) < num_sms) g.granule /= 2;
-  const long long most = units * ((keys + g.granule - 1) / g.granule);
+  g.gshift = 7;
+  const auto granules = [&] { return units * ((keys + (1 << g.gshift) - 1) >> g.gshift); };
+  while (g.gshift > 5 && (1 << g.gshift) > g.rows && granules() < num_sms) --g.gshift;
+  const long long most = granules();
   if (most > INT32_MAX) {
     set_error("too many keys: B * heads * max_pages * page_size = %lld", units * keys);
     return MTP_ERR_UNSUPPORTED_SHAPE;
