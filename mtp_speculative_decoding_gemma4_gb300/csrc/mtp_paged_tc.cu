@@ -48,7 +48,7 @@ constexpr long long kSpin = 4000000000LL;  // about 2 s
 struct Args {
   AttArgs a;
   int gshift;    // log2 of the keys of a granule, which are dealt as a whole
-  int rows;      // keys per TMA box (min(P, keys per tile))
+  int rshift;    // log2 of the keys per TMA box (min(P, keys per tile))
   int grid;      // CTAs that share the granules
   int ngrp;      // head groups per KV head
   int* meta;     // [grid][4]: first output row, heads, last CTA of the unit a CTA starts and does not end
@@ -179,6 +179,7 @@ struct Lay {
   // keys per tile: 64 where a tile of 128 keys would leave too little of the ring for loads in
   // flight (d = 512) or the query buffers no room
   static constexpr int KT = D == 512 || (D == 256 && NH == 8) ? 64 : 128;
+  static constexpr int KS = KT == 64 ? 6 : 7;           // log2 KT
   static constexpr int box = KT * 128;                  // KT keys x 64 dims
   static constexpr int slot = 2 * box;
   static constexpr int ring = kRingBytes / slot;        // 6 or 12 slots
@@ -208,7 +209,7 @@ struct Walk {
     if (g.a.list) {
       keys = hi > 0 ? g.a.n_list << g.a.c.pshift : 0;
     } else {
-      base = lo & ~(g.rows - 1);
+      base = lo >> g.rshift << g.rshift;
       keys = hi - base;
     }
     return (keys + (1 << g.gshift) - 1) >> g.gshift;
@@ -219,7 +220,7 @@ struct Walk {
   __device__ __forceinline__ int locate(const Args& g, int subs) {
     const int lane = threadIdx.x & 31, per_b = (g.a.B + 31) >> 5, b0 = min(g.a.B, lane * per_b), b1 = min(g.a.B, b0 + per_b);
     int mine = 0;
-#pragma unroll 4
+#pragma unroll 1
     for (int i = b0; i < b1; ++i) mine += count(g, i, lo, hi, base);
     mine *= subs;
     int incl = mine;
@@ -236,6 +237,7 @@ struct Walk {
     const int f = __ffs(__ballot_sync(0xffffffffu, incl > r)) - 1;
     if (lane == f) {
       int at = r - (incl - mine);
+#pragma unroll 1
       for (b = b0;; ++b) {
         n = count(g, b, lo, hi, base);
         if (at < n * subs) break;
@@ -257,10 +259,11 @@ struct Walk {
     return per;
   }
   struct Seg {
-    int b, sub, a, e, n, lo, hi, base;
+    int b, kvh, hg, a, e, n, lo, hi, base;  // KV head and group of its heads; granules [a, e) of n
   };
   __device__ __forceinline__ bool next(const Args& g, int subs, Seg& s) {
     if (r >= r1) return false;
+#pragma unroll 1
     while (off >= n) {  // the next unit
       off = 0;
       if (n == 0 || ++sub == subs) {
@@ -270,7 +273,12 @@ struct Walk {
       }
     }
     s.b = b;
-    s.sub = sub;
+    s.kvh = sub;
+    s.hg = 0;
+    if (g.ngrp > 1) {
+      s.kvh = sub / g.ngrp;
+      s.hg = sub - s.kvh * g.ngrp;
+    }
     s.a = off;
     s.e = min(n, off + (r1 - r));
     s.n = n;
@@ -348,16 +356,17 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   if (warp == 10) {
     // ---------------- pages: looks up the tiles' pages up to kAhead tiles before they are loaded
     // (a lane per row group, several tiles at once)
-    const int R = g.rows, ng = KT / R, P = 1 << c.pshift, nb = min(32 / ng, kAhead);
+    const int rs = g.rshift, ngs = LY::KS - rs, ng = 1 << ngs, P = 1 << c.pshift, nb = min(32 >> ngs, kAhead);
     int tt = 0;
     bool ok = true;
     Walk::Seg s;
     while (ok && w.next(g, subs, s)) {
-      const int kvh = s.sub / g.ngrp, i1 = w.end(g, s);
+      const int kvh = s.kvh, i1 = w.end(g, s);
       const int* list = a.list ? a.list + (static_cast<size_t>(s.b) * c.nkv + kvh) * a.n_list : nullptr;
+#pragma unroll 1
       for (int i0 = (s.a << g.gshift); i0 < i1 && ok; i0 += nb * KT) {
         int page = -1, pos = -1;
-        const int i = i0 + lane * R;  // the tiles' row groups follow one another
+        const int i = i0 + (lane << rs);  // the tiles' row groups follow one another
         if (lane < nb * ng && i < i1) {
           int lp, off;
           if (list) {
@@ -372,6 +381,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             if (page >= 0) pos = (lp << c.pshift) + off;
           }
         }
+#pragma unroll 1
         for (int j = 0; j < nb && i0 + j * KT < i1; ++j, ++tt) {
           // the load warp has begun tile tt - kAhead, so tile tt - kInfo is done with
           if (tt >= kAhead) {
@@ -386,9 +396,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             if (!ok) break;
           }
           int* in = info + (tt % kInfo) * 33;
-          if (lane / ng == j) {
-            in[lane - j * ng] = pos;
-            in[16 + lane - j * ng] = page;
+          if (lane >> ngs == j) {
+            in[lane & (ng - 1)] = pos;
+            in[16 + (lane & (ng - 1))] = page;
           }
           if (lane == 0) in[32] = kvh;
           __syncwarp();
@@ -411,7 +421,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   } else if (warp == 8) {
     // ---------------- loads
     if (elect()) {
-      const int R = g.rows, ng = KT / R, P = 1 << c.pshift;
+      const int R = 1 << g.rshift, ng = KT >> g.rshift, P = 1 << c.pshift;
       int pc = 0, slot = 0;  // slots so far, the next slot and the ring's phase there
       unsigned phase = 0;
       bool ok = true;
@@ -420,6 +430,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         const int* in = info + (tt % kInfo) * 33;
         const int kvh = in[32];
         if (kvh < 0) break;
+#pragma unroll 1
         for (int j = 0; j < PT; ++j) {
           const unsigned bar = full0 + 8 * slot;
           if (pc >= kRing && !wait_bar(empty0 + 8 * slot, phase ^ 1, dead)) {
@@ -431,6 +442,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           const int x = (j < NP ? j : j - NP) * 128;
           const CUtensorMap* map = j < NP ? &mapK : &mapV;
           unsigned dst = base + slot * LY::slot;
+#pragma unroll 1
           for (int r = 0; r < ng; ++r, dst += R * 128) {
             const int pos = in[r], off = pos < 0 ? 0 : pos & (P - 1), page = in[16 + r];  // page -1: zeros
             tma_4d(dst, map, x, off, kvh, page, bar);
@@ -444,6 +456,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         }
       }
       // no copy may be in flight when the CTA ends
+#pragma unroll 1
       for (int i = max(0, pc - kRing); i < pc; ++i) {
         const long long t0 = clock64();
         while (!try_wait(full0 + 8 * (i % kRing), (i / kRing) & 1) && clock64() - t0 < kSpin) {
@@ -571,7 +584,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     auto bar_wg = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); };
     // the queries of a unit as three bf16 terms per value: row term * NH + head
     auto put_q = [&](const Walk::Seg& u, int buf) {
-      const int kvh = u.sub / g.ngrp, h0 = kvh * G + (u.sub % g.ngrp) * NH, nh = min(NH, G - (u.sub % g.ngrp) * NH);
+      const int h0 = u.kvh * G + u.hg * NH, nh = min(NH, G - u.hg * NH);
+#pragma unroll 1
       for (int i = wt; i < NH * (D / 8); i += 128) {
         const int h = i / (D / 8), ch = i % (D / 8);
         float v[8];
@@ -597,7 +611,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(qfull0 + 8 * buf);
     };
-    const int R = g.rows;
+    const int rs = g.rshift;
     Walk::Seg s, sn;
     bool have = work && w.next(g, subs, s);
     if (have && wg == 0) put_q(s, 0);
@@ -632,10 +646,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         if (lane == 0) mbar_arrive(ofree0 + 8 * wg);
       };
       const int nt = (w.end(g, s) - (s.a << g.gshift) + KT - 1) / KT;
+#pragma unroll 1
       for (int t = wg; t < nt; t += 2, ++own) {
         const int at = tt + t;
         wait_bar(ifull0 + 8 * (at % kInfo), (at / kInfo) & 1, dead);
-        const int pb = has ? info[(at % kInfo) * 33 + key / R] : -1, pos = pb + (key & (R - 1));
+        const int pb = has ? info[(at % kInfo) * 33 + (key >> rs)] : -1, pos = pb + (key & ((1 << rs) - 1));
         const bool on = pb >= 0 && pos >= s.lo && pos < s.hi;
         wait_bar(sfull0 + 8 * wg, own & 1, dead);
         __syncwarp();
@@ -701,6 +716,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             }
           }
           if (pb >= 0 && !on) {  // a stale row of an attended page
+#pragma unroll 1
             for (int j = 0; j < NP; ++j) {
               const int pc = at * PT + (own_v ? NP : 0) + j, slot = pc % kRing;
               if (own_v && !wait_bar(full0 + 8 * slot, (pc / kRing) & 1, dead)) break;
@@ -772,7 +788,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         fence_before();
       }
       asm volatile("bar.arrive 4, 256;" ::: "memory");
-      const int kvh = s.sub / g.ngrp, h0 = kvh * G + (s.sub % g.ngrp) * NH, nh = min(NH, G - (s.sub % g.ngrp) * NH);
+      const int h0 = s.kvh * G + s.hg * NH, nh = min(NH, G - s.hg * NH);
       const size_t row0 = static_cast<size_t>(s.b) * a.nh + h0;
       const bool whole = s.a == 0 && s.e == s.n;
       {
@@ -809,11 +825,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       have = more;
     }
     // sequences with nothing to attend have no granule: out 0, lse -inf
+#pragma unroll 1
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
       int lo, hi, bs;
       if (Walk::count(g, b, lo, hi, bs) == 0) {
+#pragma unroll 1
         for (int i = tid; i < a.nh * D; i += 256) a.out[static_cast<size_t>(b) * a.nh * D + i] = 0.f;
         if (a.lse)
+#pragma unroll 1
           for (int i = tid; i < a.nh; i += 256) a.lse[static_cast<size_t>(b) * a.nh + i] = -INFINITY;
       }
     }
@@ -922,8 +941,8 @@ int launch(const Args& g, cudaStream_t st) {
   static_assert(LY::KT == 64 || LY::KT == 128, "keys per tile");
   static_assert(LY::cols <= 512 && (LY::cols & (LY::cols - 1)) == 0, "tensor memory columns");
   CUtensorMap mk, mv;
-  int rc = make_map(&mk, g.a.c, g.a.c.k, g.rows);
-  if (rc || (rc = make_map(&mv, g.a.c, g.a.c.v ? g.a.c.v : g.a.c.k, g.rows))) return rc;
+  int rc = make_map(&mk, g.a.c, g.a.c.k, 1 << g.rshift);
+  if (rc || (rc = make_map(&mv, g.a.c, g.a.c.v ? g.a.c.v : g.a.c.k, 1 << g.rshift))) return rc;
   cudaError_t e = cudaFuncSetAttribute(k_paged_tc<D, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, LY::total);
   if (e == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
@@ -972,15 +991,16 @@ int run_paged_tc(const pg::AttArgs& a, void* ws, int num_sms, cudaStream_t st) {
   g.a = a;
   const int P = 1 << a.c.pshift, G = a.nh / a.c.nkv, NH = G <= 4 ? 4 : 8;
   const int tile = a.c.d == 512 || (a.c.d == 256 && NH == 8) ? 64 : 128;  // Lay::KT
-  g.rows = P < tile ? P : tile;
+  const int rows = P < tile ? P : tile;
+  while ((1 << g.rshift) < rows) ++g.rshift;
   g.ngrp = (G + NH - 1) / NH;
   // the most keys a unit can have; with few of them, smaller granules spread them over the SMs
   long long keys = static_cast<long long>(a.list ? a.n_list : a.c.max_pages) * P;
-  if (!a.list && a.window > 0 && a.window + g.rows < keys) keys = a.window + g.rows;
+  if (!a.list && a.window > 0 && a.window + rows < keys) keys = a.window + rows;
   const long long units = static_cast<long long>(a.B) * a.c.nkv * g.ngrp;
   g.gshift = 7;
   const auto granules = [&] { return units * ((keys + (1 << g.gshift) - 1) >> g.gshift); };
-  while (g.gshift > 5 && (1 << g.gshift) > g.rows && granules() < num_sms) --g.gshift;
+  while (g.gshift > 5 && (1 << g.gshift) > rows && granules() < num_sms) --g.gshift;
   const long long most = granules();
   if (most > INT32_MAX) {
     set_error("too many keys: B * heads * max_pages * page_size = %lld", units * keys);
