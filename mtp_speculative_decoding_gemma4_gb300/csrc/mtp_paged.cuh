@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "mtp.h"
 
 namespace mtp {
@@ -36,6 +38,19 @@ __device__ __forceinline__ void key_range(const Cache& c, int b, int window, int
 __device__ __forceinline__ int phys_page(const Cache& c, int b, int lp) {
   const int page = __ldg(c.table + static_cast<size_t>(b) * c.table_stride + lp);
   return static_cast<unsigned>(page) < static_cast<unsigned>(c.n_pages) ? page : -1;
+}
+
+// Lets a kernel use BYTES of dynamic shared memory, asked of the driver once per device.
+template <auto kernel, int BYTES>
+inline cudaError_t allow_smem() {
+  static std::atomic<unsigned long long> done{0};  // a bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_relaxed) & bit))) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+  if (e == cudaSuccess) done.fetch_or(bit);
+  return e;
 }
 
 struct AttArgs {

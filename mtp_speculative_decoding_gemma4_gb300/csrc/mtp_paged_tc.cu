@@ -17,6 +17,8 @@
 // Work split: the granules (32 to 128 keys) of all (sequence, KV head, head group) units are
 // numbered through and dealt evenly over one CTA per SM, whatever the lengths. A unit that crosses
 // CTAs leaves unnormalised sums, (max, exp-sum) per part; k_paged_tc_join adds them in CTA order.
+// (Joined by the last CTA to arrive instead, the 8 long contexts took 48 us against 41: its chain
+// of round trips runs while the memory is busy with the others' keys.)
 //
 // One CTA: warp 10 finds the tiles' pages through the block table,
 // warp 8 loads them (slots of [KT keys][128 dims] in two 128-byte-swizzled boxes, a ring of 192 KB), one thread of warp 9 issues the MMAs (whichever of
@@ -28,6 +30,8 @@
 // Rows that hold no attended key but lie in an attended page are set to zero before the sums
 // (0 * NaN would not vanish). Waits are bounded; a CTA that gives up writes NaN.
 #include <cudaTypedefs.h>
+
+#include <cstring>
 
 #include "mtp_common.cuh"
 #include "mtp_launch.h"
@@ -846,57 +850,62 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 }
 
 // Adds the parts of the unit that CTA blockIdx.x of k_paged_tc starts and does not end, one head
-// per blockIdx.y, the threads over the parts and the dims; a fixed order of sums.
+// per blockIdx.y, the threads over the parts and the dims; a fixed order of sums. What bounds it
+// is its chain of reads (the unit, the weights, the sums): the first sums are requested with the
+// weights.
 template <int D>
 __global__ void __launch_bounds__(512) k_paged_tc_join(const __grid_constant__ Args g, int NH) {
   pdl_enter();
-  constexpr int VT = D / 4, GR = 512 / VT;  // threads of one part's dims, parts side by side
-  const int* meta = g.meta + 4 * blockIdx.x;
+  constexpr int VT = D / 4, GR = 512 / VT, PRE = 4;  // threads of one part's dims, parts side by side
+  const int4 meta = *reinterpret_cast<const int4*>(g.meta + 4 * blockIdx.x);
   const int h = blockIdx.y, c0 = blockIdx.x;
-  if (h >= meta[1]) return;
-  const int c1 = meta[2];
-  const size_t row = static_cast<size_t>(meta[0]) + h;
+  if (h >= meta.y) return;
+  const int n = meta.z - c0 + 1;
+  const size_t row = static_cast<size_t>(meta.x) + h;
   const AttArgs& a = g.a;
-  __shared__ float wgt[pg::kMaxSms], sden[16];
+  __shared__ float wgt[pg::kMaxSms], sden;
   __shared__ float4 sum[GR][VT];
-  const int n = c1 - c0 + 1, tid = threadIdx.x, lane = tid & 31;
-  auto part = [&](int i) { return (static_cast<size_t>(c0 + i) * 2 + (i == 0 ? 1 : 0)) * NH + h; };
+  const int tid = threadIdx.x, lane = tid & 31, v = tid % VT, gr = tid / VT;
+  // part i: slot 1 of the first CTA, slot 0 of the next ones
+  auto part = [&](int i) { return static_cast<size_t>((c0 + i) * 2 + (i == 0 ? 1 : 0)) * NH + h; };
+  auto at = [&](int i) { return reinterpret_cast<const float4*>(a.ws_acc + part(i) * D) + v; };
+  float4 y[PRE];
+#pragma unroll
+  for (int j = 0; j < PRE; ++j)
+    if (gr + j * GR < n) y[j] = *at(gr + j * GR);
   float M = -INFINITY;
   for (int i = lane; i < n; i += 32) M = fmaxf(M, a.ws_ml[part(i) * 2]);
   M = warp_max(M);
-  float den = 0.f;
   if (tid < 32) {
+    float den = 0.f;
     for (int i = lane; i < n; i += 32) {
-      const float f = M == -INFINITY ? 0.f : exp2f(a.ws_ml[part(i) * 2] - M);
+      const float2 ml = *reinterpret_cast<const float2*>(a.ws_ml + part(i) * 2);
+      const float f = M == -INFINITY ? 0.f : exp2f(ml.x - M);
       wgt[i] = f;
-      den = fmaf(f, a.ws_ml[part(i) * 2 + 1], den);
+      den = fmaf(f, ml.y, den);
     }
     den = warp_sum(den);
-    if (lane == 0) sden[0] = den;
+    if (lane == 0) sden = den;
   }
   __syncthreads();
-  den = sden[0];
-  const int v = tid % VT, gr = tid / VT;
+  const float den = sden;
   float4 x = make_float4(0, 0, 0, 0);
+  auto add = [&](float f, const float4& z) {
+    x.x = fmaf(f, z.x, x.x);
+    x.y = fmaf(f, z.y, x.y);
+    x.z = fmaf(f, z.z, x.z);
+    x.w = fmaf(f, z.w, x.w);
+  };
+#pragma unroll
+  for (int j = 0; j < PRE; ++j)
+    if (gr + j * GR < n) add(wgt[gr + j * GR], y[j]);
 #pragma unroll 4
-  for (int i = gr; i < n; i += GR) {
-    const float f = wgt[i];
-    const float4 y = *reinterpret_cast<const float4*>(a.ws_acc + part(i) * D + 4 * v);
-    x.x = fmaf(f, y.x, x.x);
-    x.y = fmaf(f, y.y, x.y);
-    x.z = fmaf(f, y.z, x.z);
-    x.w = fmaf(f, y.w, x.w);
-  }
+  for (int i = gr + PRE * GR; i < n; i += GR) add(wgt[i], *at(i));
   sum[gr][v] = x;
   __syncthreads();
   if (gr == 0) {
-    for (int i = 1; i < GR; ++i) {
-      const float4 y = sum[i][v];
-      x.x += y.x;
-      x.y += y.y;
-      x.z += y.z;
-      x.w += y.w;
-    }
+#pragma unroll
+    for (int i = 1; i < GR; ++i) add(1.f, sum[i][v]);
     const float inv = den == 0.f ? 0.f : 1.f / den;
     *reinterpret_cast<float4*>(a.out + row * D + 4 * v) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
     if (a.lse && v == 0) a.lse[row] = den == 0.f ? -INFINITY : (M + log2f(den)) * 0.6931471805599453f;
@@ -942,8 +951,10 @@ int launch(const Args& g, cudaStream_t st) {
   static_assert(LY::cols <= 512 && (LY::cols & (LY::cols - 1)) == 0, "tensor memory columns");
   CUtensorMap mk, mv;
   int rc = make_map(&mk, g.a.c, g.a.c.k, 1 << g.rshift);
-  if (rc || (rc = make_map(&mv, g.a.c, g.a.c.v ? g.a.c.v : g.a.c.k, 1 << g.rshift))) return rc;
-  cudaError_t e = cudaFuncSetAttribute(k_paged_tc<D, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, LY::total);
+  if (rc) return rc;
+  mv = mk;
+  if (g.a.c.v && (rc = make_map(&mv, g.a.c, g.a.c.v, 1 << g.rshift))) return rc;
+  cudaError_t e = pg::allow_smem<k_paged_tc<D, NH>, LY::total>();
   if (e == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];

@@ -31,34 +31,38 @@ def _need_flat(t, name: str, dtype, shape, device=None) -> torch.Tensor:
 
 
 class _On:
-    """The device and stream of a call: makes the tensors' device current and, for a stream
-    other than torch's current one, allocates on that stream."""
-
-    __slots__ = ("stream", "_dev", "_ctx")
+    """A call's device and stream where they are not the current ones: makes the tensors' device
+    current and allocates on the given stream."""
 
     def __init__(self, device: torch.device, stream: Optional[int]):
-        self._dev = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-        self._ctx = None
-        current = torch.cuda.current_stream(device).cuda_stream
-        if stream is None:
-            stream = current
-        elif stream != current:
-            self._ctx = torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if stream else
-                                          torch.cuda.default_stream(device))
-        self.stream = stream
+        self._ctx = [torch.cuda.device(device)]
+        if stream is not None:
+            self._ctx.append(torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if stream else
+                                               torch.cuda.default_stream(device)))
+        self._device, self._stream = device, stream
 
-    def __enter__(self):
-        if self._dev is not None:
-            self._dev.__enter__()
-        if self._ctx is not None:
-            self._ctx.__enter__()
-        return self.stream
+    def __enter__(self) -> int:
+        for c in self._ctx:
+            c.__enter__()
+        return _raw_stream(self._device.index) if self._stream is None else self._stream
 
     def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
-        if self._dev is not None:
-            self._dev.__exit__(*exc)
+        for c in reversed(self._ctx):
+            c.__exit__(*exc)
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream  # torch's current stream of a device, as an integer
+
+
+def _call(device: torch.device, stream: Optional[int], fn, *args):
+    """fn(stream, *args) with the call's device current and its allocations on its stream."""
+    index = device.index
+    if torch.cuda.current_device() == index:
+        current = _raw_stream(index)
+        if stream is None or stream == current:
+            return fn(current, *args)
+    with _On(device, stream) as st:
+        return fn(st, *args)
 
 
 class PagedKV:
@@ -105,6 +109,8 @@ class PagedKV:
         c.n_pages, c.page_size, c.n_kv_head, c.head_dim, c.dtype = n_pages, P, n_kv, d, _DT[k.dtype]
         self.k, self.v, self.block_table, self.ctx_len, self.codes, self.scales = k, v, block_table, ctx_len, codes, scales
         self.device, self.batch = dev, 0 if block_table is None else block_table.shape[0]
+        self._row = k.shape[2:]
+        self._ws = {}  # workspace bytes by (n_head, n_list); and of the selection
 
 
 def page_plan(old_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.Tensor, free_ring: torch.Tensor,
@@ -124,18 +130,21 @@ def page_plan(old_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.T
         raise ValueError(f"block_table must be [{Bn}][max_pages] with a contiguous last dimension")
     if max_tokens < 0:
         raise ValueError("max_tokens must be >= 0")
-    with _On(dev, stream) as st:
-        # one allocation: slot_map (16-byte aligned), then the small outputs
-        head = (max_tokens + 3) // 4 * 4
-        buf = torch.empty(head + 2 * Bn + 7, dtype=torch.int32, device=dev)
-        slots, len_out = buf[:max_tokens], buf[head:head + Bn]
-        cu, tail = buf[head + Bn:head + 2 * Bn + 1], head + 2 * Bn + 1
-        state, status = buf[tail:tail + 2], buf[tail + 2:tail + 6]
-        base = buf.data_ptr()
-        B.mtp_page_plan(old_len.data_ptr(), new_len.data_ptr(), Bn, block_table.data_ptr(),
-                        block_table.stride(0) if Bn > 1 else block_table.shape[1], block_table.shape[1],
-                        free_ring.data_ptr(), free_ring.shape[0], ring_state.data_ptr(), page_size, max_tokens,
-                        base + 4 * head, base, base + 4 * (head + Bn), base + 4 * tail, base + 4 * (tail + 2), st)
+    return _call(dev, stream, _plan, old_len, new_len, block_table, free_ring, ring_state, page_size, max_tokens)
+
+
+def _plan(st, old_len, new_len, block_table, free_ring, ring_state, page_size, max_tokens):
+    Bn, cols = block_table.shape
+    # one allocation: slot_map (16-byte aligned), then the small outputs
+    pad = -max_tokens % 4
+    buf = torch.empty(max_tokens + pad + 2 * Bn + 7, dtype=torch.int32, device=old_len.device)
+    slots, _, len_out, cu, state, status = buf.split((max_tokens, pad, Bn, Bn + 1, 2, 4))
+    at = buf.data_ptr()
+    ln = at + 4 * (max_tokens + pad)
+    B.mtp_page_plan(old_len.data_ptr(), new_len.data_ptr(), Bn, block_table.data_ptr(),
+                    block_table.stride(0) if Bn > 1 else cols, cols, free_ring.data_ptr(), free_ring.shape[0],
+                    ring_state.data_ptr(), page_size, max_tokens, ln, at, ln + 4 * Bn, ln + 4 * (2 * Bn + 1),
+                    ln + 4 * (2 * Bn + 3), st)
     return len_out, slots, cu, state, status
 
 
@@ -145,27 +154,31 @@ def page_append(kv: PagedKV, k_new: torch.Tensor, slot_map: torch.Tensor, v_new:
     (int32 [T]; slots outside the cache are skipped) and, for a cache with summaries, refreshes
     the summary of every page whose last slot is written. Rows may be strided (the last two
     dimensions contiguous)."""
-    n_kv, d = kv.k.shape[2:]
+    n_kv, d = kv._row
     for t, name in ((k_new, "k_new"), (v_new, "v_new")):
         if t is None:
             continue
         _need(t, name, kv.k.dtype, 3, kv.device)
-        if t.shape[1:] != kv.k.shape[2:] or t.shape[0] != k_new.shape[0] or t.numel() and (t.stride(2) != 1 or
+        if t.shape[1:] != kv._row or t.shape[0] != k_new.shape[0] or t.numel() and (t.stride(2) != 1 or
                 n_kv > 1 and t.stride(1) != d):
             raise ValueError(f"{name} must be [T][{n_kv}][{d}] with contiguous rows")
-    T = k_new.shape[0]
-    _need_flat(slot_map, "slot_map", torch.int32, (T,), kv.device)
-    row = lambda t: n_kv * d if t is None or T < 2 else t.stride(0)  # noqa: E731
-    with _On(kv.device, stream) as st:
-        B.mtp_page_append(kv.c, k_new.data_ptr(), 0 if v_new is None else v_new.data_ptr(), row(k_new), row(v_new),
-                          slot_map.data_ptr(), T, st)
+    _need_flat(slot_map, "slot_map", torch.int32, (k_new.shape[0],), kv.device)
+    _call(kv.device, stream, _append, kv, k_new, slot_map, v_new)
+
+
+def _append(st, kv, k_new, slot_map, v_new):
+    T, width = k_new.shape[0], kv.c.n_kv_head * kv.c.head_dim
+    B.mtp_page_append(kv.c, k_new.data_ptr(), 0 if v_new is None else v_new.data_ptr(),
+                      k_new.stride(0) if T > 1 else width, v_new.stride(0) if T > 1 and v_new is not None else width,
+                      slot_map.data_ptr(), T, st)
 
 
 def _queries(q, kv: PagedKV):
-    _need_flat(q, "q", torch.float32, (kv.batch, None, kv.c.head_dim), kv.device)
+    if not (isinstance(q, torch.Tensor) and q.dtype is torch.float32 and q.dim() == 3 and q.device == kv.device and
+            q.is_contiguous() and q.shape[0] == kv.batch and q.shape[2] == kv._row[1]):
+        _need_flat(q, "q", torch.float32, (kv.batch, None, kv._row[1]), kv.device)
     if kv.block_table is None:
         raise ValueError("the cache has no block_table")
-    return q.shape[0], q.shape[1]
 
 
 def paged_attention(q: torch.Tensor, kv: PagedKV, window: int = 0, scale: float = 0.0,
@@ -175,23 +188,28 @@ def paged_attention(q: torch.Tensor, kv: PagedKV, window: int = 0, scale: float 
     ctx_len[b] keys, the last `window` (> 0), or those of the logical pages listed in `pages`
     (int32 [B][n_kv][n], -1: none). Returns out fp32 [B][n_head][d], with want_lse (out, lse
     [B][n_head])."""
-    Bn, nh = _queries(q, kv)
-    n_list = 0
+    _queries(q, kv)
     if pages is not None:
-        _need_flat(pages, "pages", torch.int32, (Bn, kv.c.n_kv_head, None), kv.device)
-        n_list = pages.shape[2]
-        if n_list < 1:
+        _need_flat(pages, "pages", torch.int32, (kv.batch, kv._row[0], None), kv.device)
+        if pages.shape[2] < 1:
             raise ValueError("pages must list at least one entry per KV head")
     if out is not None:
         _need_flat(out, "out", torch.float32, tuple(q.shape), kv.device)
-    with _On(kv.device, stream) as st:
-        if out is None:
-            out = torch.empty_like(q)
-        lse = torch.empty((Bn, nh), dtype=torch.float32, device=kv.device) if want_lse else None
-        n = B.mtp_paged_attention_workspace(kv.c, Bn, nh, n_list)
-        ws = torch.empty(n, dtype=torch.uint8, device=kv.device) if n else None
-        B.mtp_paged_attention(kv.c, q.data_ptr(), Bn, nh, window, scale, pages.data_ptr() if n_list else 0, n_list,
-                              out.data_ptr(), lse.data_ptr() if want_lse else 0, ws.data_ptr() if n else 0, n, st)
+    return _call(kv.device, stream, _attend, q, kv, window, scale, pages, want_lse, out)
+
+
+def _attend(st, q, kv, window, scale, pages, want_lse, out):
+    Bn, nh, _ = q.shape
+    n_list = 0 if pages is None else pages.shape[2]
+    n = kv._ws.get((nh, n_list))
+    if n is None:
+        n = kv._ws[(nh, n_list)] = B.mtp_paged_attention_workspace(kv.c, Bn, nh, n_list)
+    if out is None:
+        out = torch.empty_like(q)
+    lse = torch.empty((Bn, nh), dtype=torch.float32, device=kv.device) if want_lse else None
+    ws = torch.empty(n, dtype=torch.uint8, device=kv.device) if n else None
+    B.mtp_paged_attention(kv.c, q.data_ptr(), Bn, nh, window, scale, 0 if pages is None else pages.data_ptr(), n_list,
+                          out.data_ptr(), lse.data_ptr() if want_lse else 0, ws.data_ptr() if n else 0, n, st)
     return (out, lse) if want_lse else out
 
 
@@ -201,17 +219,22 @@ def page_select(q: torch.Tensor, kv: PagedKV, n_select: int, keep_first: int = 1
     order (int32 [B][n_kv][n_select], -1 behind them): the first keep_first and last keep_last
     pages, then those whose summaries' dot product with q is largest. A list for
     paged_attention(pages=...)."""
-    Bn, nh = _queries(q, kv)
-    shape = (Bn, kv.c.n_kv_head, n_select)
-    if out is not None:
-        _need_flat(out, "out", torch.int32, shape, kv.device)
-    elif n_select < 1:
+    _queries(q, kv)
+    if n_select < 1:
         raise ValueError("n_select must be >= 1")
-    with _On(kv.device, stream) as st:
-        if out is None:
-            out = torch.empty(shape, dtype=torch.int32, device=kv.device)
-        n = B.mtp_page_select_workspace(kv.c, Bn)
-        ws = torch.empty(n, dtype=torch.uint8, device=kv.device)
-        B.mtp_page_select(kv.c, q.data_ptr(), Bn, nh, n_select, keep_first, keep_last, out.data_ptr(), ws.data_ptr(), n,
-                          st)
+    if out is not None:
+        _need_flat(out, "out", torch.int32, (kv.batch, kv._row[0], n_select), kv.device)
+    return _call(kv.device, stream, _select, q, kv, n_select, keep_first, keep_last, out)
+
+
+def _select(st, q, kv, n_select, keep_first, keep_last, out):
+    Bn, nh, _ = q.shape
+    if out is None:
+        out = torch.empty((Bn, kv._row[0], n_select), dtype=torch.int32, device=kv.device)
+    n = kv._ws.get("select")
+    if n is None:
+        n = kv._ws["select"] = B.mtp_page_select_workspace(kv.c, Bn)
+    ws = torch.empty(n, dtype=torch.uint8, device=kv.device) if n else None
+    B.mtp_page_select(kv.c, q.data_ptr(), Bn, nh, n_select, keep_first, keep_last, out.data_ptr(),
+                      ws.data_ptr() if n else 0, n, st)
     return out
