@@ -7,11 +7,13 @@ from .binding import EXPORTS, MtpError, load_library  # noqa: F401
 
 
 def __getattr__(name):
-    # The torch-facing layer is imported lazily so that the C ABI can be loaded without torch.
+    # The torch-facing layer is imported lazily so that the C ABI can be loaded without torch;
+    # a name is looked up once and then an attribute of the package.
     if name in ("Drafter", "verify_greedy", "verify_sample", "make_config", "make_kv"):
-        from . import drafter
-        return getattr(drafter, name)
-    if name in ("PagedKV", "page_plan", "page_append", "page_select", "paged_attention"):
-        from . import paged
-        return getattr(paged, name)
-    raise AttributeError(name)
+        from . import drafter as module
+    elif name in ("PagedKV", "page_plan", "page_append", "page_select", "paged_attention"):
+        from . import paged as module
+    else:
+        raise AttributeError(name)
+    value = globals()[name] = getattr(module, name)
+    return value

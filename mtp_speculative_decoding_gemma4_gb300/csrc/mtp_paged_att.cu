@@ -201,22 +201,60 @@ __global__ void __launch_bounds__(kAttWarps * 32) k_paged_att(const __grid_const
   }
 }
 
-// Joins the splits of one (sequence, head) per CTA.
-__global__ void __launch_bounds__(128) k_paged_join(const __grid_constant__ AttArgs a) {
+// Joins the splits of one (sequence, head) per CTA: the weights by one warp, the sums by all, a
+// group of threads per split and 4 dims each (head dims are multiples of 4).
+constexpr int kMaxSplits = 256;
+
+__global__ void __launch_bounds__(256) k_paged_join(const __grid_constant__ AttArgs a) {
   pdl_enter();
+  __shared__ float wgt[kMaxSplits], s_m, s_den;
+  __shared__ float4 sum[256];
   const size_t row = blockIdx.x;
-  const int d = a.c.d, n = a.nsplit;
-  const float* ml = a.ws_ml + row * n * 2;
-  float M = -INFINITY;
-  for (int s = 0; s < n; ++s) M = fmaxf(M, ml[2 * s]);
-  float den = 0.f;
-  for (int s = 0; s < n; ++s) den += pexp(ml[2 * s], M) * ml[2 * s + 1];
-  for (int e = threadIdx.x; e < d; e += 128) {
-    float num = 0.f;
-    for (int s = 0; s < n; ++s) num = fmaf(pexp(ml[2 * s], M), a.ws_acc[(row * n + s) * d + e], num);
-    a.out[row * d + e] = den == 0.f ? 0.f : num / den;  // 0: nothing attended
+  const int d = a.c.d, n = a.nsplit, tid = threadIdx.x, vt = d / 4, gr = tid / vt, v = tid - gr * vt, ng = 256 / vt;
+  if (tid < 32) {
+    const float2* ml = reinterpret_cast<const float2*>(a.ws_ml) + row * n;
+    float M = -INFINITY, den = 0.f;
+    for (int s = tid; s < n; s += 32) M = fmaxf(M, ml[s].x);
+    M = warp_max(M);
+    for (int s = tid; s < n; s += 32) {
+      const float f = pexp(ml[s].x, M);
+      wgt[s] = f;
+      den = fmaf(f, ml[s].y, den);
+    }
+    den = warp_sum(den);
+    if (tid == 0) {
+      s_m = M;
+      s_den = den;
+    }
   }
-  if (a.lse && threadIdx.x == 0) a.lse[row] = den == 0.f ? -INFINITY : (M + log2f(den)) * 0.6931471805599453f;
+  __syncthreads();
+  const float den = s_den;
+  float4 x = make_float4(0, 0, 0, 0);
+  if (gr < ng) {
+#pragma unroll 4
+    for (int s = gr; s < n; s += ng) {
+      const float f = wgt[s];
+      const float4 y = *reinterpret_cast<const float4*>(a.ws_acc + (row * n + s) * d + 4 * v);
+      x.x = fmaf(f, y.x, x.x);
+      x.y = fmaf(f, y.y, x.y);
+      x.z = fmaf(f, y.z, x.z);
+      x.w = fmaf(f, y.w, x.w);
+    }
+  }
+  sum[tid] = x;
+  __syncthreads();
+  if (tid < vt) {
+    for (int g = 1; g < ng; ++g) {
+      const float4 y = sum[g * vt + tid];
+      x.x += y.x;
+      x.y += y.y;
+      x.z += y.z;
+      x.w += y.w;
+    }
+    const float inv = den == 0.f ? 0.f : 1.f / den;  // 0: nothing attended
+    *reinterpret_cast<float4*>(a.out + row * d + 4 * tid) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+  }
+  if (a.lse && tid == 0) a.lse[row] = den == 0.f ? -INFINITY : (s_m + log2f(den)) * 0.6931471805599453f;
 }
 
 template <typename T, int LPK, int NV, int GP>
@@ -261,7 +299,7 @@ int choose_splits(const Cache& c, int B, int nh, int n_list, int window, int num
   if (window > 0 && window < keys) keys = window;
   long long n = 8LL * num_sms * (nh / c.nkv) / units;
   if (n > keys / 64) n = keys / 64;
-  if (n > 256) n = 256;
+  if (n > kMaxSplits) n = kMaxSplits;
   return n < 1 ? 1 : static_cast<int>(n);
 }
 
@@ -281,7 +319,7 @@ int run_paged_att(pg::AttArgs a, void* ws, int num_sms, cudaStream_t st) {
   a.ws_ml = a.ws_acc + static_cast<size_t>(a.B) * a.nh * a.nsplit * a.c.d;
   int rc = a.c.f32 ? pg::launch_type<float>(a, st) : pg::launch_type<__nv_bfloat16>(a, st);
   if (rc || a.nsplit == 1) return rc;
-  pg::k_paged_join<<<a.B * a.nh, 128, 0, st>>>(a);
+  pg::k_paged_join<<<a.B * a.nh, 256, 0, st>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {
     set_error("paged attention join launch: %s", cudaGetErrorString(e));

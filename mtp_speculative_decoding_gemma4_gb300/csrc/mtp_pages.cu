@@ -13,12 +13,11 @@ namespace pg {
 // from the head of the ring of free pages, in batch order, or returned to its tail. A grower is
 // granted while the running sums of pages and of tokens over the growers fit, so the granted
 // growers are a prefix and every page and slot follows from three prefix sums. Every CTA makes
-// the sums itself (B is at most kMaxSeqs) and takes its share of the pages and slots: one launch
+// the sums itself (B is at most 8192) and takes its share of the pages and slots: one launch
 // and no exchange. Pages are taken from [head, head + count) and returned behind it, so no ring
 // entry is both read and written.
 
 constexpr int kPlanThreads = 512;
-constexpr int kMaxSeqs = 8192;
 
 struct PlanArgs {
   const int *old_len, *new_len, *state;
@@ -80,6 +79,11 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(const __grid_constan
     fits = n >= 0 && n <= cap;
   };
   auto pages = [&](int n) { return (n + P - 1) >> a.pshift; };
+  // ring index below 3 n_pages (a head, at most n_pages pages and at most n_pages returned)
+  auto wrap = [&](long long i) {
+    if (i >= a.n_pages) i -= a.n_pages;
+    return i >= a.n_pages ? i % a.n_pages : i;
+  };
   long long need = 0, tok = 0, fre = 0;
   for (int b = b0; b < b1; ++b) {
     int o, n;
@@ -156,145 +160,190 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(const __grid_constan
   for (int j = gt; j < taken; j += gs) {
     const int b = find_seq(cp, B, j);
     const int lp = pages(min(static_cast<long long>(max(a.old_len[b], 0)), cap)) + j - cp[b];
-    a.table[b * a.table_stride + lp] = a.ring[(static_cast<long long>(head) + j) % a.n_pages];
+    a.table[b * a.table_stride + lp] = a.ring[wrap(static_cast<long long>(head) + j)];
   }
   for (int j = gt; j < freed; j += gs) {
     const int b = find_seq(cf, B, j);
     const int lp = pages(a.new_len[b]) + j - cf[b];
-    a.ring[(static_cast<long long>(head) + count + j) % a.n_pages] = a.table[b * a.table_stride + lp];
+    a.ring[wrap(static_cast<long long>(head) + count + j)] = a.table[b * a.table_stride + lp];
   }
-  for (int j = gt; j < (a.max_tokens + 3) / 4; j += gs) {
-    int s[4];
-    int t = 4 * j, b = -1, o = 0, n0 = 0, end = 0;
+  // slots, 4 per lane: a warp takes a run of consecutive tokens, so it searches its first
+  // sequence once and then only moves on
+  const int words = (a.max_tokens + 3) / 4, warps = gs >> 5, run = ((words + warps - 1) / warps + 31) & ~31;
+  int b = -1;
+  for (int j = (gt >> 5) * run + (tid & 31), j1 = min(words, (gt >> 5) * run + run); j < j1; j += 32) {
+    int s[4] = {-1, -1, -1, -1};
+    const int t0 = 4 * j;
+    if (t0 < total) {
+      if (b < 0) b = find_seq(cu, B, t0);
 #pragma unroll
-    for (int u = 0; u < 4; ++u, ++t) {
-      s[u] = -1;
-      if (t >= total) continue;
-      if (b < 0 || t >= end) {
-        b = b < 0 ? find_seq(cu, B, t) : b + 1;
+      for (int u = 0; u < 4; ++u) {
+        const int t = t0 + u;
+        if (t >= total) break;
         while (cu[b + 1] <= t) ++b;
-        end = cu[b + 1];
-        o = static_cast<int>(min(static_cast<long long>(max(a.old_len[b], 0)), cap));
-        n0 = pages(o);
+        const int o = static_cast<int>(min(static_cast<long long>(max(a.old_len[b], 0)), cap)), n0 = pages(o);
+        const int pos = o + t - cu[b], lp = pos >> a.pshift;
+        const int page = lp < n0 ? a.table[b * a.table_stride + lp]
+                                 : a.ring[wrap(static_cast<long long>(head) + cp[b] + lp - n0)];
+        s[u] = static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages) ? (page << a.pshift) + (pos & (P - 1)) : -1;
       }
-      const int pos = o + t - cu[b], lp = pos >> a.pshift;
-      const int page = lp < n0 ? a.table[b * a.table_stride + lp]
-                               : a.ring[(static_cast<long long>(head) + cp[b] + lp - n0) % a.n_pages];
-      s[u] = static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages) ? (page << a.pshift) + (pos & (P - 1)) : -1;
     }
-    if (4 * j + 3 < a.max_tokens) {
-      *reinterpret_cast<int4*>(a.slots + 4 * j) = make_int4(s[0], s[1], s[2], s[3]);
+    if (t0 + 3 < a.max_tokens) {
+      *reinterpret_cast<int4*>(a.slots + t0) = make_int4(s[0], s[1], s[2], s[3]);
     } else {
-      for (int u = 0; 4 * j + u < a.max_tokens; ++u) a.slots[4 * j + u] = s[u];
+      for (int u = 0; t0 + u < a.max_tokens; ++u) a.slots[t0 + u] = s[u];
     }
   }
 }
 
 // ---------------------------------------------------------------- append
 
-// Rows of k_new / v_new into their slots, 16 bytes per thread and step.
-__global__ void __launch_bounds__(256) k_page_append(const __grid_constant__ Cache c, const uint4* kn, const uint4* vn,
-                                                     long long row_k, long long row_v, const int* slots, int T) {
-  pdl_enter();
-  const int es = c.f32 ? 4 : 2, vpr = c.nkv * c.d * es / 16, vph = c.d * es / 16;
-  const long long n = static_cast<long long>(T) * vpr;
-  const int P = 1 << c.pshift;
-  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < n; i += gridDim.x * 256LL) {
-    const int t = static_cast<int>(i / vpr), v = static_cast<int>(i % vpr);
-    const int slot = slots[t], page = slot >> c.pshift;
-    if (slot < 0 || page >= c.n_pages) continue;
-    const int h = v / vph, e = v % vph;
-    const size_t at = (static_cast<size_t>(page) * c.sp + static_cast<size_t>(slot & (P - 1)) * c.st +
-                       static_cast<size_t>(h) * c.sh) * es / 16 + e;
-    static_cast<uint4*>(c.k)[at] = __ldcs(kn + t * row_k + v);
-    if (c.v) static_cast<uint4*>(c.v)[at] = __ldcs(vn + t * row_v + v);
-  }
-}
-
-// Summaries of the pages that these rows complete: m = fl32(mean of the page's rows),
-// scale = fl32(max |m| * fl32(1 / 127)), code = rint(fl32(m / scale)); a page whose mean is not
-// finite gets scale NaN and codes 0. The sum is kept as an unevaluated pair of fp32 (two-sum),
-// so m is the rounded exact mean for any order of the rows.
+// A CTA copies `rows` rows (16 bytes per thread and step) into their slots and then makes the
+// summaries of the pages that these rows complete:
+//   m = fl32(mean of the page's P rows), scale = fl32(max |m| * fl32(1 / 127)),
+//   code = rint(fl32(m / scale)); a page whose mean is not finite gets scale NaN and codes 0.
+// The sum is kept as an unevaluated pair of fp32 (two-sum), so m is the rounded exact mean for any
+// order of the rows. A page's rows are read where this call does not write: the rows of this call
+// from k_new (usually just copied, so from the L1), the older ones from the cache; so the copy and
+// the summaries need no second launch. What bounds it is the copy: each row read and written once.
 __device__ __forceinline__ void two_sum(float& hi, float& lo, float x) {
   const float s = __fadd_rn(hi, x), bb = __fsub_rn(s, hi);
   lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, bb)), __fsub_rn(x, bb)));
   hi = s;
 }
 
-constexpr int kSumThreads = 256, kSumRows = 64;  // rows of the slot map per CTA
+constexpr int kAppThreads = 256, kAppRows = 64;  // threads, most rows of a CTA
 
 template <typename T>
-__global__ void __launch_bounds__(kSumThreads) k_page_summary(const __grid_constant__ Cache c, const int* slots, int n) {
+__global__ void __launch_bounds__(kAppThreads)
+    k_page_append(const __grid_constant__ Cache c, const uint4* kn, const uint4* vn, long long row_k, long long row_v,
+                  const int* slots, int n, int rows) {
   pdl_enter();
-  __shared__ int done[kSumRows];
-  __shared__ int ndone;
-  __shared__ float part[2][kSumThreads * 8];
-  __shared__ float red[kSumThreads / 32];
-  const int tid = threadIdx.x, P = 1 << c.pshift, g = blockIdx.y;
+  __shared__ int slot_s[kAppRows], done[kAppRows], ndone;
+  const int tid = threadIdx.x, P = 1 << c.pshift, t0 = blockIdx.x * rows, nr = min(rows, n - t0);
+  constexpr int VE = Elem<T>::kVec;
+  const int vph = c.d / VE, vpr = c.nkv * vph;  // 16-byte vectors of a head and of a row
   if (tid == 0) ndone = 0;
   __syncthreads();
-  if (tid < kSumRows) {
-    const int t = blockIdx.x * kSumRows + tid;
-    const int slot = t < n ? slots[t] : -1;
-    if (slot >= 0 && (slot & (P - 1)) == P - 1 && (slot >> c.pshift) < c.n_pages) done[atomicAdd(&ndone, 1)] = slot >> c.pshift;
+  if (tid < nr) {
+    const int slot = slots[t0 + tid];
+    const bool ok = slot >= 0 && (slot >> c.pshift) < c.n_pages;
+    slot_s[tid] = ok ? slot : -1;
+    if (ok && c.codes && (slot & (P - 1)) == P - 1) done[atomicAdd(&ndone, 1)] = t0 + tid;
   }
   __syncthreads();
-  constexpr int VE = Elem<T>::kVec;
-  const int nvec = c.d / VE;               // <= 128
+  {
+    constexpr int U = 4;
+    const int total = nr * vpr;
+    for (int i0 = tid; i0 < total; i0 += U * kAppThreads) {
+      uint4 x[U], y[U];
+      size_t at[U];
+      bool on[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * kAppThreads, r = i / vpr, v = i - r * vpr;
+        on[u] = i < total && slot_s[r] >= 0;
+        if (!on[u]) continue;
+        const int h = c.nkv == 1 ? 0 : v / vph, slot = slot_s[r];
+        at[u] = (static_cast<size_t>(slot >> c.pshift) * c.sp + static_cast<size_t>(slot & (P - 1)) * c.st +
+                 static_cast<size_t>(h) * c.sh) / VE + (v - h * vph);
+        x[u] = __ldg(kn + (t0 + r) * row_k + v);
+        if (c.v) y[u] = __ldcs(vn + (t0 + r) * row_v + v);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (!on[u]) continue;
+        static_cast<uint4*>(c.k)[at[u]] = x[u];
+        if (c.v) static_cast<uint4*>(c.v)[at[u]] = y[u];
+      }
+    }
+  }
+  if (!c.codes) return;
+  __shared__ int src[256], missing;           // row of this call for each row of the page, or -1
+  __shared__ float part[2][kAppThreads * 8];
+  __shared__ float red[kAppThreads / 32];
   int lanes = 1;
-  while (lanes < nvec) lanes <<= 1;
-  const int rows = kSumThreads / lanes, v = tid % lanes, r0 = tid / lanes;
-  for (int i = 0; i < ndone; ++i) {
-    const int page = done[i];
-    const T* base = static_cast<const T*>(c.k) + static_cast<size_t>(page) * c.sp + static_cast<size_t>(g) * c.sh;
-    float hi[VE], lo[VE];
-#pragma unroll
-    for (int e = 0; e < VE; ++e) hi[e] = lo[e] = 0.f;
-    if (v < nvec)
-      for (int r = r0; r < P; r += rows) {
-        float x[VE];
-        load_vec(base + r * c.st + v * VE, x);
-#pragma unroll
-        for (int e = 0; e < VE; ++e) two_sum(hi[e], lo[e], x[e]);
-      }
-#pragma unroll
-    for (int e = 0; e < VE; ++e) {
-      part[0][tid * VE + e] = hi[e];
-      part[1][tid * VE + e] = lo[e];
+  while (lanes < vph) lanes <<= 1;
+  const int par = kAppThreads / lanes, v = tid & (lanes - 1), r0 = tid / lanes;
+  const int pages = ndone;
+  for (int it = 0; it < pages; ++it) {
+    const int t = done[it], page = slot_s[t - t0] >> c.pshift;
+    if (tid == 0) missing = 0;
+    __syncthreads();
+    if (tid < P) {  // the rows that usually come right before the last one
+      const int ti = t - (P - 1 - tid);
+      const bool here = ti >= 0 && slots[ti] == (page << c.pshift) + tid;
+      src[tid] = here ? ti : -1;
+      if (!here) missing = 1;
     }
     __syncthreads();
-    float m[8], mx = 0.f;
-    bool fin = true;
-    if (tid < lanes && v < nvec) {
+    if (missing) {  // else older rows, or rows of this call in another order
+      for (int i = tid; i < n; i += kAppThreads) {
+        const int slot = slots[i];
+        if (slot >= 0 && slot >> c.pshift == page) src[slot & (P - 1)] = i;
+      }
+      __syncthreads();
+    }
+    for (int g = 0; g < c.nkv; ++g) {
+      const T* base = static_cast<const T*>(c.k) + static_cast<size_t>(page) * c.sp + static_cast<size_t>(g) * c.sh;
+      float hi[VE], lo[VE];
 #pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        float h = part[0][tid * VE + e], l = part[1][tid * VE + e];
-        for (int r = 1; r < rows; ++r) {
-          two_sum(h, l, part[0][(tid + r * lanes) * VE + e]);
-          l += part[1][(tid + r * lanes) * VE + e];
+      for (int e = 0; e < VE; ++e) hi[e] = lo[e] = 0.f;
+      if (v < vph) {
+#pragma unroll 4
+        for (int r = r0; r < P; r += par) {
+          const int ti = src[r];
+          const T* row = ti >= 0 ? reinterpret_cast<const T*>(kn + ti * row_k + g * vph) : base + r * c.st;
+          float x[VE];
+          load_vec(row + v * VE, x);
+#pragma unroll
+          for (int e = 0; e < VE; ++e) two_sum(hi[e], lo[e], x[e]);
         }
-        m[e] = __fmul_rn(__fadd_rn(h, l), 1.0f / P);
-        fin = fin && isfinite(m[e]);
-        mx = fmaxf(mx, fabsf(m[e]));
       }
-    }
-    mx = warp_max(fin ? mx : INFINITY);
-    if ((tid & 31) == 0) red[tid >> 5] = mx;
-    __syncthreads();
-    mx = 0.f;
-#pragma unroll
-    for (int w = 0; w < kSumThreads / 32; ++w) mx = fmaxf(mx, red[w]);
-    const float scale = __fmul_rn(mx, 1.0f / 127.0f);
-    if (tid < lanes && v < nvec) {
-      signed char* out = c.codes + (static_cast<size_t>(page) * c.nkv + g) * c.d + v * VE;
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
-        const float q = scale > 0.f && isfinite(scale) ? rintf(__fdiv_rn(m[e], scale)) : 0.f;
-        out[e] = static_cast<signed char>(fminf(fmaxf(q, -127.f), 127.f));
+        part[0][e * kAppThreads + tid] = hi[e];
+        part[1][e * kAppThreads + tid] = lo[e];
       }
+      __syncthreads();
+      float m[VE], mx = 0.f;
+      bool fin = true;
+      if (tid < lanes && v < vph) {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          float h = part[0][e * kAppThreads + tid], l = part[1][e * kAppThreads + tid];
+          for (int r = 1; r < par; ++r) {
+            two_sum(h, l, part[0][e * kAppThreads + tid + r * lanes]);
+            l += part[1][e * kAppThreads + tid + r * lanes];
+          }
+          m[e] = __fmul_rn(__fadd_rn(h, l), 1.0f / P);
+          fin = fin && isfinite(m[e]);
+          mx = fmaxf(mx, fabsf(m[e]));
+        }
+      }
+      mx = warp_max(fin ? mx : INFINITY);
+      if ((tid & 31) == 0) red[tid >> 5] = mx;
+      __syncthreads();
+      mx = 0.f;
+#pragma unroll
+      for (int w = 0; w < kAppThreads / 32; ++w) mx = fmaxf(mx, red[w]);
+      const float scale = __fmul_rn(mx, 1.0f / 127.0f);
+      if (tid < lanes && v < vph) {
+        __align__(8) signed char q[VE];
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          const float f = scale > 0.f && isfinite(scale) ? rintf(__fdiv_rn(m[e], scale)) : 0.f;
+          q[e] = static_cast<signed char>(fminf(fmaxf(f, -127.f), 127.f));
+        }
+        signed char* out = c.codes + (static_cast<size_t>(page) * c.nkv + g) * c.d + v * VE;
+        if (VE == 8)
+          *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(q);
+        else
+          *reinterpret_cast<unsigned*>(out) = *reinterpret_cast<const unsigned*>(q);
+      }
+      if (tid == 0) c.scales[static_cast<size_t>(page) * c.nkv + g] = isfinite(scale) ? scale : NAN;
+      __syncthreads();
     }
-    if (tid == 0) c.scales[static_cast<size_t>(page) * c.nkv + g] = isfinite(scale) ? scale : NAN;
-    __syncthreads();
   }
 }
 
@@ -333,20 +382,17 @@ int run_page_append(const pg::Cache& c, const void* k_new, const void* v_new, lo
                     const int* slots, int T, int num_sms, cudaStream_t st) {
   if (T == 0) return MTP_OK;
   const int es = c.f32 ? 4 : 2;
-  const long long n = static_cast<long long>(T) * (c.nkv * c.d * es / 16);
-  long long grid = (n + 255) / 256;
-  if (grid > 8LL * num_sms) grid = 8LL * num_sms;
-  pg::k_page_append<<<static_cast<int>(grid), 256, 0, st>>>(c, static_cast<const uint4*>(k_new),
-                                                           static_cast<const uint4*>(v_new), row_k * es / 16,
-                                                           row_v * es / 16, slots, T);
-  MTP_PG_CHECK("page append");
-  if (!c.codes) return MTP_OK;
-  const dim3 gs((T + pg::kSumRows - 1) / pg::kSumRows, c.nkv);
+  // rows of a CTA: about 6 CTAs per SM, so that all of them run at once
+  int rows = pg::kAppRows;
+  while (rows > 1 && (T + rows - 1) / rows < 6 * num_sms) rows >>= 1;
+  const int grid = (T + rows - 1) / rows;
+  const uint4 *k = static_cast<const uint4*>(k_new), *v = static_cast<const uint4*>(v_new);
+  const long long rk = row_k * es / 16, rv = row_v * es / 16;
   if (c.f32)
-    pg::k_page_summary<float><<<gs, pg::kSumThreads, 0, st>>>(c, slots, T);
+    pg::k_page_append<float><<<grid, pg::kAppThreads, 0, st>>>(c, k, v, rk, rv, slots, T, rows);
   else
-    pg::k_page_summary<__nv_bfloat16><<<gs, pg::kSumThreads, 0, st>>>(c, slots, T);
-  MTP_PG_CHECK("page summary");
+    pg::k_page_append<__nv_bfloat16><<<grid, pg::kAppThreads, 0, st>>>(c, k, v, rk, rv, slots, T, rows);
+  MTP_PG_CHECK("page append");
   return MTP_OK;
 }
 

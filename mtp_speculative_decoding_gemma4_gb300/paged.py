@@ -25,7 +25,10 @@ def _need(t, name: str, dtype, ndim: int, device=None) -> torch.Tensor:
 
 def _need_flat(t, name: str, dtype, shape, device=None) -> torch.Tensor:
     _need(t, name, dtype, len(shape), device)
-    if not t.is_contiguous() or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+    ok = t.is_contiguous()
+    for n, m in zip(shape, t.shape):
+        ok = ok and (n is None or n == m)
+    if not ok:
         raise ValueError(f"{name} must be contiguous of shape {list(shape)} (got {list(t.shape)})")
     return t
 
@@ -119,13 +122,12 @@ def page_plan(old_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.T
     (int32 [B]): updates block_table [B][max_pages] and the ring of free pages free_ring
     [n_pages] (ring_state: head and count) in place and returns (len_out [B], slot_map
     [max_tokens], cu_new [B + 1], state_out [2], status [4]), as mtp_page_plan describes."""
-    dev = getattr(old_len, "device", None)
     _need_flat(old_len, "old_len", torch.int32, (None,))
-    Bn = old_len.shape[0]
-    _need_flat(new_len, "new_len", torch.int32, (Bn,), dev)
-    _need(block_table, "block_table", torch.int32, 2, dev)
-    _need_flat(free_ring, "free_ring", torch.int32, (None,), dev)
-    _need_flat(ring_state, "ring_state", torch.int32, (2,), dev)
+    dev, i32, Bn = old_len.device, torch.int32, old_len.shape[0]
+    _need_flat(new_len, "new_len", i32, (Bn,), dev)
+    _need(block_table, "block_table", i32, 2, dev)
+    _need_flat(free_ring, "free_ring", i32, (None,), dev)
+    _need_flat(ring_state, "ring_state", i32, (2,), dev)
     if block_table.shape[0] != Bn or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
         raise ValueError(f"block_table must be [{Bn}][max_pages] with a contiguous last dimension")
     if max_tokens < 0:
