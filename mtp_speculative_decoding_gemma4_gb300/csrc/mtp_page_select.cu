@@ -27,74 +27,146 @@ struct SelArgs {
   int B, nh, n_select, keep_first, keep_last, cl;
 };
 
-// Scores of 32 pages, one per lane, with 16-byte loads: LP lanes hold a page's codes (d / 16
-// vectors), 32 / LP pages side by side, four such groups in flight.
-template <int LP>
-__device__ __forceinline__ float score32(const SelArgs& a, int g, int G, int page, float ks, const int4* qc, const float* qs) {
-  const Cache& c = a.c;
-  constexpr int PW = 32 / LP, U = LP < 4 ? LP : 4;
-  const int lane = threadIdx.x & 31, li = lane & (LP - 1), nv = c.d >> 4;
-  float keep = -INFINITY;
+// The query heads' codes, packed [G][d / 4], and steps: a warp per head, its values in registers.
+__device__ __forceinline__ void quantise(const SelArgs& a, const float* q, int G, int* codes, float* qs) {
+  const int d = a.c.d, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nv = d >> 2;  // 4 values each, nv <= 128
+  for (int h = warp; h < G; h += kSelWarps) {
+    float4 x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      x[j] = lane + 32 * j < nv ? reinterpret_cast<const float4*>(q + static_cast<size_t>(h) * d)[lane + 32 * j]
+                                : make_float4(0, 0, 0, 0);
+    float mx = 0.f;
+    bool fin = true;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      mx = fmaxf(mx, fmaxf(fmaxf(fabsf(x[j].x), fabsf(x[j].y)), fmaxf(fabsf(x[j].z), fabsf(x[j].w))));
+      // a sum of |x| * 0 is NaN as soon as one value is not finite
+      fin = fin && fabsf(x[j].x) * 0.f + fabsf(x[j].y) * 0.f + fabsf(x[j].z) * 0.f + fabsf(x[j].w) * 0.f == 0.f;
+    }
+    mx = warp_max(mx);
+    fin = __all_sync(0xffffffffu, fin);
+    const float step = fin ? __fmul_rn(mx, 1.0f / 127.0f) : 0.f;
+    if (lane == 0) qs[h] = step;
 #pragma unroll 1
-  for (int it = 0; it < LP; it += U) {
-    int4 x[U];
+    for (int j = 0; j < 4; ++j) {
+      if (lane + 32 * j >= nv) break;
+      const float v[4] = {x[0].x, x[0].y, x[0].z, x[0].w};
+      unsigned w = 0;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int p = __shfl_sync(0xffffffffu, page, (it + u) * PW + lane / LP);
-      x[u] = p >= 0 && li < nv ? __ldcs(reinterpret_cast<const int4*>(c.codes + (static_cast<size_t>(p) * c.nkv + g) * c.d) + li)
-                               : make_int4(0, 0, 0, 0);
-    }
-    float s[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) s[u] = -INFINITY;
-    float k[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) k[u] = __shfl_sync(0xffffffffu, ks, (it + u) * PW + lane / LP);
-#pragma unroll 2
-    for (int h = 0; h < G; ++h) {
-      const int4 q = li < nv ? qc[h * nv + li] : make_int4(0, 0, 0, 0);
-      const float step = qs[h];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        int dot = __dp4a(x[u].x, q.x, __dp4a(x[u].y, q.y, __dp4a(x[u].z, q.z, __dp4a(x[u].w, q.w, 0))));
-        if (LP == 32) {
-          dot = __reduce_add_sync(0xffffffffu, dot);
-        } else {
-#pragma unroll
-          for (int o = LP / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        }
-        s[u] = fmaxf(s[u], __fmul_rn(__fmul_rn(static_cast<float>(dot), step), k[u]));
+      for (int e = 0; e < 4; ++e) {
+        const float f = step > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(v[e], step)), -127.f), 127.f) : 0.f;
+        w |= (static_cast<unsigned>(static_cast<int>(f)) & 255u) << (8 * e);
       }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const float v = __shfl_sync(0xffffffffu, s[u], (lane & (PW - 1)) * LP);
-      if (lane / PW == it + u) keep = v;
+      codes[h * nv + lane + 32 * j] = static_cast<int>(w);
+      x[0] = x[1];
+      x[1] = x[2];
+      x[2] = x[3];
     }
   }
-  return keep;
+}
+
+// Scores of this CTA's share of n pages: 8 lanes hold a page's codes (VL 16-byte vectors each),
+// 4 pages side by side, U such groups in flight. A warp takes `per` pages at a time, one per lane,
+// and requests its first codes before the query is quantised.
+template <int VL>
+__device__ __forceinline__ void score_pages(const SelArgs& a, int b, int g, int G, int n, int rank, const float* q,
+                                            int* codes, float* qs, unsigned* score) {
+  const Cache& c = a.c;
+  constexpr int U = VL == 4 ? 2 : 4;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, li = lane & 7, nv = c.d >> 4;
+  // with few pages every warp of the cluster gets some
+  const int warps = a.cl * kSelWarps, per = min(32, (n + warps - 1) / warps);
+  int4 x[U][VL];
+  int page = -1;
+  auto fetch = [&](int i) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = i + 4 * u + (lane >> 3), p = __shfl_sync(0xffffffffu, page, at & 31);
+      const int4* row = reinterpret_cast<const int4*>(c.codes + (static_cast<size_t>(max(p, 0)) * c.nkv + g) * c.d);
+#pragma unroll
+      for (int v = 0; v < VL; ++v)
+        x[u][v] = at < per && p >= 0 && li + 8 * v < nv ? __ldcs(row + li + 8 * v) : make_int4(0, 0, 0, 0);
+    }
+  };
+  bool first = true;
+  for (int i0 = (rank * kSelWarps + warp) * per; i0 < n || first; i0 += warps * per) {
+    const int lp = lane < per ? i0 + lane : n;
+    page = lp < n ? phys_page(c, b, lp) : -1;
+    fetch(0);
+    const float ks = page >= 0 ? c.scales[static_cast<size_t>(page) * c.nkv + g] : 0.f;
+    if (first) {
+      quantise(a, q, G, codes, qs);
+      __syncthreads();
+      first = false;
+    }
+    float keep = -INFINITY;
+#pragma unroll 1
+    for (int i = 0; i < per; i += 4 * U) {
+      if (i > 0) fetch(i);
+      float s[U], k[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        s[u] = -INFINITY;
+        k[u] = __shfl_sync(0xffffffffu, ks, (i + 4 * u + (lane >> 3)) & 31);
+      }
+#pragma unroll 1
+      for (int h = 0; h < G; ++h) {
+        int dot[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) dot[u] = 0;
+#pragma unroll
+        for (int v = 0; v < VL; ++v) {
+          const int4 w = li + 8 * v < nv ? reinterpret_cast<const int4*>(codes)[h * nv + li + 8 * v] : make_int4(0, 0, 0, 0);
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            dot[u] = __dp4a(x[u][v].x, w.x, __dp4a(x[u][v].y, w.y, __dp4a(x[u][v].z, w.z, __dp4a(x[u][v].w, w.w, dot[u]))));
+        }
+        const float step = qs[h];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+          for (int o = 4; o > 0; o >>= 1) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], o);
+          s[u] = fmaxf(s[u], __fmul_rn(__fmul_rn(static_cast<float>(dot[u]), step), k[u]));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float v = __shfl_sync(0xffffffffu, s[u], (lane & 3) * 8);
+        if (lane >> 2 == (i >> 2) + u) keep = v;
+      }
+    }
+    if (page < 0) keep = -INFINITY;
+    if (isnan(ks)) keep = INFINITY;  // a page whose keys are not finite is always read
+    if (lp < a.keep_first || lp >= n - a.keep_last) keep = INFINITY;
+    if (lp < n) score[lp] = ord_f32(keep);
+  }
 }
 
 // The same for a head dim that is no multiple of 16: 4-byte loads, a page at a time.
-__device__ __noinline__ float score32_any(const SelArgs& a, int g, int G, int page, float ks, const int* qc, const float* qs) {
+__device__ __noinline__ void score_pages_any(const SelArgs& a, int b, int g, int G, int n, int rank, const float* q,
+                                             int* codes, float* qs, unsigned* score) {
   const Cache& c = a.c;
-  const int lane = threadIdx.x & 31, nw = c.d >> 2;
-  float keep = -INFINITY;
-  for (int p = 0; p < 32; ++p) {
-    const int pg = __shfl_sync(0xffffffffu, page, p);
-    if (pg < 0) continue;
-    const int* row = reinterpret_cast<const int*>(c.codes + (static_cast<size_t>(pg) * c.nkv + g) * c.d);
-    const float k = __shfl_sync(0xffffffffu, ks, p);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = c.d >> 2;
+  quantise(a, q, G, codes, qs);
+  __syncthreads();
+  for (int lp = rank * kSelWarps + warp; lp < n; lp += a.cl * kSelWarps) {
+    const int page = phys_page(c, b, lp);
     float s = -INFINITY;
-    for (int h = 0; h < G; ++h) {
-      int dot = 0;
-      for (int i = lane; i < nw; i += 32) dot = __dp4a(row[i], qc[h * nw + i], dot);
-      dot = __reduce_add_sync(0xffffffffu, dot);
-      s = fmaxf(s, __fmul_rn(__fmul_rn(static_cast<float>(dot), qs[h]), k));
+    if (page >= 0) {
+      const int* row = reinterpret_cast<const int*>(c.codes + (static_cast<size_t>(page) * c.nkv + g) * c.d);
+      const float k = c.scales[static_cast<size_t>(page) * c.nkv + g];
+      for (int h = 0; h < G; ++h) {
+        int dot = 0;
+        for (int i = lane; i < nw; i += 32) dot = __dp4a(row[i], codes[h * nw + i], dot);
+        dot = __reduce_add_sync(0xffffffffu, dot);
+        s = fmaxf(s, __fmul_rn(__fmul_rn(static_cast<float>(dot), qs[h]), k));
+      }
+      if (isnan(k)) s = INFINITY;
     }
-    if (lane == p) keep = s;
+    if (lp < a.keep_first || lp >= n - a.keep_last) s = INFINITY;
+    if (lane == 0) score[lp] = ord_f32(s);
   }
-  return keep;
 }
 
 __global__ void __launch_bounds__(kSelThreads) k_page_select(const __grid_constant__ SelArgs a) {
@@ -114,39 +186,11 @@ __global__ void __launch_bounds__(kSelThreads) k_page_select(const __grid_consta
     return;
   }
   unsigned* score = a.score + static_cast<size_t>(unit) * c.max_pages;
-  for (int h = warp; h < G; h += kSelWarps) {
-    const float* q = a.q + (static_cast<size_t>(b) * a.nh + g * G + h) * d;
-    float mx = 0.f;
-    bool fin = true;
-    for (int i = lane; i < d; i += 32) {
-      mx = fmaxf(mx, fabsf(q[i]));
-      fin = fin && isfinite(q[i]);
-    }
-    mx = warp_max(mx);
-    fin = __all_sync(0xffffffffu, fin);
-    const float step = fin ? __fmul_rn(mx, 1.0f / 127.0f) : 0.f;
-    if (lane == 0) qs[h] = step;
-    signed char* out = reinterpret_cast<signed char*>(sm_sel + h * (d / 4));
-    for (int i = lane; i < d; i += 32)
-      out[i] = step > 0.f ? static_cast<signed char>(fminf(fmaxf(rintf(__fdiv_rn(q[i], step)), -127.f), 127.f)) : 0;
-  }
-  __syncthreads();
-  const int4* qc = reinterpret_cast<const int4*>(sm_sel);
-  for (int i0 = (rank * kSelWarps + warp) * 32; i0 < n; i0 += a.cl * kSelWarps * 32) {
-    const int lp = i0 + lane;
-    const int page = lp < n ? phys_page(c, b, lp) : -1;
-    const float ks = page >= 0 ? c.scales[static_cast<size_t>(page) * c.nkv + g] : 0.f;
-    float s;
-    if (d % 16 != 0) s = score32_any(a, g, G, page, ks, sm_sel, qs);
-    else if (d > 256) s = score32<32>(a, g, G, page, ks, qc, qs);
-    else if (d > 128) s = score32<16>(a, g, G, page, ks, qc, qs);
-    else if (d > 64) s = score32<8>(a, g, G, page, ks, qc, qs);
-    else s = score32<4>(a, g, G, page, ks, qc, qs);
-    if (page < 0) s = -INFINITY;
-    if (isnan(ks)) s = INFINITY;  // a page whose keys are not finite is always read
-    if (lp < a.keep_first || lp >= n - a.keep_last) s = INFINITY;
-    if (lp < n) score[lp] = ord_f32(s);
-  }
+  const float* q = a.q + (static_cast<size_t>(b) * a.nh + g * G) * d;
+  if (d % 16 != 0) score_pages_any(a, b, g, G, n, rank, q, sm_sel, qs, score);
+  else if (d > 256) score_pages<4>(a, b, g, G, n, rank, q, sm_sel, qs, score);
+  else if (d > 128) score_pages<2>(a, b, g, G, n, rank, q, sm_sel, qs, score);
+  else score_pages<1>(a, b, g, G, n, rank, q, sm_sel, qs, score);
   // the scores of the whole cluster are in place; only the first CTA goes on
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (rank != 0) return;
