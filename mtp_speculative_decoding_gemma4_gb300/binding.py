@@ -188,15 +188,19 @@ def mtp_set_debug(handle: int, skip_arrival_cta: int, spin_limit_cycles: int) ->
 def mtp_page_plan(old_len: int, new_len: int, B: int, block_table: int, table_stride: int, max_pages: int,
                   free_ring: int, n_pages: int, ring_state: int, page_size: int, max_tokens: int, len_out: int,
                   slot_map: int, cu_new: int, state_out: int, status: int, stream: int = 0) -> None:
-    _check(load_library().mtp_page_plan(old_len, new_len, B, block_table, table_stride, max_pages, free_ring, n_pages,
-                                        ring_state, page_size, max_tokens, len_out, slot_map or None, cu_new,
-                                        state_out, status, stream or None), "mtp_page_plan")
+    rc = (_lib or load_library()).mtp_page_plan(old_len, new_len, B, block_table, table_stride, max_pages, free_ring,
+                                                n_pages, ring_state, page_size, max_tokens, len_out, slot_map or None,
+                                                cu_new, state_out, status, stream or None)
+    if rc:
+        _check(rc, "mtp_page_plan")
 
 
 def mtp_page_append(kv: mtp_paged_kv, k_new: int, v_new: int, row_stride_k: int, row_stride_v: int, slot_map: int,
                     T: int, stream: int = 0) -> None:
-    _check(load_library().mtp_page_append(kv, k_new or None, v_new or None, row_stride_k, row_stride_v,
-                                          slot_map or None, T, stream or None), "mtp_page_append")
+    rc = (_lib or load_library()).mtp_page_append(kv, k_new or None, v_new or None, row_stride_k, row_stride_v,
+                                                  slot_map or None, T, stream or None)
+    if rc:
+        _check(rc, "mtp_page_append")
 
 
 def mtp_paged_attention_workspace(kv: mtp_paged_kv, B: int, n_head: int, n_list: int) -> int:
@@ -209,9 +213,10 @@ def mtp_paged_attention_workspace(kv: mtp_paged_kv, B: int, n_head: int, n_list:
 def mtp_paged_attention(kv: mtp_paged_kv, q: int, B: int, n_head: int, window: int, scale: float, pages: int,
                         n_list: int, out: int, lse: int, workspace: int, workspace_bytes: int,
                         stream: int = 0) -> None:
-    _check(load_library().mtp_paged_attention(kv, q, B, n_head, window, scale, pages or None, n_list, out,
-                                              lse or None, workspace or None, workspace_bytes, stream or None),
-           "mtp_paged_attention")
+    rc = (_lib or load_library()).mtp_paged_attention(kv, q, B, n_head, window, scale, pages or None, n_list, out,
+                                                      lse or None, workspace or None, workspace_bytes, stream or None)
+    if rc:
+        _check(rc, "mtp_paged_attention")
 
 
 def mtp_page_select_workspace(kv: mtp_paged_kv, B: int) -> int:
@@ -222,8 +227,10 @@ def mtp_page_select_workspace(kv: mtp_paged_kv, B: int) -> int:
 
 def mtp_page_select(kv: mtp_paged_kv, q: int, B: int, n_head: int, n_select: int, keep_first: int, keep_last: int,
                     sel: int, workspace: int, workspace_bytes: int, stream: int = 0) -> None:
-    _check(load_library().mtp_page_select(kv, q, B, n_head, n_select, keep_first, keep_last, sel, workspace or None,
-                                          workspace_bytes, stream or None), "mtp_page_select")
+    rc = (_lib or load_library()).mtp_page_select(kv, q, B, n_head, n_select, keep_first, keep_last, sel,
+                                                  workspace or None, workspace_bytes, stream or None)
+    if rc:
+        _check(rc, "mtp_page_select")
 
 
 def mtp_destroy(handle: int) -> None:

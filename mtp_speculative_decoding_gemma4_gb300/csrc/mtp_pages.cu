@@ -198,150 +198,214 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(const __grid_constan
 
 // ---------------------------------------------------------------- append
 
-// A CTA copies `rows` rows (16 bytes per thread and step) into their slots and then makes the
-// summaries of the pages that these rows complete:
+// Rows of a call into their slots, 16 bytes per thread and step. With summaries a page's sum is
+// taken as its rows pass through: a run is a stretch of rows in consecutive slots of one page, and
+// the CTA in whose share a run begins copies all of it and, where it completes the page, makes
 //   m = fl32(mean of the page's P rows), scale = fl32(max |m| * fl32(1 / 127)),
 //   code = rint(fl32(m / scale)); a page whose mean is not finite gets scale NaN and codes 0.
-// The sum is kept as an unevaluated pair of fp32 (two-sum), so m is the rounded exact mean for any
-// order of the rows. A page's rows are read where this call does not write: the rows of this call
-// from k_new (usually just copied, so from the L1), the older ones from the cache; so the copy and
-// the summaries need no second launch. What bounds it is the copy: each row read and written once.
+// The sum is kept as an unevaluated pair of fp32 (two-sum, 6 operations a value); bf16 rows are
+// first added four at a time in fp32, which rounds nothing unless the four differ by more than
+// 2^14, and then less than 2^-24 of their largest. So m is the exact mean, rounded, in any order of
+// the rows, and the arithmetic stays below the copy. The page's other rows are read where this call does not write: rows of this
+// call in another order from k_new, older ones from the cache; so one launch does. What bounds it
+// is the copy: each row read and written once.
 __device__ __forceinline__ void two_sum(float& hi, float& lo, float x) {
   const float s = __fadd_rn(hi, x), bb = __fsub_rn(s, hi);
   lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, bb)), __fsub_rn(x, bb)));
   hi = s;
 }
+constexpr int kAppThreads = 256, kAppRows = 64;  // threads, most rows of a CTA's share
 
-constexpr int kAppThreads = 256, kAppRows = 64;  // threads, most rows of a CTA
+struct AppArgs {
+  Cache c;
+  const uint4 *kn, *vn;   // new rows
+  long long row_k, row_v; // 16-byte vectors between them
+  const int* slots;
+  int n, rows;            // rows of the call, of a CTA's share
+  int vph, vshift;        // vectors of a head; log2 of a row's (-1: no power of two)
+};
 
+// The copy alone.
 template <typename T>
-__global__ void __launch_bounds__(kAppThreads)
-    k_page_append(const __grid_constant__ Cache c, const uint4* kn, const uint4* vn, long long row_k, long long row_v,
-                  const int* slots, int n, int rows) {
+__global__ void __launch_bounds__(kAppThreads) k_page_append(const __grid_constant__ AppArgs a) {
   pdl_enter();
-  __shared__ int slot_s[kAppRows], done[kAppRows], ndone;
-  const int tid = threadIdx.x, P = 1 << c.pshift, t0 = blockIdx.x * rows, nr = min(rows, n - t0);
-  constexpr int VE = Elem<T>::kVec;
-  const int vph = c.d / VE, vpr = c.nkv * vph;  // 16-byte vectors of a head and of a row
-  if (tid == 0) ndone = 0;
-  __syncthreads();
+  __shared__ long long dst_s[kAppRows];  // first 16-byte vector of a row's place in the cache, or -1
+  const Cache& c = a.c;
+  constexpr int VE = Elem<T>::kVec, U = 4;
+  const int tid = threadIdx.x, P = 1 << c.pshift, t0 = blockIdx.x * a.rows, nr = min(a.rows, a.n - t0);
+  const int vpr = c.nkv * a.vph, total = nr * vpr;
   if (tid < nr) {
-    const int slot = slots[t0 + tid];
+    const int slot = a.slots[t0 + tid];
     const bool ok = slot >= 0 && (slot >> c.pshift) < c.n_pages;
-    slot_s[tid] = ok ? slot : -1;
-    if (ok && c.codes && (slot & (P - 1)) == P - 1) done[atomicAdd(&ndone, 1)] = t0 + tid;
+    dst_s[tid] = ok ? ((slot >> c.pshift) * c.sp + (slot & (P - 1)) * c.st) / VE : -1;
   }
   __syncthreads();
-  {
-    constexpr int U = 4;
-    const int total = nr * vpr;
-    for (int i0 = tid; i0 < total; i0 += U * kAppThreads) {
-      uint4 x[U], y[U];
-      size_t at[U];
-      bool on[U];
+  for (int i0 = tid; i0 < total; i0 += U * kAppThreads) {
+    uint4 x[U], y[U];
+    long long at[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * kAppThreads, r = i / vpr, v = i - r * vpr;
-        on[u] = i < total && slot_s[r] >= 0;
-        if (!on[u]) continue;
-        const int h = c.nkv == 1 ? 0 : v / vph, slot = slot_s[r];
-        at[u] = (static_cast<size_t>(slot >> c.pshift) * c.sp + static_cast<size_t>(slot & (P - 1)) * c.st +
-                 static_cast<size_t>(h) * c.sh) / VE + (v - h * vph);
-        x[u] = __ldg(kn + (t0 + r) * row_k + v);
-        if (c.v) y[u] = __ldcs(vn + (t0 + r) * row_v + v);
-      }
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kAppThreads, r = a.vshift >= 0 ? i >> a.vshift : i / vpr, v = i - r * vpr;
+      at[u] = i < total ? dst_s[r] : -1;
+      if (at[u] < 0) continue;
+      at[u] += v;
+      if (c.nkv > 1) at[u] += v / a.vph * (c.sh / VE - a.vph);  // a head begins c.sh elements after the one before
+      x[u] = __ldcs(a.kn + (t0 + r) * a.row_k + v);
+      if (c.v) y[u] = __ldcs(a.vn + (t0 + r) * a.row_v + v);
+    }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (!on[u]) continue;
-        static_cast<uint4*>(c.k)[at[u]] = x[u];
-        if (c.v) static_cast<uint4*>(c.v)[at[u]] = y[u];
-      }
+    for (int u = 0; u < U; ++u) {
+      if (at[u] < 0) continue;
+      static_cast<uint4*>(c.k)[at[u]] = x[u];
+      if (c.v) static_cast<uint4*>(c.v)[at[u]] = y[u];
     }
   }
-  if (!c.codes) return;
-  __shared__ int src[256], missing;           // row of this call for each row of the page, or -1
+}
+
+// The copy with the summaries of the pages that it completes.
+template <typename T>
+__global__ void __launch_bounds__(kAppThreads, 4) k_page_append_sum(const __grid_constant__ AppArgs a) {
+  pdl_enter();
+  constexpr int VE = Elem<T>::kVec;
+  const Cache& c = a.c;
+  const int tid = threadIdx.x, P = 1 << c.pshift, t0 = blockIdx.x * a.rows, nr = min(a.rows, a.n - t0);
+  __shared__ int win[kAppRows + 257];    // slots of rows t0 - 1 .. t0 + nr + P - 1 (-2: no slot)
+  __shared__ int begin[kAppRows], nbegin, run_len;
+  __shared__ int src[256];               // row of this call for each row of the page, or -1
   __shared__ float part[2][kAppThreads * 8];
-  __shared__ float red[kAppThreads / 32];
-  int lanes = 1;
-  while (lanes < vph) lanes <<= 1;
-  const int par = kAppThreads / lanes, v = tid & (lanes - 1), r0 = tid / lanes;
-  const int pages = ndone;
-  for (int it = 0; it < pages; ++it) {
-    const int t = done[it], page = slot_s[t - t0] >> c.pshift;
-    if (tid == 0) missing = 0;
+  __shared__ int hmax[kAppThreads];      // max |m| of each head of a block of columns, as an integer
+  if (tid == 0) nbegin = 0;
+  const int slot_end = c.n_pages << c.pshift;
+  for (int i = tid; i < nr + P; i += kAppThreads) {
+    const int t = t0 - 1 + i, slot = t >= 0 && t < a.n ? a.slots[t] : -1;
+    win[i] = slot >= 0 && slot < slot_end ? slot : -2;
+  }
+  __syncthreads();
+  // row t0 + r has slot win[r + 1]; it goes on a run if it follows the row before in the same page
+  auto goes_on = [&](int r) { return win[r + 1] == win[r] + 1 && (win[r + 1] & (P - 1)) != 0; };
+  if (tid < nr && win[tid + 1] >= 0 && !goes_on(tid)) begin[atomicAdd(&nbegin, 1)] = tid;
+  __syncthreads();
+  // blocks of whole heads, at most a vector per thread; the threads left over take other rows
+  const int hpb = min(c.nkv, max(1, kAppThreads / a.vph)), cols = hpb * a.vph, par = kAppThreads / cols;
+  const int r0 = tid / cols, v = tid - r0 * cols, hv = v / a.vph;
+  const bool act = r0 < par;
+  const int runs = nbegin;
+  for (int it = 0; it < runs; ++it) {
+    const int first = begin[it], slot = win[first + 1], page = slot >> c.pshift, off = slot & (P - 1);
+    if (tid == 0) run_len = P - off;
     __syncthreads();
-    if (tid < P) {  // the rows that usually come right before the last one
-      const int ti = t - (P - 1 - tid);
-      const bool here = ti >= 0 && slots[ti] == (page << c.pshift) + tid;
-      src[tid] = here ? ti : -1;
-      if (!here) missing = 1;
-    }
+    if (tid + 1 < P - off && !goes_on(first + 1 + tid)) atomicMin(&run_len, tid + 1);
     __syncthreads();
-    if (missing) {  // else older rows, or rows of this call in another order
-      for (int i = tid; i < n; i += kAppThreads) {
-        const int slot = slots[i];
-        if (slot >= 0 && slot >> c.pshift == page) src[slot & (P - 1)] = i;
-      }
+    const int len = run_len;
+    const bool done = off + len == P, whole = len == P;
+    if (done && !whole) {  // the page's other rows: of this call, or older
+      if (tid < P) src[tid] = -1;
       __syncthreads();
+      for (int i = tid; i < a.n; i += kAppThreads) {
+        const int s = a.slots[i];
+        if (s >= 0 && s >> c.pshift == page) src[s & (P - 1)] = i;
+      }
     }
-    for (int g = 0; g < c.nkv; ++g) {
-      const T* base = static_cast<const T*>(c.k) + static_cast<size_t>(page) * c.sp + static_cast<size_t>(g) * c.sh;
+    for (int h0 = 0; h0 < c.nkv; h0 += hpb) {
+      const int h = h0 + hv;
+      const bool on = act && h < c.nkv;
+      if (tid < hpb) hmax[tid] = 0;
+      __syncthreads();  // src and hmax are set, part of the block before is read
       float hi[VE], lo[VE];
 #pragma unroll
       for (int e = 0; e < VE; ++e) hi[e] = lo[e] = 0.f;
-      if (v < vph) {
-#pragma unroll 4
-        for (int r = r0; r < P; r += par) {
-          const int ti = src[r];
-          const T* row = ti >= 0 ? reinterpret_cast<const T*>(kn + ti * row_k + g * vph) : base + r * c.st;
-          float x[VE];
-          load_vec(row + v * VE, x);
+      auto add = [&](const uint4& u) {
+        float x[VE];
+        load_vec(reinterpret_cast<const T*>(&u), x);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) two_sum(hi[e], lo[e], x[e]);
+      };
+      auto add4 = [&](const uint4 (&u)[4]) {  // rows that are not there are zero
+        if (VE == 4) {                        // fp32 rows
+#pragma unroll
+          for (int i = 0; i < 4; ++i) add(u[i]);
+        } else {
+          float x[VE], y[VE];
+          load_vec(reinterpret_cast<const T*>(&u[0]), x);
+#pragma unroll
+          for (int i = 1; i < 4; ++i) {
+            load_vec(reinterpret_cast<const T*>(&u[i]), y);
+#pragma unroll
+            for (int e = 0; e < VE; ++e) x[e] = __fadd_rn(x[e], y[e]);
+          }
 #pragma unroll
           for (int e = 0; e < VE; ++e) two_sum(hi[e], lo[e], x[e]);
         }
+      };
+      if (on) {
+        const long long at = (page * c.sp + (off + r0) * c.st + h * c.sh) / VE + (v - hv * a.vph);
+        const long long st = c.st / VE * par, row = t0 + first + r0, col = h0 * a.vph + v;
+        // loads of 4 rows, then their stores
+        auto pass = [&](const uint4* from, long long step, uint4* to, bool sum) {
+          for (int r = r0; r < len; r += 4 * par) {
+            uint4 x[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) x[u] = r + u * par < len ? __ldcs(from + u * step) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              if (r + u * par < len) to[u * st] = x[u];
+            if (sum) add4(x);
+            from += 4 * step;
+            to += 4 * st;
+          }
+        };
+        pass(a.kn + row * a.row_k + col, par * a.row_k, static_cast<uint4*>(c.k) + at, done);
+        if (c.v) pass(a.vn + row * a.row_v + col, par * a.row_v, static_cast<uint4*>(c.v) + at, false);
+        if (done && !whole) {
+          const uint4* old = static_cast<const uint4*>(c.k) + (page * c.sp + h * c.sh) / VE + (v - hv * a.vph);
+#pragma unroll 4
+          for (int r = r0; r < off; r += par) {
+            const int ti = src[r];
+            add(ti >= 0 ? a.kn[ti * a.row_k + col] : old[r * (c.st / VE)]);
+          }
+        }
       }
+      if (!done) continue;
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
         part[0][e * kAppThreads + tid] = hi[e];
         part[1][e * kAppThreads + tid] = lo[e];
       }
       __syncthreads();
-      float m[VE], mx = 0.f;
-      bool fin = true;
-      if (tid < lanes && v < vph) {
+      float m[VE];
+      if (on && r0 == 0) {
+        float mx = 0.f;
+        bool fin = true;
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
-          float h = part[0][e * kAppThreads + tid], l = part[1][e * kAppThreads + tid];
+          float x = part[0][e * kAppThreads + tid], l = part[1][e * kAppThreads + tid];
           for (int r = 1; r < par; ++r) {
-            two_sum(h, l, part[0][e * kAppThreads + tid + r * lanes]);
-            l += part[1][e * kAppThreads + tid + r * lanes];
+            two_sum(x, l, part[0][e * kAppThreads + tid + r * cols]);
+            l += part[1][e * kAppThreads + tid + r * cols];
           }
-          m[e] = __fmul_rn(__fadd_rn(h, l), 1.0f / P);
+          m[e] = __fmul_rn(__fadd_rn(x, l), 1.0f / P);
           fin = fin && isfinite(m[e]);
           mx = fmaxf(mx, fabsf(m[e]));
         }
+        atomicMax(&hmax[hv], __float_as_int(fin ? mx : INFINITY));
       }
-      mx = warp_max(fin ? mx : INFINITY);
-      if ((tid & 31) == 0) red[tid >> 5] = mx;
       __syncthreads();
-      mx = 0.f;
-#pragma unroll
-      for (int w = 0; w < kAppThreads / 32; ++w) mx = fmaxf(mx, red[w]);
-      const float scale = __fmul_rn(mx, 1.0f / 127.0f);
-      if (tid < lanes && v < vph) {
+      if (on && r0 == 0) {
+        const float scale = __fmul_rn(__int_as_float(hmax[hv]), 1.0f / 127.0f);
         __align__(8) signed char q[VE];
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
           const float f = scale > 0.f && isfinite(scale) ? rintf(__fdiv_rn(m[e], scale)) : 0.f;
           q[e] = static_cast<signed char>(fminf(fmaxf(f, -127.f), 127.f));
         }
-        signed char* out = c.codes + (static_cast<size_t>(page) * c.nkv + g) * c.d + v * VE;
+        const int i = v - hv * a.vph;
+        signed char* out = c.codes + (static_cast<size_t>(page) * c.nkv + h) * c.d + i * VE;
         if (VE == 8)
           *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(q);
         else
           *reinterpret_cast<unsigned*>(out) = *reinterpret_cast<const unsigned*>(q);
+        if (i == 0) c.scales[static_cast<size_t>(page) * c.nkv + h] = isfinite(scale) ? scale : NAN;
       }
-      if (tid == 0) c.scales[static_cast<size_t>(page) * c.nkv + g] = isfinite(scale) ? scale : NAN;
       __syncthreads();
     }
   }
@@ -382,16 +446,25 @@ int run_page_append(const pg::Cache& c, const void* k_new, const void* v_new, lo
                     const int* slots, int T, int num_sms, cudaStream_t st) {
   if (T == 0) return MTP_OK;
   const int es = c.f32 ? 4 : 2;
-  // rows of a CTA: about 6 CTAs per SM, so that all of them run at once
-  int rows = pg::kAppRows;
-  while (rows > 1 && (T + rows - 1) / rows < 6 * num_sms) rows >>= 1;
-  const int grid = (T + rows - 1) / rows;
-  const uint4 *k = static_cast<const uint4*>(k_new), *v = static_cast<const uint4*>(v_new);
-  const long long rk = row_k * es / 16, rv = row_v * es / 16;
-  if (c.f32)
-    pg::k_page_append<float><<<grid, pg::kAppThreads, 0, st>>>(c, k, v, rk, rv, slots, T, rows);
-  else
-    pg::k_page_append<__nv_bfloat16><<<grid, pg::kAppThreads, 0, st>>>(c, k, v, rk, rv, slots, T, rows);
+  pg::AppArgs a{c, static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new), row_k * es / 16, row_v * es / 16,
+                slots, T, pg::kAppRows, c.d * es / 16, 0};
+  // about 6 CTAs per SM, so that all of them run at once
+  while (a.rows > 1 && (T + a.rows - 1) / a.rows < 6 * num_sms) a.rows >>= 1;
+  const int vpr = c.nkv * a.vph;
+  while ((1 << a.vshift) < vpr) ++a.vshift;
+  if ((1 << a.vshift) != vpr) a.vshift = -1;
+  const int grid = (T + a.rows - 1) / a.rows;
+  if (c.codes) {
+    if (c.f32)
+      pg::k_page_append_sum<float><<<grid, pg::kAppThreads, 0, st>>>(a);
+    else
+      pg::k_page_append_sum<__nv_bfloat16><<<grid, pg::kAppThreads, 0, st>>>(a);
+  } else {
+    if (c.f32)
+      pg::k_page_append<float><<<grid, pg::kAppThreads, 0, st>>>(a);
+    else
+      pg::k_page_append<__nv_bfloat16><<<grid, pg::kAppThreads, 0, st>>>(a);
+  }
   MTP_PG_CHECK("page append");
   return MTP_OK;
 }

@@ -136,17 +136,16 @@ def page_plan(old_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.T
 
 
 def _plan(st, old_len, new_len, block_table, free_ring, ring_state, page_size, max_tokens):
-    Bn, cols = block_table.shape
-    # one allocation: slot_map (16-byte aligned), then the small outputs
-    pad = -max_tokens % 4
-    buf = torch.empty(max_tokens + pad + 2 * Bn + 7, dtype=torch.int32, device=old_len.device)
-    slots, _, len_out, cu, state, status = buf.split((max_tokens, pad, Bn, Bn + 1, 2, 4))
-    at = buf.data_ptr()
-    ln = at + 4 * (max_tokens + pad)
+    (Bn, cols), dev, i32 = block_table.shape, old_len.device, torch.int32
+    len_out = torch.empty(Bn, dtype=i32, device=dev)
+    slots = torch.empty(max_tokens, dtype=i32, device=dev)
+    cu = torch.empty(Bn + 1, dtype=i32, device=dev)
+    state = torch.empty(2, dtype=i32, device=dev)
+    status = torch.empty(4, dtype=i32, device=dev)
     B.mtp_page_plan(old_len.data_ptr(), new_len.data_ptr(), Bn, block_table.data_ptr(),
                     block_table.stride(0) if Bn > 1 else cols, cols, free_ring.data_ptr(), free_ring.shape[0],
-                    ring_state.data_ptr(), page_size, max_tokens, ln, at, ln + 4 * Bn, ln + 4 * (2 * Bn + 1),
-                    ln + 4 * (2 * Bn + 3), st)
+                    ring_state.data_ptr(), page_size, max_tokens, len_out.data_ptr(), slots.data_ptr(), cu.data_ptr(),
+                    state.data_ptr(), status.data_ptr(), st)
     return len_out, slots, cu, state, status
 
 
