@@ -170,23 +170,30 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(const __grid_constan
   // slots, 4 per lane: a warp takes a run of consecutive tokens, so it searches its first
   // sequence once and then only moves on
   const int words = (a.max_tokens + 3) / 4, warps = gs >> 5, run = ((words + warps - 1) / warps + 31) & ~31;
-  int b = -1;
+  int b = -1, end = 0, shift = 0, n0 = 0, last = -1, page = -1;  // sequence, its end, position - token; the page at hand
   for (int j = (gt >> 5) * run + (tid & 31), j1 = min(words, (gt >> 5) * run + run); j < j1; j += 32) {
     int s[4] = {-1, -1, -1, -1};
     const int t0 = 4 * j;
-    if (t0 < total) {
-      if (b < 0) b = find_seq(cu, B, t0);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int t = t0 + u;
-        if (t >= total) break;
+    for (int u = 0; u < 4; ++u) {
+      const int t = t0 + u;
+      if (t >= total) break;
+      if (t >= end) {
+        b = b < 0 ? find_seq(cu, B, t) : b + 1;
         while (cu[b + 1] <= t) ++b;
-        const int o = static_cast<int>(min(static_cast<long long>(max(a.old_len[b], 0)), cap)), n0 = pages(o);
-        const int pos = o + t - cu[b], lp = pos >> a.pshift;
-        const int page = lp < n0 ? a.table[b * a.table_stride + lp]
-                                 : a.ring[wrap(static_cast<long long>(head) + cp[b] + lp - n0)];
-        s[u] = static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages) ? (page << a.pshift) + (pos & (P - 1)) : -1;
+        end = cu[b + 1];
+        const int o = static_cast<int>(min(static_cast<long long>(max(a.old_len[b], 0)), cap));
+        shift = o - cu[b];
+        n0 = pages(o);
+        last = -1;
       }
+      const int pos = t + shift, lp = pos >> a.pshift;
+      if (lp != last) {
+        last = lp;
+        page = lp < n0 ? a.table[b * a.table_stride + lp] : a.ring[wrap(static_cast<long long>(head) + cp[b] + lp - n0)];
+        if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.n_pages)) page = -1;
+      }
+      s[u] = page >= 0 ? (page << a.pshift) + (pos & (P - 1)) : -1;
     }
     if (t0 + 3 < a.max_tokens) {
       *reinterpret_cast<int4*>(a.slots + t0) = make_int4(s[0], s[1], s[2], s[3]);
