@@ -452,6 +452,25 @@ MTP_API int mtp_page_select(const mtp_paged_kv *kv, const float *q, int32_t B, i
                             int64_t workspace_bytes, void *stream);
 MTP_API int mtp_page_select_workspace(const mtp_paged_kv *kv, int32_t B, int64_t *bytes);
 
+/* mtp_draft_block over paged caches: the same drafter steps, with every block's attention read
+ * through the block tables (sliding blocks attend the last `window` keys). With n_select > 0 the
+ * full-attention blocks attend, per KV head, the n_select pages that mtp_page_select picks for the
+ * block's queries (keep_first and keep_last always among them): fewer keys read per draft step at
+ * the price of a lower accept rate; what is emitted after verification is the target's either way.
+ * n_select == 0 attends every page. dtype, n_kv_head and head_dim of the caches are the drafter's;
+ * max_pages * page_size may exceed mtp_config.max_ctx.
+ * Runs on path 5 when the handle has it, else 1 (mtp_set_path 1 or 5 selects; other forced paths
+ * are refused), replayed as a CUDA graph while the same arguments come again.
+ *   workspace  device scratch of mtp_draft_block_paged_workspace bytes, 16-byte aligned
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, CUDA. */
+MTP_API int mtp_draft_block_paged(mtp_handle *h, const void *hidden, const int32_t *last_token,
+                                  const mtp_paged_kv *kv_sliding, const mtp_paged_kv *kv_full, const int32_t *pos,
+                                  int32_t B, int32_t n_draft, int32_t n_select, int32_t keep_first, int32_t keep_last,
+                                  int32_t *out_tokens, float *out_hidden, void *workspace, int64_t workspace_bytes,
+                                  void *stream);
+MTP_API int mtp_draft_block_paged_workspace(mtp_handle *h, const mtp_paged_kv *kv_sliding, const mtp_paged_kv *kv_full,
+                                            int32_t B, int32_t n_select, int64_t *bytes);
+
 /* Free the workspace and the handle (synchronises). NULL is ignored. */
 MTP_API void mtp_destroy(mtp_handle *h);
 

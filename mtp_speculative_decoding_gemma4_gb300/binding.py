@@ -20,7 +20,8 @@ MTP_LAYER_SLIDING, MTP_LAYER_FULL = 0, 1
 EXPORTS = ("mtp_init_weights", "mtp_draft_block", "mtp_centroid_head", "mtp_verify_greedy", "mtp_get_status",
            "mtp_set_path", "mtp_destroy", "mtp_last_error", "mtp_centroid_head_noalloc", "mtp_set_logit_mask",
            "mtp_verify_sample", "mtp_set_sparse_head", "mtp_set_debug", "mtp_page_plan", "mtp_page_append",
-           "mtp_page_select", "mtp_page_select_workspace", "mtp_paged_attention", "mtp_paged_attention_workspace")
+           "mtp_page_select", "mtp_page_select_workspace", "mtp_paged_attention", "mtp_paged_attention_workspace",
+           "mtp_draft_block_paged", "mtp_draft_block_paged_workspace")
 MASK_NEG_1E30, MASK_MIN_MINUS_ONE = 0, 1  # enum mtp_logit_mask
 HEAD_AUTO, HEAD_PER_SEQUENCE, HEAD_CLUSTER_MAJOR = 0, 1, 2  # enum mtp_sparse_head
 
@@ -96,6 +97,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mtp_paged_attention_workspace.argtypes = [pkv, i32, i32, i32, ctypes.POINTER(i64)]
     lib.mtp_page_select.argtypes = [pkv, vp, i32, i32, i32, i32, i32, vp, vp, i64, vp]
     lib.mtp_page_select_workspace.argtypes = [pkv, i32, ctypes.POINTER(i64)]
+    lib.mtp_draft_block_paged.argtypes = [vp, vp, vp, pkv, pkv, vp, i32, i32, i32, i32, i32, vp, vp, vp, i64, vp]
+    lib.mtp_draft_block_paged_workspace.argtypes = [vp, pkv, pkv, i32, i32, ctypes.POINTER(i64)]
     lib.mtp_destroy.argtypes = [vp]
     lib.mtp_destroy.restype = None
     lib.mtp_last_error.argtypes = []
@@ -104,7 +107,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                  "mtp_get_status", "mtp_set_path", "mtp_centroid_head_noalloc", "mtp_set_logit_mask",
                  "mtp_verify_sample", "mtp_set_sparse_head", "mtp_set_debug", "mtp_page_plan", "mtp_page_append",
                  "mtp_page_select", "mtp_page_select_workspace", "mtp_paged_attention",
-                 "mtp_paged_attention_workspace"):
+                 "mtp_paged_attention_workspace", "mtp_draft_block_paged", "mtp_draft_block_paged_workspace"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -231,6 +234,22 @@ def mtp_page_select(kv: mtp_paged_kv, q: int, B: int, n_head: int, n_select: int
                                                   workspace or None, workspace_bytes, stream or None)
     if rc:
         _check(rc, "mtp_page_select")
+
+
+def mtp_draft_block_paged_workspace(handle: int, kv_sliding, kv_full, B: int, n_select: int) -> int:
+    n = ctypes.c_int64()
+    _check(load_library().mtp_draft_block_paged_workspace(handle, kv_sliding, kv_full, B, n_select, ctypes.byref(n)),
+           "mtp_draft_block_paged_workspace")
+    return n.value
+
+
+def mtp_draft_block_paged(handle: int, hidden: int, last_token: int, kv_sliding, kv_full, pos: int, B: int,
+                          n_draft: int, n_select: int, keep_first: int, keep_last: int, out_tokens: int,
+                          out_hidden: int, workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _check(load_library().mtp_draft_block_paged(handle, hidden, last_token, kv_sliding, kv_full, pos, B, n_draft,
+                                                n_select, keep_first, keep_last, out_tokens, out_hidden or None,
+                                                workspace or None, workspace_bytes, stream or None),
+           "mtp_draft_block_paged")
 
 
 def mtp_destroy(handle: int) -> None:

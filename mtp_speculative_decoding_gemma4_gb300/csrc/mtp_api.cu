@@ -9,6 +9,7 @@
 
 #include "mtp.h"
 #include "mtp_launch.h"
+#include "mtp_paged.cuh"
 #include "mtp_c2.cuh"
 #include "mtp_grid.cuh"
 #include "mtp_tc.cuh"
@@ -60,6 +61,7 @@ struct mtp_handle {
   struct {
     int valid, path;
     mtp::Params key;
+    mtp::PagedCall pkey;  // of a paged draft block, else zero
     cudaGraphExec_t exec;
     cudaStream_t cs;
     cudaEvent_t ev_in, ev_out;
@@ -682,10 +684,14 @@ int set_device(const mtp_handle* h) {
 // ones, else captures run() on the internal stream and instantiates it. Falls back to
 // direct launches on the caller's stream when graphs are not available.
 template <typename Run>
-int run_graph_cached(mtp_handle* h, int path, const mtp::Params& p, cudaStream_t st, Run run) {
+int run_graph_cached(mtp_handle* h, int path, const mtp::Params& p, cudaStream_t st, Run run,
+                     const mtp::PagedCall* pc = nullptr) {
   auto& G = h->gc;
   if (!G.cs) return run(st);
-  if (!G.valid || G.path != path || memcmp(&G.key, &p, sizeof(p)) != 0) {
+  mtp::PagedCall pkey;
+  memset(&pkey, 0, sizeof(pkey));
+  if (pc) memcpy(&pkey, pc, sizeof(pkey));
+  if (!G.valid || G.path != path || memcmp(&G.key, &p, sizeof(p)) != 0 || memcmp(&G.pkey, &pkey, sizeof(pkey)) != 0) {
     if (G.valid) {
       cudaGraphExecDestroy(G.exec);
       G.valid = 0;
@@ -705,6 +711,7 @@ int run_graph_cached(mtp_handle* h, int path, const mtp::Params& p, cudaStream_t
     cudaGraphDestroy(graph);
     if (e != cudaSuccess) return cuda_fail("instantiating the draft-block graph", e);
     memcpy(&G.key, &p, sizeof(p));
+    memcpy(&G.pkey, &pkey, sizeof(pkey));
     G.path = path;
     G.valid = 1;
   }
@@ -1007,6 +1014,113 @@ int mtp_draft_block(mtp_handle* h, const void* hidden, const int32_t* last_token
                                                    h->nsplit_max) : 1;
   return run_graph_cached(h, 1, p, st,
                           [&](cudaStream_t s2) { return bf16 ? mtp::run_phases_bf16(p, s2) : mtp::run_phases_f32(p, s2); });
+}
+
+// The paged caches of a draft block: checked against the handle and put into pc (zeroed before).
+static int paged_caches(const mtp_handle* h, const mtp_paged_kv* kv_sliding, const mtp_paged_kv* kv_full, int32_t B,
+                        int32_t n_select, int32_t keep_first, int32_t keep_last, mtp::PagedCall* pc) {
+  const mtp_config& c = h->cfg;
+  if (B < 1 || B > c.max_batch) {
+    set_error("B=%d outside [1, max_batch=%d]", B, c.max_batch);
+    return MTP_ERR_INVALID_ARG;
+  }
+  const mtp_paged_kv* kvs[2] = {kv_sliding, kv_full};
+  for (int t = 0; t < 2; ++t) {
+    if (!has_type(c, t)) continue;
+    const int rc = mtp::pg::make_cache(kvs[t], true, &pc->c[t]);
+    if (rc) return rc;
+    const int d = t ? c.head_dim_full : c.head_dim_swa;
+    if (kvs[t]->dtype != c.dtype || kvs[t]->n_kv_head != c.n_kv_head || kvs[t]->head_dim != d) {
+      set_error("%s paged cache: dtype %d, n_kv_head %d and head_dim %d are not the drafter's (%d, %d, %d)",
+                t ? "full" : "sliding", kvs[t]->dtype, kvs[t]->n_kv_head, kvs[t]->head_dim, c.dtype, c.n_kv_head, d);
+      return MTP_ERR_INVALID_ARG;
+    }
+  }
+  if (n_select < 0 || n_select > 1 << 20 ||
+      (n_select > 0 && (!has_type(c, 1) || !pc->c[1].codes || keep_first < 0 || keep_last < 1 ||
+                        static_cast<long long>(keep_first) + keep_last > n_select))) {
+    set_error("n_select=%d (0: every page) needs a full-attention layer, a cache with page summaries, keep_first >= 0, "
+              "keep_last >= 1 and keep_first + keep_last <= n_select (%d, %d)", n_select, keep_first, keep_last);
+    return MTP_ERR_INVALID_ARG;
+  }
+  if (n_select > 0 && c.n_head / c.n_kv_head > 32) {
+    set_error("at most 32 query heads per KV head with n_select (%d)", c.n_head / c.n_kv_head);
+    return MTP_ERR_UNSUPPORTED_SHAPE;
+  }
+  pc->n_select = n_select;
+  pc->keep_first = n_select > 0 ? keep_first : 0;
+  pc->keep_last = n_select > 0 ? keep_last : 0;
+  pc->num_sms = h->num_sms < mtp::pg::kMaxSms ? h->num_sms : mtp::pg::kMaxSms;
+  return MTP_OK;
+}
+
+int mtp_draft_block_paged_workspace(mtp_handle* h, const mtp_paged_kv* kv_sliding, const mtp_paged_kv* kv_full,
+                                    int32_t B, int32_t n_select, int64_t* bytes) {
+  mtp::g_err[0] = 0;
+  if (!h || !bytes) {
+    set_error("handle and bytes must be non-NULL");
+    return MTP_ERR_INVALID_ARG;
+  }
+  mtp::PagedCall pc;
+  memset(&pc, 0, sizeof(pc));
+  const int rc = paged_caches(h, kv_sliding, kv_full, B, n_select, 0, 1, &pc);
+  if (rc) return rc;
+  *bytes = mtp::paged_draft_workspace(pc, B, h->cfg.n_head, h->dmax, has_type(h->cfg, 0), has_type(h->cfg, 1), nullptr);
+  return MTP_OK;
+}
+
+int mtp_draft_block_paged(mtp_handle* h, const void* hidden, const int32_t* last_token, const mtp_paged_kv* kv_sliding,
+                          const mtp_paged_kv* kv_full, const int32_t* pos, int32_t B, int32_t n_draft, int32_t n_select,
+                          int32_t keep_first, int32_t keep_last, int32_t* out_tokens, float* out_hidden, void* workspace,
+                          int64_t workspace_bytes, void* stream) {
+  mtp::g_err[0] = 0;
+  if (!h) {
+    set_error("handle is NULL");
+    return MTP_ERR_INVALID_ARG;
+  }
+  const mtp_config& c = h->cfg;
+  if (!hidden || !last_token || !pos || !out_tokens || !aligned16(hidden)) {
+    set_error("hidden (16-byte aligned), last_token, pos and out_tokens must be non-NULL");
+    return MTP_ERR_INVALID_ARG;
+  }
+  if (n_draft < 1 || n_draft > 1024) {
+    set_error("n_draft=%d outside [1, 1024]", n_draft);
+    return MTP_ERR_INVALID_ARG;
+  }
+  mtp::PagedCall pc;
+  memset(&pc, 0, sizeof(pc));
+  int rc = paged_caches(h, kv_sliding, kv_full, B, n_select, keep_first, keep_last, &pc);
+  if (rc) return rc;
+  const long long need =
+      mtp::paged_draft_workspace(pc, B, c.n_head, h->dmax, has_type(c, 0), has_type(c, 1), static_cast<char*>(workspace));
+  if ((rc = mtp::pg::check_workspace(workspace, workspace_bytes, need))) return rc;
+  const int path = h->path ? h->path : (h->tc ? 5 : 1);
+  if (path != 1 && path != 5) {
+    set_error("a paged draft block runs on path 1 or 5 (path %d is set)", path);
+    return MTP_ERR_UNSUPPORTED_SHAPE;
+  }
+  if (path == 5 && !h->tc) {
+    set_error("the tensor-core path needs a bf16 drafter with max_batch in [2, %d] on this device", mtp::tc::kMaxB);
+    return MTP_ERR_UNSUPPORTED_SHAPE;
+  }
+  if ((rc = set_device(h))) return rc;
+  mtp::Params p = base_params(h, B);
+  p.hidden_in = hidden;
+  p.tok_in = last_token;
+  p.pos = pos;
+  p.out_tokens = out_tokens;
+  p.out_hidden = out_hidden;
+  p.n_draft = n_draft;
+  p.s.ncta_hint = 2 * h->num_sms;
+  p.s.nsplit[0] = p.s.nsplit[1] = 1;
+  const bool bf16 = c.dtype == MTP_DTYPE_BF16;
+  return run_graph_cached(
+      h, path, p, static_cast<cudaStream_t>(stream),
+      [&](cudaStream_t s2) {
+        return path == 5 ? mtp::run_phases_tc_bf16(p, *h->tc, s2, &pc)
+                         : bf16 ? mtp::run_phases_bf16(p, s2, &pc) : mtp::run_phases_f32(p, s2, &pc);
+      },
+      &pc);
 }
 
 int mtp_centroid_head(mtp_handle* h, const float* y, int32_t B, float* out_logits, int32_t* out_token,

@@ -5,6 +5,7 @@
 #include <cstdio>
 
 #include "mtp_launch.h"
+#include "mtp_paged.cuh"
 #include "mtp_phases.cuh"
 #include "mtp_tc.cuh"
 
@@ -325,7 +326,7 @@ int launch_att(const Params& p, int l, int grid, cudaStream_t st) {
 
 // One launch per phase.
 template <typename WT>
-int run_phases(const Params& p, cudaStream_t st) {
+int run_phases(const Params& p, cudaStream_t st, const PagedCall* pc) {
   const PhaseSizes z = phase_sizes<WT>(p);
   const ShapeP& s = p.s;
   MTP_LAUNCH(k_rope<WT>, s.B, 0, p);
@@ -336,8 +337,13 @@ int run_phases(const Params& p, cudaStream_t st) {
       const int t = p.L[l].type;
       MTP_LAUNCH(k_q<WT>, z.q[l], z.smem_q, p, l, par);
       if (l > 0) par ^= 1;
-      MTP_LAUNCH_ATT(l);
-      MTP_LAUNCH(k_cmb<WT>, z.cmb[l], 2 * (kThreads / kCmbDims) * kCmbDims * 4, p, l);
+      if (pc) {
+        const int rc = run_paged_layer(p, *pc, l, nullptr, 0, st);
+        if (rc) return rc;
+      } else {
+        MTP_LAUNCH_ATT(l);
+        MTP_LAUNCH(k_cmb<WT>, z.cmb[l], 2 * (kThreads / kCmbDims) * kCmbDims * 4, p, l);
+      }
       MTP_LAUNCH(k_o<WT>, o_items(p, l), z.smem_o[t], p, l);
       MTP_LAUNCH(k_gu<WT>, z.gu, z.smem_gu, p, l, par);
       par ^= 1;
@@ -358,7 +364,7 @@ int run_phases(const Params& p, cudaStream_t st) {
 // One launch per phase, every GEMV split into staging (the phase kernel with p.tc_xs set, one
 // CTA per batch group) and tcgen05 GEMMs over the staged terms.
 template <typename WT>
-int run_phases_tc(const Params& p, const TcPlan& plan, cudaStream_t st) {
+int run_phases_tc(const Params& p, const TcPlan& plan, cudaStream_t st, const PagedCall* pc) {
   const PhaseSizes z = phase_sizes<WT>(p);
   const ShapeP& s = p.s;
   Params ps = p;
@@ -387,13 +393,17 @@ int run_phases_tc(const Params& p, const TcPlan& plan, cudaStream_t st) {
                      nullptr)))
         return rc;
       if (l > 0) par ^= 1;
-      if (att_tc_supported(p, l)) {  // split-KV attention on tensor cores (bf16, V = K)
-        if ((rc = run_att_tc(p, l, st))) return rc;
+      if (pc) {
+        if ((rc = run_paged_layer(p, *pc, l, plan.xs, plan.bp, st))) return rc;
       } else {
-        MTP_LAUNCH_ATT(l);
+        if (att_tc_supported(p, l)) {  // split-KV attention on tensor cores (bf16, V = K)
+          if ((rc = run_att_tc(p, l, st))) return rc;
+        } else {
+          MTP_LAUNCH_ATT(l);
+        }
+        // the combine of the attention splits writes the O projection's staged operand
+        MTP_LAUNCH_PDL(k_cmb<WT>, z.cmb[l], 2 * (kThreads / kCmbDims) * kCmbDims * 4, ps, l);
       }
-      // the combine of the attention splits writes the O projection's staged operand
-      MTP_LAUNCH_PDL(k_cmb<WT>, z.cmb[l], 2 * (kThreads / kCmbDims) * kCmbDims * 4, ps, l);
       if ((rc = gemm(plan.o[l], plan.xs_o[t], s.H, QD, p.w.ao, s.H, nullptr, 0, nullptr))) return rc;
       MTP_LAUNCH_PDL(k_gu<WT>, groups(s.H), z.smem_gu, ps, l, par);
       if (plan.gu_ok) {

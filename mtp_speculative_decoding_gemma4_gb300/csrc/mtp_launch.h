@@ -11,6 +11,7 @@
 namespace mtp {
 
 struct Params;
+struct PagedCall;
 namespace c2 {
 struct Params;
 }
@@ -21,12 +22,13 @@ struct Params;
 // Records the calling thread's last error text (printf-style).
 void set_error(const char* fmt, ...);
 
-int run_phases_bf16(const Params& p, cudaStream_t st);
+// pc: the caches of a paged draft block, else null.
+int run_phases_bf16(const Params& p, cudaStream_t st, const PagedCall* pc = nullptr);
 int run_persistent_bf16(const Params& p, cudaStream_t st);
 int persistent_capacity_bf16(const Params& p, int num_sms);
 int run_head_bf16(const Params& p, cudaStream_t st);
 
-int run_phases_f32(const Params& p, cudaStream_t st);
+int run_phases_f32(const Params& p, cudaStream_t st, const PagedCall* pc = nullptr);
 int run_persistent_f32(const Params& p, cudaStream_t st);
 int persistent_capacity_f32(const Params& p, int num_sms);
 int run_head_f32(const Params& p, cudaStream_t st);
@@ -87,7 +89,7 @@ int att_tc_smem(int D, int hpg);  // shared-memory bytes of one CTA (0: no kerne
 int run_att_tc(const Params& p, int l, cudaStream_t st);
 
 // One launch per phase with every GEMV as staging + tcgen05 GEMMs (bf16, B <= bp).
-int run_phases_tc_bf16(const Params& p, const TcPlan& plan, cudaStream_t st);
+int run_phases_tc_bf16(const Params& p, const TcPlan& plan, cudaStream_t st, const PagedCall* pc = nullptr);
 
 int run_verify(const void* logits, const int* draft, int B, int n, int V, int* accept_len, int* out_tokens,
                cudaStream_t st);

@@ -3,6 +3,7 @@
 // sequence b at position t lies in physical page block_table[b][t / P] at offset t % P.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -84,5 +85,27 @@ int run_page_append(const pg::Cache& c, const void* k_new, const void* v_new, lo
                     const int* slots, int T, int num_sms, cudaStream_t st);
 int run_page_select(const pg::Cache& c, const float* q, int B, int nh, int n_select, int keep_first, int keep_last,
                     int* sel, void* ws, int num_sms, cudaStream_t st);
+
+struct Params;
+// What a paged draft block adds to its Params: the caches by attention type, the selection of the
+// full layers (n_select 0: every page) and the caller's workspace, carved.
+struct PagedCall {
+  pg::Cache c[2];
+  float* qn;
+  int* sel;
+  void *sel_ws, *att_ws;
+  int n_select, keep_first, keep_last, num_sms;
+};
+// Workspace bytes; with a base the pointers of pc are set.
+long long paged_draft_workspace(PagedCall& pc, int B, int nh, int dmax, int has_sliding, int has_full, char* base);
+// The attention of layer l: into p.w.o and, for the tensor-core phases, the O projection's operand
+// xs [3][bp][n_head * head_dim].
+int run_paged_layer(const Params& p, const PagedCall& pc, int l, __nv_bfloat16* xs, int bp, cudaStream_t st);
+
+namespace pg {
+// mtp_paged_kv -> Cache, every check made before the device is touched (mtp_paged_api.cu).
+int make_cache(const mtp_paged_kv* kv, bool tables, Cache* c);
+int check_workspace(const void* ws, int64_t have, long long need);
+}  // namespace pg
 
 }  // namespace mtp

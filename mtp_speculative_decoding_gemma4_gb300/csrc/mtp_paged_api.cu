@@ -105,7 +105,7 @@ static int check_batch(const Cache& c, int B, int n_head) {
   return MTP_OK;
 }
 
-static int check_workspace(const void* ws, int64_t have, long long need) {
+int check_workspace(const void* ws, int64_t have, long long need) {
   if (need > 0 && (!ws || !aligned(ws, 16) || have < need)) {
     set_error("the workspace must be 16-byte aligned and hold %lld bytes (%lld given)", need,
               static_cast<long long>(have));

@@ -9,6 +9,7 @@ from typing import Optional
 import torch
 
 from . import binding as B
+from .paged import call_on
 
 _DT = {"bf16": (B.MTP_DTYPE_BF16, torch.bfloat16), "f32": (B.MTP_DTYPE_F32, torch.float32)}
 
@@ -58,6 +59,7 @@ class Drafter:
         self.shape = shape
         self.torch_dtype = _DT[shape.dtype][1]
         self._keep = [target_embed]
+        self._paged_ws = None
         self.config = make_config(shape, max_batch, max_ctx)
         w = B.mtp_weights()
         for f in ("pre_proj", "post_proj", "token_embd", "centroids", "out_norm", "token_ordering"):
@@ -90,6 +92,36 @@ class Drafter:
         B.mtp_draft_block(self.handle, _ptr(hidden), _ptr(last_token), kv_s, kv_f, _ptr(pos), Bn, n_draft,
                           _ptr(out_tokens), _ptr(out_hidden), stream)
         return out_tokens, out_hidden
+
+    def draft_block_paged(self, hidden, last_token, kv_swa, kv_full, pos, n_draft: int, n_select: int = 0,
+                          keep_first: int = 1, keep_last: int = 1, want_hidden: bool = True, out_tokens=None,
+                          out_hidden=None, stream: Optional[int] = None):
+        """draft_block over paged caches (paged.PagedKV with block_table and ctx_len, or None for an
+        attention type that no block has). n_select > 0: full-attention blocks attend the n_select
+        pages that their queries select. stream: None is torch's current stream."""
+        Bn, dev = hidden.shape[0], hidden.device
+        for kv in (kv_swa, kv_full):
+            if kv is not None and kv.batch != Bn:
+                raise ValueError(f"the cache's block_table holds {kv.batch} sequences, hidden {Bn}")
+        kvs = [None if kv is None else kv.c for kv in (kv_swa, kv_full)]
+        n = B.mtp_draft_block_paged_workspace(self.handle, kvs[0], kvs[1], Bn, n_select)
+
+        def run(st):
+            if self._paged_ws is None or self._paged_ws.numel() < n:
+                # kept with the handle, whose calls follow one another; an outgrown one stays
+                # alive, a call that uses it may still be running
+                self._paged_ws = torch.empty(n, dtype=torch.uint8, device=dev)
+                self._keep.append(self._paged_ws)
+            tokens = torch.empty((Bn, n_draft), dtype=torch.int32, device=dev) if out_tokens is None else out_tokens
+            hid = out_hidden
+            if hid is None and want_hidden:
+                hid = torch.empty((Bn, n_draft, self.shape.backbone), dtype=torch.float32, device=dev)
+            B.mtp_draft_block_paged(self.handle, _ptr(hidden), _ptr(last_token), kvs[0], kvs[1], _ptr(pos), Bn, n_draft,
+                                    n_select, keep_first, keep_last, _ptr(tokens), _ptr(hid), _ptr(self._paged_ws), n,
+                                    st)
+            return tokens, hid
+
+        return call_on(dev, stream, run)
 
     def centroid_head(self, y: torch.Tensor, want_logits: bool = False, want_centroids: bool = False,
                       stream: int = 0):

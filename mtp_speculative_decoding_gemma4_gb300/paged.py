@@ -57,7 +57,7 @@ class _On:
 _raw_stream = torch._C._cuda_getCurrentRawStream  # torch's current stream of a device, as an integer
 
 
-def _call(device: torch.device, stream: Optional[int], fn, *args):
+def call_on(device: torch.device, stream: Optional[int], fn, *args):
     """fn(stream, *args) with the call's device current and its allocations on its stream."""
     index = device.index
     if torch.cuda.current_device() == index:
@@ -132,7 +132,7 @@ def page_plan(old_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.T
         raise ValueError(f"block_table must be [{Bn}][max_pages] with a contiguous last dimension")
     if max_tokens < 0:
         raise ValueError("max_tokens must be >= 0")
-    return _call(dev, stream, _plan, old_len, new_len, block_table, free_ring, ring_state, page_size, max_tokens)
+    return call_on(dev, stream, _plan, old_len, new_len, block_table, free_ring, ring_state, page_size, max_tokens)
 
 
 def _plan(st, old_len, new_len, block_table, free_ring, ring_state, page_size, max_tokens):
@@ -164,7 +164,7 @@ def page_append(kv: PagedKV, k_new: torch.Tensor, slot_map: torch.Tensor, v_new:
                 n_kv > 1 and t.stride(1) != d):
             raise ValueError(f"{name} must be [T][{n_kv}][{d}] with contiguous rows")
     _need_flat(slot_map, "slot_map", torch.int32, (k_new.shape[0],), kv.device)
-    _call(kv.device, stream, _append, kv, k_new, slot_map, v_new)
+    call_on(kv.device, stream, _append, kv, k_new, slot_map, v_new)
 
 
 def _append(st, kv, k_new, slot_map, v_new):
@@ -196,7 +196,7 @@ def paged_attention(q: torch.Tensor, kv: PagedKV, window: int = 0, scale: float 
             raise ValueError("pages must list at least one entry per KV head")
     if out is not None:
         _need_flat(out, "out", torch.float32, tuple(q.shape), kv.device)
-    return _call(kv.device, stream, _attend, q, kv, window, scale, pages, want_lse, out)
+    return call_on(kv.device, stream, _attend, q, kv, window, scale, pages, want_lse, out)
 
 
 def _attend(st, q, kv, window, scale, pages, want_lse, out):
@@ -225,7 +225,7 @@ def page_select(q: torch.Tensor, kv: PagedKV, n_select: int, keep_first: int = 1
         raise ValueError("n_select must be >= 1")
     if out is not None:
         _need_flat(out, "out", torch.int32, (kv.batch, kv._row[0], n_select), kv.device)
-    return _call(kv.device, stream, _select, q, kv, n_select, keep_first, keep_last, out)
+    return call_on(kv.device, stream, _select, q, kv, n_select, keep_first, keep_last, out)
 
 
 def _select(st, q, kv, n_select, keep_first, keep_last, out):
