@@ -100,11 +100,12 @@ __device__ __noinline__ bool wait_slow(unsigned bar, unsigned parity, volatile i
 __device__ __forceinline__ bool wait_bar(unsigned bar, unsigned parity, volatile int* dead) {
   return test_wait(bar, parity) || wait_slow(bar, parity, dead);
 }
-__device__ __forceinline__ void tma_4d(unsigned dst, const CUtensorMap* map, int x, int t, int h, int page, unsigned bar) {
+__device__ __forceinline__ void tma_4d(unsigned dst, const CUtensorMap* map, int x, int t, int h, int page, unsigned bar,
+                                       unsigned long long policy) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
-          dst),
-      "l"(map), "r"(x), "r"(t), "r"(h), "r"(page), "r"(bar)
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+      "l"(map), "r"(x), "r"(t), "r"(h), "r"(page), "r"(bar), "l"(policy)
       : "memory");
 }
 // Shared-memory descriptors, 128-byte swizzle: 8-row groups are 1024 bytes apart; in the MN-major
@@ -426,6 +427,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     // ---------------- loads
     if (elect()) {
       const int R = 1 << g.rshift, ng = KT >> g.rshift, P = 1 << c.pshift;
+      // keys pass through once: they leave the L2 before the tables, the code and the parts do
+      unsigned long long policy;
+      asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
       int pc = 0, slot = 0;  // slots so far, the next slot and the ring's phase there
       unsigned phase = 0;
       bool ok = true;
@@ -449,8 +453,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 #pragma unroll 1
           for (int r = 0; r < ng; ++r, dst += R * 128) {
             const int pos = in[r], off = pos < 0 ? 0 : pos & (P - 1), page = in[16 + r];  // page -1: zeros
-            tma_4d(dst, map, x, off, kvh, page, bar);
-            tma_4d(dst + LY::box, map, x + 64, off, kvh, page, bar);
+            tma_4d(dst, map, x, off, kvh, page, bar, policy);
+            tma_4d(dst + LY::box, map, x + 64, off, kvh, page, bar, policy);
           }
           ++pc;
           if (++slot == kRing) {
