@@ -6,9 +6,9 @@
 //
 // One thread-block cluster per (sequence, KV head): its CTAs score their shares of the pages (one
 // read of d + 4 bytes per page, the only large one), and after a cluster barrier the first CTA
-// picks. The pick is a chain of small steps on one SM: the threshold key by 8-bit digits from the
-// top (one count per distinct digit of a warp, not one atomic per score: most scores share their
-// leading bits), then one ordered compaction.
+// picks. The pick is a chain of small steps on one SM: the range of the scores, the threshold key
+// by 8-bit digits from the highest bit in which they differ (so that the first digit already
+// spreads over its counters), then one ordered compaction.
 #include "mtp_common.cuh"
 #include "mtp_launch.h"
 #include "mtp_paged.cuh"
@@ -198,22 +198,54 @@ __global__ void __launch_bounds__(kSelThreads) k_page_select(const __grid_consta
   __shared__ unsigned hist[256], s_key;
   __shared__ int s_left, s_all;
   __shared__ long long wsum[kSelWarps];
+  __shared__ unsigned wmin[kSelWarps], wmax[kSelWarps];
+  __shared__ int winf[kSelWarps];
+  static_assert(kSelWarps <= 32, "the reductions over warps take one lane per warp");
   const bool cached = n <= kSelCache;
   if (cached)
     for (int i = tid; i < n; i += kSelThreads) cache[i] = __ldcg(score + i);
   auto get = [&](int i) { return cached ? cache[i] : __ldcg(score + i); };
-  unsigned key = 0, mask = 0;
-  int left = k;  // of the scores that share the key's digits so far, how many are selected
-  for (int shift = 24; shift >= 0; shift -= 8) {
+  // range of the scores below +inf, and how many are +inf
+  constexpr unsigned kInf = 0xff800000u;  // ord_f32(+inf)
+  unsigned least = 0xffffffffu, most = 0;
+  int infs = 0;
+  for (int i = tid; i < n; i += kSelThreads) {
+    const unsigned x = get(i);
+    if (x >= kInf) {
+      ++infs;
+    } else {
+      least = min(least, x);
+      most = max(most, x);
+    }
+  }
+  least = __reduce_min_sync(0xffffffffu, least);
+  most = __reduce_max_sync(0xffffffffu, most);
+  infs = __reduce_add_sync(0xffffffffu, infs);
+  if (lane == 0) {
+    wmin[warp] = least;
+    wmax[warp] = most;
+    winf[warp] = infs;
+  }
+  __syncthreads();
+  least = __reduce_min_sync(0xffffffffu, wmin[lane % kSelWarps]);
+  most = __reduce_max_sync(0xffffffffu, wmax[lane % kSelWarps]);
+  infs = __reduce_add_sync(0xffffffffu, lane < kSelWarps ? winf[lane] : 0);
+  // the scores' common leading bits; of those that have them, `left` are selected
+  unsigned key = kInf, mask = 0xffffffffu;
+  int left = k, top = -1;  // top: highest bit in which the scores still differ
+  if (infs < k) {
+    left = k - infs;
+    top = 31 - __clz(least ^ most);  // -1: all equal
+    mask = top < 31 ? ~0u << (top + 1) : 0u;
+    key = most & mask;
+  }
+  while (top >= 0) {
+    const int shift = max(top - 7, 0);
     if (tid < 256) hist[tid] = 0;
     __syncthreads();
-    for (int i0 = warp * 32; i0 < n; i0 += kSelThreads) {
-      const int i = i0 + lane;
-      const unsigned x = i < n ? get(i) : 0;
-      const bool in = i < n && (x & mask) == key;
-      const unsigned digit = in ? (x >> shift) & 255 : 256;
-      const unsigned same = __match_any_sync(0xffffffffu, digit);
-      if (in && lane == __ffs(same) - 1) atomicAdd(&hist[digit], static_cast<unsigned>(__popc(same)));
+    for (int i = tid; i < n; i += kSelThreads) {
+      const unsigned x = get(i);
+      if ((x & mask) == key && x < kInf) atomicAdd(&hist[(x >> shift) & (0xffu >> (7 - (top - shift)))], 1u);
     }
     __syncthreads();
     if (tid < 32) {
@@ -248,16 +280,22 @@ __global__ void __launch_bounds__(kSelThreads) k_page_select(const __grid_consta
     __syncthreads();
     key = s_key;
     left = s_left;
-    mask |= 255u << shift;
+    mask = ~0u << shift;
+    top = shift - 1;
     if (s_all) break;
   }
   // scores above the key are all taken, of those equal to it the first `left`: a run of pages per
   // thread, one prefix sum over (above, equal)
+  const bool in_infs = infs >= k;
+  auto rank_of = [&](unsigned x) {  // 2: above, 1: equal
+    if (x >= kInf) return in_infs ? 1 : 2;
+    return in_infs ? 0 : (x & mask) > key ? 2 : (x & mask) == key ? 1 : 0;
+  };
   const int run = (n + kSelThreads - 1) / kSelThreads, i0 = min(n, tid * run), i1 = min(n, i0 + run);
   long long mine = 0;
   for (int i = i0; i < i1; ++i) {
-    const unsigned x = get(i) & mask;
-    mine += x > key ? 1ll << 32 : (x == key ? 1 : 0);
+    const int r = rank_of(get(i));
+    mine += r == 2 ? 1ll << 32 : r;
   }
   long long incl = mine;
 #pragma unroll
@@ -271,11 +309,11 @@ __global__ void __launch_bounds__(kSelThreads) k_page_select(const __grid_consta
   for (int w = 0; w < warp; ++w) before += wsum[w];
   int above = static_cast<int>(before >> 32), equal = static_cast<int>(before & 0xffffffffll);
   for (int i = i0; i < i1; ++i) {
-    const unsigned x = get(i) & mask;
-    if (x > key) {
+    const int r = rank_of(get(i));
+    if (r == 2) {
       sel[above + min(equal, left)] = i;
       ++above;
-    } else if (x == key) {
+    } else if (r == 1) {
       if (equal < left) sel[above + equal] = i;
       ++equal;
     }
@@ -292,12 +330,16 @@ int run_page_select(const pg::Cache& c, const float* q, int B, int nh, int n_sel
                     int* sel, void* ws, int num_sms, cudaStream_t st) {
   pg::SelArgs a{c, q, static_cast<unsigned*>(ws), sel, B, nh, n_select, keep_first, keep_last, 1};
   const int G = nh / c.nkv, units = B * c.nkv;
-  // CTAs of a cluster: about two waves over the batch, at least 64 pages each
-  while (a.cl < 8 && 2 * a.cl * units <= 2 * num_sms && 64 * 2 * a.cl <= c.max_pages) a.cl *= 2;
+  // CTAs of a cluster: one wave over the batch (the last doubling, beyond the portable size, only
+  // where clusters of 16 still fit side by side), at least 64 pages each
+  while (a.cl < 16 && 2 * a.cl * units <= num_sms - (a.cl == 8 ? num_sms / 8 : 0) && 64 * 2 * a.cl <= c.max_pages)
+    a.cl *= 2;
   const int kept = c.max_pages < pg::kSelCache ? c.max_pages : pg::kSelCache;
   const int smem = G * (c.d + 4) + 4 * kept;
   static_assert(32 * (512 + 4) + 4 * pg::kSelCache <= 64 * 1024, "shared memory of the selection");
   cudaError_t e = pg::allow_smem<pg::k_page_select, 64 * 1024>();
+  if (e == cudaSuccess && a.cl > 8)
+    e = cudaFuncSetAttribute(pg::k_page_select, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[2];
