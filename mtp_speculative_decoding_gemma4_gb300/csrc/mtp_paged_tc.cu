@@ -15,7 +15,9 @@
 // nearest.
 //
 // Work split: the granules (32 to 128 keys) of all (sequence, KV head, head group) units are
-// numbered through and dealt evenly over one CTA per SM, whatever the lengths. A unit that crosses
+// numbered through and dealt evenly over one CTA per SM, whatever the lengths; a unit's beginning
+// counts as `extra` granules, since a CTA that goes from one unit to the next drains and refills
+// its pipeline (3 us at d = 512, where such CTAs were the last to finish). A unit that crosses
 // CTAs leaves unnormalised sums, (max, exp-sum) per part; k_paged_tc_join adds them in CTA order.
 // (Joined by the last CTA to arrive instead, the 8 long contexts took 48 us against 41: its chain
 // of round trips runs while the memory is busy with the others' keys.)
@@ -52,6 +54,7 @@ constexpr long long kSpin = 4000000000LL;  // about 2 s
 struct Args {
   AttArgs a;
   int gshift;    // log2 of the keys of a granule, which are dealt as a whole
+  int extra;     // what beginning a unit costs, in granules
   int rshift;    // log2 of the keys per TMA box (min(P, keys per tile))
   int grid;      // CTAs that share the granules
   int ngrp;      // head groups per KV head
@@ -203,7 +206,8 @@ struct Lay {
   static constexpr int cols = 4 * NP * N;                // 2 score and 2 sum regions of NP * N columns
 };
 
-// Walks the segments (parts of units) of a CTA's granules [r, r1).
+// Walks the segments (parts of units) of a CTA's share: costs [r, r1), where a unit of n granules
+// is `extra` costs without a granule and then one cost per granule.
 struct Walk {
   int r, r1, b, sub, off, n, lo, hi, base;
   // granules of a unit of sequence b
@@ -219,14 +223,14 @@ struct Walk {
     }
     return (keys + (1 << g.gshift) - 1) >> g.gshift;
   }
-  __device__ __forceinline__ void load(const Args& g) { n = count(g, b, lo, hi, base); }
-  // This CTA's granules and the unit they begin in: the whole warp, a lane for 1/32 of the
-  // sequences. Returns the granules per CTA.
+  __device__ __forceinline__ static int cost(const Args& g, int n) { return n > 0 ? n + g.extra : 0; }
+  // This CTA's share and the unit it begins in: the whole warp, a lane for 1/32 of the sequences.
+  // Returns the costs per CTA.
   __device__ __forceinline__ int locate(const Args& g, int subs) {
     const int lane = threadIdx.x & 31, per_b = (g.a.B + 31) >> 5, b0 = min(g.a.B, lane * per_b), b1 = min(g.a.B, b0 + per_b);
     int mine = 0;
 #pragma unroll 1
-    for (int i = b0; i < b1; ++i) mine += count(g, i, lo, hi, base);
+    for (int i = b0; i < b1; ++i) mine += cost(g, count(g, i, lo, hi, base));
     mine *= subs;
     int incl = mine;
 #pragma unroll
@@ -241,16 +245,17 @@ struct Walk {
     if (r >= r1) return per;
     const int f = __ffs(__ballot_sync(0xffffffffu, incl > r)) - 1;
     if (lane == f) {
-      int at = r - (incl - mine);
+      int at = r - (incl - mine), c;
 #pragma unroll 1
       for (b = b0;; ++b) {
         n = count(g, b, lo, hi, base);
-        if (at < n * subs) break;
-        at -= n * subs;
+        c = cost(g, n);
+        if (at < c * subs) break;
+        at -= c * subs;
       }
       if (subs > 1) {
-        sub = at / n;
-        at -= sub * n;
+        sub = at / c;
+        at -= sub * c;
       }
       off = at;
     }
@@ -265,36 +270,44 @@ struct Walk {
   }
   struct Seg {
     int b, kvh, hg, a, e, n, lo, hi, base;  // KV head and group of its heads; granules [a, e) of n
+    int end;                                // one past the unit's last cost
   };
   __device__ __forceinline__ bool next(const Args& g, int subs, Seg& s) {
-    if (r >= r1) return false;
 #pragma unroll 1
-    while (off >= n) {  // the next unit
-      off = 0;
-      if (n == 0 || ++sub == subs) {
-        sub = 0;
-        ++b;
-        load(g);
+    while (r < r1) {
+      const int c = cost(g, n);
+      if (off >= c) {  // the next unit
+        off = 0;
+        if (n == 0 || ++sub == subs) {
+          sub = 0;
+          ++b;
+          n = count(g, b, lo, hi, base);
+        }
+        continue;
       }
+      const int to = min(c, off + (r1 - r));
+      s.a = max(off - g.extra, 0);
+      s.e = max(to - g.extra, 0);
+      s.end = r - off + c;
+      r += to - off;
+      off = to;
+      if (s.e == s.a) continue;
+      s.b = b;
+      s.kvh = sub;
+      s.hg = 0;
+      if (g.ngrp > 1) {
+        s.kvh = sub / g.ngrp;
+        s.hg = sub - s.kvh * g.ngrp;
+      }
+      s.n = n;
+      s.lo = lo;
+      s.hi = hi;
+      s.base = base;
+      return true;
     }
-    s.b = b;
-    s.kvh = sub;
-    s.hg = 0;
-    if (g.ngrp > 1) {
-      s.kvh = sub / g.ngrp;
-      s.hg = sub - s.kvh * g.ngrp;
-    }
-    s.a = off;
-    s.e = min(n, off + (r1 - r));
-    s.n = n;
-    s.lo = lo;
-    s.hi = hi;
-    s.base = base;
-    r += s.e - s.a;
-    off = s.e;
-    return true;
+    return false;
   }
-  // one past the last key number of a segment (its first is s.a * granule)
+  // one past the last key number of a segment (its first is s.a << g.gshift)
   __device__ __forceinline__ int end(const Args& g, const Seg& s) const {
     return min(g.a.list ? g.a.n_list << g.a.c.pshift : s.hi - s.base, s.e << g.gshift);
   }
@@ -820,11 +833,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           }
         }
         if (!whole && s.a == 0 && wt == 0) {
-          // a unit that goes on in the next CTA ends this CTA's granules
-          const int first = static_cast<int>(blockIdx.x) * per + (per - (s.e - s.a));
           meta[0] = static_cast<int>(row0);
           meta[1] = nh;
-          meta[2] = (first + s.n - 1) / per;
+          meta[2] = (s.end - 1) / per;
         }
       }
       tt += nt;
@@ -1013,11 +1024,14 @@ int run_paged_tc(const pg::AttArgs& a, void* ws, int num_sms, cudaStream_t st) {
   long long keys = static_cast<long long>(a.list ? a.n_list : a.c.max_pages) * P;
   if (!a.list && a.window > 0 && a.window + rows < keys) keys = a.window + rows;
   const long long units = static_cast<long long>(a.B) * a.c.nkv * g.ngrp;
-  g.gshift = 7;
+  g.gshift = a.c.d == 512 ? 6 : 7;
   const auto granules = [&] { return units * ((keys + (1 << g.gshift) - 1) >> g.gshift); };
   while (g.gshift > 5 && (1 << g.gshift) > rows && granules() < num_sms) --g.gshift;
   const long long most = granules();
-  if (most > INT32_MAX) {
+  // beginning a unit, in the time of so many bytes loaded (longer with one query buffer)
+  const int begin = a.c.d == 512 ? 128 * 1024 : 64 * 1024, bytes = (a.c.d * (a.c.v ? 4 : 2)) << g.gshift;
+  g.extra = most > num_sms ? (begin + bytes - 1) / bytes : 0;
+  if (most + units * g.extra > INT32_MAX) {
     set_error("too many keys: B * heads * max_pages * page_size = %lld", units * keys);
     return MTP_ERR_UNSUPPORTED_SHAPE;
   }
