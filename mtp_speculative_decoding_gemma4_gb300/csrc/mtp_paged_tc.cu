@@ -864,46 +864,50 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   }
 }
 
-// Adds the parts of the unit that CTA blockIdx.x of k_paged_tc starts and does not end, one head
-// per blockIdx.y, the threads over the parts and the dims; a fixed order of sums. What bounds it
-// is its chain of reads (the unit, the weights, the sums): the first sums are requested with the
-// weights.
-template <int D>
-__global__ void __launch_bounds__(512) k_paged_tc_join(const __grid_constant__ Args g, int NH) {
+// Adds the parts of the unit that CTA blockIdx.x of k_paged_tc starts and does not end, HB heads per
+// blockIdx.y, the threads over the parts and the dims; a fixed order of sums. What bounds it is its
+// chain of reads (the unit, the weights, the sums: the first sums are requested with the weights)
+// and the number of blocks, most of which find nothing: with a head per block at d = 128 the 61
+// short sequences took 34.6 us in all, with four 32.5.
+constexpr int kJoinThreads = 512;
+
+template <int D, int HB>
+__global__ void __launch_bounds__(kJoinThreads) k_paged_tc_join(const __grid_constant__ Args g, int NH) {
   pdl_enter();
-  constexpr int VT = D / 4, GR = 512 / VT, PRE = 4;  // threads of one part's dims, parts side by side
-  const int4 meta = *reinterpret_cast<const int4*>(g.meta + 4 * blockIdx.x);
-  const int h = blockIdx.y, c0 = blockIdx.x;
-  if (h >= meta.y) return;
-  const int n = meta.z - c0 + 1;
-  const size_t row = static_cast<size_t>(meta.x) + h;
+  constexpr int VT = D / 4, PT = HB * VT, GR = kJoinThreads / PT, PRE = 4;  // threads of a head and a part, parts side by side
+  const int4 meta = *reinterpret_cast<const int4*>(g.meta + 4 * blockIdx.x);  // first row, heads, last CTA
+  const int h0 = blockIdx.y * HB, c0 = blockIdx.x;
+  if (h0 >= meta.y) return;
+  const int n = meta.z - c0 + 1, nh = min(HB, meta.y - h0);
   const AttArgs& a = g.a;
-  __shared__ float wgt[pg::kMaxSms], sden;
-  __shared__ float4 sum[GR][VT];
-  const int tid = threadIdx.x, lane = tid & 31, v = tid % VT, gr = tid / VT;
+  __shared__ float wgt[HB][pg::kMaxSms], sden[HB], sm[HB];
+  __shared__ float4 sum[GR][PT];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, at = tid % PT, gr = tid / PT, h = at / VT, v = at % VT;
   // part i: slot 1 of the first CTA, slot 0 of the next ones
-  auto part = [&](int i) { return static_cast<size_t>((c0 + i) * 2 + (i == 0 ? 1 : 0)) * NH + h; };
-  auto at = [&](int i) { return reinterpret_cast<const float4*>(a.ws_acc + part(i) * D) + v; };
+  auto part = [&](int i, int hh) { return static_cast<size_t>((c0 + i) * 2 + (i == 0 ? 1 : 0)) * NH + h0 + hh; };
+  auto from = [&](int i) { return reinterpret_cast<const float4*>(a.ws_acc + part(i, h) * D) + v; };
+  const bool on = h < nh && gr < GR;
   float4 y[PRE];
 #pragma unroll
   for (int j = 0; j < PRE; ++j)
-    if (gr + j * GR < n) y[j] = *at(gr + j * GR);
-  float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, a.ws_ml[part(i) * 2]);
-  M = warp_max(M);
-  if (tid < 32) {
-    float den = 0.f;
+    if (on && gr + j * GR < n) y[j] = *from(gr + j * GR);
+  if (warp < nh) {  // a warp per head: the weights of the parts
+    float M = -INFINITY, den = 0.f;
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, a.ws_ml[part(i, warp) * 2]);
+    M = warp_max(M);
     for (int i = lane; i < n; i += 32) {
-      const float2 ml = *reinterpret_cast<const float2*>(a.ws_ml + part(i) * 2);
+      const float2 ml = *reinterpret_cast<const float2*>(a.ws_ml + part(i, warp) * 2);
       const float f = M == -INFINITY ? 0.f : exp2f(ml.x - M);
-      wgt[i] = f;
+      wgt[warp][i] = f;
       den = fmaf(f, ml.y, den);
     }
     den = warp_sum(den);
-    if (lane == 0) sden = den;
+    if (lane == 0) {
+      sm[warp] = M;
+      sden[warp] = den;
+    }
   }
   __syncthreads();
-  const float den = sden;
   float4 x = make_float4(0, 0, 0, 0);
   auto add = [&](float f, const float4& z) {
     x.x = fmaf(f, z.x, x.x);
@@ -911,19 +915,26 @@ __global__ void __launch_bounds__(512) k_paged_tc_join(const __grid_constant__ A
     x.z = fmaf(f, z.z, x.z);
     x.w = fmaf(f, z.w, x.w);
   };
+  if (on) {
 #pragma unroll
-  for (int j = 0; j < PRE; ++j)
-    if (gr + j * GR < n) add(wgt[gr + j * GR], y[j]);
+    for (int j = 0; j < PRE; ++j)
+      if (gr + j * GR < n) add(wgt[h][gr + j * GR], y[j]);
 #pragma unroll 4
-  for (int i = gr + PRE * GR; i < n; i += GR) add(wgt[i], *at(i));
-  sum[gr][v] = x;
-  __syncthreads();
-  if (gr == 0) {
+    for (int i = gr + PRE * GR; i < n; i += GR) add(wgt[h][i], *from(i));
+  }
+  if (GR > 1) {
+    if (gr < GR) sum[gr][at] = x;
+    __syncthreads();
+    if (gr == 0) {
 #pragma unroll
-    for (int i = 1; i < GR; ++i) add(1.f, sum[i][v]);
-    const float inv = den == 0.f ? 0.f : 1.f / den;
+      for (int i = 1; i < GR; ++i) add(1.f, sum[i][at]);
+    }
+  }
+  if (gr == 0 && on) {
+    const size_t row = static_cast<size_t>(meta.x) + h0 + h;
+    const float den = sden[h], inv = den == 0.f ? 0.f : 1.f / den;
     *reinterpret_cast<float4*>(a.out + row * D + 4 * v) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-    if (a.lse && v == 0) a.lse[row] = den == 0.f ? -INFINITY : (M + log2f(den)) * 0.6931471805599453f;
+    if (a.lse && v == 0) a.lse[row] = den == 0.f ? -INFINITY : (sm[h] + log2f(den)) * 0.6931471805599453f;
   }
 }
 
@@ -983,10 +994,11 @@ int launch(const Args& g, cudaStream_t st) {
     cfg.stream = st;
     e = cudaLaunchKernelEx(&cfg, k_paged_tc<D, NH>, mk, mv, g);
     if (e == cudaSuccess) {
-      cfg.gridDim = dim3(g.grid, NH);
-      cfg.blockDim = dim3(512);
+      constexpr int HB = 512 / D;  // 128 threads per part
+      cfg.gridDim = dim3(g.grid, NH / HB);
+      cfg.blockDim = dim3(kJoinThreads);
       cfg.dynamicSmemBytes = 0;
-      e = cudaLaunchKernelEx(&cfg, k_paged_tc_join<D>, g, NH);
+      e = cudaLaunchKernelEx(&cfg, k_paged_tc_join<D, HB>, g, NH);
     }
   }
   if (e != cudaSuccess) {
