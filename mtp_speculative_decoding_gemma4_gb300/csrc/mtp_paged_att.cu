@@ -8,9 +8,13 @@
 // (16-byte vectors), 32 / LPK rows side by side in a warp, U row blocks in flight; every lane
 // keeps its vectors of GP queries and GP running sums in registers, so a key row is read once
 // for all heads of the group. Scores, maxima, sums and outputs are fp32.
+// What bounds it is instruction issue (43 % of the slots at 26 us for 16 fp32 contexts to 8000, the
+// memory at 26 %), most of it around the products. So the U * GP scores of a block are reduced by
+// one reduce-scatter, each lane takes the softmax of one score, and probabilities are broadcast.
 #include "mtp_common.cuh"
 #include "mtp_launch.h"
 #include "mtp_paged.cuh"
+#include "mtp_phases.cuh"
 
 namespace mtp {
 namespace pg {
@@ -42,7 +46,10 @@ __device__ __forceinline__ float pexp(float x, float m) { return exp2f(x - (m ==
 template <typename T, int LPK, int NV, int GP>
 __global__ void __launch_bounds__(kAttWarps * 32) k_paged_att(const __grid_constant__ AttArgs a) {
   pdl_enter();
-  constexpr int VE = Elem<T>::kVec, U = NV >= 4 ? 1 : 4 / NV, KPW = 32 / LPK;
+  constexpr int VE = Elem<T>::kVec, KPW = 32 / LPK;
+  constexpr int U0 = NV >= 4 ? 1 : 4 / NV, U = U0 * GP <= LPK ? U0 : LPK / GP;  // at most a score per lane
+  constexpr int N = U * GP, DUP = LPK / N;  // scores of a block, lanes that hold the same one
+  static_assert(U >= 1 && DUP >= 1, "lanes for the scores");
   extern __shared__ __align__(16) float sm_att[];  // [warps][GP][d] sums, then [warps][GP] m, l
   const Cache& c = a.c;
   const int d = c.d, nvec = d / VE, G = a.nh / c.nkv, ngrp = (G + GP - 1) / GP;
@@ -58,17 +65,18 @@ __global__ void __launch_bounds__(kAttWarps * 32) k_paged_att(const __grid_const
   key_range(c, b, a.window, lo, hi);
   // keys are numbered by position (dense), or by (list entry, offset)
   const int P = 1 << c.pshift;
-  const int i0 = a.list ? 0 : lo, i1 = a.list ? a.n_list << c.pshift : hi;
-  const int step = KPW * U * kAttWarps;
+  constexpr int R = KPW * U, step = R * kAttWarps;  // rows of a warp's block, of the CTA's
+  // blocks begin at multiples of R, so that a block lies in one page when R <= P
+  const int i0 = a.list ? 0 : lo / R * R, i1 = a.list ? a.n_list << c.pshift : hi;
   const int chunk = ((max(i1 - i0, 0) + a.nsplit - 1) / a.nsplit + step - 1) / step * step;
   const int j0 = i0 + sp * chunk, j1 = min(i1, j0 + chunk);
   const int* list = a.list ? a.list + (static_cast<size_t>(b) * c.nkv + g) * a.n_list : nullptr;
 
-  float q[GP][NV * VE], acc[GP][NV * VE], m[GP], l[GP];
+  // this lane's score of a block: row block su, head sh; its head's reference and its rows' sum
+  const int sid = li / DUP, su = sid / GP;
+  float q[GP][NV * VE], acc[GP][NV * VE], m = -INFINITY, l = 0.f;
 #pragma unroll
   for (int h = 0; h < GP; ++h) {
-    m[h] = -INFINITY;
-    l[h] = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int v = li + LPK * j;
@@ -79,36 +87,61 @@ __global__ void __launch_bounds__(kAttWarps * 32) k_paged_att(const __grid_const
       }
     }
   }
-  for (int base = j0 + warp * KPW * U; base < j1; base += step) {
+  const bool one_page = R <= P, whole = nvec == LPK * NV;
+  const long long row_step = KPW * c.st;
+  for (int base = j0 + warp * R; base < j1; base += step) {
     uint4 kv[U][NV], vv[U][NV];
     bool on[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = base + u * KPW + sub;
-      int pos = i, lp = i >> c.pshift;
-      on[u] = i < j1;
-      if (on[u] && list) {
-        lp = list[i >> c.pshift];
+    long long at[U];
+    auto find = [&](int i, int& pos) -> int {  // physical page of row i of the range (or -1), its position
+      int lp = i >> c.pshift;
+      pos = i;
+      if (list) {
+        lp = list[lp];
         pos = (lp << c.pshift) + (i & (P - 1));
-        on[u] = lp >= 0 && lp < c.max_pages && pos >= lo && pos < hi;
+        if (lp < 0 || lp >= c.max_pages) return -1;
       }
-      const int page = on[u] ? phys_page(c, b, lp) : -1;
-      on[u] = page >= 0;
-      const size_t at = on[u] ? static_cast<size_t>(page) * c.sp + static_cast<size_t>(pos & (P - 1)) * c.st +
-                                    static_cast<size_t>(g) * c.sh
-                              : 0;
+      return phys_page(c, b, lp);
+    };
+    bool all = whole;
+    if (one_page) {
+      int pos;
+      const int page = find(base, pos);
+      const long long first = page * c.sp + ((pos & (P - 1)) + sub) * c.st + g * c.sh;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int v = li + LPK * j;
-        const bool rd = on[u] && v < nvec;
-        kv[u][j] = rd ? __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(c.k) + at + v * VE))
-                      : make_uint4(0, 0, 0, 0);
-        if (c.v)
-          vv[u][j] = rd ? __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(c.v) + at + v * VE))
-                        : make_uint4(0, 0, 0, 0);
+      for (int u = 0; u < U; ++u) {
+        const int p = pos + u * KPW + sub;
+        on[u] = page >= 0 && p >= lo && p < hi;
+        at[u] = first + u * row_step;
+        all = all && on[u];
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = base + u * KPW + sub;
+        int pos = 0;
+        const int page = i < i1 ? find(i, pos) : -1;
+        on[u] = page >= 0 && pos >= lo && pos < hi;
+        at[u] = page * c.sp + (pos & (P - 1)) * c.st + g * c.sh;
+        all = all && on[u];
       }
     }
-    float s[U][GP];
+    auto load = [&](const void* from, uint4 (&x)[U][NV], bool every) {
+      const uint4* base_v = static_cast<const uint4*>(from) + li;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          x[u][j] = every || (on[u] && li + LPK * j < nvec) ? __ldcs(base_v + at[u] / VE + LPK * j) : make_uint4(0, 0, 0, 0);
+    };
+    if (__all_sync(0xffffffffu, all)) {
+      load(c.k, kv, true);
+      if (c.v) load(c.v, vv, true);
+    } else {
+      load(c.k, kv, false);
+      if (c.v) load(c.v, vv, false);
+    }
+    float s[N];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float x[NV * VE];
@@ -119,25 +152,27 @@ __global__ void __launch_bounds__(kAttWarps * 32) k_paged_att(const __grid_const
         float t = 0.f;
 #pragma unroll
         for (int e = 0; e < NV * VE; ++e) t = fmaf(q[h][e], x[e], t);
-#pragma unroll
-        for (int o = LPK / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-        s[u][h] = on[u] ? t * a.scale_log2 : -INFINITY;
+        s[u * GP + h] = t;
       }
     }
+    reduce_scatter<N, LPK / 2>(s, lane);
+    bool mine = false;
 #pragma unroll
-    for (int h = 0; h < GP; ++h) {
-      float mn = m[h];
+    for (int u = 0; u < U; ++u) mine = mine || (su == u && on[u]);
+    const float x0 = mine ? s[0] * a.scale_log2 : -INFINITY;
+    float mn = x0;
 #pragma unroll
-      for (int u = 0; u < U; ++u) mn = fmaxf(mn, s[u][h]);
-      const float corr = pexp(m[h], mn);
-      m[h] = mn;
-      l[h] *= corr;
+    for (int o = GP * DUP; o < LPK; o <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    mn = fmaxf(m, mn);
+    const float corr = pexp(m, mn), p = pexp(x0, mn);
+    m = mn;
+    l = fmaf(l, corr, p);
+    if (__any_sync(0xffffffffu, corr != 1.f)) {
 #pragma unroll
-      for (int e = 0; e < NV * VE; ++e) acc[h][e] *= corr;
+      for (int h = 0; h < GP; ++h) {
+        const float f = __shfl_sync(0xffffffffu, corr, h * DUP, LPK);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        s[u][h] = pexp(s[u][h], mn);
-        l[h] += s[u][h];
+        for (int e = 0; e < NV * VE; ++e) acc[h][e] *= f;
       }
     }
 #pragma unroll
@@ -146,22 +181,28 @@ __global__ void __launch_bounds__(kAttWarps * 32) k_paged_att(const __grid_const
 #pragma unroll
       for (int j = 0; j < NV; ++j) unpack<T>(c.v ? vv[u][j] : kv[u][j], x + j * VE);
 #pragma unroll
-      for (int h = 0; h < GP; ++h)
+      for (int h = 0; h < GP; ++h) {
+        const float f = __shfl_sync(0xffffffffu, p, (u * GP + h) * DUP, LPK);
 #pragma unroll
-        for (int e = 0; e < NV * VE; ++e) acc[h][e] = fmaf(s[u][h], x[e], acc[h][e]);
+        for (int e = 0; e < NV * VE; ++e) acc[h][e] = fmaf(f, x[e], acc[h][e]);
+      }
     }
   }
+  // the row blocks' parts of a head's sum
+#pragma unroll
+  for (int o = GP * DUP; o < LPK; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   // join the rows held side by side in the warp, then the warps
   float* ml = sm_att + kAttWarps * GP * d;
 #pragma unroll
   for (int h = 0; h < GP; ++h) {
-    float mn = m[h];
+    const float mh = __shfl_sync(0xffffffffu, m, h * DUP, LPK);
+    float mn = mh, lh = __shfl_sync(0xffffffffu, l, h * DUP, LPK);
 #pragma unroll
     for (int o = LPK; o < 32; o <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-    const float corr = pexp(m[h], mn);
-    l[h] *= corr;
+    const float corr = pexp(mh, mn);
+    lh *= corr;
 #pragma unroll
-    for (int o = LPK; o < 32; o <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
+    for (int o = LPK; o < 32; o <<= 1) lh += __shfl_xor_sync(0xffffffffu, lh, o);
 #pragma unroll
     for (int e = 0; e < NV * VE; ++e) {
       float t = acc[h][e] * corr;
@@ -172,7 +213,7 @@ __global__ void __launch_bounds__(kAttWarps * 32) k_paged_att(const __grid_const
     }
     if (lane == 0) {
       ml[warp * GP + h] = mn;
-      ml[(kAttWarps + warp) * GP + h] = l[h];
+      ml[(kAttWarps + warp) * GP + h] = lh;
     }
   }
   __syncthreads();
