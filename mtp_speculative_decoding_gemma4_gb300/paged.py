@@ -6,6 +6,7 @@ torch's current stream of the tensors' device, else the cudaStream_t passed as `
 """
 from __future__ import annotations
 
+import threading
 from typing import Optional
 
 import torch
@@ -114,6 +115,24 @@ class PagedKV:
         self.device, self.batch = dev, 0 if block_table is None else block_table.shape[0]
         self._row = k.shape[2:]
         self._ws = {}  # workspace bytes by (n_head, n_list); and of the selection
+        self._scratch, self._lock = None, threading.Lock()
+
+
+def _with_workspace(kv: PagedKV, st: int, n: int, launch) -> None:
+    """launch(pointer, n) with a workspace of n bytes for a call on stream st. The default stream's
+    calls on a cache follow one another (and are never captured), so they share one buffer kept with
+    the descriptor, under a lock that keeps the launches of a call together: an allocation costs 3 us
+    of a call's 17 on the host. Any other stream's calls get a buffer of their own."""
+    if not n:
+        launch(0, 0)
+    elif st != 0:
+        ws = torch.empty(n, dtype=torch.uint8, device=kv.device)
+        launch(ws.data_ptr(), n)
+    else:
+        with kv._lock:
+            if kv._scratch is None or kv._scratch.numel() < n:
+                kv._scratch = torch.empty(n, dtype=torch.uint8, device=kv.device)
+            launch(kv._scratch.data_ptr(), n)
 
 
 def page_plan(old_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.Tensor, free_ring: torch.Tensor,
@@ -208,9 +227,9 @@ def _attend(st, q, kv, window, scale, pages, want_lse, out):
     if out is None:
         out = torch.empty_like(q)
     lse = torch.empty((Bn, nh), dtype=torch.float32, device=kv.device) if want_lse else None
-    ws = torch.empty(n, dtype=torch.uint8, device=kv.device) if n else None
-    B.mtp_paged_attention(kv.c, q.data_ptr(), Bn, nh, window, scale, 0 if pages is None else pages.data_ptr(), n_list,
-                          out.data_ptr(), lse.data_ptr() if want_lse else 0, ws.data_ptr() if n else 0, n, st)
+    _with_workspace(kv, st, n, lambda ws, n: B.mtp_paged_attention(
+        kv.c, q.data_ptr(), Bn, nh, window, scale, 0 if pages is None else pages.data_ptr(), n_list, out.data_ptr(),
+        lse.data_ptr() if want_lse else 0, ws, n, st))
     return (out, lse) if want_lse else out
 
 
@@ -235,7 +254,6 @@ def _select(st, q, kv, n_select, keep_first, keep_last, out):
     n = kv._ws.get("select")
     if n is None:
         n = kv._ws["select"] = B.mtp_page_select_workspace(kv.c, Bn)
-    ws = torch.empty(n, dtype=torch.uint8, device=kv.device) if n else None
-    B.mtp_page_select(kv.c, q.data_ptr(), Bn, nh, n_select, keep_first, keep_last, out.data_ptr(),
-                      ws.data_ptr() if n else 0, n, st)
+    _with_workspace(kv, st, n, lambda ws, n: B.mtp_page_select(
+        kv.c, q.data_ptr(), Bn, nh, n_select, keep_first, keep_last, out.data_ptr(), ws, n, st))
     return out

@@ -643,3 +643,42 @@ def test_explicit_stream_and_argument_checks():
         PagedKV(c.dk.half())
     with pytest.raises(ValueError):
         page_plan(_dev(c.L), _dev(c.L), _dev(c.table[:1]), _dev(c.L), _dev(c.L), 16, 4)
+
+
+@gpu
+def test_calls_of_several_threads_and_streams_keep_apart():
+    # two host threads on the default stream and two on streams of their own, over one descriptor
+    import threading
+    from mtp_speculative_decoding_gemma4_gb300 import page_select, paged_attention
+    c = Case(11, [3000, 4096, 777, 1], 16, 4, 1, 128, "bf16")
+    codes, scales = _summarised(c, 11)
+    kv = c.kv(codes=_dev(codes), scales=_dev(scales))
+    qs = [torch.randn(c.q.shape, generator=torch.Generator().manual_seed(i)) for i in range(4)]
+    want = []
+    for q in qs:
+        c.q = q
+        want.append((c.want(), np.stack([OP.page_select(q[b].numpy(), codes, scales, c.table[b], int(c.L[b]), 16,
+                                                        len(codes), 9, 1, 1) for b in range(4)])))
+    got, streams, errors = [[] for _ in qs], [None, None, torch.cuda.Stream(), torch.cuda.Stream()], []
+    dq = [q.cuda() for q in qs]
+    torch.cuda.synchronize()
+
+    def work(i):
+        try:
+            with torch.cuda.stream(streams[i]):
+                for _ in range(20):
+                    got[i].append((paged_attention(dq[i], kv, want_lse=True), page_select(dq[i], kv, 9)))
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for i in range(4):
+        for att, sel in got[i]:
+            _close(att, want[i][0])
+            np.testing.assert_array_equal(sel.cpu().numpy(), want[i][1])
