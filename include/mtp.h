@@ -411,7 +411,7 @@ MTP_API int mtp_page_plan(const int32_t *old_len, const int32_t *new_len, int32_
  * codes = rint(fl32(m / scale)); a mean that is not finite gives scale NaN and codes 0. A slot
  * may occur once in slot_map.
  *   k_new, v_new device rows of [n_kv][head_dim], model dtype, row_stride_k / row_stride_v
- *                elements apart (>= n_kv * head_dim, multiples of 16 bytes)
+ *                elements apart (>= n_kv * head_dim, multiples of 16 bytes), not in the cache
  *   slot_map     device [T] int32
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, CUDA. */
 MTP_API int mtp_page_append(const mtp_paged_kv *kv, const void *k_new, const void *v_new, int64_t row_stride_k,
@@ -439,9 +439,9 @@ MTP_API int mtp_paged_attention_workspace(const mtp_paged_kv *kv, int32_t B, int
 /* Pages a query attends, by a cheap score of each page: per query head the step
  * s = fl32(max |q| * fl32(1 / 127)) and codes c = rint(fl32(q / s)) (all 0 when q is not
  * finite), the page's score per KV head = max over its query heads of
- * fl32(fl32((c . codes) * s) * scale) with the integer dot product. The first keep_first and the
- * last keep_last pages of a sequence score +inf, as does a page of scale NaN; a block_table entry
- * that is no page scores -inf. sel[b][g] lists the n_select pages of the highest scores (ties:
+ * fl32(fl32((c . codes) * s) * scale) with the integer dot product. A page of scale NaN scores
+ * +inf (a page whose keys are not finite is read), a block_table entry that is no page -inf; the
+ * first keep_first and the last keep_last pages of a sequence come before all others. sel[b][g] lists the n_select pages of the highest scores (ties:
  * lower page) in increasing order, -1 behind them when the sequence has fewer. Only complete
  * pages need a summary when keep_last >= 1.
  *   q    device [B][n_head][head_dim] fp32;  sel device [B][n_kv_head][n_select] int32

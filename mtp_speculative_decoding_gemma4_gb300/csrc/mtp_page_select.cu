@@ -19,6 +19,8 @@ namespace pg {
 constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kSelCache = 8192;  // scores that the picking CTA keeps in shared memory
 
+constexpr unsigned kInf = 0xff800000u, kKept = 0xffffffffu;  // ord_f32(+inf); above it: a page that is kept
+
 struct SelArgs {
   Cache c;
   const float* q;
@@ -138,8 +140,7 @@ __device__ __forceinline__ void score_pages(const SelArgs& a, int b, int g, int 
     }
     if (page < 0) keep = -INFINITY;
     if (isnan(ks)) keep = INFINITY;  // a page whose keys are not finite is always read
-    if (lp < a.keep_first || lp >= n - a.keep_last) keep = INFINITY;
-    if (lp < n) score[lp] = ord_f32(keep);
+    if (lp < n) score[lp] = lp < a.keep_first || lp >= n - a.keep_last ? kKept : ord_f32(keep);
   }
 }
 
@@ -164,8 +165,7 @@ __device__ __noinline__ void score_pages_any(const SelArgs& a, int b, int g, int
       }
       if (isnan(k)) s = INFINITY;
     }
-    if (lp < a.keep_first || lp >= n - a.keep_last) s = INFINITY;
-    if (lane == 0) score[lp] = ord_f32(s);
+    if (lane == 0) score[lp] = lp < a.keep_first || lp >= n - a.keep_last ? kKept : ord_f32(s);
   }
 }
 
@@ -205,8 +205,7 @@ __global__ void __launch_bounds__(kSelThreads) k_page_select(const __grid_consta
   if (cached)
     for (int i = tid; i < n; i += kSelThreads) cache[i] = __ldcg(score + i);
   auto get = [&](int i) { return cached ? cache[i] : __ldcg(score + i); };
-  // range of the scores below +inf, and how many are +inf
-  constexpr unsigned kInf = 0xff800000u;  // ord_f32(+inf)
+  // range of the scores below +inf, and how many are at least that
   unsigned least = 0xffffffffu, most = 0;
   int infs = 0;
   for (int i = tid; i < n; i += kSelThreads) {
@@ -232,7 +231,7 @@ __global__ void __launch_bounds__(kSelThreads) k_page_select(const __grid_consta
   infs = __reduce_add_sync(0xffffffffu, lane < kSelWarps ? winf[lane] : 0);
   // the scores' common leading bits; of those that have them, `left` are selected
   unsigned key = kInf, mask = 0xffffffffu;
-  int left = k, top = -1;  // top: highest bit in which the scores still differ
+  int left = k - a.keep_first - a.keep_last, top = -1;  // top: highest bit in which the scores still differ
   if (infs < k) {
     left = k - infs;
     top = 31 - __clz(least ^ most);  // -1: all equal
@@ -288,7 +287,7 @@ __global__ void __launch_bounds__(kSelThreads) k_page_select(const __grid_consta
   // thread, one prefix sum over (above, equal)
   const bool in_infs = infs >= k;
   auto rank_of = [&](unsigned x) {  // 2: above, 1: equal
-    if (x >= kInf) return in_infs ? 1 : 2;
+    if (x >= kInf) return in_infs && x == kInf ? 1 : 2;
     return in_infs ? 0 : (x & mask) > key ? 2 : (x & mask) == key ? 1 : 0;
   };
   const int run = (n + kSelThreads - 1) / kSelThreads, i0 = min(n, tid * run), i1 = min(n, i0 + run);

@@ -214,6 +214,10 @@ int mtp_paged_attention(const mtp_paged_kv* kv, const float* q, int32_t B, int32
     set_error("q and out must be non-NULL and 16-byte aligned");
     return MTP_ERR_INVALID_ARG;
   }
+  if (out == q || lse == out) {
+    set_error("out and lse must be buffers of their own");
+    return MTP_ERR_INVALID_ARG;
+  }
   if (window < 0 || !(scale >= 0.f) || !std::isfinite(scale)) {
     set_error("need window >= 0 and a finite scale >= 0 (window=%d scale=%g)", window, static_cast<double>(scale));
     return MTP_ERR_INVALID_ARG;

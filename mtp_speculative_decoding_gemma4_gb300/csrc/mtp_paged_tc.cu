@@ -1042,7 +1042,7 @@ int run_paged_tc(const pg::AttArgs& a, void* ws, int num_sms, cudaStream_t st) {
   g.ngrp = (G + NH - 1) / NH;
   // the most keys a unit can have; with few of them, smaller granules spread them over the SMs
   long long keys = static_cast<long long>(a.list ? a.n_list : a.c.max_pages) * P;
-  if (!a.list && a.window > 0 && a.window + rows < keys) keys = a.window + rows;
+  if (!a.list && a.window > 0 && static_cast<long long>(a.window) + rows < keys) keys = a.window + rows;
   const long long units = static_cast<long long>(a.B) * a.c.nkv * g.ngrp;
   g.gshift = a.c.d == 512 ? 6 : 7;
   const auto granules = [&] { return units * ((keys + (1 << g.gshift) - 1) >> g.gshift); };

@@ -89,8 +89,9 @@ def page_select(q, codes, scales, table, L, P, n_pages, k, first, last):
         at = np.where(ok, pages, 0)
         s = np.where(ok, page_scores(q[g * G:(g + 1) * G], codes[at, g], scales[at, g]), -np.inf)
         i = np.arange(n)
-        s = np.where((i < first) | (i >= n - last), np.inf, s) + 0.0
-        sel[g] = np.sort(np.argsort(-s, kind="stable")[:k])
+        kept = (i < first) | (i >= n - last)
+        # kept pages first, then by score, then by page
+        sel[g] = np.sort(np.lexsort((i, -(s + 0.0), ~kept))[:k])
     return sel
 
 

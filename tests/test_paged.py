@@ -71,7 +71,7 @@ def test_bad_caches_are_refused_before_the_device(lib, over, code):
     kv, n = _kv(**over), ctypes.c_int64()
     assert lib.mtp_paged_attention_workspace(kv, 1, 4, 0, ctypes.byref(n)) == code, B.mtp_last_error()
     assert B.mtp_last_error()
-    assert lib.mtp_paged_attention(kv, FAKE, 1, 4, 0, 0.0, None, 0, FAKE, None, FAKE, 1 << 30, None) == code
+    assert lib.mtp_paged_attention(kv, FAKE, 1, 4, 0, 0.0, None, 0, 2 * FAKE, None, FAKE, 1 << 30, None) == code
     assert lib.mtp_page_select(kv, FAKE, 1, 4, 4, 1, 1, FAKE, FAKE, 1 << 30, None) == code
     if (over, code) in BAD_KV:
         assert lib.mtp_page_append(kv, FAKE, None, 64, 64, FAKE, 1, None) == code
@@ -82,7 +82,7 @@ def test_bad_caches_are_refused_before_the_device(lib, over, code):
     dict(window=-1), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(pages=FAKE, n_list=0),
     dict(n_list=4), dict(pages=FAKE, n_list=-1), dict(ws_bytes=0), dict(ws=FAKE + 8), dict(ws=None)])
 def test_bad_attention_arguments_are_refused_before_the_device(lib, args):
-    a = dict(q=FAKE, B=1, nh=4, window=0, scale=0.0, pages=None, n_list=0, out=FAKE, lse=None, ws=FAKE,
+    a = dict(q=FAKE, B=1, nh=4, window=0, scale=0.0, pages=None, n_list=0, out=2 * FAKE, lse=None, ws=FAKE,
              ws_bytes=1 << 40, n_kv=1)
     a.update(args)
     # long contexts, so that a workspace is needed
@@ -682,3 +682,31 @@ def test_calls_of_several_threads_and_streams_keep_apart():
         for att, sel in got[i]:
             _close(att, want[i][0])
             np.testing.assert_array_equal(sel.cpu().numpy(), want[i][1])
+
+
+@gpu
+@pytest.mark.parametrize("n_nan", [5, 9, 10, 64])
+def test_kept_pages_come_before_pages_that_are_not_finite(n_nan):
+    c = Case(8, [64 * 16], 16, 4, 1, 128, "bf16")
+    codes, scales = _summarised(c, 8)
+    nan = np.random.RandomState(n_nan).permutation(64)[:n_nan]
+    scales[c.table[0, nan]] = np.nan
+    _check_select(c, codes, scales, 10)
+    _check_select(c, codes, scales, 10, first=3, last=7)
+    _, got = _check_select(c, codes, scales, 10, first=0, last=2)
+    assert {62, 63} <= set(got[0, 0].tolist())
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_the_widest_window_is_every_key(d):
+    from mtp_speculative_decoding_gemma4_gb300 import paged_attention
+    c = Case(d, [100, 1], 16, 4, 1, d, "bf16")
+    _close(paged_attention(c.q.cuda(), c.kv(), window=2 ** 31 - 1, want_lse=True), c.want())
+
+
+def test_outputs_over_inputs_are_refused_before_the_device(lib):
+    kv = _kv()
+    for q, out, lse in ((FAKE, FAKE, None), (FAKE, 2 * FAKE, 2 * FAKE)):
+        assert lib.mtp_paged_attention(kv, q, 1, 4, 0, 0.0, None, 0, out, lse, FAKE, 1 << 30,
+                                       None) == B.MTP_ERR_INVALID_ARG

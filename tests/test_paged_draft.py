@@ -185,3 +185,23 @@ def test_null_arguments_are_refused_without_a_device():
                                      None) == B.MTP_ERR_INVALID_ARG
     assert lib.mtp_draft_block_paged_workspace(None, None, None, 1, 0, ctypes.byref(n)) == B.MTP_ERR_INVALID_ARG
     assert B.mtp_last_error()
+
+
+@gpu
+def test_one_sequence_of_a_batched_drafter():
+    # B = 1 on a handle made for more takes the tensor-core phases
+    shape = replace(C.TINY_F32, dtype="bf16", layer_types=("S", "F"), window=24, n_head=4, n_kv_head=1, head_dim_swa=128,
+                    head_dim_full=256)
+    L = np.array([77], np.int32)
+    w = G.make_weights(shape, 21)
+    inp = G.make_step_inputs(shape, C.Workload(batch=1, ctx=80, n_draft=3), 21, ctx_len=L)
+    ref = O.draft_block(O.Shape.of(shape), O.decode_weights(w), inp.hidden, inp.last_token, inp.k_swa, inp.k_full, L,
+                        inp.pos, 3)
+    dr = _drafter(shape, w, 4, 80)
+    dd = inputs_to_device(inp, "bf16")
+    kv_s, _ = _paged(dd["k_swa"], L, 32, 1)
+    kv_f, _ = _paged(dd["k_full"], L, 16, 2)
+    for path in (0, 5, 1):
+        dr.set_path(path)
+        compare_block(*_run(dr, dd, kv_s, kv_f, 3), ref, "bf16")
+    dr.close()
