@@ -22,6 +22,10 @@
 // (Joined by the last CTA to arrive instead, the 8 long contexts took 48 us against 41: its chain
 // of round trips runs while the memory is busy with the others' keys.)
 //
+// With few, short units (kCluster CTAs for each fit, a CTA's share is a few tiles) a thread-block
+// cluster takes a unit instead: the parts stay in shared memory, and after a cluster barrier every
+// CTA joins a slice of the outputs through distributed shared memory; no second launch.
+//
 // One CTA: warp 10 finds the tiles' pages through the block table,
 // warp 8 loads them (slots of [KT keys][128 dims] in two 128-byte-swizzled boxes, a ring of 192 KB), one thread of warp 9 issues the MMAs (whichever of
 // the next score slot and the next sum is ready), and two warpgroups take the tiles in turn, each
@@ -33,6 +37,7 @@
 // (0 * NaN would not vanish). Waits are bounded; a CTA that gives up writes NaN.
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cstring>
 
 #include "mtp_common.cuh"
@@ -47,6 +52,8 @@ using pg::Cache;
 
 constexpr int kRingBytes = 192 * 1024;     // loaded keys
 constexpr int kThreadsTc = 352;            // two warpgroups for the softmax; load, MMA and find warps
+constexpr int kCluster = 8;                // CTAs of a unit in the clustered form
+constexpr int kClusterBytes = 256 * 1024;  // most keys of one of them
 constexpr int kAhead = 8;                  // tiles that the find warp runs ahead of the load warp
 constexpr int kInfo = 2 * kAhead;          // tiles whose pages and positions are kept
 constexpr long long kSpin = 4000000000LL;  // about 2 s
@@ -57,6 +64,7 @@ struct Args {
   int extra;     // what beginning a unit costs, in granules
   int rshift;    // log2 of the keys per TMA box (min(P, keys per tile))
   int grid;      // CTAs that share the granules
+  int clustered; // a cluster per unit
   int ngrp;      // head groups per KV head
   int* meta;     // [grid][4]: first output row, heads, last CTA of the unit a CTA starts and does not end
 };
@@ -159,6 +167,29 @@ __device__ __forceinline__ void st4(unsigned t, const float* v) {
                : "memory");
 }
 __device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Shared memory of a peer of the cluster, at this CTA's address of the same variable.
+__device__ __forceinline__ unsigned peer(unsigned addr, int rank) {
+  unsigned r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float peer_f32(unsigned addr, int rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer(addr, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 peer_f32x4(unsigned addr, int rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(peer(addr, rank))
+               : "memory");
+  return v;
+}
 
 // The three term columns of NH heads at tensor-memory address t: v[3 * NH].
 template <int NH>
@@ -268,6 +299,16 @@ struct Walk {
     base = __shfl_sync(0xffffffffu, base, f);
     return per;
   }
+  // The clustered form: this CTA's part of its cluster's unit (extra is 0).
+  __device__ __forceinline__ void place(const Args& g, int subs) {
+    const int unit = blockIdx.x / kCluster, rank = blockIdx.x % kCluster;
+    b = unit / subs;
+    sub = unit - b * subs;
+    n = count(g, b, lo, hi, base);
+    off = static_cast<int>(static_cast<long long>(n) * rank / kCluster);
+    r = 0;
+    r1 = static_cast<int>(static_cast<long long>(n) * (rank + 1) / kCluster) - off;
+  }
   struct Seg {
     int b, kvh, hg, a, e, n, lo, hi, base;  // KV head and group of its heads; granules [a, e) of n
     int end;                                // one past the unit's last cost
@@ -365,11 +406,15 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 
   // ---- this CTA's share: granules [r, r1) of all units (every warp for itself: no exchange)
   Walk w;
-  const int per = w.locate(g, subs);
+  int per = 0;
+  if (g.clustered)
+    w.place(g, subs);
+  else
+    per = w.locate(g, subs);
   const bool work = w.r < w.r1;
   // a unit that starts here and goes on in the next CTAs
   int* meta = g.meta + 4 * blockIdx.x;
-  if (tid == 0) meta[1] = 0;
+  if (tid == 0 && !g.clustered) meta[1] = 0;
 
   if (warp == 10) {
     // ---------------- pages: looks up the tiles' pages up to kAhead tiles before they are loaded
@@ -811,6 +856,20 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       asm volatile("bar.arrive 4, 256;" ::: "memory");
       const int h0 = s.kvh * G + s.hg * NH, nh = min(NH, G - s.hg * NH);
       const size_t row0 = static_cast<size_t>(s.b) * a.nh + h0;
+      if (g.clustered) {
+        // the ring is idle: every copy has landed and every product of this CTA's one segment is done
+        float* part = reinterpret_cast<float*>(sm);
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+#pragma unroll
+          for (int b = 0; b < NP; ++b) part[h * D + b * 128 + wt] = acc[b][h];
+          if (wt == 0) {
+            part[NH * D + 2 * h] = m[h];
+            part[NH * D + 2 * h + 1] = den[h];
+          }
+        }
+        break;
+      }
       const bool whole = s.a == 0 && s.e == s.n;
       {
         const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + (s.a == 0 ? 1 : 0)) * NH;
@@ -845,7 +904,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     }
     // sequences with nothing to attend have no granule: out 0, lse -inf
 #pragma unroll 1
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    for (int b = g.clustered ? a.B : blockIdx.x; b < a.B; b += gridDim.x) {
       int lo, hi, bs;
       if (Walk::count(g, b, lo, hi, bs) == 0) {
 #pragma unroll 1
@@ -862,6 +921,50 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(LY::cols) : "memory");
   }
+  if (!g.clustered) return;
+
+  // ---- the clustered form's join
+  const int rank = blockIdx.x % kCluster;
+  if (!work && tid < NH) {
+    reinterpret_cast<float*>(sm)[NH * D + 2 * tid] = -INFINITY;
+    reinterpret_cast<float*>(sm)[NH * D + 2 * tid + 1] = 0.f;
+  }
+  cluster_barrier();
+  // every rank's (max, exp-sum) of every head
+  float2* ml = reinterpret_cast<float2*>(sm + LY::q);
+  if (tid < kCluster * NH)
+    ml[tid] = make_float2(peer_f32(base + 4 * (NH * D + 2 * (tid % NH)), tid / NH),
+                          peer_f32(base + 4 * (NH * D + 2 * (tid % NH) + 1), tid / NH));
+  __syncthreads();
+  const int kvh = w.sub / g.ngrp, hg = w.sub - kvh * g.ngrp, nh = min(NH, G - hg * NH);
+  const size_t row0 = static_cast<size_t>(w.b) * a.nh + kvh * G + hg * NH;
+  const int total = nh * (D / 4), i1 = total * (rank + 1) / kCluster;
+  for (int i = total * rank / kCluster + tid; i < i1; i += kThreadsTc) {
+    const int h = i / (D / 4);
+    float M = -INFINITY, den = 0.f;
+#pragma unroll
+    for (int j = 0; j < kCluster; ++j) M = fmaxf(M, ml[j * NH + h].x);
+    float4 y[kCluster], x = make_float4(0, 0, 0, 0);
+    float f[kCluster];
+#pragma unroll
+    for (int j = 0; j < kCluster; ++j) {
+      f[j] = exp2f(ml[j * NH + h].x - (M == -INFINITY ? 0.f : M));
+      den = fmaf(f[j], ml[j * NH + h].y, den);
+      // a rank without keys has written no sums
+      y[j] = ml[j * NH + h].y != 0.f ? peer_f32x4(base + 16 * i, j) : make_float4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < kCluster; ++j) {
+      x.x = fmaf(f[j], y[j].x, x.x);
+      x.y = fmaf(f[j], y[j].y, x.y);
+      x.z = fmaf(f[j], y[j].z, x.z);
+      x.w = fmaf(f[j], y[j].w, x.w);
+    }
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    reinterpret_cast<float4*>(a.out + row0 * D)[i] = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+    if (a.lse && i % (D / 4) == 0) a.lse[row0 + h] = den == 0.f ? -INFINITY : (M + log2f(den)) * 0.6931471805599453f;
+  }
+  cluster_barrier();  // peers may still read this CTA's part
 }
 
 // Adds the parts of the unit that CTA blockIdx.x of k_paged_tc starts and does not end, HB heads per
@@ -977,6 +1080,34 @@ static int make_map(CUtensorMap* map, const Cache& c, const void* p, int rows) {
   return MTP_OK;
 }
 
+// Clusters of the clustered form that the current device runs side by side (each CTA takes an SM, and
+// a cluster's SMs share a GPC), asked once per device.
+template <int D, int NH>
+int clusters_at_once() {
+  static std::atomic<int> known[64];  // 1 + the number
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n - 1;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = kCluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(kCluster);
+  cfg.blockDim = dim3(kThreadsTc);
+  cfg.dynamicSmemBytes = Lay<D, NH>::total;
+  n = 0;
+  if (pg::allow_smem<k_paged_tc<D, NH>, Lay<D, NH>::total>() != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, k_paged_tc<D, NH>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  if (dev < 64) known[dev].store(n + 1);
+  return n;
+}
+
 template <int D, int NH>
 int launch(const Args& g, cudaStream_t st) {
   using LY = Lay<D, NH>;
@@ -991,17 +1122,20 @@ int launch(const Args& g, cudaStream_t st) {
   cudaError_t e = pg::allow_smem<k_paged_tc<D, NH>, LY::total>();
   if (e == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = kCluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = g.clustered ? 2 : 1;
     cfg.gridDim = dim3(g.grid);
     cfg.blockDim = dim3(kThreadsTc);
     cfg.dynamicSmemBytes = LY::total;
     cfg.stream = st;
     e = cudaLaunchKernelEx(&cfg, k_paged_tc<D, NH>, mk, mv, g);
-    if (e == cudaSuccess) {
+    if (e == cudaSuccess && !g.clustered) {
       constexpr int HB = 512 / D;  // 128 threads per part
       cfg.gridDim = dim3(g.grid, NH / HB);
       cfg.blockDim = dim3(kJoinThreads);
@@ -1018,6 +1152,11 @@ int launch(const Args& g, cudaStream_t st) {
 }
 
 }  // namespace pgt
+
+static int clusters_fit(int d, int NH) {
+  if (NH == 4) return d == 128 ? pgt::clusters_at_once<128, 4>() : d == 256 ? pgt::clusters_at_once<256, 4>() : pgt::clusters_at_once<512, 4>();
+  return d == 128 ? pgt::clusters_at_once<128, 8>() : d == 256 ? pgt::clusters_at_once<256, 8>() : pgt::clusters_at_once<512, 8>();
+}
 
 // The tensor-core kernel serves bf16 caches of head_dim 128, 256 or 512 (128-dim MMA rows) with
 // pages of at least 8 tokens (one swizzle block) whose strides fit a tensor map.
@@ -1044,18 +1183,24 @@ int run_paged_tc(const pg::AttArgs& a, void* ws, int num_sms, cudaStream_t st) {
   long long keys = static_cast<long long>(a.list ? a.n_list : a.c.max_pages) * P;
   if (!a.list && a.window > 0 && static_cast<long long>(a.window) + rows < keys) keys = a.window + rows;
   const long long units = static_cast<long long>(a.B) * a.c.nkv * g.ngrp;
+  // a cluster per unit where they fit side by side and a CTA's share of the longest unit is at most
+  // kClusterBytes: with one launch less 7 us against 9 for 512 keys at d = 256, level at 2048 keys
+  // at d = 512 (256 KB); in two waves of clusters 14 us against 10
+  const long long unit_bytes = keys * a.c.d * (a.c.v ? 4 : 2);
+  g.clustered = units * kCluster <= num_sms && unit_bytes <= static_cast<long long>(kCluster) * kClusterBytes &&
+                units <= clusters_fit(a.c.d, NH);
   g.gshift = a.c.d == 512 ? 6 : 7;
   const auto granules = [&] { return units * ((keys + (1 << g.gshift) - 1) >> g.gshift); };
-  while (g.gshift > 5 && (1 << g.gshift) > rows && granules() < num_sms) --g.gshift;
+  while (g.gshift > 5 && (1 << g.gshift) > rows && (granules() < num_sms || g.clustered)) --g.gshift;
   const long long most = granules();
   // beginning a unit, in the time of so many bytes loaded (longer with one query buffer)
   const int begin = a.c.d == 512 ? 128 * 1024 : 64 * 1024, bytes = (a.c.d * (a.c.v ? 4 : 2)) << g.gshift;
-  g.extra = most > num_sms ? (begin + bytes - 1) / bytes : 0;
+  g.extra = most > num_sms && !g.clustered ? (begin + bytes - 1) / bytes : 0;
   if (most + units * g.extra > INT32_MAX) {
     set_error("too many keys: B * heads * max_pages * page_size = %lld", units * keys);
     return MTP_ERR_UNSUPPORTED_SHAPE;
   }
-  g.grid = static_cast<int>(most < num_sms ? most : num_sms);
+  g.grid = g.clustered ? static_cast<int>(units) * kCluster : static_cast<int>(most < num_sms ? most : num_sms);
   g.meta = static_cast<int*>(ws);
   g.a.ws_ml = reinterpret_cast<float*>(g.meta + 4 * pg::kMaxSms);
   g.a.ws_acc = g.a.ws_ml + pg::kMaxSms * 2 * 8 * 2;

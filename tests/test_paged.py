@@ -710,3 +710,27 @@ def test_outputs_over_inputs_are_refused_before_the_device(lib):
     for q, out, lse in ((FAKE, FAKE, None), (FAKE, 2 * FAKE, 2 * FAKE)):
         assert lib.mtp_paged_attention(kv, q, 1, 4, 0, 0.0, None, 0, out, lse, FAKE, 1 << 30,
                                        None) == B.MTP_ERR_INVALID_ARG
+
+
+@gpu
+@pytest.mark.parametrize("d,n_head", [(128, 4), (128, 8), (256, 3), (256, 8), (512, 4), (512, 7)])
+@pytest.mark.parametrize("P,window", [(8, 0), (32, 100), (128, 0), (256, 333)])
+def test_many_ragged_sequences(d, n_head, P, window):
+    # more units than clusters fit: the keys of all sequences dealt evenly over the SMs
+    from mtp_speculative_decoding_gemma4_gb300 import paged_attention
+    L = np.random.RandomState(d + P).randint(0, 900, 47)
+    L[[0, 5, 46]] = 0
+    c = Case(d + P + n_head, L, P, n_head, 1, d, "bf16", own_v=P == 32)
+    _close(paged_attention(c.q.cuda(), c.kv(), window=window, want_lse=True), c.want(window=window))
+    pages = np.random.RandomState(P).randint(-1, c.cols, (47, 1, 7)).astype(np.int32)
+    _close(paged_attention(c.q.cuda(), c.kv(), window=window, pages=_dev(pages), want_lse=True),
+           c.want(window=window, pages=pages))
+
+
+@gpu
+@pytest.mark.parametrize("d,n_head", [(128, 4), (256, 8), (512, 4), (512, 8)])
+def test_one_sequence_over_all_sms(d, n_head):
+    # a unit in as many parts as there are SMs
+    from mtp_speculative_decoding_gemma4_gb300 import paged_attention
+    c = Case(d + n_head, [40000], 64, n_head, 1, d, "bf16", own_v=d == 128)
+    _close(paged_attention(c.q.cuda(), c.kv(), want_lse=True), c.want())
