@@ -15,6 +15,7 @@ namespace mtp {
 namespace pg {
 
 constexpr int kMaxSms = 160;  // grids and workspaces are sized for at most this many SMs
+constexpr int kPlanMaxB = 8192;  // sequences of a page plan
 
 // A validated mtp_paged_kv, in the form the kernels take.
 struct Cache {

@@ -142,7 +142,7 @@ int mtp_page_plan(const int32_t* old_len, const int32_t* new_len, int32_t B, int
     return MTP_ERR_UNSUPPORTED_SHAPE;
   }
   const long long tok = 1LL << 30;
-  if (B < 1 || B > 8192 || max_pages < 1 || n_pages < 1 || max_tokens < 0 || max_tokens > tok ||
+  if (B < 1 || B > pg::kPlanMaxB || max_pages < 1 || n_pages < 1 || max_tokens < 0 || max_tokens > tok ||
       static_cast<long long>(max_pages) * page_size > tok || static_cast<long long>(n_pages) * page_size > tok ||
       static_cast<long long>(B) * max_pages > INT32_MAX || table_stride < max_pages) {
     set_error("need 1 <= B <= 8192, max_pages, n_pages >= 1 with max_pages * page_size, n_pages * page_size and "

@@ -435,12 +435,11 @@ int run_page_plan(const int* old_len, const int* new_len, int B, int* table, lon
   const pg::PlanArgs a{old_len, new_len, state, table, ring, len_out, slots, cu_new, state_out, status,
                        table_stride, B, max_pages, n_pages, pshift, max_tokens};
   const int smem = 3 * (B + 1) * 4;
-  if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(pg::k_page_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) {
-      set_error("page plan: %s", cudaGetErrorString(e));
-      return MTP_ERR_CUDA;
-    }
+  // always the most that a call can need: another thread's call may be between this and its launch
+  const cudaError_t e = pg::allow_smem<pg::k_page_plan, 3 * (pg::kPlanMaxB + 1) * 4>();
+  if (e != cudaSuccess) {
+    set_error("page plan: %s", cudaGetErrorString(e));
+    return MTP_ERR_CUDA;
   }
   long long grid = (static_cast<long long>(max_tokens) / 4 + B) / pg::kPlanThreads + 1;
   if (grid > num_sms) grid = num_sms;

@@ -734,3 +734,34 @@ def test_one_sequence_over_all_sms(d, n_head):
     from mtp_speculative_decoding_gemma4_gb300 import paged_attention
     c = Case(d + n_head, [40000], 64, n_head, 1, d, "bf16", own_v=d == 128)
     _close(paged_attention(c.q.cuda(), c.kv(), want_lse=True), c.want())
+
+
+@gpu
+def test_plans_of_two_threads_with_different_batches():
+    # calls that need different amounts of shared memory, side by side
+    import threading
+    from mtp_speculative_decoding_gemma4_gb300 import page_plan
+    cases, errors = [], []
+    for Bn in (8192, 4097):
+        old, new, table, ring, state = _plan_case(Bn, Bn, 4, 3, 9000, "any")
+        cases.append((OP.page_plan(old, new, table[:, :3], ring, state, 4, 40000),
+                      [_dev(x) for x in (old, new, np.ascontiguousarray(table[:, :3]), ring, state)], torch.cuda.Stream()))
+    torch.cuda.synchronize()
+
+    def work(want, dev, stream):
+        try:
+            with torch.cuda.stream(stream):
+                for _ in range(200):
+                    got = page_plan(*dev, 4, 40000)
+                for name, g, w in zip(("len", "slots", "cu", "state", "status"), got, want):
+                    np.testing.assert_array_equal(g.cpu().numpy(), w, err_msg=name)
+        except BaseException as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=c) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
