@@ -210,12 +210,14 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(const __grid_constan
 // the CTA in whose share a run begins copies all of it and, where it completes the page, makes
 //   m = fl32(mean of the page's P rows), scale = fl32(max |m| * fl32(1 / 127)),
 //   code = rint(fl32(m / scale)); a page whose mean is not finite gets scale NaN and codes 0.
-// The sum is kept as an unevaluated pair of fp32 (two-sum, 6 operations a value); bf16 rows are
-// first added four at a time in fp32, which rounds nothing unless the four differ by more than
-// 2^14, and then less than 2^-24 of their largest. So m is the exact mean, rounded, in any order of
-// the rows, and the arithmetic stays below the copy. The page's other rows are read where this call does not write: rows of this
-// call in another order from k_new, older ones from the cache; so one launch does. What bounds it
-// is the copy: each row read and written once.
+// Every row enters as x / P (a power of two: exact), so that no sum leaves the range that the mean
+// lies in. The sum is kept as an unevaluated pair of fp32 (two-sum, 6 operations a value); bf16
+// rows are first added four at a time in fp32, which rounds nothing unless the four differ by more
+// than 2^14, and then less than 2^-24 of their largest. So but for such spreads m is the exact
+// mean, rounded, in any order of the rows, and the arithmetic stays below the copy. The page's
+// other rows are read where this call does not write: rows of this call in another order from
+// k_new, older ones from the cache; so one launch does. What bounds it is the copy: each row read
+// and written once.
 __device__ __forceinline__ void two_sum(float& hi, float& lo, float x) {
   const float s = __fadd_rn(hi, x), bb = __fsub_rn(s, hi);
   lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, bb)), __fsub_rn(x, bb)));
@@ -297,6 +299,7 @@ __global__ void __launch_bounds__(kAppThreads, 4) k_page_append_sum(const __grid
   const int r0 = tid / cols, v = tid - r0 * cols, hv = v / a.vph;
   const bool act = r0 < par;
   const int runs = nbegin;
+  const float part_of = 1.0f / P;
   for (int it = 0; it < runs; ++it) {
     const int first = begin[it], slot = win[first + 1], page = slot >> c.pshift, off = slot & (P - 1);
     if (tid == 0) run_len = P - off;
@@ -325,7 +328,7 @@ __global__ void __launch_bounds__(kAppThreads, 4) k_page_append_sum(const __grid
         float x[VE];
         load_vec(reinterpret_cast<const T*>(&u), x);
 #pragma unroll
-        for (int e = 0; e < VE; ++e) two_sum(hi[e], lo[e], x[e]);
+        for (int e = 0; e < VE; ++e) two_sum(hi[e], lo[e], __fmul_rn(x[e], part_of));
       };
       auto add4 = [&](const uint4 (&u)[4]) {  // rows that are not there are zero
         if (VE == 4) {                        // fp32 rows
@@ -335,10 +338,12 @@ __global__ void __launch_bounds__(kAppThreads, 4) k_page_append_sum(const __grid
           float x[VE], y[VE];
           load_vec(reinterpret_cast<const T*>(&u[0]), x);
 #pragma unroll
+          for (int e = 0; e < VE; ++e) x[e] = __fmul_rn(x[e], part_of);
+#pragma unroll
           for (int i = 1; i < 4; ++i) {
             load_vec(reinterpret_cast<const T*>(&u[i]), y);
 #pragma unroll
-            for (int e = 0; e < VE; ++e) x[e] = __fadd_rn(x[e], y[e]);
+            for (int e = 0; e < VE; ++e) x[e] = __fmaf_rn(y[e], part_of, x[e]);
           }
 #pragma unroll
           for (int e = 0; e < VE; ++e) two_sum(hi[e], lo[e], x[e]);
@@ -390,7 +395,7 @@ __global__ void __launch_bounds__(kAppThreads, 4) k_page_append_sum(const __grid
             two_sum(x, l, part[0][e * kAppThreads + tid + r * cols]);
             l += part[1][e * kAppThreads + tid + r * cols];
           }
-          m[e] = __fmul_rn(__fadd_rn(x, l), 1.0f / P);
+          m[e] = __fadd_rn(x, l);
           fin = fin && isfinite(m[e]);
           mx = fmaxf(mx, fabsf(m[e]));
         }

@@ -765,3 +765,31 @@ def test_plans_of_two_threads_with_different_batches():
         t.join()
     torch.cuda.synchronize()
     assert not errors, errors
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("P", [1, 4, 64, 256])
+def test_summaries_of_the_largest_values(dtype, P):
+    # rows at the ends of the type's range: the sums would leave it, the mean does not
+    from mtp_speculative_decoding_gemma4_gb300 import page_append
+    d, n = 64, 4
+    c = Case(2, [1], P, 1, 1, d, dtype, spare=8)
+    rs, most = np.random.RandomState(P), torch.finfo(c.k.dtype).max
+    rows = torch.full((n * P, 1, d), most, dtype=c.k.dtype)
+    rows[P:2 * P] = -most
+    rows[2 * P:3 * P, 0, : d // 2] *= -1
+    # the last page in runs: half of the sum's weight on either side
+    rows[3 * P:] *= torch.from_numpy(np.where(rs.uniform(size=(P, 1, d)) < 0.75, 1.0, -1.0)).to(c.k.dtype)
+    m = c.k.shape[0]
+    for cut in (0, P // 2):  # in one call, and the pages in two
+        codes, scales = torch.zeros((m, 1, d), dtype=torch.int8).cuda(), torch.zeros((m, 1)).cuda()
+        slots = np.arange(n * P, dtype=np.int32)
+        first = slots % P < cut
+        kv = c.kv(codes=codes, scales=scales)
+        for part in (first, ~first):
+            page_append(kv, rows[torch.from_numpy(part)].contiguous().cuda(), _dev(slots[part]))
+        for p in range(n):
+            a, b = OP.page_summary(rows[p * P:(p + 1) * P, 0].float().numpy())
+            np.testing.assert_array_equal(codes[p, 0].cpu().numpy(), a)
+            np.testing.assert_array_equal(scales[p].cpu().numpy(), [b])
