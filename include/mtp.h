@@ -409,7 +409,7 @@ MTP_API int mtp_page_plan(const int32_t *old_len, const int32_t *new_len, int32_
  * summaries, every page whose last slot is written gets its summary from all P rows it then
  * holds: per KV head m = the mean key rounded to fp32, scale = fl32(max |m| * fl32(1 / 127)),
  * codes = rint(fl32(m / scale)); a mean that is not finite gives scale NaN and codes 0. A slot
- * may occur once in slot_map.
+ * may occur once in slot_map; T <= 2^30.
  *   k_new, v_new device rows of [n_kv][head_dim], model dtype, row_stride_k / row_stride_v
  *                elements apart (>= n_kv * head_dim, multiples of 16 bytes), not in the cache
  *   slot_map     device [T] int32
@@ -422,12 +422,13 @@ MTP_API int mtp_page_append(const mtp_paged_kv *kv, const void *k_new, const voi
  * positions: [0, L), the last `window` of them when window > 0, and with `pages` only those in
  * the listed logical pages of the head's KV head (entries outside the sequence's pages are
  * skipped; a page listed twice counts twice). fp32 arithmetic; bf16 keys enter exactly. A
- * sequence with nothing to attend gets out 0 and lse -inf. Query head h reads KV head
+ * sequence with nothing to attend gets out 0 and lse -inf. What is not attended may hold anything;
+ * an attended row or a query that is not finite makes the outputs it reaches NaN or infinite. Query head h reads KV head
  * h / (n_head / n_kv_head).
  *   q         device [B][n_head][head_dim] fp32
  *   pages     device [B][n_kv_head][n_list] int32 or NULL
  *   scale     softmax scale, 0 -> 1 / sqrt(head_dim)
- *   out       device [B][n_head][head_dim] fp32
+ *   out       device [B][n_head][head_dim] fp32, not over q
  *   lse       device [B][n_head] fp32 log of the sum of exponentials, or NULL
  * Errors: INVALID_ARG (workspace too small included), UNSUPPORTED_SHAPE, CUDA. */
 MTP_API int mtp_paged_attention(const mtp_paged_kv *kv, const float *q, int32_t B, int32_t n_head, int32_t window,
@@ -441,9 +442,9 @@ MTP_API int mtp_paged_attention_workspace(const mtp_paged_kv *kv, int32_t B, int
  * finite), the page's score per KV head = max over its query heads of
  * fl32(fl32((c . codes) * s) * scale) with the integer dot product. A page of scale NaN scores
  * +inf (a page whose keys are not finite is read), a block_table entry that is no page -inf; the
- * first keep_first and the last keep_last pages of a sequence come before all others. sel[b][g] lists the n_select pages of the highest scores (ties:
- * lower page) in increasing order, -1 behind them when the sequence has fewer. Only complete
- * pages need a summary when keep_last >= 1.
+ * first keep_first and the last keep_last pages of a sequence come before all others. sel[b][g]
+ * lists the n_select pages of the highest scores (ties: lower page) in increasing order, -1 behind
+ * them when the sequence has fewer. Only complete pages need a summary when keep_last >= 1.
  *   q    device [B][n_head][head_dim] fp32;  sel device [B][n_kv_head][n_select] int32
  * Errors: INVALID_ARG (keep_first < 0, keep_last < 1, n_select < keep_first + keep_last, no
  * summaries, workspace too small), UNSUPPORTED_SHAPE, CUDA. */

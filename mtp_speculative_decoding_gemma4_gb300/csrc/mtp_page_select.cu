@@ -192,6 +192,7 @@ __global__ void __launch_bounds__(kSelThreads) k_page_select(const __grid_consta
   else if (d > 128) score_pages<2>(a, b, g, G, n, rank, q, sm_sel, qs, score);
   else score_pages<1>(a, b, g, G, n, rank, q, sm_sel, qs, score);
   // the scores of the whole cluster are in place; only the first CTA goes on
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (rank != 0) return;
 

@@ -12,6 +12,11 @@ namespace pg {
 
 static bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+static bool overlap(const void* p, long long np, const void* q, long long nq) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + static_cast<uintptr_t>(nq) && b < a + static_cast<uintptr_t>(np);
+}
+
 static int log2_exact(int n) {
   int s = 0;
   while ((1 << s) < n) ++s;
@@ -167,8 +172,8 @@ int mtp_page_append(const mtp_paged_kv* kv, const void* k_new, const void* v_new
   pg::Cache c;
   int rc = pg::make_cache(kv, false, &c);
   if (rc) return rc;
-  if (T < 0 || (T > 0 && (!k_new || !slot_map || (c.v && !v_new)))) {
-    set_error("need T >= 0 and, for T > 0, k_new, slot_map and (a cache with a V) v_new");
+  if (T < 0 || T > 1 << 30 || (T > 0 && (!k_new || !slot_map || (c.v && !v_new)))) {
+    set_error("need 0 <= T <= 2^30 and, for T > 0, k_new, slot_map and (a cache with a V) v_new");
     return MTP_ERR_INVALID_ARG;
   }
   if (!c.v && v_new && v_new != k_new) {
@@ -177,9 +182,10 @@ int mtp_page_append(const mtp_paged_kv* kv, const void* k_new, const void* v_new
   }
   const int vec = c.f32 ? 4 : 8;
   const int64_t width = static_cast<int64_t>(c.nkv) * c.d;
-  if (row_stride_k < width || row_stride_k % vec || (c.v && (row_stride_v < width || row_stride_v % vec)) ||
+  auto bad_row = [&](int64_t stride) { return stride < width || stride % vec || stride > (1LL << 40); };
+  if (bad_row(row_stride_k) || (c.v && bad_row(row_stride_v)) ||
       !pg::aligned(k_new, 16) || !pg::aligned(v_new, 16) || !pg::aligned(slot_map, 4)) {
-    set_error("new rows must be 16-byte aligned, at least n_kv_head * head_dim = %lld elements apart, in multiples of %d",
+    set_error("new rows must be 16-byte aligned, n_kv_head * head_dim = %lld to 2^40 elements apart, in multiples of %d",
               static_cast<long long>(width), vec);
     return MTP_ERR_INVALID_ARG;
   }
@@ -214,12 +220,16 @@ int mtp_paged_attention(const mtp_paged_kv* kv, const float* q, int32_t B, int32
     set_error("q and out must be non-NULL and 16-byte aligned");
     return MTP_ERR_INVALID_ARG;
   }
-  if (out == q || lse == out) {
+  const long long row_bytes = 4LL * B * n_head, q_bytes = row_bytes * a.c.d;
+  if (pg::overlap(out, q_bytes, q, q_bytes) ||
+      (lse && (pg::overlap(lse, row_bytes, q, q_bytes) || pg::overlap(lse, row_bytes, out, q_bytes)))) {
     set_error("out and lse must be buffers of their own");
     return MTP_ERR_INVALID_ARG;
   }
-  if (window < 0 || !(scale >= 0.f) || !std::isfinite(scale)) {
-    set_error("need window >= 0 and a finite scale >= 0 (window=%d scale=%g)", window, static_cast<double>(scale));
+  const double s = scale > 0.f ? static_cast<double>(scale) : 1.0 / std::sqrt(static_cast<double>(a.c.d));
+  a.scale_log2 = static_cast<float>(s * 1.4426950408889634);
+  if (window < 0 || !(scale >= 0.f) || !std::isfinite(a.scale_log2)) {
+    set_error("need window >= 0 and a scale in [0, 2^127] (window=%d scale=%g)", window, static_cast<double>(scale));
     return MTP_ERR_INVALID_ARG;
   }
   if (pages ? (n_list < 1 || (static_cast<long long>(n_list) << a.c.pshift) > (1LL << 30)) : n_list != 0) {
@@ -235,8 +245,6 @@ int mtp_paged_attention(const mtp_paged_kv* kv, const float* q, int32_t B, int32
   a.B = B;
   a.nh = n_head;
   a.window = window;
-  const double s = scale > 0.f ? static_cast<double>(scale) : 1.0 / std::sqrt(static_cast<double>(a.c.d));
-  a.scale_log2 = static_cast<float>(s * 1.4426950408889634);
   int sms = 0;
   if ((rc = pg::sm_count(&sms))) return rc;
   return run_paged_att(a, workspace, sms, static_cast<cudaStream_t>(stream));

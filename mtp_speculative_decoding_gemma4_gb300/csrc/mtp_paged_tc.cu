@@ -169,6 +169,7 @@ __device__ __forceinline__ void st4(unsigned t, const float* v) {
 __device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void cluster_barrier() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // Shared memory of a peer of the cluster, at this CTA's address of the same variable.
@@ -1071,7 +1072,7 @@ static int make_map(CUtensorMap* map, const Cache& c, const void* p, int rows) {
   if (r == CUDA_ERROR_INVALID_CONTEXT || r == CUDA_ERROR_NOT_INITIALIZED) {
     // a host thread whose first CUDA call this is: bind the device's primary context to it
     int dev = 0;
-    if (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && cudaFree(nullptr) == cudaSuccess) r = encode();
+    if (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) r = encode();
   }
   if (r != CUDA_SUCCESS) {
     set_error("cuTensorMapEncodeTiled failed (%d) for a paged cache", static_cast<int>(r));
@@ -1196,7 +1197,7 @@ int run_paged_tc(const pg::AttArgs& a, void* ws, int num_sms, cudaStream_t st) {
   // beginning a unit, in the time of so many bytes loaded (longer with one query buffer)
   const int begin = a.c.d == 512 ? 128 * 1024 : 64 * 1024, bytes = (a.c.d * (a.c.v ? 4 : 2)) << g.gshift;
   g.extra = most > num_sms && !g.clustered ? (begin + bytes - 1) / bytes : 0;
-  if (most + units * g.extra > INT32_MAX) {
+  if (most + units * g.extra > INT32_MAX - pg::kMaxSms) {
     set_error("too many keys: B * heads * max_pages * page_size = %lld", units * keys);
     return MTP_ERR_UNSUPPORTED_SHAPE;
   }

@@ -793,3 +793,16 @@ def test_summaries_of_the_largest_values(dtype, P):
             a, b = OP.page_summary(rows[p * P:(p + 1) * P, 0].float().numpy())
             np.testing.assert_array_equal(codes[p, 0].cpu().numpy(), a)
             np.testing.assert_array_equal(scales[p].cpu().numpy(), [b])
+
+
+def test_sizes_past_the_limits_are_refused_before_the_device(lib):
+    kv = _kv()
+    assert lib.mtp_page_append(kv, FAKE, None, 64, 64, FAKE, (1 << 30) + 1, None) == B.MTP_ERR_INVALID_ARG
+    assert lib.mtp_page_append(kv, FAKE, None, 1 << 41, 64, FAKE, 2, None) == B.MTP_ERR_INVALID_ARG
+    # outputs that begin inside the queries [4][64]; a scale that is infinite in base 2
+    for q, out, lse, scale in ((2 * FAKE, 2 * FAKE + 512, None, 0.0), (2 * FAKE, 2 * FAKE - 512, None, 0.0),
+                               (FAKE, 2 * FAKE, FAKE + 1020, 0.0), (FAKE, 2 * FAKE, 2 * FAKE - 4, 0.0),
+                               (FAKE, 2 * FAKE, None, 3e38)):
+        assert lib.mtp_paged_attention(kv, q, 1, 4, 0, scale, None, 0, out, lse, FAKE, 1 << 30,
+                                       None) == B.MTP_ERR_INVALID_ARG
+        assert B.mtp_last_error()
