@@ -9,7 +9,7 @@ from typing import Optional
 import torch
 
 from . import binding as B
-from .paged import call_on
+from .paged import _need_flat, call_on
 
 _DT = {"bf16": (B.MTP_DTYPE_BF16, torch.bfloat16), "f32": (B.MTP_DTYPE_F32, torch.float32)}
 
@@ -99,10 +99,17 @@ class Drafter:
         """draft_block over paged caches (paged.PagedKV with block_table and ctx_len, or None for an
         attention type that no block has). n_select > 0: full-attention blocks attend the n_select
         pages that their queries select. stream: None is torch's current stream."""
+        _need_flat(hidden, "hidden", self.torch_dtype, (None, self.shape.backbone))
         Bn, dev = hidden.shape[0], hidden.device
+        for t, name in ((last_token, "last_token"), (pos, "pos")):
+            _need_flat(t, name, torch.int32, (Bn,), dev)
+        if out_tokens is not None:
+            _need_flat(out_tokens, "out_tokens", torch.int32, (Bn, n_draft), dev)
+        if out_hidden is not None:
+            _need_flat(out_hidden, "out_hidden", torch.float32, (Bn, n_draft, self.shape.backbone), dev)
         for kv in (kv_swa, kv_full):
-            if kv is not None and kv.batch != Bn:
-                raise ValueError(f"the cache's block_table holds {kv.batch} sequences, hidden {Bn}")
+            if kv is not None and (kv.batch != Bn or kv.device != dev):
+                raise ValueError(f"the cache holds {kv.batch} sequences on {kv.device}, hidden {Bn} on {dev}")
         kvs = [None if kv is None else kv.c for kv in (kv_swa, kv_full)]
         n = B.mtp_draft_block_paged_workspace(self.handle, kvs[0], kvs[1], Bn, n_select)
 

@@ -205,3 +205,25 @@ def test_one_sequence_of_a_batched_drafter():
         dr.set_path(path)
         compare_block(*_run(dr, dd, kv_s, kv_f, 3), ref, "bf16")
     dr.close()
+
+
+@gpu
+def test_paged_block_checks_its_tensors():
+    shape = replace(C.TINY_F32, dtype="bf16", layer_types=("F",), n_head=4, n_kv_head=1, head_dim_swa=128,
+                    head_dim_full=128)
+    L = np.array([90, 40], np.int32)
+    w = G.make_weights(shape, 9)
+    inp = G.make_step_inputs(shape, C.Workload(batch=2, ctx=100, n_draft=1), 9, ctx_len=L)
+    dd = inputs_to_device(inp, "bf16")
+    dr = _drafter(shape, w, 2, 100)
+    kv, _ = _paged(dd["k_full"], L, 16, 1)
+    good = dict(hidden=dd["hidden"], last_token=dd["last_token"], pos=dd["pos"], out_tokens=None, out_hidden=None)
+    for bad in (dict(hidden=dd["hidden"].float()), dict(hidden=dd["hidden"].cpu()), dict(hidden=dd["hidden"][:, 8:]),
+                dict(last_token=dd["last_token"].long()), dict(pos=dd["pos"][:1]), dict(pos=dd["pos"].cpu()),
+                dict(out_tokens=torch.empty((2, 2), dtype=torch.int32, device="cuda")),
+                dict(out_hidden=torch.empty((2, 1, shape.backbone), dtype=torch.bfloat16, device="cuda"))):
+        a = {**good, **bad}
+        with pytest.raises(ValueError):
+            dr.draft_block_paged(a["hidden"], a["last_token"], None, kv, a["pos"], 1, out_tokens=a["out_tokens"],
+                                 out_hidden=a["out_hidden"])
+    dr.close()
