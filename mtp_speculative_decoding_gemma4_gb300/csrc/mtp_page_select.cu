@@ -9,6 +9,10 @@
 // picks. The pick is a chain of small steps on one SM: the range of the scores, the threshold key
 // by 8-bit digits from the highest bit in which they differ (so that the first digit already
 // spreads over its counters), then one ordered compaction.
+//
+// What bounds it is that chain: length, table, codes, the cluster barrier, up to 4 digits, the
+// compaction, and the code's own first fetches. One sequence of 1024 pages takes 9 us, 16
+// sequences of 2048 pages (17 MB of codes, 2.5 us at the copy rate) 14 us.
 #include "mtp_common.cuh"
 #include "mtp_launch.h"
 #include "mtp_paged.cuh"

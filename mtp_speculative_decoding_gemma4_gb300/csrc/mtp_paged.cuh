@@ -10,6 +10,7 @@
 #include <atomic>
 
 #include "mtp.h"
+#include "mtp_launch.h"
 
 namespace mtp {
 namespace pg {
@@ -53,6 +54,29 @@ inline cudaError_t allow_smem() {
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
   if (e == cudaSuccess) done.fetch_or(bit);
   return e;
+}
+
+// Launches a kernel that begins with pdl_enter() so that it may be set up while the kernel before
+// it on the stream still runs.
+template <typename... A>
+int launch_pdl(const char* what, void (*kernel)(A...), dim3 grid, int threads, int smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    set_error("%s launch: %s", what, cudaGetErrorString(e));
+    return MTP_ERR_CUDA;
+  }
+  return MTP_OK;
 }
 
 struct AttArgs {

@@ -8,9 +8,12 @@
 // (16-byte vectors), 32 / LPK rows side by side in a warp, U row blocks in flight; every lane
 // keeps its vectors of GP queries and GP running sums in registers, so a key row is read once
 // for all heads of the group. Scores, maxima, sums and outputs are fp32.
-// What bounds it is instruction issue (43 % of the slots at 26 us for 16 fp32 contexts to 8000, the
-// memory at 26 %), most of it around the products. So the U * GP scores of a block are reduced by
-// one reduce-scatter, each lane takes the softmax of one score, and probabilities are broadcast.
+// What bounds it: 16 fp32 contexts to 8000 (66 MB of K and V) take 20 us with the join, 3.3 TB/s
+// or half of the copy rate; issue slots are 39 % busy and warps wait for their loads, with 5 CTAs
+// per SM (registers) and the two launches' starts in the time. Most instructions are around the
+// products, so the U * GP scores of a block are reduced by one reduce-scatter, each lane takes the
+// softmax of one score, and probabilities are broadcast (27 us without). 5 to 16 CTAs per SM from
+// the split and 6 resident CTAs are within 5 % of this.
 #include "mtp_common.cuh"
 #include "mtp_launch.h"
 #include "mtp_paged.cuh"
@@ -303,13 +306,8 @@ int launch_att(const AttArgs& a, cudaStream_t st) {
   const int G = a.nh / a.c.nkv, ngrp = (G + GP - 1) / GP;
   const long long grid = static_cast<long long>(a.B) * a.c.nkv * ngrp * a.nsplit;
   const int smem = kAttWarps * GP * (a.c.d + 2) * 4;
-  k_paged_att<T, LPK, NV, GP><<<static_cast<unsigned>(grid), kAttWarps * 32, smem, st>>>(a);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) {
-    set_error("paged attention launch: %s", cudaGetErrorString(e));
-    return MTP_ERR_CUDA;
-  }
-  return MTP_OK;
+  return launch_pdl("paged attention", k_paged_att<T, LPK, NV, GP>, dim3(static_cast<unsigned>(grid)), kAttWarps * 32,
+                    smem, st, a);
 }
 
 // Heads per CTA: the queries and sums of GP heads have to stay in registers (GP * NV * VE <= 64).
@@ -360,13 +358,7 @@ int run_paged_att(pg::AttArgs a, void* ws, int num_sms, cudaStream_t st) {
   a.ws_ml = a.ws_acc + static_cast<size_t>(a.B) * a.nh * a.nsplit * a.c.d;
   int rc = a.c.f32 ? pg::launch_type<float>(a, st) : pg::launch_type<__nv_bfloat16>(a, st);
   if (rc || a.nsplit == 1) return rc;
-  pg::k_paged_join<<<a.B * a.nh, 256, 0, st>>>(a);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) {
-    set_error("paged attention join launch: %s", cudaGetErrorString(e));
-    return MTP_ERR_CUDA;
-  }
-  return MTP_OK;
+  return pg::launch_pdl("paged attention join", pg::k_paged_join, dim3(a.B * a.nh), 256, 0, st, a);
 }
 
 }  // namespace mtp

@@ -44,25 +44,6 @@ __global__ void __launch_bounds__(kThreads) k_paged_stage(const __grid_constant_
 }
 
 namespace {
-template <typename... A>
-int launch_pdl(const char* what, void (*kernel)(A...), dim3 grid, cudaStream_t st, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = st;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    set_error("%s launch: %s", what, cudaGetErrorString(e));
-    return MTP_ERR_CUDA;
-  }
-  return MTP_OK;
-}
 long long round16(long long n) { return (n + 15) & ~15ll; }
 }  // namespace
 
@@ -88,7 +69,7 @@ long long paged_draft_workspace(PagedCall& pc, int B, int nh, int dmax, int has_
 
 int run_paged_layer(const Params& p, const PagedCall& pc, int l, __nv_bfloat16* xs, int bp, cudaStream_t st) {
   const int t = p.L[l].type, B = p.s.B;
-  int rc = launch_pdl("paged query", k_paged_q, dim3(ceil_div(B * p.s.nh, kWarps)), st, p, l, pc.qn);
+  int rc = pg::launch_pdl("paged query", k_paged_q, dim3(ceil_div(B * p.s.nh, kWarps)), kThreads, 0, st, p, l, pc.qn);
   if (rc) return rc;
   pg::AttArgs a;
   memset(&a, 0, sizeof(a));
@@ -108,8 +89,8 @@ int run_paged_layer(const Params& p, const PagedCall& pc, int l, __nv_bfloat16* 
   }
   if ((rc = run_paged_att(a, pc.att_ws, pc.num_sms, st))) return rc;
   if (!xs) return MTP_OK;
-  return launch_pdl("paged attention staging", k_paged_stage, dim3(B, ceil_div(p.s.nh * p.s.d[t], kThreads)), st, p, l,
-                    xs, bp);
+  return pg::launch_pdl("paged attention staging", k_paged_stage, dim3(B, ceil_div(p.s.nh * p.s.d[t], kThreads)), kThreads, 0,
+                    st, p, l, xs, bp);
 }
 
 }  // namespace mtp
