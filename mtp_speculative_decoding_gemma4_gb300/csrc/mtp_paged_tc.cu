@@ -2,7 +2,7 @@
 // 256 or 512, pages of at least 8 tokens): the formula of mtp_paged_att.cu.
 //
 // What bounds it is reading the cache once: with the join 151 MB take 35.6 us at d = 512 (8 long
-// ragged contexts, 4.2 TB/s), 134 MB 30.8 us at d = 256 (32 x 8192, 4.4 TB/s), 128 MB of K and V
+// ragged contexts, 4.2 TB/s), 134 MB 30.8 us at d = 128 (32 x 8192, 4.4 TB/s), 128 MB of K and V
 // 32.5 us at d = 128 (61 short contexts, 3.9 TB/s). Between its start (3 us: length, table, keys),
 // its tail and the join (3 to 4 us) the keys come in at the rate that TMA copies alone reach here
 // (6.0 TB/s). On CUDA cores it is the arithmetic instead: with G
