@@ -6,6 +6,7 @@ torch's current stream of the tensors' device, else the cudaStream_t passed as `
 """
 from __future__ import annotations
 
+import ctypes
 import threading
 from typing import Optional
 
@@ -14,6 +15,15 @@ import torch
 from . import binding as B
 
 _DT = {torch.bfloat16: B.MTP_DTYPE_BF16, torch.float32: B.MTP_DTYPE_F32}
+
+
+_i32, _f32 = torch.int32, torch.float32
+
+
+def _flat_like(t, dtype, device, shape) -> bool:
+    """Whether t is what _need_flat asks for; the common case of a check, without its message."""
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device and t.shape == shape and \
+        t.is_contiguous()
 
 
 def _need(t, name: str, dtype, ndim: int, device=None) -> torch.Tensor:
@@ -56,12 +66,13 @@ class _On:
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream  # torch's current stream of a device, as an integer
+_current_device = torch._C._cuda_getDevice
 
 
 def call_on(device: torch.device, stream: Optional[int], fn, *args):
     """fn(stream, *args) with the call's device current and its allocations on its stream."""
     index = device.index
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         current = _raw_stream(index)
         if stream is None or stream == current:
             return fn(current, *args)
@@ -113,9 +124,10 @@ class PagedKV:
         c.n_pages, c.page_size, c.n_kv_head, c.head_dim, c.dtype = n_pages, P, n_kv, d, _DT[k.dtype]
         self.k, self.v, self.block_table, self.ctx_len, self.codes, self.scales = k, v, block_table, ctx_len, codes, scales
         self.device, self.batch = dev, 0 if block_table is None else block_table.shape[0]
-        self._row = k.shape[2:]
-        self._ws = {}  # workspace bytes by (n_head, n_list); and of the selection
-        self._scratch, self._lock = None, threading.Lock()
+        self._row = (n_kv, d)
+        self.p = ctypes.byref(c)  # the descriptor as the C entry points take it
+        self._ws = {}  # workspace bytes by (n_head, n_list); and of the selection by "select"
+        self._scratch, self._scratch_at, self._scratch_n, self._lock = None, 0, 0, threading.Lock()
 
 
 def _with_workspace(kv: PagedKV, st: int, n: int, launch) -> None:
@@ -130,9 +142,10 @@ def _with_workspace(kv: PagedKV, st: int, n: int, launch) -> None:
         launch(ws.data_ptr(), n)
     else:
         with kv._lock:
-            if kv._scratch is None or kv._scratch.numel() < n:
+            if kv._scratch_n < n:
                 kv._scratch = torch.empty(n, dtype=torch.uint8, device=kv.device)
-            launch(kv._scratch.data_ptr(), n)
+                kv._scratch_at, kv._scratch_n = kv._scratch.data_ptr(), n
+            launch(kv._scratch_at, n)
 
 
 def page_plan(old_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.Tensor, free_ring: torch.Tensor,
@@ -141,12 +154,15 @@ def page_plan(old_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.T
     (int32 [B]): updates block_table [B][max_pages] and the ring of free pages free_ring
     [n_pages] (ring_state: head and count) in place and returns (len_out [B], slot_map
     [max_tokens], cu_new [B + 1], state_out [2], status [4]), as mtp_page_plan describes."""
-    _need_flat(old_len, "old_len", torch.int32, (None,))
-    dev, i32, Bn = old_len.device, torch.int32, old_len.shape[0]
-    _need_flat(new_len, "new_len", i32, (Bn,), dev)
-    _need(block_table, "block_table", i32, 2, dev)
-    _need_flat(free_ring, "free_ring", i32, (None,), dev)
-    _need_flat(ring_state, "ring_state", i32, (2,), dev)
+    _need_flat(old_len, "old_len", _i32, (None,))
+    dev, shape = old_len.device, old_len.shape
+    Bn = shape[0]
+    if not _flat_like(new_len, _i32, dev, shape):
+        _need_flat(new_len, "new_len", _i32, shape, dev)
+    _need(block_table, "block_table", _i32, 2, dev)
+    _need_flat(free_ring, "free_ring", _i32, (None,), dev)
+    if not _flat_like(ring_state, _i32, dev, (2,)):
+        _need_flat(ring_state, "ring_state", _i32, (2,), dev)
     if block_table.shape[0] != Bn or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
         raise ValueError(f"block_table must be [{Bn}][max_pages] with a contiguous last dimension")
     if max_tokens < 0:
@@ -155,11 +171,11 @@ def page_plan(old_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.T
 
 
 def _plan(st, old_len, new_len, block_table, free_ring, ring_state, page_size, max_tokens):
-    (Bn, cols), dev, i32 = block_table.shape, old_len.device, torch.int32
-    len_out = torch.empty(Bn, dtype=i32, device=dev)
+    (Bn, cols), dev, i32 = block_table.shape, old_len.device, _i32
+    len_out = torch.empty_like(old_len)
     slots = torch.empty(max_tokens, dtype=i32, device=dev)
     cu = torch.empty(Bn + 1, dtype=i32, device=dev)
-    state = torch.empty(2, dtype=i32, device=dev)
+    state = torch.empty_like(ring_state)
     status = torch.empty(4, dtype=i32, device=dev)
     B.mtp_page_plan(old_len.data_ptr(), new_len.data_ptr(), Bn, block_table.data_ptr(),
                     block_table.stride(0) if Bn > 1 else cols, cols, free_ring.data_ptr(), free_ring.shape[0],
@@ -179,26 +195,30 @@ def page_append(kv: PagedKV, k_new: torch.Tensor, slot_map: torch.Tensor, v_new:
         if t is None:
             continue
         _need(t, name, kv.k.dtype, 3, kv.device)
-        if t.shape[1:] != kv._row or t.shape[0] != k_new.shape[0] or t.numel() and (t.stride(2) != 1 or
-                n_kv > 1 and t.stride(1) != d):
+        T = k_new.shape[0]
+        if t.shape != (T, n_kv, d) or T and (t.stride(2) != 1 or n_kv > 1 and t.stride(1) != d):
             raise ValueError(f"{name} must be [T][{n_kv}][{d}] with contiguous rows")
-    _need_flat(slot_map, "slot_map", torch.int32, (k_new.shape[0],), kv.device)
+    if not _flat_like(slot_map, _i32, kv.device, k_new.shape[:1]):
+        _need_flat(slot_map, "slot_map", _i32, (k_new.shape[0],), kv.device)
     call_on(kv.device, stream, _append, kv, k_new, slot_map, v_new)
 
 
 def _append(st, kv, k_new, slot_map, v_new):
     T, width = k_new.shape[0], kv.c.n_kv_head * kv.c.head_dim
-    B.mtp_page_append(kv.c, k_new.data_ptr(), 0 if v_new is None else v_new.data_ptr(),
+    B.mtp_page_append(kv.p, k_new.data_ptr(), 0 if v_new is None else v_new.data_ptr(),
                       k_new.stride(0) if T > 1 else width, v_new.stride(0) if T > 1 and v_new is not None else width,
                       slot_map.data_ptr(), T, st)
 
 
 def _queries(q, kv: PagedKV):
-    if not (isinstance(q, torch.Tensor) and q.dtype is torch.float32 and q.dim() == 3 and q.device == kv.device and
-            q.is_contiguous() and q.shape[0] == kv.batch and q.shape[2] == kv._row[1]):
-        _need_flat(q, "q", torch.float32, (kv.batch, None, kv._row[1]), kv.device)
+    """Checks the queries; their shape."""
+    shape = q.shape if isinstance(q, torch.Tensor) else ()
+    if not (len(shape) == 3 and shape[0] == kv.batch and shape[2] == kv._row[1] and
+            _flat_like(q, _f32, kv.device, shape)):
+        _need_flat(q, "q", _f32, (kv.batch, None, kv._row[1]), kv.device)
     if kv.block_table is None:
         raise ValueError("the cache has no block_table")
+    return shape
 
 
 def paged_attention(q: torch.Tensor, kv: PagedKV, window: int = 0, scale: float = 0.0,
@@ -208,27 +228,26 @@ def paged_attention(q: torch.Tensor, kv: PagedKV, window: int = 0, scale: float 
     ctx_len[b] keys, the last `window` (> 0), or those of the logical pages listed in `pages`
     (int32 [B][n_kv][n], -1: none). Returns out fp32 [B][n_head][d], with want_lse (out, lse
     [B][n_head])."""
-    _queries(q, kv)
+    shape, n_list = _queries(q, kv), 0
     if pages is not None:
-        _need_flat(pages, "pages", torch.int32, (kv.batch, kv._row[0], None), kv.device)
-        if pages.shape[2] < 1:
+        _need_flat(pages, "pages", _i32, (kv.batch, kv._row[0], None), kv.device)
+        n_list = pages.shape[2]
+        if n_list < 1:
             raise ValueError("pages must list at least one entry per KV head")
     if out is not None:
-        _need_flat(out, "out", torch.float32, tuple(q.shape), kv.device)
-    return call_on(kv.device, stream, _attend, q, kv, window, scale, pages, want_lse, out)
+        _need_flat(out, "out", _f32, shape, kv.device)
+    return call_on(kv.device, stream, _attend, q, kv, shape[0], shape[1], window, scale, pages, n_list, want_lse, out)
 
 
-def _attend(st, q, kv, window, scale, pages, want_lse, out):
-    Bn, nh, _ = q.shape
-    n_list = 0 if pages is None else pages.shape[2]
+def _attend(st, q, kv, Bn, nh, window, scale, pages, n_list, want_lse, out):
     n = kv._ws.get((nh, n_list))
     if n is None:
-        n = kv._ws[(nh, n_list)] = B.mtp_paged_attention_workspace(kv.c, Bn, nh, n_list)
+        n = kv._ws[(nh, n_list)] = B.mtp_paged_attention_workspace(kv.p, Bn, nh, n_list)
     if out is None:
         out = torch.empty_like(q)
-    lse = torch.empty((Bn, nh), dtype=torch.float32, device=kv.device) if want_lse else None
+    lse = torch.empty((Bn, nh), dtype=_f32, device=kv.device) if want_lse else None
     _with_workspace(kv, st, n, lambda ws, n: B.mtp_paged_attention(
-        kv.c, q.data_ptr(), Bn, nh, window, scale, 0 if pages is None else pages.data_ptr(), n_list, out.data_ptr(),
+        kv.p, q.data_ptr(), Bn, nh, window, scale, 0 if pages is None else pages.data_ptr(), n_list, out.data_ptr(),
         lse.data_ptr() if want_lse else 0, ws, n, st))
     return (out, lse) if want_lse else out
 
@@ -239,21 +258,20 @@ def page_select(q: torch.Tensor, kv: PagedKV, n_select: int, keep_first: int = 1
     order (int32 [B][n_kv][n_select], -1 behind them): the first keep_first and last keep_last
     pages, then those whose summaries' dot product with q is largest. A list for
     paged_attention(pages=...)."""
-    _queries(q, kv)
+    Bn, nh, _ = _queries(q, kv)
     if n_select < 1:
         raise ValueError("n_select must be >= 1")
     if out is not None:
-        _need_flat(out, "out", torch.int32, (kv.batch, kv._row[0], n_select), kv.device)
-    return call_on(kv.device, stream, _select, q, kv, n_select, keep_first, keep_last, out)
+        _need_flat(out, "out", _i32, (kv.batch, kv._row[0], n_select), kv.device)
+    return call_on(kv.device, stream, _select, q, kv, Bn, nh, n_select, keep_first, keep_last, out)
 
 
-def _select(st, q, kv, n_select, keep_first, keep_last, out):
-    Bn, nh, _ = q.shape
+def _select(st, q, kv, Bn, nh, n_select, keep_first, keep_last, out):
     if out is None:
-        out = torch.empty((Bn, kv._row[0], n_select), dtype=torch.int32, device=kv.device)
+        out = torch.empty((Bn, kv._row[0], n_select), dtype=_i32, device=kv.device)
     n = kv._ws.get("select")
     if n is None:
-        n = kv._ws["select"] = B.mtp_page_select_workspace(kv.c, Bn)
+        n = kv._ws["select"] = B.mtp_page_select_workspace(kv.p, Bn)
     _with_workspace(kv, st, n, lambda ws, n: B.mtp_page_select(
-        kv.c, q.data_ptr(), Bn, nh, n_select, keep_first, keep_last, out.data_ptr(), ws, n, st))
+        kv.p, q.data_ptr(), Bn, nh, n_select, keep_first, keep_last, out.data_ptr(), ws, n, st))
     return out
