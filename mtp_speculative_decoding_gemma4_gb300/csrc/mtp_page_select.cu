@@ -11,8 +11,8 @@
 // spreads over its counters), then one ordered compaction.
 //
 // What bounds it is that chain: length, table, codes, the cluster barrier, up to 4 digits, the
-// compaction, and the code's own first fetches. One sequence of 1024 pages takes 9 us, 16
-// sequences of 2048 pages (17 MB of codes, 2.5 us at the copy rate) 14 us.
+// compaction, and the code's own first fetches. One sequence of 1024 pages takes 8 us, 16
+// sequences of 2048 pages (17 MB of codes, 2.5 us at the copy rate) about 9.
 #include "mtp_common.cuh"
 #include "mtp_launch.h"
 #include "mtp_paged.cuh"
@@ -73,27 +73,25 @@ __device__ __forceinline__ void quantise(const SelArgs& a, const float* q, int G
 }
 
 // Scores of this CTA's share of n pages: 8 lanes hold a page's codes (VL 16-byte vectors each),
-// 4 pages side by side, U such groups in flight. A warp takes `per` pages at a time, one per lane,
-// and requests its first codes before the query is quantised.
+// 4 pages side by side. A warp takes `per` pages at a time, one per lane, and requests its first
+// codes before the query is quantised. The warps' loads are enough in flight: with two or four
+// groups of pages per warp the longer code costs more than they bring (55 and 53 us against 50
+// with the attention after it, 16 sequences of 2048 pages; 21.3 against 20.4 for one of 1024).
 template <int VL>
 __device__ __forceinline__ void score_pages(const SelArgs& a, int b, int g, int G, int n, int rank, const float* q,
                                             int* codes, float* qs, unsigned* score) {
   const Cache& c = a.c;
-  constexpr int U = VL == 4 ? 2 : 4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, li = lane & 7, nv = c.d >> 4;
   // with few pages every warp of the cluster gets some
   const int warps = a.cl * kSelWarps, per = min(32, (n + warps - 1) / warps);
-  int4 x[U][VL];
+  int4 x[VL];
   int page = -1;
   auto fetch = [&](int i) {
+    const int at = i + (lane >> 3), p = __shfl_sync(0xffffffffu, page, at & 31);
+    const int4* row = reinterpret_cast<const int4*>(c.codes + (static_cast<size_t>(max(p, 0)) * c.nkv + g) * c.d);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int at = i + 4 * u + (lane >> 3), p = __shfl_sync(0xffffffffu, page, at & 31);
-      const int4* row = reinterpret_cast<const int4*>(c.codes + (static_cast<size_t>(max(p, 0)) * c.nkv + g) * c.d);
-#pragma unroll
-      for (int v = 0; v < VL; ++v)
-        x[u][v] = at < per && p >= 0 && li + 8 * v < nv ? __ldcs(row + li + 8 * v) : make_int4(0, 0, 0, 0);
-    }
+    for (int v = 0; v < VL; ++v)
+      x[v] = at < per && p >= 0 && li + 8 * v < nv ? __ldcs(row + li + 8 * v) : make_int4(0, 0, 0, 0);
   };
   bool first = true;
   for (int i0 = (rank * kSelWarps + warp) * per; i0 < n || first; i0 += warps * per) {
@@ -108,39 +106,24 @@ __device__ __forceinline__ void score_pages(const SelArgs& a, int b, int g, int 
     }
     float keep = -INFINITY;
 #pragma unroll 1
-    for (int i = 0; i < per; i += 4 * U) {
+    for (int i = 0; i < per; i += 4) {
       if (i > 0) fetch(i);
-      float s[U], k[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        s[u] = -INFINITY;
-        k[u] = __shfl_sync(0xffffffffu, ks, (i + 4 * u + (lane >> 3)) & 31);
-      }
+      float s = -INFINITY;
+      const float k = __shfl_sync(0xffffffffu, ks, (i + (lane >> 3)) & 31);
 #pragma unroll 1
       for (int h = 0; h < G; ++h) {
-        int dot[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) dot[u] = 0;
+        int dot = 0;
 #pragma unroll
         for (int v = 0; v < VL; ++v) {
           const int4 w = li + 8 * v < nv ? reinterpret_cast<const int4*>(codes)[h * nv + li + 8 * v] : make_int4(0, 0, 0, 0);
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-            dot[u] = __dp4a(x[u][v].x, w.x, __dp4a(x[u][v].y, w.y, __dp4a(x[u][v].z, w.z, __dp4a(x[u][v].w, w.w, dot[u]))));
+          dot = __dp4a(x[v].x, w.x, __dp4a(x[v].y, w.y, __dp4a(x[v].z, w.z, __dp4a(x[v].w, w.w, dot))));
         }
-        const float step = qs[h];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-#pragma unroll
-          for (int o = 4; o > 0; o >>= 1) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], o);
-          s[u] = fmaxf(s[u], __fmul_rn(__fmul_rn(static_cast<float>(dot[u]), step), k[u]));
-        }
+        for (int o = 4; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        s = fmaxf(s, __fmul_rn(__fmul_rn(static_cast<float>(dot), qs[h]), k));
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float v = __shfl_sync(0xffffffffu, s[u], (lane & 3) * 8);
-        if (lane >> 2 == (i >> 2) + u) keep = v;
-      }
+      const float v = __shfl_sync(0xffffffffu, s, (lane & 3) * 8);
+      if (lane >> 2 == i >> 2) keep = v;
     }
     if (page < 0) keep = -INFINITY;
     if (isnan(ks)) keep = INFINITY;  // a page whose keys are not finite is always read
