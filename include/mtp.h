@@ -357,9 +357,10 @@ MTP_API int mtp_set_path(mtp_handle *h, int32_t path);
  * outside [0, n_pages) is no page: its keys are left out (and never read). ctx_len is clamped to
  * [0, max_pages * page_size] on the device. Rows of a page at or past ctx_len are never used,
  * whatever they hold.
- * These calls keep no state, need no handle and use the current device; scratch is the caller's
- * `workspace` (16-byte aligned, not shared by calls that may overlap), sized by the
- * *_workspace call with the same arguments. They may be captured into CUDA graphs. */
+ * Except for the draft block at the end, these calls keep no state, need no handle, use the
+ * current device and may be captured into CUDA graphs. Scratch is the caller's `workspace`
+ * (16-byte aligned, not shared by calls that may overlap), sized by the *_workspace call with the
+ * same arguments. */
 typedef struct mtp_paged_kv {
   void *k;                    /* device, model dtype */
   void *v;                    /* device, the layout of k, or NULL (V = K) */
