@@ -227,7 +227,7 @@ struct Lay {
   static constexpr int box = KT * 128;                  // KT keys x 64 dims
   static constexpr int slot = 2 * box;
   static constexpr int ring = kRingBytes / slot;        // 6 or 12 slots
-  static constexpr int RB = NH == 4 ? 2048 : 3072;      // bytes of one 64-element block of the N side
+  static constexpr int RB = (NH == 4 ? 16 : 24) * 128;  // bytes of one 64-element block of the N side (3 NH rows, whole swizzle blocks)
   static constexpr int QB = D == 512 ? 1 : 2;           // query buffers
   static constexpr int PBY = KT / 64 * RB;              // bytes of one probability buffer
   static constexpr int q = kRingBytes;
