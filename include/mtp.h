@@ -408,9 +408,11 @@ MTP_API int mtp_page_plan(const int32_t *old_len, const int32_t *new_len, int32_
 /* Writes T rows into their slots: row t of k_new (and of v_new when the cache has a V) to slot
  * slot_map[t]; rows whose slot is outside [0, n_pages * P) are skipped. When the cache has
  * summaries, every page whose last slot is written gets its summary from all P rows it then
- * holds: per KV head m = the mean key rounded to fp32, scale = fl32(max |m| * fl32(1 / 127)),
- * codes = rint(fl32(m / scale)); a mean that is not finite gives scale NaN and codes 0. A slot
- * may occur once in slot_map; T <= 2^30.
+ * holds: per KV head m = the mean key in fp32, scale = fl32(max |m| * fl32(1 / 127)),
+ * codes = rint(fl32(m / scale)); a mean that is not finite gives scale NaN and codes 0. The mean
+ * of a bf16 dimension whose non-zero values lie within 2^24 of one another is exact, rounded once,
+ * whatever the order of the rows and calls; otherwise it is off by at most 2^-24 of itself and
+ * P^2 2^-48 of the dimension's largest value (and, from fp32 values below 2^-118, 2^-142). A slot may occur once in slot_map; T <= 2^30.
  *   k_new, v_new device rows of [n_kv][head_dim], model dtype, row_stride_k / row_stride_v
  *                elements apart (>= n_kv * head_dim, multiples of 16 bytes), not in the cache
  *   slot_map     device [T] int32

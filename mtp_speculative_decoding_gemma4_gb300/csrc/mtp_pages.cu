@@ -212,16 +212,20 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(const __grid_constan
 //   m = fl32(mean of the page's P rows), scale = fl32(max |m| * fl32(1 / 127)),
 //   code = rint(fl32(m / scale)); a page whose mean is not finite gets scale NaN and codes 0.
 // Every row enters as x / P (a power of two: exact), so that no sum leaves the range that the mean
-// lies in. The sum is kept as an unevaluated pair of fp32 (two-sum, 6 operations a value); bf16
-// rows are first added four at a time in fp32, which rounds nothing unless the four differ by more
-// than 2^14, and then less than 2^-24 of their largest. So but for such spreads m is the exact
-// mean, rounded, in any order of the rows, and the arithmetic stays below the copy. The page's
-// other rows are read where this call does not write: rows of this call in another order from
-// k_new, older ones from the cache; so one launch does. What bounds it is the copy: each row read
-// and written once, 134 MB for two prompts of 32768 rows at d = 512 in 25 us (5.3 TB/s).
-__device__ __forceinline__ void two_sum(float& hi, float& lo, float x) {
-  const float s = __fadd_rn(hi, x), bb = __fsub_rn(s, hi);
-  lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, bb)), __fsub_rn(x, bb)));
+// lies in. The sum is an unevaluated pair of fp32: hi, and in lo the running sum of what each
+// addition to hi rounded away (two-sum, 7 operations a value with the scaling). lo loses nothing
+// while the values' spread is below 2^24 (bf16, any P): m is then the exact mean, rounded once, in
+// any order of the rows. Beyond that, and in fp32, lo's own roundings add at most P^2 2^-48 of the
+// largest value. The page's other rows are read where this call does not write: rows of this call
+// in another order from k_new, older ones from the cache; so one launch does. What bounds it is the
+// copy: each row read and written once, 134 MB for two prompts of 32768 rows at d = 512 in 25 us
+// (5.3 TB/s). Four bf16 rows added in fp32 before they enter the pair would take 0.2 us less, but
+// lose the mean where large values cancel.
+
+// hi + lo += x * f (f a power of two)
+__device__ __forceinline__ void two_sum(float& hi, float& lo, float x, float f) {
+  const float s = __fmaf_rn(x, f, hi), bb = __fsub_rn(s, hi);
+  lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, bb)), __fmaf_rn(x, f, -bb)));
   hi = s;
 }
 constexpr int kAppThreads = 256, kAppRows = 64;  // threads, most rows of a CTA's share
@@ -329,26 +333,7 @@ __global__ void __launch_bounds__(kAppThreads, 4) k_page_append_sum(const __grid
         float x[VE];
         load_vec(reinterpret_cast<const T*>(&u), x);
 #pragma unroll
-        for (int e = 0; e < VE; ++e) two_sum(hi[e], lo[e], __fmul_rn(x[e], part_of));
-      };
-      auto add4 = [&](const uint4 (&u)[4]) {  // rows that are not there are zero
-        if (VE == 4) {                        // fp32 rows
-#pragma unroll
-          for (int i = 0; i < 4; ++i) add(u[i]);
-        } else {
-          float x[VE], y[VE];
-          load_vec(reinterpret_cast<const T*>(&u[0]), x);
-#pragma unroll
-          for (int e = 0; e < VE; ++e) x[e] = __fmul_rn(x[e], part_of);
-#pragma unroll
-          for (int i = 1; i < 4; ++i) {
-            load_vec(reinterpret_cast<const T*>(&u[i]), y);
-#pragma unroll
-            for (int e = 0; e < VE; ++e) x[e] = __fmaf_rn(y[e], part_of, x[e]);
-          }
-#pragma unroll
-          for (int e = 0; e < VE; ++e) two_sum(hi[e], lo[e], x[e]);
-        }
+        for (int e = 0; e < VE; ++e) two_sum(hi[e], lo[e], x[e], part_of);
       };
       if (on) {
         const long long at = (page * c.sp + (off + r0) * c.st + h * c.sh) / VE + (v - hv * a.vph);
@@ -362,7 +347,10 @@ __global__ void __launch_bounds__(kAppThreads, 4) k_page_append_sum(const __grid
 #pragma unroll
             for (int u = 0; u < 4; ++u)
               if (r + u * par < len) to[u * st] = x[u];
-            if (sum) add4(x);
+            if (sum) {
+#pragma unroll
+              for (int u = 0; u < 4; ++u) add(x[u]);  // rows that are not there are zero
+            }
             from += 4 * step;
             to += 4 * st;
           }
@@ -393,7 +381,7 @@ __global__ void __launch_bounds__(kAppThreads, 4) k_page_append_sum(const __grid
         for (int e = 0; e < VE; ++e) {
           float x = part[0][e * kAppThreads + tid], l = part[1][e * kAppThreads + tid];
           for (int r = 1; r < par; ++r) {
-            two_sum(x, l, part[0][e * kAppThreads + tid + r * cols]);
+            two_sum(x, l, part[0][e * kAppThreads + tid + r * cols], 1.f);
             l += part[1][e * kAppThreads + tid + r * cols];
           }
           m[e] = __fadd_rn(x, l);

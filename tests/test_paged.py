@@ -806,3 +806,71 @@ def test_sizes_past_the_limits_are_refused_before_the_device(lib):
         assert lib.mtp_paged_attention(kv, q, 1, 4, 0, scale, None, 0, out, lse, FAKE, 1 << 30,
                                        None) == B.MTP_ERR_INVALID_ARG
         assert B.mtp_last_error()
+
+
+# ---------------------------------------------------------------- summaries of pages of large spread
+
+
+def _cancelling(rs, P, d):
+    """Rows of values of size 2^-3 to 4 and, in about half of the places, pairs of -2^20 and 2^20:
+    a spread below 2^24, so that a mean is the rounded sum, whatever its order."""
+    x = rs.choice([-1, 1], (P, d)) * 2.0 ** rs.uniform(-2.9, 2, (P, d))
+    for j in range(d):
+        at = rs.permutation(P)[:2 * (P // 4)]
+        x[at[::2], j], x[at[1::2], j] = 2.0 ** 20, -2.0 ** 20
+    return torch.from_numpy(x.astype(np.float32)).bfloat16()
+
+
+@gpu
+@pytest.mark.parametrize("n_kv,d", [(1, 512), (1, 64), (2, 128), (3, 200)])
+@pytest.mark.parametrize("P", [4, 16, 32, 256])
+def test_summaries_where_large_values_cancel(P, n_kv, d):
+    # the mean rounded once: exact sums in 64 bits have one value, so codes and scales are equal
+    # bit by bit, for pages written whole, in two calls, and row by row in any order of one call
+    from mtp_speculative_decoding_gemma4_gb300 import page_append
+    rs = np.random.RandomState(P + d)
+    n = 3
+    c = Case(1, [1], P, n_kv, n_kv, d, "bf16", spare=n + 1)
+    m = c.k.shape[0]
+    rows = _cancelling(rs, n * P, n_kv * d).view(n * P, n_kv, d)
+    want = [[OP.page_summary(rows[p * P:(p + 1) * P, g].float().numpy()) for g in range(n_kv)] for p in range(n)]
+    slots = np.arange(n * P, dtype=np.int32)
+    cut = slots % P < max(1, P // 3)
+    for how in ("whole", "two calls", "any order"):
+        parts = {"whole": [slots], "two calls": [slots[cut], slots[~cut]], "any order": [rs.permutation(slots)]}[how]
+        codes, scales = torch.zeros((m, n_kv, d), dtype=torch.int8).cuda(), torch.zeros((m, n_kv)).cuda()
+        kv = c.kv(codes=codes, scales=scales)
+        for at in parts:
+            page_append(kv, rows[torch.from_numpy(at.astype(np.int64))].contiguous().cuda(), _dev(at))
+        for p in range(n):
+            for g in range(n_kv):
+                np.testing.assert_array_equal(codes[p, g].cpu().numpy(), want[p][g][0], err_msg=f"{how}, page {p}")
+                np.testing.assert_array_equal(scales[p, g].cpu().numpy(), want[p][g][1], err_msg=f"{how}, page {p}")
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("P", [8, 32, 256])
+def test_summaries_of_any_spread_stay_within_the_bound(dtype, P):
+    # beyond that spread a mean is off by at most 2^-24 of itself and P^2 2^-48 of the largest
+    # value (the sum's running errors, each 2^-24 of a partial sum, are summed in fp32). One
+    # dimension of a page holds values, so the scale is |m| / 127, rounded twice more.
+    from mtp_speculative_decoding_gemma4_gb300 import page_append
+    import math
+    rs = np.random.RandomState(P)
+    n, d = 200, 8
+    c = Case(1, [1], P, 1, 1, d, dtype, spare=n)
+    rows = torch.zeros((n * P, 1, d))
+    rows[:, 0, 0] = torch.from_numpy((rs.choice([-1, 1], n * P) * 2.0 ** rs.uniform(-30, 30, n * P)).astype(np.float32))
+    rows = rows.to(c.k.dtype)
+    for p in range(n):  # the largest values come in pairs that cancel
+        x = rows[p * P:(p + 1) * P, 0, 0]
+        order = x.abs().argsort(descending=True)
+        x[order[1:P // 2:2]] = -x[order[0:P // 2:2]][:len(order[1:P // 2:2])]
+    codes, scales = torch.zeros((n + 1, 1, d), dtype=torch.int8).cuda(), torch.zeros((n + 1, 1)).cuda()
+    page_append(c.kv(codes=codes, scales=scales), rows.cuda(), _dev(np.arange(n * P, dtype=np.int32)))
+    got = scales.cpu().double().numpy()[:, 0] * 127
+    for p in range(n):
+        x = rows[p * P:(p + 1) * P, 0, 0].double().tolist()
+        mean, most = math.fsum(x) / P, max(map(abs, x))
+        assert abs(got[p] - abs(mean)) <= 4 * 2.0 ** -24 * abs(mean) + P * P * 2.0 ** -48 * most, p
