@@ -412,7 +412,8 @@ MTP_API int mtp_page_plan(const int32_t *old_len, const int32_t *new_len, int32_
  * codes = rint(fl32(m / scale)); a mean that is not finite gives scale NaN and codes 0. The mean
  * of a bf16 dimension whose non-zero values lie within 2^24 of one another is exact, rounded once,
  * whatever the order of the rows and calls; otherwise it is off by at most 2^-24 of itself and
- * P^2 2^-48 of the dimension's largest value (and, from fp32 values below 2^-118, 2^-142). A slot may occur once in slot_map; T <= 2^30.
+ * P^2 2^-48 of the dimension's largest value (and, from fp32 values below 2^-118, 2^-142). A slot
+ * may occur once in slot_map; T <= 2^30.
  *   k_new, v_new device rows of [n_kv][head_dim], model dtype, row_stride_k / row_stride_v
  *                elements apart (>= n_kv * head_dim, multiples of 16 bytes), not in the cache
  *   slot_map     device [T] int32
@@ -425,8 +426,10 @@ MTP_API int mtp_page_append(const mtp_paged_kv *kv, const void *k_new, const voi
  * positions: [0, L), the last `window` of them when window > 0, and with `pages` only those in
  * the listed logical pages of the head's KV head (entries outside the sequence's pages are
  * skipped; a page listed twice counts twice). fp32 arithmetic; bf16 keys enter exactly. A
- * sequence with nothing to attend gets out 0 and lse -inf. What is not attended may hold anything;
- * an attended row or a query that is not finite makes the outputs it reaches NaN or infinite. Query head h reads KV head
+ * sequence with nothing to attend gets out 0 and lse -inf. What is not attended may hold anything.
+ * Where an attended row or the query is not finite, or a score leaves the range of fp32, the
+ * outputs that it reaches are NaN, infinite, or those without the keys of score -inf; a sequence
+ * whose every attended key scores -inf gets NaN. Query head h reads KV head
  * h / (n_head / n_kv_head).
  *   q         device [B][n_head][head_dim] fp32
  *   pages     device [B][n_kv_head][n_list] int32 or NULL

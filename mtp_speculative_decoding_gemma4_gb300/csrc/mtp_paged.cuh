@@ -8,6 +8,8 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <cfloat>
+#include <cmath>
 
 #include "mtp.h"
 #include "mtp_launch.h"
@@ -42,6 +44,12 @@ __device__ __forceinline__ int phys_page(const Cache& c, int b, int lp) {
   const int page = __ldg(c.table + static_cast<size_t>(b) * c.table_stride + lp);
   return static_cast<unsigned>(page) < static_cast<unsigned>(c.n_pages) ? page : -1;
 }
+
+// An attended key of score -inf enters as the lowest finite score: beside other keys it has no
+// weight, and a row of such keys alone (0 / 0: NaN) is told from one with nothing to attend.
+__device__ __forceinline__ float attended(float score) { return score == -INFINITY ? -FLT_MAX : score; }
+// The exp-sum `den` of a row whose largest score is M, as its outputs are divided by it.
+__device__ __forceinline__ float row_sum(float M, float den) { return M == -FLT_MAX ? NAN : den; }
 
 // Lets a kernel use BYTES of dynamic shared memory, asked of the driver once per device.
 template <auto kernel, int BYTES>

@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kAttWarps * 32) k_paged_att(const __grid_const
     bool mine = false;
 #pragma unroll
     for (int u = 0; u < U; ++u) mine = mine || (su == u && on[u]);
-    const float x0 = mine ? s[0] * a.scale_log2 : -INFINITY;
+    const float x0 = mine ? attended(s[0] * a.scale_log2) : -INFINITY;
     float mn = x0;
 #pragma unroll
     for (int o = GP * DUP; o < LPK; o <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
@@ -233,6 +233,7 @@ __global__ void __launch_bounds__(kAttWarps * 32) k_paged_att(const __grid_const
     }
     const size_t row = static_cast<size_t>(b) * a.nh + h0 + h;
     if (a.nsplit == 1) {
+      den = row_sum(M, den);
       a.out[row * d + e] = den == 0.f ? 0.f : num / den;  // 0: nothing attended
       if (a.lse && e == 0) a.lse[row] = den == 0.f ? -INFINITY : (M + log2f(den)) * 0.6931471805599453f;
     } else {
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(256) k_paged_join(const __grid_constant__ AttA
     den = warp_sum(den);
     if (tid == 0) {
       s_m = M;
-      s_den = den;
+      s_den = row_sum(M, den);
     }
   }
   __syncthreads();

@@ -743,7 +743,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         bool up = false;
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-          sc[h] = on ? sc[h] * a.scale_log2 : -INFINITY;
+          sc[h] = on ? pg::attended(sc[h] * a.scale_log2) : -INFINITY;
           up = up || (on && !(sc[h] <= m[h] + 8.f));  // NaN counts
         }
         int any;
@@ -882,6 +882,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         for (int h = 0; h < NH; ++h) {
           if (h >= nh) break;
           if (whole) {
+            den[h] = pg::row_sum(m[h], den[h]);
             const float inv = den[h] == 0.f ? 0.f : 1.f / den[h];  // 0: nothing attended
 #pragma unroll
             for (int b = 0; b < NP; ++b) a.out[(row0 + h) * D + b * 128 + wt] = acc[b][h] * inv;
@@ -965,6 +966,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       x.z = fmaf(f[j], y[j].z, x.z);
       x.w = fmaf(f[j], y[j].w, x.w);
     }
+    den = pg::row_sum(M, den);
     const float inv = den == 0.f ? 0.f : 1.f / den;
     reinterpret_cast<float4*>(a.out + row0 * D)[i] = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
     if (a.lse && i % (D / 4) == 0) a.lse[row0 + h] = den == 0.f ? -INFINITY : (M + log2f(den)) * 0.6931471805599453f;
@@ -1012,7 +1014,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_tc_join(const __grid_con
     den = warp_sum(den);
     if (lane == 0) {
       sm[warp] = M;
-      sden[warp] = den;
+      sden[warp] = pg::row_sum(M, den);
     }
   }
   __syncthreads();

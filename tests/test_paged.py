@@ -874,3 +874,50 @@ def test_summaries_of_any_spread_stay_within_the_bound(dtype, P):
         x = rows[p * P:(p + 1) * P, 0, 0].double().tolist()
         mean, most = math.fsum(x) / P, max(map(abs, x))
         assert abs(got[p] - abs(mean)) <= 4 * 2.0 ** -24 * abs(mean) + P * P * 2.0 ** -48 * most, p
+
+
+# ---------------------------------------------------------------- scores below the range of fp32
+
+
+@gpu
+@pytest.mark.parametrize("own_v", [False, True])
+@pytest.mark.parametrize("n_kv,d,dtype,cols", [(1, 64, "bf16", 8), (2, 32, "f32", 8), (1, 64, "f32", 600),
+                                               (1, 128, "bf16", 8), (2, 256, "bf16", 300), (1, 512, "bf16", 8)])
+def test_keys_of_score_minus_infinity_are_not_an_empty_sequence(n_kv, d, dtype, cols, own_v):
+    # every attended key scores -inf (0 / 0): NaN, not the 0 and -inf of nothing to attend; the
+    # other sequences keep their values
+    from mtp_speculative_decoding_gemma4_gb300 import paged_attention
+    P = 16
+    c = Case(d, [0, 3, 40, min(cols * P, 5000)], P, 2 * n_kv, n_kv, d, dtype, cols=cols, own_v=own_v)
+    want = c.want()
+    for b in (1, 3):
+        c.q[b, :, 0] = 1 + 2.0 ** -9 + 2.0 ** -18  # three terms of one sign
+        for lp in range(-(-int(c.L[b]) // P)):
+            c.dk[int(c.table[b, lp]), :, :, 0] = float("-inf")
+    for window in (0, 2):
+        out, lse = (x.cpu() for x in paged_attention(c.q.cuda(), c.kv(), window=window, want_lse=True))
+        for b in (1, 3):
+            assert not torch.isfinite(out[b, :, 0]).any() and torch.isnan(lse[b]).all()
+            if own_v:
+                assert torch.isnan(out[b]).all()
+        if window == 0:
+            assert np.max(np.abs(out[2].numpy() - want[0][2])) <= ATT_TOL
+            assert np.max(np.abs(lse[2].numpy() - want[1][2])) <= ATT_TOL
+        assert (out[0] == 0).all() and torch.isneginf(lse[0]).all()
+
+
+@gpu
+def test_one_key_of_score_minus_infinity_has_no_weight():
+    from mtp_speculative_decoding_gemma4_gb300 import paged_attention
+    c = Case(1, [50], 16, 2, 1, 64, "f32", own_v=True)
+    c.q[0, :, 0] = 1
+    page = int(c.table[0, 0])
+    c.dk[page, 3, 0, 0] = float("-inf")
+    k = c.k.double().numpy()
+    keep = [t for t in range(50) if t != 3]
+    s = c.q[0].double().numpy() @ np.stack([k[c.table[0, t // 16], t % 16, 0] for t in keep]).T / 8
+    v = np.stack([c.v[int(c.table[0, t // 16]), t % 16, 0].double().numpy() for t in keep])
+    p = np.exp(s - s.max(1, keepdims=True))
+    out, lse = paged_attention(c.q.cuda(), c.kv(), want_lse=True)
+    assert np.max(np.abs(out[0].cpu().numpy() - p @ v / p.sum(1, keepdims=True))) <= ATT_TOL
+    assert np.max(np.abs(lse[0].cpu().numpy() - (s.max(1) + np.log(p.sum(1))))) <= ATT_TOL
