@@ -16,7 +16,8 @@
 // three bf16 terms (hi + mid + lo, exact), N = 3 columns per head, so every product is exact and
 // the sums are fp32. The tensor-memory adder truncates, so no chain is long: scores accumulate
 // 128 dims (8 instructions), sums 128 keys, and the parts are added in registers, rounded to
-// nearest.
+// nearest; a score's parts term by term, so that a part of the first term does not round away what
+// the last term adds in another.
 //
 // Work split: the granules (32 to 128 keys) of all (sequence, KV head, head group) units are
 // numbered through and dealt evenly over one CTA per SM, whatever the lengths; a unit's beginning
@@ -726,17 +727,20 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         wait_bar(sfull0 + 8 * wg, own & 1, dead);
         __syncwarp();
         fence_after();
-        float sc[NH];
+        // the terms' parts of 128 dims, term by term
+        float sc[3 * NH];
+        ld_terms<NH>(tS, sc);
+        ld_wait();
 #pragma unroll
-        for (int h = 0; h < NH; ++h) sc[h] = 0.f;
-#pragma unroll
-        for (int b = 0; b < NP; ++b) {
+        for (int b = 1; b < NP; ++b) {
           float v[3 * NH];
           ld_terms<NH>(tS + b * N, v);
           ld_wait();
 #pragma unroll
-          for (int h = 0; h < NH; ++h) sc[h] += (v[2 * NH + h] + v[NH + h]) + v[h];
+          for (int i = 0; i < 3 * NH; ++i) sc[i] += v[i];
         }
+#pragma unroll
+        for (int h = 0; h < NH; ++h) sc[h] += sc[2 * NH + h] + sc[NH + h];
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(sfree0 + 8 * wg);

@@ -1,6 +1,7 @@
 """Paged-cache operators: the page plan, the append with page summaries, the selection of pages
 and the attention of one new token, against the NumPy forms; refusals without a device."""
 import ctypes
+import math
 
 import numpy as np
 import pytest
@@ -856,7 +857,6 @@ def test_summaries_of_any_spread_stay_within_the_bound(dtype, P):
     # value (the sum's running errors, each 2^-24 of a partial sum, are summed in fp32). One
     # dimension of a page holds values, so the scale is |m| / 127, rounded twice more.
     from mtp_speculative_decoding_gemma4_gb300 import page_append
-    import math
     rs = np.random.RandomState(P)
     n, d = 200, 8
     c = Case(1, [1], P, 1, 1, d, dtype, spare=n)
@@ -921,3 +921,63 @@ def test_one_key_of_score_minus_infinity_has_no_weight():
     out, lse = paged_attention(c.q.cuda(), c.kv(), want_lse=True)
     assert np.max(np.abs(out[0].cpu().numpy() - p @ v / p.sum(1, keepdims=True))) <= ATT_TOL
     assert np.max(np.abs(lse[0].cpu().numpy() - (s.max(1) + np.log(p.sum(1))))) <= ATT_TOL
+
+
+# ---------------------------------------------------------------- the three terms
+
+
+def _terms(x):
+    """The three bf16 terms of fp32 values."""
+    hi = x.bfloat16().float()
+    mid = (x - hi).bfloat16().float()
+    return hi, mid, x - hi - mid
+
+
+@gpu
+@pytest.mark.parametrize("n_head", [4, 8])
+@pytest.mark.parametrize("d", [128, 256, 512])
+def test_the_last_bits_of_a_query_count(d, n_head):
+    # two dims whose keys are equal and whose query values differ in the third bf16 term alone: the
+    # first two terms' products cancel exactly in any order, so a score is the third term's
+    # product, about 8, rounded twice (it and its scale): 2^-22 of 8. Without it every score is 0.
+    from mtp_speculative_decoding_gemma4_gb300 import paged_attention
+    c = Case(d, [40, 300, 16], 16, n_head, 1, d, "bf16", own_v=True)
+    g = torch.Generator().manual_seed(d)
+    x = (1 + torch.rand((3, n_head), generator=g)) * 2.0 ** 20 * math.sqrt(d)
+    hi, mid, lo = _terms(x)
+    c.q.zero_()
+    at = 3 * (d // 4)
+    c.q[:, :, at], c.q[:, :, 5] = x, -(hi + mid)
+    assert lo.abs().max() >= 2.0 ** 3
+    for kk in (c.k, c.dk):
+        kk[..., at] = kk[..., 5]
+    out, lse = paged_attention(c.q.cuda(), c.kv(), want_lse=True)
+    want = c.want()
+    # |k| <= 5 and |lo| <= 2^-17 x <= 2^4 sqrt(d): scores up to 80, off by 2^-22 of that
+    tol = ATT_TOL + 80 * 2.0 ** -22 * 4
+    assert np.max(np.abs(out.cpu().numpy() - want[0])) <= tol
+    assert np.max(np.abs(lse.cpu().numpy() - want[1])) <= tol
+
+
+@gpu
+@pytest.mark.parametrize("n_head", [4, 8])
+@pytest.mark.parametrize("d", [128, 256, 512])
+def test_the_last_bits_of_a_probability_count(d, n_head):
+    # two keys of values 1 and -1 and scores s in (-1, 0) and 0: out = (p - 1) / (p + 1) at p = e^s. p is
+    # off by its exponent's two roundings and exp2f's 2 units (3 2^-23 in all), the sums and the
+    # quotient by 3 2^-24: below 2^-20. Without the third term p is off by up to 2^-17.
+    from mtp_speculative_decoding_gemma4_gb300 import paged_attention
+    Bn = 64
+    c = Case(d, [2] * Bn, 16, n_head, 1, d, "bf16", own_v=True)
+    c.q.zero_()
+    c.q[:, :, 9] = -torch.rand((Bn, n_head), generator=torch.Generator().manual_seed(d))
+    for b in range(Bn):
+        page = int(c.table[b, 0])
+        for kk in (c.k, c.dk):
+            kk[page, :2] = 0
+            kk[page, 0, 0, 9] = 1
+        for vv in (c.v, c.dv):
+            vv[page, 0], vv[page, 1] = 1, -1
+    out, _ = paged_attention(c.q.cuda(), c.kv(), scale=1.0, want_lse=True)
+    p = np.exp(c.q[:, :, 9].double().numpy())
+    assert np.max(np.abs(out.cpu().numpy() - ((p - 1) / (p + 1))[..., None])) <= 2.0 ** -20
