@@ -19,6 +19,7 @@ namespace pg {
 
 constexpr int kMaxSms = 160;  // grids and workspaces are sized for at most this many SMs
 constexpr int kPlanMaxB = 8192;  // sequences of a page plan
+constexpr long long kSpin = 4000000000LL;  // bound of a device wait, about 2 s of clock64 cycles
 
 // A validated mtp_paged_kv, in the form the kernels take.
 struct Cache {
@@ -96,6 +97,9 @@ struct AttArgs {
   float* ws_acc;            // partial sums of the splits
   float* ws_ml;             // their (max, exp-sum)
   float scale_log2;         // softmax scale * log2(e)
+  int* status;              // gets MTP_ERR_TIMEOUT when a device wait gives up, or null
+  long long spin;           // bound of the device waits, in clock64 cycles
+  int skip;                 // testing: the tensor-core kernel looks up no page of this sequence (-1: none)
   int B, nh, n_list, window, nsplit;
 };
 

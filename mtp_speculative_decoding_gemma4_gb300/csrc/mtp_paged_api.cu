@@ -245,6 +245,8 @@ int mtp_paged_attention(const mtp_paged_kv* kv, const float* q, int32_t B, int32
   a.B = B;
   a.nh = n_head;
   a.window = window;
+  a.spin = pg::kSpin;
+  a.skip = -1;
   int sms = 0;
   if ((rc = pg::sm_count(&sms))) return rc;
   return run_paged_att(a, workspace, sms, static_cast<cudaStream_t>(stream));

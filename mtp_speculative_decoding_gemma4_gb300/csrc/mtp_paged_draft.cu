@@ -80,6 +80,9 @@ int run_paged_layer(const Params& p, const PagedCall& pc, int l, __nv_bfloat16* 
   a.B = B;
   a.nh = p.s.nh;
   a.window = t == 0 ? p.s.W : 0;
+  a.status = p.w.status;
+  a.spin = p.spin_limit;
+  a.skip = l == 0 ? p.dbg_skip - 1 : -1;
   if (t == 1 && pc.n_select > 0) {
     if ((rc = run_page_select(a.c, pc.qn, B, p.s.nh, pc.n_select, pc.keep_first, pc.keep_last, pc.sel, pc.sel_ws,
                               pc.num_sms, st)))

@@ -39,7 +39,8 @@
 // only when a score exceeds it by 2^8 (one barrier per tile agrees on that), so running sums are
 // rarely rescaled.
 // Rows that hold no attended key but lie in an attended page are set to zero before the sums
-// (0 * NaN would not vanish). Waits are bounded; a CTA that gives up writes NaN.
+// (0 * NaN would not vanish). Waits are bounded; a CTA that gives up writes NaN and reports it in
+// the caller's status word, if there is one.
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -54,6 +55,7 @@ namespace pgt {
 
 using pg::AttArgs;
 using pg::Cache;
+using pg::kSpin;
 
 constexpr int kRingBytes = 192 * 1024;     // loaded keys
 constexpr int kThreadsTc = 352;            // two warpgroups for the softmax; load, MMA and find warps
@@ -61,7 +63,6 @@ constexpr int kCluster = 8;                // CTAs of a unit in the clustered fo
 constexpr int kClusterBytes = 256 * 1024;  // most keys of one of them
 constexpr int kAhead = 8;                  // tiles that the find warp runs ahead of the load warp
 constexpr int kInfo = 2 * kAhead;          // tiles whose pages and positions are kept
-constexpr long long kSpin = 4000000000LL;  // about 2 s
 
 struct Args {
   AttArgs a;
@@ -102,19 +103,19 @@ __device__ __forceinline__ bool try_wait(unsigned bar, unsigned parity) {
   return ok != 0;
 }
 // Bounded wait; false when this CTA has given up (the word `dead`) or gives up here.
-__device__ __noinline__ bool wait_slow(unsigned bar, unsigned parity, volatile int* dead) {
+__device__ __noinline__ bool wait_slow(unsigned bar, unsigned parity, volatile int* dead, long long limit) {
   const long long t0 = clock64();
   while (!try_wait(bar, parity)) {
     if (*dead) return false;
-    if (clock64() - t0 > kSpin) {
+    if (clock64() - t0 > limit) {
       *dead = 1;
       return false;
     }
   }
   return true;
 }
-__device__ __forceinline__ bool wait_bar(unsigned bar, unsigned parity, volatile int* dead) {
-  return test_wait(bar, parity) || wait_slow(bar, parity, dead);
+__device__ __forceinline__ bool wait_bar(unsigned bar, unsigned parity, volatile int* dead, long long limit) {
+  return test_wait(bar, parity) || wait_slow(bar, parity, dead, limit);
 }
 __device__ __forceinline__ void tma_4d(unsigned dst, const CUtensorMap* map, int x, int t, int h, int page, unsigned bar,
                                        unsigned long long policy) {
@@ -430,6 +431,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     bool ok = true;
     Walk::Seg s;
     while (ok && w.next(g, subs, s)) {
+      if (s.b == a.skip) {  // testing: the other warps wait for these tiles until they give up
+        ok = false;
+        break;
+      }
       const int kvh = s.kvh, i1 = w.end(g, s);
       const int* list = a.list ? a.list + (static_cast<size_t>(s.b) * c.nkv + kvh) * a.n_list : nullptr;
 #pragma unroll 1
@@ -456,7 +461,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           if (tt >= kAhead) {
             const long long t0 = clock64();
             while (*begun < tt - kAhead + 1 && ok) {
-              if (*dead || clock64() - t0 > kSpin) {
+              if (*dead || clock64() - t0 > a.spin) {
                 *dead = 1;
                 ok = false;
               }
@@ -478,7 +483,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     if (ok) {  // the end
       if (tt >= kAhead) {
         const long long t0 = clock64();
-        while (*begun < tt - kAhead + 1 && !*dead && clock64() - t0 < kSpin) {
+        while (*begun < tt - kAhead + 1 && !*dead && clock64() - t0 < a.spin) {
         }
       }
       __syncwarp();
@@ -498,14 +503,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       unsigned phase = 0;
       bool ok = true;
       for (int tt = 0; ok; ++tt) {
-        if (!wait_bar(ifull0 + 8 * (tt % kInfo), (tt / kInfo) & 1, dead)) break;
+        if (!wait_bar(ifull0 + 8 * (tt % kInfo), (tt / kInfo) & 1, dead, a.spin)) break;
         const int* in = info + (tt % kInfo) * 33;
         const int kvh = in[32];
         if (kvh < 0) break;
 #pragma unroll 1
         for (int j = 0; j < PT; ++j) {
           const unsigned bar = full0 + 8 * slot;
-          if (pc >= kRing && !wait_bar(empty0 + 8 * slot, phase ^ 1, dead)) {
+          if (pc >= kRing && !wait_bar(empty0 + 8 * slot, phase ^ 1, dead, a.spin)) {
             ok = false;
             break;
           }
@@ -568,7 +573,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           const int wp = owner & 1, use = wp ? np1 : np0;
           if (test_wait(pfull0 + 8 * wp, use & 1) && (use == 0 || test_wait(ofree0 + 8 * wp, (use - 1) & 1))) {
             if (own_v)
-              for (int i = 0; i < NP; ++i) wait_bar(full0 + 8 * (sp + i), fp, dead);
+              for (int i = 0; i < NP; ++i) wait_bar(full0 + 8 * (sp + i), fp, dead, a.spin);
             fence_after();
             const unsigned v0 = vd + sp * (LY::slot >> 4), p0 = pd + wp * (LY::PBY >> 4), d = tO + wp * NP * N;
 #pragma unroll
@@ -626,7 +631,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           t0 = clock64();
         } else if (*dead) {
           break;
-        } else if (clock64() - t0 > kSpin) {
+        } else if (clock64() - t0 > a.spin) {
           *dead = 1;
           break;
         }
@@ -702,7 +707,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         for (int b = 0; b < NP; ++b) acc[b][h] = 0.f;
       }
       auto take_o = [&](int use) {  // the sums of this warpgroup's tile `use`
-        wait_bar(ofull0 + 8 * wg, use & 1, dead);
+        wait_bar(ofull0 + 8 * wg, use & 1, dead, a.spin);
         __syncwarp();
         fence_after();
 #pragma unroll
@@ -721,10 +726,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 #pragma unroll 1
       for (int t = wg; t < nt; t += 2, ++own) {
         const int at = tt + t;
-        wait_bar(ifull0 + 8 * (at % kInfo), (at / kInfo) & 1, dead);
+        wait_bar(ifull0 + 8 * (at % kInfo), (at / kInfo) & 1, dead, a.spin);
         const int pb = has ? info[(at % kInfo) * 33 + (key >> rs)] : -1, pos = pb + (key & ((1 << rs) - 1));
         const bool on = pb >= 0 && pos >= s.lo && pos < s.hi;
-        wait_bar(sfull0 + 8 * wg, own & 1, dead);
+        wait_bar(sfull0 + 8 * wg, own & 1, dead, a.spin);
         __syncwarp();
         fence_after();
         // the terms' parts of 128 dims, term by term
@@ -794,7 +799,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 #pragma unroll 1
             for (int j = 0; j < NP; ++j) {
               const int pc = at * PT + (own_v ? NP : 0) + j, slot = pc % kRing;
-              if (own_v && !wait_bar(full0 + 8 * slot, (pc / kRing) & 1, dead)) break;
+              if (own_v && !wait_bar(full0 + 8 * slot, (pc / kRing) & 1, dead, a.spin)) break;
 #pragma unroll
               for (int x = 0; x < 16; ++x)
                 *reinterpret_cast<uint4*>(sm + slot * LY::slot + (x >> 3) * LY::box + key * 128 + (x & 7) * 16) =
@@ -866,15 +871,16 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       const int h0 = s.kvh * G + s.hg * NH, nh = min(NH, G - s.hg * NH);
       const size_t row0 = static_cast<size_t>(s.b) * a.nh + h0;
       if (g.clustered) {
-        // the ring is idle: every copy has landed and every product of this CTA's one segment is done
-        float* part = reinterpret_cast<float*>(sm);
+        // the ring is idle: every copy has landed and every product of this CTA's one segment is
+        // done. (Unless a wait gave up: then the exp-sums are NaN, and no copy comes to where they are.)
+        float *part = reinterpret_cast<float*>(sm), *ml = reinterpret_cast<float*>(sm + LY::p);
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
 #pragma unroll
           for (int b = 0; b < NP; ++b) part[h * D + b * 128 + wt] = acc[b][h];
           if (wt == 0) {
-            part[NH * D + 2 * h] = m[h];
-            part[NH * D + 2 * h + 1] = den[h];
+            ml[2 * h] = m[h];
+            ml[2 * h + 1] = den[h];
           }
         }
         break;
@@ -927,6 +933,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     fence_before();
   }
   __syncthreads();
+  if (tid == 0 && *dead && a.status) atomicCAS(a.status, 0, static_cast<int>(MTP_ERR_TIMEOUT));
   if (warp == 0) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(LY::cols) : "memory");
@@ -936,15 +943,15 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   // ---- the clustered form's join
   const int rank = blockIdx.x % kCluster;
   if (!work && tid < NH) {
-    reinterpret_cast<float*>(sm)[NH * D + 2 * tid] = -INFINITY;
-    reinterpret_cast<float*>(sm)[NH * D + 2 * tid + 1] = 0.f;
+    reinterpret_cast<float*>(sm + LY::p)[2 * tid] = -INFINITY;
+    reinterpret_cast<float*>(sm + LY::p)[2 * tid + 1] = 0.f;
   }
   cluster_barrier();
   // every rank's (max, exp-sum) of every head
   float2* ml = reinterpret_cast<float2*>(sm + LY::q);
   if (tid < kCluster * NH)
-    ml[tid] = make_float2(peer_f32(base + 4 * (NH * D + 2 * (tid % NH)), tid / NH),
-                          peer_f32(base + 4 * (NH * D + 2 * (tid % NH) + 1), tid / NH));
+    ml[tid] = make_float2(peer_f32(base + LY::p + 8 * (tid % NH), tid / NH),
+                          peer_f32(base + LY::p + 8 * (tid % NH) + 4, tid / NH));
   __syncthreads();
   const int kvh = w.sub / g.ngrp, hg = w.sub - kvh * g.ngrp, nh = min(NH, G - hg * NH);
   const size_t row0 = static_cast<size_t>(w.b) * a.nh + kvh * G + hg * NH;

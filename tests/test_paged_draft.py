@@ -227,3 +227,43 @@ def test_paged_block_checks_its_tensors():
             dr.draft_block_paged(a["hidden"], a["last_token"], None, kv, a["pos"], 1, out_tokens=a["out_tokens"],
                                  out_hidden=a["out_hidden"])
     dr.close()
+
+
+@gpu
+@pytest.mark.parametrize("cols,layers", [(16, "SF"), (1024, "SF"), (1024, "FS")])
+def test_attention_timeout_is_reported_and_the_handle_recovers(cols, layers):
+    # failure detection without a fault: the first layer's tensor-core attention looks up no page of
+    # sequence 0, the waits for its keys give up after ~10 ms of cycles, the sequence's outputs are
+    # NaN, the status word reads MTP_ERR_TIMEOUT, and the next call matches the oracle (path 1 has
+    # no other waits). A full layer first and 1024 columns: keys dealt over the SMs; else a cluster
+    # per sequence
+    P, L = 16, np.array([200, 131, 77], np.int32)
+    shape = replace(C.TINY_F32, dtype="bf16", layer_types=tuple(layers), window=24, n_head=4, n_kv_head=1,
+                    head_dim_swa=128, head_dim_full=128)
+    wl = C.Workload(batch=3, ctx=200, n_draft=2)
+    w = G.make_weights(shape, 5)
+    inp = G.make_step_inputs(shape, wl, 5, ctx_len=L)
+    ref = O.draft_block(O.Shape.of(shape), O.decode_weights(w), inp.hidden, inp.last_token, inp.k_swa, inp.k_full,
+                        inp.ctx_len, inp.pos, 2)
+    dd = inputs_to_device(inp, "bf16")
+    from mtp_speculative_decoding_gemma4_gb300 import PagedKV
+
+    def wide(k, seed):
+        kv, table = _paged(k, L, P, seed)
+        t = np.full((3, cols), -1, np.int32)
+        t[:, :min(cols, table.shape[1])] = table[:, :cols]
+        return PagedKV(kv.k, torch.from_numpy(t).cuda(), kv.ctx_len)
+
+    kv_s, kv_f = wide(dd["k_swa"], 1), wide(dd["k_full"], 2)
+    dr = _drafter(shape, w, 3, 200)
+    dr.set_path(1)
+    dr.set_debug(skip_arrival_cta=0, spin_limit_cycles=20_000_000)
+    tok, hid = dr.draft_block_paged(dd["hidden"], dd["last_token"], kv_s, kv_f, dd["pos"], 2)
+    torch.cuda.synchronize()
+    assert torch.isnan(hid[0, 0]).all()
+    assert dr.status() == B.MTP_ERR_TIMEOUT
+    assert dr.status() == B.MTP_OK
+    dr.set_debug()
+    tok, hid = _run(dr, dd, kv_s, kv_f, 2)
+    compare_block(tok, hid, ref, "bf16")
+    dr.close()
