@@ -40,9 +40,11 @@ __device__ __forceinline__ void key_range(const Cache& c, int b, int window, int
   hi = min(max(c.ctx_len[b], 0), cap);
   lo = window > 0 ? max(0, hi - window) : 0;
 }
-// Physical page of logical page lp of sequence b, or -1 when the table's entry is no page.
+// Physical page of logical page lp of sequence b, or -1 when the table's entry is no page. An
+// ordinary load: this kernel may have been launched, as a programmatic dependent, while a plan
+// still writes the table, and the read-only path would ask that nothing write it meanwhile.
 __device__ __forceinline__ int phys_page(const Cache& c, int b, int lp) {
-  const int page = __ldg(c.table + static_cast<size_t>(b) * c.table_stride + lp);
+  const int page = c.table[static_cast<size_t>(b) * c.table_stride + lp];
   return static_cast<unsigned>(page) < static_cast<unsigned>(c.n_pages) ? page : -1;
 }
 

@@ -2,6 +2,7 @@
 and the attention of one new token, against the NumPy forms; refusals without a device."""
 import ctypes
 import math
+import os
 
 import numpy as np
 import pytest
@@ -981,3 +982,47 @@ def test_the_last_bits_of_a_probability_count(d, n_head):
     out, _ = paged_attention(c.q.cuda(), c.kv(), scale=1.0, want_lse=True)
     p = np.exp(c.q[:, :, 9].double().numpy())
     assert np.max(np.abs(out.cpu().numpy() - ((p - 1) / (p + 1))[..., None])) <= 2.0 ** -20
+
+
+# ---------------------------------------------------------------- loads of what earlier kernels write
+
+
+def test_paged_kernels_do_not_use_the_read_only_path():
+    # they are programmatic dependents, resident while an earlier kernel may still write the block
+    # table, the lengths, the pages and the summaries; ld.global.nc asks that nothing does
+    csrc = os.path.join(os.path.dirname(B.__file__), "csrc")
+    names = [n for n in sorted(os.listdir(csrc)) if n.startswith(("mtp_paged", "mtp_page"))]
+    assert len(names) >= 7
+    for name in names:
+        with open(os.path.join(csrc, name)) as f:
+            text = f.read()
+        assert "__ldg(" not in text and "global.nc" not in text and "__restrict__" not in text, name
+
+
+@gpu
+def test_attention_right_behind_the_plan_that_writes_its_table():
+    # a plan, an attention of other sequences and an attention over the plan's table, queued
+    # together many times: the second attention is launched while the plan may still run
+    from mtp_speculative_decoding_gemma4_gb300 import PagedKV, page_plan, paged_attention
+    P, d, cols, n_pages = 16, 128, 64, 200
+    rs = np.random.RandomState(3)
+    cache = _rows(rs, (n_pages, P, 1, d), "bf16")
+    dk, q = cache.cuda(), torch.randn((2, 4, d), generator=torch.Generator().manual_seed(3))
+    zero, lens = torch.zeros(2, dtype=torch.int32).cuda(), _dev(np.array([1000, 333], np.int32))
+    state, dq = _dev(np.array([0, n_pages], np.int32)), q.cuda()
+    other = PagedKV(dk, torch.zeros((2, 1), dtype=torch.int32).cuda(), _dev(np.array([1, 2], np.int32)))
+    rings = [rs.permutation(n_pages).astype(np.int32) for _ in range(40)]
+    held = [(torch.full((2, cols), -1, dtype=torch.int32).cuda(), _dev(r)) for r in rings]
+    kvs, got = [PagedKV(dk, t, lens) for t, _ in held], []
+    torch.cuda.synchronize()
+    for kv, (table, ring) in zip(kvs, held):
+        page_plan(zero, lens, table, ring, state, P, 1400)
+        paged_attention(dq, other)
+        got.append(paged_attention(dq, kv, want_lse=True))
+    torch.cuda.synchronize()
+    k = cache.double().numpy()
+    for ring, r in zip(rings, got):
+        table = np.full((2, cols), -1, np.int32)
+        table[0, :63], table[1, :21] = ring[:63], ring[63:84]
+        want = [OP.paged_attention(q[b].numpy(), k, k, table[b], L, 1 / np.sqrt(d)) for b, L in enumerate((1000, 333))]
+        _close(r, (np.stack([w[0] for w in want]), np.stack([w[1] for w in want])))
