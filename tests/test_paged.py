@@ -1026,3 +1026,152 @@ def test_attention_right_behind_the_plan_that_writes_its_table():
         table[0, :63], table[1, :21] = ring[:63], ring[63:84]
         want = [OP.paged_attention(q[b].numpy(), k, k, table[b], L, 1 / np.sqrt(d)) for b, L in enumerate((1000, 333))]
         _close(r, (np.stack([w[0] for w in want]), np.stack([w[1] for w in want])))
+
+
+# ---------------------------------------------------------------- rounds, far rows, rows alone
+
+
+@gpu
+def test_a_captured_round_over_a_kept_descriptor():
+    # plan, append, selection and attention of a round in one graph: the descriptor keeps its
+    # length tensor, into which the round copies the plan's lengths
+    from mtp_speculative_decoding_gemma4_gb300 import PagedKV, page_append, page_plan, page_select, paged_attention
+    rs = np.random.RandomState(4)
+    Bn, P, d, nh, cols, n_pages, T, k = 5, 16, 128, 4, 12, 60, 128, 4
+    cache = torch.full((n_pages, P, 1, d), float("nan"), dtype=torch.bfloat16).cuda()
+    codes, scales = torch.zeros((n_pages, 1, d), dtype=torch.int8).cuda(), torch.zeros((n_pages, 1)).cuda()
+    table = torch.full((Bn, cols), -1, dtype=torch.int32).cuda()
+    ring, state = torch.arange(n_pages, dtype=torch.int32).cuda(), _dev(np.array([0, n_pages], np.int32))
+    lens, new = torch.zeros(Bn, dtype=torch.int32).cuda(), torch.zeros(Bn, dtype=torch.int32).cuda()
+    rows, q = torch.zeros((T, 1, d), dtype=torch.bfloat16).cuda(), torch.zeros((Bn, nh, d)).cuda()
+    kv = PagedKV(cache, table, lens, codes=codes, scales=scales)
+
+    def turn():
+        len_out, slots, cu, state_out, status = page_plan(lens, new, table, ring, state, P, T)
+        page_append(kv, rows, slots)
+        lens.copy_(len_out)
+        state.copy_(state_out)
+        sel = page_select(q, kv, k)
+        return cu, sel, paged_attention(q, kv, want_lse=True), paged_attention(q, kv, pages=sel, want_lse=True)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        turn()  # nothing grows: no lengths, no rows
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            cu, sel, full, some = turn()
+    torch.cuda.synchronize()
+    kept = [np.zeros((0, d), np.float32) for _ in range(Bn)]
+    for step in range(8):
+        old = lens.cpu().numpy()
+        grow = old + rs.randint(0, 25, Bn)
+        if step % 3 == 2:
+            grow[rs.randint(Bn)] = 0
+            b = rs.randint(Bn)
+            grow[b] = max(0, old[b] - 17)
+        new.copy_(_dev(np.minimum(grow, cols * P).astype(np.int32)))
+        fresh = _rows(rs, (T, 1, d), "bf16")
+        rows.copy_(fresh)
+        hq = torch.randn((Bn, nh, d), generator=torch.Generator().manual_seed(step))
+        q.copy_(hq)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        out, at = lens.cpu().numpy(), cu.cpu().numpy()
+        assert int(state[1]) + sum(-(-out // P)) == n_pages
+        for pages, got in ((None, full), (sel.cpu().numpy(), some)):
+            want = []
+            for b in range(Bn):
+                if pages is None:
+                    kept[b] = kept[b][:out[b]]
+                    if out[b] > old[b]:
+                        kept[b] = np.concatenate([kept[b], fresh[at[b]:at[b + 1], 0].float().numpy()])
+                    assert len(kept[b]) == out[b]
+                n = max(1, -(-out[b] // P))
+                plain = np.zeros((n, P, 1, d))
+                plain.reshape(-1, d)[:out[b]] = kept[b]
+                if pages is not None:
+                    sums = [OP.page_summary(plain[p, :, 0].astype(np.float32)) for p in range(n)]
+                    np.testing.assert_array_equal(pages[b], OP.page_select(
+                        hq[b].numpy(), np.stack([s[0] for s in sums])[:, None], np.stack([s[1] for s in sums])[:, None],
+                        np.arange(-(-out[b] // P)), out[b], P, n, k, 1, 1))
+                want.append(OP.paged_attention(hq[b].numpy(), plain, plain, np.arange(n), out[b], 1 / np.sqrt(d),
+                                               pages=None if pages is None else pages[b]))
+            _close(got, (np.stack([w[0] for w in want]), np.stack([w[1] for w in want])))
+
+
+@gpu
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("f32", 64)])
+def test_pages_farther_apart_than_32_bits(dtype, d):
+    from mtp_speculative_decoding_gemma4_gb300 import PagedKV, page_append, page_select, paged_attention
+    P, n, far = 16, 3, (1 << 31) + 64
+    c = Case(d, [40], P, 4, 1, d, dtype, spare=0)
+    c.table[0] = [2, 0, 1]
+    rows = _rows(np.random.RandomState(1), (n * P, 1, d), dtype)
+    buf = torch.zeros((n - 1) * far + P * d, dtype=rows.dtype, device="cuda")
+    k = buf.as_strided((n, P, 1, d), (far, d, d, 1))
+    codes, scales = torch.zeros((n, 1, d), dtype=torch.int8).cuda(), torch.zeros((n, 1)).cuda()
+    kv = PagedKV(k, _dev(c.table), _dev(c.L), codes=codes, scales=scales)
+    slots = (c.table[0][:, None] * P + np.arange(P)).reshape(-1).astype(np.int32)
+    page_append(kv, rows.cuda(), _dev(slots))
+    c.k = torch.zeros((n, P, 1, d), dtype=rows.dtype)
+    for i, s in enumerate(slots):
+        c.k[s // P, s % P] = rows[i]
+        assert torch.equal(k[s // P, s % P].cpu(), rows[i])
+    for p in range(n):
+        np.testing.assert_array_equal(codes[p, 0].cpu().numpy(), OP.page_summary(c.k[p, :, 0].float().numpy())[0])
+    _close(paged_attention(c.q.cuda(), kv, want_lse=True), c.want())
+    sel = page_select(c.q.cuda(), kv, 2)
+    assert sel.tolist() == [[[0, 2]]]
+    _close(paged_attention(c.q.cuda(), kv, pages=sel, want_lse=True), c.want(pages=sel.cpu().numpy()))
+    # rows alone, from a source whose rows are as far apart
+    src = torch.zeros(far + d, dtype=rows.dtype, device="cuda").as_strided((2, 1, d), (far, d, 1))
+    src.copy_(rows[:2])
+    page_append(PagedKV(k), src, _dev(np.array([2 * P + 7, 2 * P + 9], np.int32)))
+    assert torch.equal(k[2, 7].cpu(), rows[0]) and torch.equal(k[2, 9].cpu(), rows[1])
+
+
+@gpu
+def test_summaries_past_32_bits():
+    from mtp_speculative_decoding_gemma4_gb300 import PagedKV, page_append, page_select
+    d, n, cols = 512, (1 << 23) + 40, 90
+    k = torch.empty((n, 1, 1, d), dtype=torch.bfloat16, device="cuda")
+    codes, scales = torch.empty((n, 1, d), dtype=torch.int8, device="cuda"), torch.empty((n, 1), device="cuda")
+    rs = np.random.RandomState(0)
+    table = (n - 1 - rs.permutation(cols)).astype(np.int32)[None]
+    rows, q = _rows(rs, (cols, 1, d), "bf16"), torch.randn((1, 4, d), generator=torch.Generator().manual_seed(1))
+    kv = PagedKV(k, _dev(table), _dev(np.array([cols], np.int32)), codes=codes, scales=scales)
+    page_append(kv, rows.cuda(), _dev(table[0]))
+    sums = [OP.page_summary(rows[i].float().numpy()) for i in range(cols)]
+    got = codes[torch.from_numpy(table[0].astype(np.int64)).cuda(), 0].cpu().numpy()
+    np.testing.assert_array_equal(got, np.stack([s[0] for s in sums]))
+    want = OP.page_select(q[0].numpy(), np.stack([s[0] for s in sums])[:, None], np.stack([s[1] for s in sums])[:, None],
+                          np.arange(cols), cols, 1, cols, 7, 1, 1)
+    np.testing.assert_array_equal(page_select(q.cuda(), kv, 7).cpu().numpy()[0], want)
+
+
+@gpu
+@pytest.mark.parametrize("T", [0, 1, 7, 300, 2049])
+@pytest.mark.parametrize("n_kv,d,dtype,own_v,layout,P", [
+    (1, 512, "bf16", False, "token", 32), (2, 128, "bf16", True, "head", 16), (3, 64, "f32", True, "both", 8),
+    (1, 8, "bf16", False, "token", 1), (4, 200, "f32", False, "head", 64), (1, 256, "bf16", True, "token", 256)])
+def test_append_of_rows_alone(T, n_kv, d, dtype, own_v, layout, P):
+    # a cache without summaries: every row in its slot, everything else as it was
+    from mtp_speculative_decoding_gemma4_gb300 import page_append
+    rs = np.random.RandomState(T + d)
+    c = Case(T + d, [1], P, n_kv, n_kv, d, dtype, own_v=own_v, layout=layout, spare=2 + 2 * T // P)
+    n = c.k.shape[0]
+    slots = rs.permutation(n * P)[:T].astype(np.int32)
+    slots[rs.uniform(size=T) < 0.1] = -1
+    if T > 5:
+        slots[3], slots[4], slots[5] = n * P, 2 ** 31 - 1, -2 ** 31
+    k_new, v_new = _rows(rs, (T, n_kv, d), dtype), _rows(rs, (T, n_kv, d), dtype) if own_v else None
+    page_append(c.kv(), k_new.cuda(), _dev(slots), v_new=None if v_new is None else v_new.cuda())
+    for cache, rows, dev in ((c.k, k_new, c.dk), (c.v, v_new, c.dv)):
+        if cache is None:
+            continue
+        for t, s in enumerate(slots):
+            if 0 <= s < n * P:
+                cache[s // P, s % P] = rows[t]
+        np.testing.assert_array_equal(_bits(dev), _bits(cache))
