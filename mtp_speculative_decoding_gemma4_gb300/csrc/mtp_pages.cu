@@ -216,11 +216,11 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(const __grid_constan
 // addition to hi rounded away (two-sum, 7 operations a value with the scaling). lo loses nothing
 // while the values' spread is below 2^24 (bf16, any P): m is then the exact mean, rounded once, in
 // any order of the rows. Beyond that, and in fp32, lo's own roundings add at most P^2 2^-48 of the
-// largest value. The page's other rows are read where this call does not write: rows of this call
-// in another order from k_new, older ones from the cache; so one launch does. What bounds it is the
-// copy: each row read and written once, 134 MB for two prompts of 32768 rows at d = 512 in 25 us
-// (5.3 TB/s). Four bf16 rows added in fp32 before they enter the pair would take 0.2 us less, but
-// lose the mean where large values cancel.
+// largest value. The page's other rows are read where the launch does not write: rows of this call
+// in another order from k_new, older ones from the cache; so up to kAppScan rows one launch does.
+// What bounds it is the copy: each row read and written once, 134 MB for two prompts of 32768 rows
+// at d = 512 in 26.5 us (5.1 TB/s). Four bf16 rows added in fp32 before they enter the pair would
+// take 1.7 us less, but lose the mean where large values cancel; packed two-sums take 0.4 us less.
 
 // hi + lo += x * f (f a power of two)
 __device__ __forceinline__ void two_sum(float& hi, float& lo, float x, float f) {
@@ -229,6 +229,13 @@ __device__ __forceinline__ void two_sum(float& hi, float& lo, float x, float f) 
   hi = s;
 }
 constexpr int kAppThreads = 256, kAppRows = 64;  // threads, most rows of a CTA's share
+// Most rows of a call whose pages are all summed in one launch. There a run that completes a page
+// without covering it looks through all slots of the call, so that the work grows with the square
+// of the rows where they come in any order: 12 ms for 2^19 rows at P = 16, d = 8, against 2.3 ms
+// where a second launch sums such pages, finding every row in the cache. 131072 rows in order at
+// P = 64, d = 512 take 54 us in one launch and 59 in two when they begin with a page, 89 and 64 when
+// they begin inside one.
+constexpr int kAppScan = 1 << 16;
 
 struct AppArgs {
   Cache c;
@@ -276,8 +283,10 @@ __global__ void __launch_bounds__(kAppThreads) k_page_append(const __grid_consta
   }
 }
 
-// The copy with the summaries of the pages that it completes.
-template <typename T>
+// The copy with the summaries of the pages that it completes: all of them (kOne), or those that a
+// run covers (kFirst), the others from the cache in a launch behind it that copies nothing (kRest).
+enum AppPart { kOne, kFirst, kRest };
+template <typename T, AppPart PART>
 __global__ void __launch_bounds__(kAppThreads, 4) k_page_append_sum(const __grid_constant__ AppArgs a) {
   pdl_enter();
   constexpr int VE = Elem<T>::kVec;
@@ -312,8 +321,12 @@ __global__ void __launch_bounds__(kAppThreads, 4) k_page_append_sum(const __grid
     if (tid + 1 < P - off && !goes_on(first + 1 + tid)) atomicMin(&run_len, tid + 1);
     __syncthreads();
     const int len = run_len;
-    const bool done = off + len == P, whole = len == P;
-    if (done && !whole) {  // the page's other rows: of this call, or older
+    const bool whole = len == P, done = off + len == P && (PART == kOne || (PART == kFirst) == whole);
+    if (PART == kRest && !done) {
+      __syncthreads();  // run_len is read
+      continue;
+    }
+    if (PART == kOne && done && !whole) {  // the page's other rows: of this call, or older
       if (tid < P) src[tid] = -1;
       __syncthreads();
       for (int i = tid; i < a.n; i += kAppThreads) {
@@ -355,13 +368,15 @@ __global__ void __launch_bounds__(kAppThreads, 4) k_page_append_sum(const __grid
             to += 4 * st;
           }
         };
-        pass(a.kn + row * a.row_k + col, par * a.row_k, static_cast<uint4*>(c.k) + at, done);
-        if (c.v) pass(a.vn + row * a.row_v + col, par * a.row_v, static_cast<uint4*>(c.v) + at, false);
-        if (done && !whole) {
+        if (PART != kRest) {
+          pass(a.kn + row * a.row_k + col, par * a.row_k, static_cast<uint4*>(c.k) + at, done);
+          if (c.v) pass(a.vn + row * a.row_v + col, par * a.row_v, static_cast<uint4*>(c.v) + at, false);
+        }
+        if (PART != kFirst && done && !whole) {
           const uint4* old = static_cast<const uint4*>(c.k) + (page * c.sp + h * c.sh) / VE + (v - hv * a.vph);
 #pragma unroll 4
-          for (int r = r0; r < off; r += par) {
-            const int ti = src[r];
+          for (int r = r0; r < (PART == kRest ? P : off); r += par) {
+            const int ti = PART == kRest ? -1 : src[r];
             add(ti >= 0 ? a.kn[ti * a.row_k + col] : old[r * (c.st / VE)]);
           }
         }
@@ -442,9 +457,14 @@ int run_page_append(const pg::Cache& c, const void* k_new, const void* v_new, lo
   const int vpr = c.nkv * a.vph;
   while ((1 << a.vshift) < vpr) ++a.vshift;
   if ((1 << a.vshift) != vpr) a.vshift = -1;
-  void (*kernel)(pg::AppArgs) = c.f32 ? pg::k_page_append<float> : pg::k_page_append<__nv_bfloat16>;
-  if (c.codes) kernel = c.f32 ? pg::k_page_append_sum<float> : pg::k_page_append_sum<__nv_bfloat16>;
-  return pg::launch_pdl("page append", kernel, dim3((T + a.rows - 1) / a.rows), pg::kAppThreads, 0, st, a);
+  const auto launch = [&](void (*f32)(pg::AppArgs), void (*bf16)(pg::AppArgs)) {
+    return pg::launch_pdl("page append", c.f32 ? f32 : bf16, dim3((T + a.rows - 1) / a.rows), pg::kAppThreads, 0, st, a);
+  };
+  using bf = __nv_bfloat16;
+  if (!c.codes) return launch(pg::k_page_append<float>, pg::k_page_append<bf>);
+  if (T <= pg::kAppScan) return launch(pg::k_page_append_sum<float, pg::kOne>, pg::k_page_append_sum<bf, pg::kOne>);
+  const int rc = launch(pg::k_page_append_sum<float, pg::kFirst>, pg::k_page_append_sum<bf, pg::kFirst>);
+  return rc ? rc : launch(pg::k_page_append_sum<float, pg::kRest>, pg::k_page_append_sum<bf, pg::kRest>);
 }
 
 }  // namespace mtp

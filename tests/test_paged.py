@@ -1175,3 +1175,56 @@ def test_append_of_rows_alone(T, n_kv, d, dtype, own_v, layout, P):
             if 0 <= s < n * P:
                 cache[s // P, s % P] = rows[t]
         np.testing.assert_array_equal(_bits(dev), _bits(cache))
+
+
+@gpu
+@pytest.mark.parametrize("n_kv,d,dtype", [(1, 8, "bf16"), (2, 64, "bf16"), (1, 16, "f32")])
+@pytest.mark.parametrize("how", ["any order", "from inside a page", "runs of nine"])
+def test_appends_of_many_rows_in_any_order(n_kv, d, dtype, how):
+    # more rows than one launch sums: pages written whole, completed by a later run of the call, by
+    # rows in any order, or behind older rows; the bound of the sums is the one of small calls
+    from mtp_speculative_decoding_gemma4_gb300 import PagedKV, page_append
+    T, P = 70001, 16
+    n = T // 8 // P * 16 + 40
+    rs = np.random.RandomState(d)
+    cache = _rows(rs, (n, P, n_kv, d), dtype)
+    rows = _rows(rs, (T, n_kv, d), dtype)
+    if how == "any order":
+        slots = rs.permutation(n * P)[:T]
+    elif how == "from inside a page":
+        slots = 7 + np.arange(T)
+    else:
+        start = rs.permutation(n * P // 9)[:T // 9 + 1]
+        slots = (start[:, None] * 9 + np.arange(9)).reshape(-1)[:T]
+    slots = slots.astype(np.int32)
+    dk, codes, scales = cache.cuda(), torch.zeros((n, n_kv, d), dtype=torch.int8).cuda(), torch.zeros((n, n_kv)).cuda()
+    page_append(PagedKV(dk, codes=codes, scales=scales), rows.cuda(), _dev(slots))
+    cache.view(n * P, n_kv, d)[torch.from_numpy(slots.astype(np.int64))] = rows
+    np.testing.assert_array_equal(_bits(dk), _bits(cache))
+    done = slots[slots % P == P - 1] // P
+    mean = (cache.double().sum(1) / P).float().numpy()
+    scale = np.abs(mean).max(-1) * OP.INV127
+    code = np.clip(np.rint(mean / scale[..., None]), -127, 127)
+    want_codes, want_scales = np.zeros((n, n_kv, d), np.int8), np.zeros((n, n_kv), np.float32)
+    want_codes[done], want_scales[done] = code[done], scale[done]
+    np.testing.assert_array_equal(codes.cpu().numpy(), want_codes)
+    np.testing.assert_array_equal(scales.cpu().numpy(), want_scales)
+
+
+@gpu
+def test_the_time_of_an_append_grows_with_its_rows():
+    # 2^20 rows in any order: some 3 ms, with every page looked up among all rows 50 ms
+    from mtp_speculative_decoding_gemma4_gb300 import PagedKV, page_append
+    T, P, d = 1 << 20, 16, 8
+    k, rows = torch.zeros((T // P, P, 1, d), dtype=torch.bfloat16).cuda(), torch.zeros((T, 1, d), dtype=torch.bfloat16).cuda()
+    codes, scales = torch.zeros((T // P, 1, d), dtype=torch.int8).cuda(), torch.zeros((T // P, 1)).cuda()
+    kv, slots = PagedKV(k, codes=codes, scales=scales), _dev(np.random.RandomState(0).permutation(T).astype(np.int32))
+    times = []
+    for _ in range(4):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        page_append(kv, rows, slots)
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b))
+    assert min(times) <= 15
