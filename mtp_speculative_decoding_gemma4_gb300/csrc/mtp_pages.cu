@@ -213,19 +213,40 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(const __grid_constan
 //   code = rint(fl32(m / scale)); a page whose mean is not finite gets scale NaN and codes 0.
 // Every row enters as x / P (a power of two: exact), so that no sum leaves the range that the mean
 // lies in. The sum is an unevaluated pair of fp32: hi, and in lo the running sum of what each
-// addition to hi rounded away (two-sum, 7 operations a value with the scaling). lo loses nothing
-// while the values' spread is below 2^24 (bf16, any P): m is then the exact mean, rounded once, in
-// any order of the rows. Beyond that, and in fp32, lo's own roundings add at most P^2 2^-48 of the
-// largest value. The page's other rows are read where the launch does not write: rows of this call
-// in another order from k_new, older ones from the cache; so up to kAppScan rows one launch does.
-// What bounds it is the copy: each row read and written once, 134 MB for two prompts of 32768 rows
-// at d = 512 in 26.5 us (5.1 TB/s). Four bf16 rows added in fp32 before they enter the pair would
-// take 1.7 us less, but lose the mean where large values cancel; packed two-sums take 0.4 us less.
+// addition to hi rounded away (two-sum, 7 operations a value with the scaling, two values in each).
+// lo loses nothing while the values' spread is below 2^24 (bf16, any P): m is then the exact mean,
+// rounded once, in any order of the rows. Beyond that, and in fp32, lo's own roundings add at most
+// P^2 2^-48 of the largest value. The page's other rows are read where the launch does not write:
+// rows of this call in another order from k_new, older ones from the cache; so up to kAppScan rows
+// one launch does. What bounds it is the copy: each row read and written once, 134 MB for two
+// prompts of 32768 rows at d = 512 in 26 us (5.2 TB/s); with two-sums of one value each 26.5. (Four
+// bf16 rows added in fp32 before they enter the pair would take 25, but lose the mean where large
+// values cancel.)
 
-// hi + lo += x * f (f a power of two)
-__device__ __forceinline__ void two_sum(float& hi, float& lo, float x, float f) {
-  const float s = __fmaf_rn(x, f, hi), bb = __fsub_rn(s, hi);
-  lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, bb)), __fmaf_rn(x, f, -bb)));
+// hi + lo += x
+__device__ __forceinline__ void two_sum(float& hi, float& lo, float x) {
+  const float s = __fadd_rn(hi, x), bb = __fsub_rn(s, hi);
+  lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, bb)), __fsub_rn(x, bb)));
+  hi = s;
+}
+// Packed instructions: two values an issue slot.
+__device__ __forceinline__ unsigned long long& u64(float2& a) { return reinterpret_cast<unsigned long long&>(a); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(u64(a)) : "l"(u64(b)));
+  return a;
+}
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
+  asm("sub.rn.f32x2 %0, %0, %1;" : "+l"(u64(a)) : "l"(u64(b)));
+  return a;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(u64(c)) : "l"(u64(a)), "l"(u64(b)));
+  return c;
+}
+// hi + lo += x * f for two sums at once, f a power of two.
+__device__ __forceinline__ void two_sum2(float2& hi, float2& lo, float2 x, float2 f) {
+  const float2 s = fma2(x, f, hi), b = sub2(hi, s);
+  lo = add2(lo, add2(sub2(hi, add2(s, b)), fma2(x, f, b)));
   hi = s;
 }
 constexpr int kAppThreads = 256, kAppRows = 64;  // threads, most rows of a CTA's share
@@ -339,14 +360,15 @@ __global__ void __launch_bounds__(kAppThreads, 4) k_page_append_sum(const __grid
       const bool on = act && h < c.nkv;
       if (tid < hpb) hmax[tid] = 0;
       __syncthreads();  // src and hmax are set, part of the block before is read
-      float hi[VE], lo[VE];
+      float2 hi[VE / 2], lo[VE / 2];
 #pragma unroll
-      for (int e = 0; e < VE; ++e) hi[e] = lo[e] = 0.f;
+      for (int e = 0; e < VE / 2; ++e) hi[e] = lo[e] = make_float2(0.f, 0.f);
       auto add = [&](const uint4& u) {
         float x[VE];
         load_vec(reinterpret_cast<const T*>(&u), x);
 #pragma unroll
-        for (int e = 0; e < VE; ++e) two_sum(hi[e], lo[e], x[e], part_of);
+        for (int e = 0; e < VE / 2; ++e)
+          two_sum2(hi[e], lo[e], make_float2(x[2 * e], x[2 * e + 1]), make_float2(part_of, part_of));
       };
       if (on) {
         const long long at = (page * c.sp + (off + r0) * c.st + h * c.sh) / VE + (v - hv * a.vph);
@@ -384,8 +406,8 @@ __global__ void __launch_bounds__(kAppThreads, 4) k_page_append_sum(const __grid
       if (!done) continue;
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
-        part[0][e * kAppThreads + tid] = hi[e];
-        part[1][e * kAppThreads + tid] = lo[e];
+        part[0][e * kAppThreads + tid] = e & 1 ? hi[e / 2].y : hi[e / 2].x;
+        part[1][e * kAppThreads + tid] = e & 1 ? lo[e / 2].y : lo[e / 2].x;
       }
       __syncthreads();
       float m[VE];
@@ -396,7 +418,7 @@ __global__ void __launch_bounds__(kAppThreads, 4) k_page_append_sum(const __grid
         for (int e = 0; e < VE; ++e) {
           float x = part[0][e * kAppThreads + tid], l = part[1][e * kAppThreads + tid];
           for (int r = 1; r < par; ++r) {
-            two_sum(x, l, part[0][e * kAppThreads + tid + r * cols], 1.f);
+            two_sum(x, l, part[0][e * kAppThreads + tid + r * cols]);
             l += part[1][e * kAppThreads + tid + r * cols];
           }
           m[e] = __fadd_rn(x, l);
