@@ -11,8 +11,8 @@
 // spreads over its counters), then one ordered compaction.
 //
 // What bounds it is that chain: length, table, codes, the cluster barrier, up to 4 digits, the
-// compaction, and the code's own first fetches. One sequence of 1024 pages takes 8 us, 16
-// sequences of 2048 pages (17 MB of codes, 2.5 us at the copy rate) about 9.
+// compaction, and the code's own first fetches. One sequence of 1024 pages (a cluster of 16) takes
+// 8.5 us, 16 sequences of 2048 pages (clusters of 8; 17 MB of codes, 2.5 us at the copy rate) 17.5.
 #include "mtp_common.cuh"
 #include "mtp_launch.h"
 #include "mtp_paged.cuh"

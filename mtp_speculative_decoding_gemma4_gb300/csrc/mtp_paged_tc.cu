@@ -1,11 +1,12 @@
 // Attention of one new token over a paged key cache on tensor cores (bf16 cache, head_dim 128,
 // 256 or 512, pages of at least 8 tokens): the formula of mtp_paged_att.cu.
 //
-// What bounds it is reading the cache once: with the join 151 MB take 35.6 us at d = 512 (8 long
-// ragged contexts, 4.2 TB/s), 134 MB 30.8 us at d = 128 (32 x 8192, 4.4 TB/s), 128 MB of K and V
-// 32.5 us at d = 128 (61 short contexts, 3.9 TB/s). Between its start (3 us: length, table, keys),
-// its tail and the join (3 to 4 us) the keys come in at the rate that TMA copies alone reach here
-// (6.0 TB/s). On CUDA cores it is the arithmetic instead: with G
+// What bounds it is reading the cache once: with the join 151 MB take 35.3 us at d = 512 (8 long
+// ragged contexts, 4.3 TB/s), 134 MB 30.7 us at d = 128 (32 x 8192, 4.4 TB/s), 128 MB of K and V
+// 32.9 us at d = 128 (61 short contexts, 3.9 TB/s). From one length to the double the time grows by
+// the keys at 6.6 to 7.1 TB/s (8 x 8192 to 8 x 32768 keys at d = 512, 32 x 4096 to 32 x 16384 at
+// d = 128); the rest, 10 to 11 us, is the start (3 us: length, table, keys), the tail and the join
+// (3 to 4 us). On CUDA cores it is the arithmetic instead: with G
 // query heads per KV head and V = K a 2-byte key element costs 4 G flops, 16 flop per byte at
 // G = 8, which at the cache's bandwidth is more than the fp32 pipes give. So both products run as
 // tcgen05.mma with the *keys* as the 128-row operand, straight from the TMA-loaded tile:

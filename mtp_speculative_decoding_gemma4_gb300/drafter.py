@@ -98,7 +98,9 @@ class Drafter:
                           out_hidden=None, stream: Optional[int] = None):
         """draft_block over paged caches (paged.PagedKV with block_table and ctx_len, or None for an
         attention type that no block has). n_select > 0: full-attention blocks attend the n_select
-        pages that their queries select. stream: None is torch's current stream."""
+        pages that their queries select. A call with the tensors of the one before (out_tokens and
+        out_hidden passed, the same descriptors) replays its graph. stream: None is torch's current
+        stream."""
         _need_flat(hidden, "hidden", self.torch_dtype, (None, self.shape.backbone))
         Bn, dev = hidden.shape[0], hidden.device
         for t, name in ((last_token, "last_token"), (pos, "pos")):
