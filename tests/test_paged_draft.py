@@ -12,7 +12,7 @@ from mtp_speculative_decoding_gemma4_gb300 import build as build_mod
 from mtp_synth import configs as C
 from mtp_synth import gen as G
 
-from _util import TOL, compare_block, config_data, inputs_to_device, weights_to_device
+from _util import TOL, compare_block, config_data, inputs_to_device, oracle_block, weights_to_device
 
 gpu = pytest.mark.gpu
 
@@ -266,4 +266,20 @@ def test_attention_timeout_is_reported_and_the_handle_recovers(cols, layers):
     dr.set_debug()
     tok, hid = _run(dr, dd, kv_s, kv_f, 2)
     compare_block(tok, hid, ref, "bf16")
+    dr.close()
+
+
+@gpu
+@pytest.mark.parametrize("index,P,batch", [(2, 64, 0), (3, 32, 6), (4, 16, 9)])
+def test_paged_block_of_the_benchmark_shapes_matches_the_oracle(index, P, batch):
+    # tokens may differ only where the oracle's own margin is a near tie
+    shape, wl, w, inp = config_data(index, batch)
+    ref = oracle_block(index, n_draft=2, batch=batch)
+    dr = _drafter(shape, w, wl.batch, wl.ctx)
+    d = inputs_to_device(inp, shape.dtype)
+    kv_s, _ = _paged(d["k_swa"], inp.ctx_len, P, 1)
+    kv_f, _ = _paged(d["k_full"], inp.ctx_len, P, 2)
+    tok, hid = _run(dr, d, kv_s, kv_f, 2)
+    cmp = compare_block(tok, hid, ref, shape.dtype)
+    assert len(cmp.tie_divergences) <= max(1, cmp.steps_compared // 50)
     dr.close()
