@@ -309,8 +309,8 @@ MTP_API int mtp_get_status(mtp_handle *h);
  * skip_arrival_cta of the cluster sends none of its rows in the launch's first exchange; on
  * the tensor-core path (5), CTA skip_arrival_cta of the first projection GEMM issues no copy
  * for its last k stage; in a paged draft block (paths 1 and 5), the first layer's tensor-core
- * attention looks up no page of sequence skip_arrival_cta. Each has the same timeout outcome, and the bound applies to the
- * waits of these paths too. (-1, 0) restores the defaults. No other path is affected.
+ * attention looks up no page of sequence skip_arrival_cta. Each has the same timeout outcome, and
+ * the bound applies to the waits of these paths too. (-1, 0) restores the defaults. No other path is affected.
  * Errors: INVALID_ARG (NULL handle, skip_arrival_cta < -1, spin_limit_cycles < 0). */
 MTP_API int mtp_set_debug(mtp_handle *h, int32_t skip_arrival_cta, int64_t spin_limit_cycles);
 
@@ -432,8 +432,7 @@ MTP_API int mtp_page_append(const mtp_paged_kv *kv, const void *k_new, const voi
  * outputs that it reaches are NaN, infinite, or those without the keys of score -inf; a sequence
  * whose every attended key scores -inf gets NaN. So do the outputs concerned when a device wait
  * gives up after about 2 s (mtp_draft_block_paged reports that through mtp_get_status, too).
- * Query head h reads KV head
- * h / (n_head / n_kv_head).
+ * Query head h reads KV head h / (n_head / n_kv_head).
  *   q         device [B][n_head][head_dim] fp32
  *   pages     device [B][n_kv_head][n_list] int32 or NULL
  *   scale     softmax scale, 0 -> 1 / sqrt(head_dim)
