@@ -445,6 +445,36 @@ MTP_API int mtp_paged_attention(const mtp_paged_kv *kv, const float *q, int32_t 
 MTP_API int mtp_paged_attention_workspace(const mtp_paged_kv *kv, int32_t B, int32_t n_head, int32_t n_list,
                                           int64_t *bytes);
 
+/* Attention of a chunk of new tokens per sequence over the paged cache, which holds their keys
+ * already: the last n_b = cu_new[b + 1] - cu_new[b] of the ctx_len[b] tokens of sequence b are the
+ * rows cu_new[b] .. cu_new[b + 1] - 1 of q and out (mtp_page_plan's cu_new; slices of a prompt, or
+ * the tokens of a draft block to verify). The row of position t attends the keys j <= t of its
+ * sequence, with window > 0 those with j > t - window: out = sum_j p_j v_j, p = softmax(scale q . k_j).
+ * q, out and the cache have the model dtype: an output is rounded to it once. fp32 models are
+ * computed in fp32. For bf16 the products are exact and sums, maxima and exp-sums fp32; on tensor
+ * cores (head_dim 128, 256 or 512, page_size >= 8) the probabilities enter the second product as
+ * bf16 and their sum is of the rounded values, so that an output is a weighted mean of the values
+ * with weights off by at most 2^-9 each.
+ * A row with nothing to attend (a sequence that holds fewer tokens than its new ones, pages that are
+ * none) gets out 0 and lse -inf. What a row does not attend may hold anything and does not reach it;
+ * where a row's query or an attended key or value is not finite, or a score leaves the range of
+ * fp32, its outputs are NaN, infinite, or those without the keys of score -inf (a row whose every
+ * attended key scores -inf gets NaN). A device wait that gives up after about 2 s leaves NaN.
+ * cu_new must not decrease; its entries are clamped to [0, T] on the device. Rows of out and lse
+ * outside [cu_new[0], cu_new[B]) are left as they were, and q is not read there.
+ *   q         device, token t and head h at q + t * q_stride + h * head_dim, 16-byte aligned
+ *   q_stride  elements between tokens (>= n_head * head_dim, a multiple of 16 bytes)
+ *   cu_new    device [B + 1] int32
+ *   T         rows of out and lse; T <= 2^24 and T * n_head <= 2^26
+ *   out       device [T][n_head][head_dim], not over q
+ *   lse       device [T][n_head] fp32 log of the sum of exponentials, or NULL
+ * Errors: INVALID_ARG (workspace too small included), UNSUPPORTED_SHAPE, CUDA. */
+MTP_API int mtp_paged_attention_chunk(const mtp_paged_kv *kv, const void *q, int64_t q_stride, const int32_t *cu_new,
+                                      int32_t B, int32_t T, int32_t n_head, int32_t window, float scale, void *out,
+                                      float *lse, void *workspace, int64_t workspace_bytes, void *stream);
+MTP_API int mtp_paged_attention_chunk_workspace(const mtp_paged_kv *kv, int32_t B, int32_t T, int32_t n_head,
+                                                int64_t *bytes);
+
 /* Pages a query attends, by a cheap score of each page: per query head the step
  * s = fl32(max |q| * fl32(1 / 127)) and codes c = rint(fl32(q / s)) (all 0 when q is not
  * finite), the page's score per KV head = max over its query heads of

@@ -21,7 +21,8 @@ EXPORTS = ("mtp_init_weights", "mtp_draft_block", "mtp_centroid_head", "mtp_veri
            "mtp_set_path", "mtp_destroy", "mtp_last_error", "mtp_centroid_head_noalloc", "mtp_set_logit_mask",
            "mtp_verify_sample", "mtp_set_sparse_head", "mtp_set_debug", "mtp_page_plan", "mtp_page_append",
            "mtp_page_select", "mtp_page_select_workspace", "mtp_paged_attention", "mtp_paged_attention_workspace",
-           "mtp_draft_block_paged", "mtp_draft_block_paged_workspace")
+           "mtp_draft_block_paged", "mtp_draft_block_paged_workspace", "mtp_paged_attention_chunk",
+           "mtp_paged_attention_chunk_workspace")
 MASK_NEG_1E30, MASK_MIN_MINUS_ONE = 0, 1  # enum mtp_logit_mask
 HEAD_AUTO, HEAD_PER_SEQUENCE, HEAD_CLUSTER_MAJOR = 0, 1, 2  # enum mtp_sparse_head
 
@@ -95,6 +96,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mtp_page_append.argtypes = [pkv, vp, vp, i64, i64, vp, i32, vp]
     lib.mtp_paged_attention.argtypes = [pkv, vp, i32, i32, i32, f32, vp, i32, vp, vp, vp, i64, vp]
     lib.mtp_paged_attention_workspace.argtypes = [pkv, i32, i32, i32, ctypes.POINTER(i64)]
+    lib.mtp_paged_attention_chunk.argtypes = [pkv, vp, i64, vp, i32, i32, i32, i32, f32, vp, vp, vp, i64, vp]
+    lib.mtp_paged_attention_chunk_workspace.argtypes = [pkv, i32, i32, i32, ctypes.POINTER(i64)]
     lib.mtp_page_select.argtypes = [pkv, vp, i32, i32, i32, i32, i32, vp, vp, i64, vp]
     lib.mtp_page_select_workspace.argtypes = [pkv, i32, ctypes.POINTER(i64)]
     lib.mtp_draft_block_paged.argtypes = [vp, vp, vp, pkv, pkv, vp, i32, i32, i32, i32, i32, vp, vp, vp, i64, vp]
@@ -107,7 +110,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                  "mtp_get_status", "mtp_set_path", "mtp_centroid_head_noalloc", "mtp_set_logit_mask",
                  "mtp_verify_sample", "mtp_set_sparse_head", "mtp_set_debug", "mtp_page_plan", "mtp_page_append",
                  "mtp_page_select", "mtp_page_select_workspace", "mtp_paged_attention",
-                 "mtp_paged_attention_workspace", "mtp_draft_block_paged", "mtp_draft_block_paged_workspace"):
+                 "mtp_paged_attention_workspace", "mtp_draft_block_paged", "mtp_draft_block_paged_workspace",
+                 "mtp_paged_attention_chunk", "mtp_paged_attention_chunk_workspace"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -220,6 +224,23 @@ def mtp_paged_attention(kv: mtp_paged_kv, q: int, B: int, n_head: int, window: i
                                                       lse or None, workspace or None, workspace_bytes, stream or None)
     if rc:
         _check(rc, "mtp_paged_attention")
+
+
+def mtp_paged_attention_chunk_workspace(kv: mtp_paged_kv, B: int, T: int, n_head: int) -> int:
+    n = ctypes.c_int64()
+    _check(load_library().mtp_paged_attention_chunk_workspace(kv, B, T, n_head, ctypes.byref(n)),
+           "mtp_paged_attention_chunk_workspace")
+    return n.value
+
+
+def mtp_paged_attention_chunk(kv: mtp_paged_kv, q: int, q_stride: int, cu_new: int, B: int, T: int, n_head: int,
+                              window: int, scale: float, out: int, lse: int, workspace: int, workspace_bytes: int,
+                              stream: int = 0) -> None:
+    rc = (_lib or load_library()).mtp_paged_attention_chunk(kv, q or None, q_stride, cu_new, B, T, n_head, window, scale,
+                                                            out or None, lse or None, workspace or None,
+                                                            workspace_bytes, stream or None)
+    if rc:
+        _check(rc, "mtp_paged_attention_chunk")
 
 
 def mtp_page_select_workspace(kv: mtp_paged_kv, B: int) -> int:

@@ -105,7 +105,34 @@ struct AttArgs {
   int B, nh, n_list, window, nsplit;
 };
 
+// Attention of a chunk of new tokens per sequence.
+struct ChunkArgs {
+  Cache c;
+  const void* q;            // token t, head h at t * q_stride + h * d, model dtype
+  const int* cu;            // [B + 1]: sequence b's tokens are [cu[b], cu[b + 1])
+  void* out;                // [T][nh][d], model dtype
+  float* lse;               // [T][nh] or null
+  float* ws_acc;            // partial sums of the splits
+  float* ws_ml;             // their (max, exp-sum)
+  long long q_stride;
+  float scale_log2;         // softmax scale * log2(e)
+  int B, T, nh, window, nsplit;
+};
+
+// The new tokens of sequence b: rows [s0, s0 + n) of the call, at positions first, first + 1, ...
+// of L keys (first < 0 where the sequence holds fewer than its new ones: those attend nothing).
+__device__ __forceinline__ void chunk_range(const ChunkArgs& a, int b, int& s0, int& n, int& first, int& L) {
+  s0 = min(max(a.cu[b], 0), a.T);
+  n = min(max(a.cu[b + 1], s0), a.T) - s0;
+  L = min(max(a.c.ctx_len[b], 0), a.c.max_pages << a.c.pshift);
+  first = L - n;
+}
+
 }  // namespace pg
+
+// Workspace bytes and launch of the attention of a chunk.
+long long chunk_att_workspace(const pg::ChunkArgs& a);
+int run_chunk_att(pg::ChunkArgs a, void* ws, int num_sms, cudaStream_t st);
 
 // Workspace bytes and launch of the one-token attention.
 long long paged_att_workspace(const pg::Cache& c, int B, int nh, int n_list);

@@ -110,6 +110,20 @@ static int check_batch(const Cache& c, int B, int n_head) {
   return MTP_OK;
 }
 
+// Whether a chunk's batch, tokens and heads are served; fills a's sizes.
+static int check_chunk(ChunkArgs* a, int B, int T, int n_head) {
+  if (B < 1 || B > 1 << 20 || T < 0 || T > 1 << 24 || n_head < 1 || n_head % a->c.nkv || n_head / a->c.nkv > 1024 ||
+      static_cast<long long>(T) * n_head > 1 << 26) {
+    set_error("need 1 <= B <= 2^20, 0 <= T <= 2^24, n_head a positive multiple of n_kv_head=%d and T * n_head <= 2^26 "
+              "(B=%d T=%d n_head=%d)", a->c.nkv, B, T, n_head);
+    return MTP_ERR_INVALID_ARG;
+  }
+  a->B = B;
+  a->T = T;
+  a->nh = n_head;
+  return MTP_OK;
+}
+
 int check_workspace(const void* ws, int64_t have, long long need) {
   if (need > 0 && (!ws || !aligned(ws, 16) || have < need)) {
     set_error("the workspace must be 16-byte aligned and hold %lld bytes (%lld given)", need,
@@ -250,6 +264,66 @@ int mtp_paged_attention(const mtp_paged_kv* kv, const float* q, int32_t B, int32
   int sms = 0;
   if ((rc = pg::sm_count(&sms))) return rc;
   return run_paged_att(a, workspace, sms, static_cast<cudaStream_t>(stream));
+}
+
+int mtp_paged_attention_chunk_workspace(const mtp_paged_kv* kv, int32_t B, int32_t T, int32_t n_head, int64_t* bytes) {
+  set_error("%s", "");
+  pg::ChunkArgs a;
+  memset(&a, 0, sizeof(a));
+  int rc = pg::make_cache(kv, true, &a.c);
+  if (rc || (rc = pg::check_chunk(&a, B, T, n_head))) return rc;
+  if (!bytes) {
+    set_error("bytes must be non-NULL");
+    return MTP_ERR_INVALID_ARG;
+  }
+  *bytes = T ? chunk_att_workspace(a) : 0;
+  return MTP_OK;
+}
+
+int mtp_paged_attention_chunk(const mtp_paged_kv* kv, const void* q, int64_t q_stride, const int32_t* cu_new, int32_t B,
+                              int32_t T, int32_t n_head, int32_t window, float scale, void* out, float* lse,
+                              void* workspace, int64_t workspace_bytes, void* stream) {
+  set_error("%s", "");
+  pg::ChunkArgs a;
+  memset(&a, 0, sizeof(a));
+  int rc = pg::make_cache(kv, true, &a.c);
+  if (rc || (rc = pg::check_chunk(&a, B, T, n_head))) return rc;
+  if (!cu_new || !pg::aligned(cu_new, 4) || (T > 0 && (!q || !out)) || !pg::aligned(q, 16) || !pg::aligned(out, 16) ||
+      !pg::aligned(lse, 4)) {
+    set_error("cu_new, q and out must be non-NULL, q and out 16-byte aligned");
+    return MTP_ERR_INVALID_ARG;
+  }
+  const int vec = a.c.f32 ? 4 : 8, size = a.c.f32 ? 4 : 2;
+  const long long width = static_cast<long long>(n_head) * a.c.d;
+  if (T > 0 && (q_stride < width || q_stride % vec || q_stride > (1LL << 40))) {
+    set_error("q_stride=%lld must be n_head * head_dim = %lld to 2^40 elements, a multiple of %d",
+              static_cast<long long>(q_stride), width, vec);
+    return MTP_ERR_INVALID_ARG;
+  }
+  const long long q_bytes = T ? ((T - 1LL) * q_stride + width) * size : 0, out_bytes = T * width * size,
+                  lse_bytes = 4LL * T * n_head;
+  if (pg::overlap(out, out_bytes, q, q_bytes) ||
+      (lse && (pg::overlap(lse, lse_bytes, q, q_bytes) || pg::overlap(lse, lse_bytes, out, out_bytes)))) {
+    set_error("out and lse must be buffers of their own");
+    return MTP_ERR_INVALID_ARG;
+  }
+  const double s = scale > 0.f ? static_cast<double>(scale) : 1.0 / std::sqrt(static_cast<double>(a.c.d));
+  a.scale_log2 = static_cast<float>(s * 1.4426950408889634);
+  if (window < 0 || !(scale >= 0.f) || !std::isfinite(a.scale_log2)) {
+    set_error("need window >= 0 and a scale in [0, 2^127] (window=%d scale=%g)", window, static_cast<double>(scale));
+    return MTP_ERR_INVALID_ARG;
+  }
+  if (!T) return MTP_OK;
+  if ((rc = pg::check_workspace(workspace, workspace_bytes, chunk_att_workspace(a)))) return rc;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.cu = cu_new;
+  a.out = out;
+  a.lse = lse;
+  a.window = window;
+  int sms = 0;
+  if ((rc = pg::sm_count(&sms))) return rc;
+  return run_chunk_att(a, workspace, sms, static_cast<cudaStream_t>(stream));
 }
 
 int mtp_page_select_workspace(const mtp_paged_kv* kv, int32_t B, int64_t* bytes) {

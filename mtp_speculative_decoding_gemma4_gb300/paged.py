@@ -252,6 +252,41 @@ def _attend(st, q, kv, Bn, nh, window, scale, pages, n_list, want_lse, out):
     return (out, lse) if want_lse else out
 
 
+def paged_attention_chunk(q: torch.Tensor, kv: PagedKV, cu_new: torch.Tensor, window: int = 0, scale: float = 0.0,
+                          want_lse: bool = False, out: Optional[torch.Tensor] = None, stream: Optional[int] = None):
+    """Attention of the new tokens of every sequence, q [T][n_head][d] of the cache's dtype, over the
+    paged cache, which holds their keys already: rows [cu_new[b], cu_new[b + 1]) (int32 [B + 1]) are
+    the last tokens of sequence b, and each attends the keys up to its own position, the last `window`
+    of them where that is > 0. Rows may be strided (the last two dimensions contiguous). Returns out
+    [T][n_head][d] (q's dtype), with want_lse (out, lse fp32 [T][n_head]). Rows of no sequence are
+    left as they were, unset in tensors that the call allocates."""
+    if kv.block_table is None:
+        raise ValueError("the cache has no block_table")
+    _need(q, "q", kv.k.dtype, 3, kv.device)
+    T, nh, d = q.shape
+    if d != kv._row[1] or T and (q.stride(2) != 1 or nh > 1 and q.stride(1) != d):
+        raise ValueError(f"q must be [T][n_head][{kv._row[1]}] with contiguous rows (got {list(q.shape)})")
+    if not _flat_like(cu_new, _i32, kv.device, (kv.batch + 1,)):
+        _need_flat(cu_new, "cu_new", _i32, (kv.batch + 1,), kv.device)
+    if out is not None:
+        _need_flat(out, "out", q.dtype, q.shape, kv.device)
+    return call_on(kv.device, stream, _attend_chunk, q, kv, cu_new, window, scale, want_lse, out)
+
+
+def _attend_chunk(st, q, kv, cu_new, window, scale, want_lse, out):
+    T, nh, d = q.shape
+    n = kv._ws.get(("chunk", T, nh))
+    if n is None:
+        n = kv._ws[("chunk", T, nh)] = B.mtp_paged_attention_chunk_workspace(kv.p, kv.batch, T, nh)
+    if out is None:
+        out = torch.empty((T, nh, d), dtype=q.dtype, device=kv.device)
+    lse = torch.empty((T, nh), dtype=_f32, device=kv.device) if want_lse else None
+    _with_workspace(kv, st, n, lambda ws, n: B.mtp_paged_attention_chunk(
+        kv.p, q.data_ptr(), q.stride(0) if T > 1 else nh * d, cu_new.data_ptr(), kv.batch, T, nh, window, scale,
+        out.data_ptr(), lse.data_ptr() if want_lse else 0, ws, n, st))
+    return (out, lse) if want_lse else out
+
+
 def page_select(q: torch.Tensor, kv: PagedKV, n_select: int, keep_first: int = 1, keep_last: int = 1,
                 out: Optional[torch.Tensor] = None, stream: Optional[int] = None) -> torch.Tensor:
     """The n_select logical pages of the highest scores per sequence and KV head, in increasing
