@@ -394,12 +394,14 @@ int launch_dims(const ChunkArgs& a, int R, cudaStream_t st) {
 }  // namespace pg
 
 long long chunk_att_workspace(const pg::ChunkArgs& a) {
+  if (paged_tc_supported(a.c)) return chunk_tc_workspace(a);
   // a window only shortens the key range and fewer SMs take fewer splits, so this is a bound
   const long long n = pg::choose_chunk_splits(a, pg::rows_of(a), 0, pg::kMaxSms);
   return n > 1 ? static_cast<long long>(a.T) * a.nh * n * (a.c.d + 2) * 4 : 0;
 }
 
 int run_chunk_att(pg::ChunkArgs a, void* ws, int num_sms, cudaStream_t st) {
+  if (paged_tc_supported(a.c)) return run_chunk_tc(a, ws, num_sms, st);
   const int R = pg::rows_of(a);
   a.nsplit = pg::choose_chunk_splits(a, R, a.window, num_sms);
   a.ws_acc = static_cast<float*>(ws);

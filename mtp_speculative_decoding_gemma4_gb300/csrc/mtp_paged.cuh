@@ -133,6 +133,9 @@ __device__ __forceinline__ void chunk_range(const ChunkArgs& a, int b, int& s0, 
 // Workspace bytes and launch of the attention of a chunk.
 long long chunk_att_workspace(const pg::ChunkArgs& a);
 int run_chunk_att(pg::ChunkArgs a, void* ws, int num_sms, cudaStream_t st);
+// Its tensor-core form (mtp_chunk_tc.cu), which run_chunk_att takes where paged_tc_supported.
+long long chunk_tc_workspace(const pg::ChunkArgs& a);
+int run_chunk_tc(const pg::ChunkArgs& a, void* ws, int num_sms, cudaStream_t st);
 
 // Workspace bytes and launch of the one-token attention.
 long long paged_att_workspace(const pg::Cache& c, int B, int nh, int n_list);
