@@ -16,12 +16,15 @@
 // truncates: over 32768 keys, 2048 additions, that is some 10^-4 of a sum, beside the 2^-9 of the
 // output's own rounding and that of the probabilities, which enter as bf16; their sum is fp32.)
 //
-// One CTA per SM: warp 10 finds the tiles' pages through the block table, warp 8 loads them (slots of
-// [KT keys][128 dims]), one thread of warp 9 issues the products (whichever of the next scores and the
-// next sums is ready; scores are double-buffered), and two warpgroups take the softmax of one half of
-// the columns each, a thread per key. The key tiles of all units are numbered through and dealt evenly
-// over the CTAs (mtp_chunk.cuh); a unit that crosses CTAs leaves unnormalised sums and (max, exp-sum)
-// per part, which k_chunk_tc_join adds in CTA order.
+// One CTA per SM. Four warpgroups (two at N = 32) take the softmax of a quarter of the columns each, a
+// thread per key: with two, of twice the columns, a tile of 128 x 128 scores took 5000 cycles, since
+// two warps per scheduler do not cover for the latencies of tensor memory, barriers and exponentials.
+// Of four more warps one finds the units of this CTA's share (a ring of their descriptions) and the
+// tiles' pages, one loads the tiles (slots of [KT keys][128 dims]), one loads queries, and one thread
+// of the last issues the products (whichever of the next scores and the next sums is ready; scores are
+// double-buffered). The key tiles of all units are numbered through and dealt evenly over the CTAs
+// (mtp_chunk.cuh); a unit that crosses CTAs leaves unnormalised sums and (max, exp-sum) per part,
+// which k_chunk_tc_join adds in CTA order.
 //
 // Keys that no row of the unit attends are zero before the sums (0 * NaN would not vanish). Of a key
 // that only some rows attend, values that are not finite are zeroed and the attending rows get NaN.
@@ -44,23 +47,26 @@ using pg::ChunkArgs;
 using pg::kSpin;
 using pg::Tiles;
 
-constexpr int kThreads = 384;   // two warpgroups for the softmax; load, MMA, find and no-work warps
 constexpr int kAhead = 4;       // tiles that the find warp runs ahead of the load warp
 constexpr int kInfo = 12;       // tiles whose pages are kept: kAhead and those between load and softmax
+constexpr int kSegs = 4;        // units whose descriptions are kept
 constexpr int kExtra = 2;       // what beginning a unit costs, in key tiles
 
 struct Args {
   ChunkArgs a;
   int rshift;   // log2 of the keys per TMA box (min(P, keys per tile))
   int grid;
-  int tpt;      // tokens of a tile
+  int ts;       // log2 of the tokens of a tile
   int hgs;      // groups of N query heads per KV head (1 unless it has more than N)
+  int qbytes;   // of a box of queries: 64 dims x min(N, heads per KV head) x 2^ts tokens
   int* meta;    // [grid][4]: sequence, KV head and group, tile, last CTA of the unit a CTA starts and does not end
 };
 
 template <int D, int N_>
 struct Lay {
-  static constexpr int N = N_, NC = N / 2;               // rows; of a warpgroup
+  static constexpr int N = N_;                           // rows
+  static constexpr int WG = N == 32 ? 2 : 4, NC = N / WG;  // softmax warpgroups, columns of each
+  static constexpr int threads = 128 * (WG + 1);
   static constexpr int NP = D / 128;                     // 128-dim slots per tile and operand
   static constexpr int KT = D == 512 ? 64 : 128;         // keys per tile
   static constexpr int KS = KT == 64 ? 6 : 7;
@@ -69,25 +75,37 @@ struct Lay {
   static constexpr int QBY = D * N * 2;                  // 64-dim blocks of [N][128 bytes]
   static constexpr int PBY = KT * 128 * ((N + 63) / 64); // 64-row blocks of [KT][128 bytes]
   static constexpr int PB = D == 256 && N == 128 ? 1 : 2;  // probability buffers
-  // the softmax's scratch, [5][NC] floats per warpgroup: with 128 rows a 64-row block of the
-  // probabilities is one warpgroup's alone and serves; fewer rows share a block, but leave room
-  static constexpr int scratch_bytes = N == 128 ? 0 : 5 * N * 4;
-  static constexpr int misc_bytes = 2048 - 64 + scratch_bytes;
-  static constexpr int room = 232448 - 1024 - misc_bytes - QBY - PB * PBY;
+  static constexpr int misc_bytes = 3072;
+  static constexpr int room = 232448 - misc_bytes - QBY - PB * PBY;
   static constexpr int ring0 = room / slot > 16 ? 16 : room / slot;
   static constexpr int ring = ring0 / NP * NP;           // a tile's slots of one operand are neighbours
   static constexpr int q = ring * slot;
   static constexpr int p = q + QBY;
   static constexpr int mref = p + PB * PBY;              // [N] minus the rows' references
-  static constexpr int info = mref + N * 4;              // [kInfo][16] physical pages of a tile's boxes
+  static constexpr int top = mref + N * 4;               // [N] a tile's maxima, as ordered integers
+  static constexpr int fac = top + N * 4;                // [N] factors of the sums under a new reference
+  static constexpr int segs = fac + N * 4;               // [kSegs][12] units (Seg below)
+  static constexpr int info = segs + kSegs * 48;         // [kInfo][16] physical pages of a tile's boxes
   static constexpr int bad = info + kInfo * 64;          // per warpgroup [4]: rows that attend values that are not finite
-  static constexpr int scratch = bad + 32;
-  static constexpr int bars = scratch + scratch_bytes;
-  static constexpr int nbars = 2 * ring + 2 * 4 + 3 + kInfo;
+  static constexpr int bars = bad + WG * 16;
+  static constexpr int nbars = 2 * ring + 2 * 4 + 3 + 2 * kSegs + kInfo;
   static constexpr int misc = bars + nbars * 8;          // tensor-memory address, dead word, tiles begun
-  static constexpr int total = misc + 16 + 1024;         // + alignment
+  static constexpr int total = misc + 16;
   static constexpr int want = (NP + 2) * N;              // tensor-memory columns: sums, two of scores
   static constexpr int cols = want <= 128 ? 128 : want <= 256 ? 256 : 512;
+};
+
+// A part of a unit (a tile of rows of one KV head, and group of its heads, of one sequence) as the
+// warps of a CTA take it.
+struct Seg {
+  int tiles;           // key tiles; -1: no more units
+  int k0;              // the first one
+  int kvh;
+  int tok0, nt, pos0;  // first token of the rows in q and out, tokens, position of the first
+  int h0, heads;       // first query head, heads
+  int lo, hi;          // keys that a row of the unit attends
+  int whole;           // the whole unit is here
+  int part;            // else: its place among the parts
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -98,6 +116,29 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ unsigned pack2(float lo, float hi) {
   unsigned r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two fp32 values in one register pair, and what is done to both at once.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 two(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split2(f2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ __forceinline__ void ld16(unsigned t, float* v) {
@@ -116,33 +157,41 @@ __device__ __forceinline__ void st16(unsigned t, const float* v) {
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// The largest of the warp's values (NaN left out).
-__device__ __forceinline__ float warp_max_redux(float v) {
-  int i = __float_as_int(fmaxf(v, -INFINITY));
-  i ^= (i >> 31) & 0x7fffffff;
-  i = __reduce_max_sync(0xffffffffu, i);
-  return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+// fp32 values as integers of the same order (NaN as the lowest value), and back.
+__device__ __forceinline__ int ordered(float v) {
+  const int i = __float_as_int(fmaxf(v, -INFINITY));
+  return i ^ ((i >> 31) & 0x7fffffff);
 }
+__device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
+constexpr int kLowest = static_cast<int>(0xff800000u ^ 0x7fffffffu);  // ordered(-inf)
 
-// A unit: a tile of rows of one KV head (and group of its heads) of one sequence.
-struct Unit {
-  int b, sub, tile;      // sub: KV head * hgs + group
-  int s0, nt, pos0;      // first token of the sequence in q; tokens of the tile; position of its first
-  int lo, hi;            // its keys
-  int k0, n;             // first key tile, number of key tiles
-};
+// Bounded wait; false when this CTA has given up (the word `dead`) or gives up here. (Inlined: a call
+// would keep the softmax from its registers.)
+__device__ __forceinline__ bool wait_in(unsigned bar, unsigned parity, volatile int* dead, long long limit) {
+  if (test_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+#pragma unroll 1
+  while (!try_wait(bar, parity)) {
+    if (*dead) return false;
+    if (clock64() - t0 > limit) {
+      *dead = 1;
+      return false;
+    }
+  }
+  return true;
+}
 
 __device__ __forceinline__ Tiles tiles_of(const Args& g, int ks, int b, int& s0) {
   Tiles t;
   pg::chunk_range(g.a, b, s0, t.n, t.first, t.L);
   t.window = g.a.window;
-  t.tpt = g.tpt;
+  t.ts = g.ts;
   t.ks = ks;
   t.extra = kExtra;
   return t;
 }
 
-// Walks the segments (parts of units) of a CTA's share: costs [r, r1).
+// Walks the parts of units of a CTA's share: costs [r, r1).
 template <int KS>
 struct Walk {
   long long r, r1, per;
@@ -166,7 +215,7 @@ struct Walk {
       if (lane >= o) incl += y;
     }
     const long long total = __shfl_sync(0xffffffffu, incl, 31);
-    per = (total + g.grid - 1) / g.grid;
+    per = total < (1 << 30) ? static_cast<unsigned>(total + g.grid - 1) / static_cast<unsigned>(g.grid) : (total + g.grid - 1) / g.grid;
     r = min(total, blockIdx.x * per);
     r1 = min(total, r + per);
     b = sub = tile = off = 0;
@@ -181,7 +230,7 @@ struct Walk {
         if (at < c * subs) break;
         at -= c * subs;
       }
-      sub = static_cast<int>(at / c);
+      sub = subs > 1 ? static_cast<int>(at / c) : 0;
       at -= sub * c;
       int lo = 0, hi = t.count() - 1;  // the last tile that begins at or before `at`
       while (lo < hi) {
@@ -197,13 +246,14 @@ struct Walk {
     off = __shfl_sync(0xffffffffu, off, f);
     t = tiles_of(g, KS, b, s0);
   }
-  struct Seg : Unit {
-    int a, e;        // key tiles [a, e) of n
-    bool begins;     // the unit's first key tile is here (or it has none)
-    long long last;  // the unit's last cost
+  struct Part {
+    int b, sub, tile;  // sub: KV head * groups + group
+    int k, a, e;       // the unit's key tiles, those of this part [a, e)
+    bool begins;       // the unit's first key tile is here (or it has none)
+    long long last;    // the unit's last cost
   };
-  // The next segment. Units without a key tile come with n = 0.
-  __device__ __forceinline__ bool next(const Args& g, int subs, Seg& s) {
+  // The next part of a unit. Units without a key tile come with k = 0.
+  __device__ __forceinline__ bool next(const Args& g, int subs, Part& s) {
 #pragma unroll 1
     while (r < r1) {
       const int nt = t.count();
@@ -218,57 +268,50 @@ struct Walk {
       }
       const int k = t.tiles(tile), c = k + kExtra;
       const int to = static_cast<int>(min(static_cast<long long>(c), off + (r1 - r)));
+      s.b = b;
+      s.sub = sub;
+      s.tile = tile;
+      s.k = k;
       s.a = max(off - kExtra, 0);
       s.e = max(to - kExtra, 0);
       s.begins = k > 0 ? s.a == 0 : off == 0;
       s.last = r - off + c - 1;
       r += to - off;
-      const bool none = s.e == s.a && !(k == 0 && s.begins);
-      s.b = b;
-      s.sub = sub;
-      s.tile = tile;
-      s.s0 = s0;
-      s.nt = min(g.tpt, t.n - tile * g.tpt);
-      s.pos0 = static_cast<int>(t.pos(tile));
-      s.lo = t.begin(tile);
-      s.hi = t.end(tile);
-      s.k0 = s.lo >> KS;
-      s.n = k;
       off = to;
       if (off >= c) {
         off = 0;
         ++tile;
       }
-      if (none) continue;
-      return true;
+      if (s.e > s.a || (k == 0 && s.begins)) return true;
     }
     return false;
   }
 };
 
 template <int D, int N>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Lay<D, N>::threads, 1)
     k_chunk_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
-               const __grid_constant__ Args g) {
+               const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ Args g) {
   using LY = Lay<D, N>;
-  constexpr int NP = LY::NP, KT = LY::KT, kRing = LY::ring, NC = LY::NC, PB = LY::PB;
-  extern __shared__ __align__(1024) char sm_raw[];
+  constexpr int NP = LY::NP, KT = LY::KT, kRing = LY::ring, NC = LY::NC, PB = LY::PB, WG = LY::WG;
+  extern __shared__ __align__(1024) char sm[];  // (swizzled tiles begin at multiples of 1024)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  char* sm = sm_raw + ((1024u - (sa(sm_raw) & 1023u)) & 1023u);
   const unsigned base = sa(sm);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   // barriers: loaded slots, free slots; per score buffer: scores done, scores read; per parity of a
-  // tile: probabilities written, sums done; queries written, sums read, drained; pages of a tile found
+  // tile: probabilities written, sums done; queries loaded, queries used, drained; per place of a
+  // unit: its sums are read, it is found; pages of a tile found
   const unsigned full0 = base + LY::bars, empty0 = full0 + 8 * kRing, sfull0 = empty0 + 8 * kRing, sfree0 = sfull0 + 16,
-                 pfull0 = sfree0 + 16, odone0 = pfull0 + 16, qfull = odone0 + 16, ofree = qfull + 8, drain = ofree + 8,
-                 ifull0 = drain + 8;
+                 pfull0 = sfree0 + 16, odone0 = pfull0 + 16, qfull = odone0 + 16, qused = qfull + 8, drain = qused + 8,
+                 ofree0 = drain + 8, seg0 = ofree0 + 8 * kSegs, ifull0 = seg0 + 8 * kSegs;
   int* info = reinterpret_cast<int*>(sm + LY::info);
+  Seg* segs = reinterpret_cast<Seg*>(sm + LY::segs);
   int* misc = reinterpret_cast<int*>(sm + LY::misc);  // 0: tensor memory, 1: dead, 2: begun
-  volatile int *dead = misc + 1, *begun = misc + 2;  // begun: tiles that the load warp has begun
+  volatile int *dead = misc + 1, *begun = misc + 2;   // begun: tiles that the load warp has begun
   const ChunkArgs& a = g.a;
   const Cache& c = a.c;
   const bool own_v = c.v != nullptr;
-  const int G = a.nh / c.nkv, subs = c.nkv * g.hgs, PT = own_v ? 2 * NP : NP;
+  const int PT = own_v ? 2 * NP : NP;
 
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
@@ -277,17 +320,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(sfull0 + 8 * i, 1);
-      mbar_init(sfree0 + 8 * i, 8);
-      mbar_init(pfull0 + 8 * i, 8);
+      mbar_init(sfree0 + 8 * i, 4 * WG);
+      mbar_init(pfull0 + 8 * i, 4 * WG);
       mbar_init(odone0 + 8 * i, 1);
     }
-    mbar_init(qfull, 8);
-    mbar_init(ofree, 8);
+    mbar_init(qfull, 1);
+    mbar_init(qused, 1);
     mbar_init(drain, 1);
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(ofree0 + 8 * i, 4 * WG);
+      mbar_init(seg0 + 8 * i, 1);
+    }
     for (int i = 0; i < kInfo; ++i) mbar_init(ifull0 + 8 * i, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    misc[1] = misc[2] = 0;
+    misc[1] = (base & 1023u) != 0;  // (every wait then gives up)
+    misc[2] = 0;
   }
+  for (int i = tid; i < N; i += LY::threads) reinterpret_cast<int*>(sm + LY::top)[i] = kLowest;
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sa(misc)), "r"(LY::cols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -298,28 +347,73 @@ __global__ void __launch_bounds__(kThreads, 1)
   const unsigned tmem = *reinterpret_cast<volatile unsigned*>(misc);
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  // ---- this CTA's share (every warp for itself: no exchange)
-  using W = Walk<LY::KS>;
-  W w;
-  w.locate(g, subs);
-  typename W::Seg s;
-  int* meta = g.meta + 4 * blockIdx.x;
-  if (tid == 0) meta[3] = -1;
+  // unit i of this CTA, once it is found; false behind the last
+  auto get_seg = [&](int i, Seg& s) {
+    if (!wait_in(seg0 + 8 * (i % kSegs), (i / kSegs) & 1, dead, kSpin)) return false;
+    s = segs[i % kSegs];
+    return s.tiles > 0;
+  };
 
-  if (warp == 10) {
-    // ---------------- pages: looks up the tiles' pages up to kAhead tiles before they are loaded
+  if (warp == 4 * WG + 2) {
+    // ---------------- finds the units, and their tiles' pages up to kAhead tiles before they are loaded
     // (a lane per box, several tiles at once)
+    const int G = a.nh / c.nkv, subs = c.nkv * g.hgs;
     const int rs = g.rshift, ngs = LY::KS - rs, ng = 1 << ngs, nb = min(32 >> ngs, kAhead);
-    int tt = 0;
+    Walk<LY::KS> w;
+    w.locate(g, subs);
+    int* meta = g.meta + 4 * blockIdx.x;
+    if (lane == 0) meta[3] = -1;
+    int tt = 0, ns = 0, slot = 0;
     bool ok = true;
-    while (ok && w.next(g, subs, s)) {
+    typename Walk<LY::KS>::Part u;
+    auto put_seg = [&](const Seg& s) {  // its place is free once the unit kSegs before is answered
+      if (ns >= kSegs) ok = __all_sync(0xffffffffu, wait_in(ofree0 + 8 * (ns % kSegs), (ns / kSegs - 1) & 1, dead, kSpin));
+      if (ok && lane == 0) {
+        segs[ns % kSegs] = s;
+        mbar_arrive(seg0 + 8 * (ns % kSegs));
+      }
+      __syncwarp();
+      ++ns;
+    };
+    Seg s;
+    while (ok && w.next(g, subs, u)) {
+      const int hg = u.sub % g.hgs;
+      s.kvh = u.sub / g.hgs;
+      s.heads = min(N, G - hg * N);
+      s.h0 = s.kvh * G + hg * N;
+      s.tok0 = w.s0 + (u.tile << g.ts);
+      s.nt = min(1 << g.ts, w.t.n - (u.tile << g.ts));
+      s.pos0 = static_cast<int>(w.t.pos(u.tile));
+      s.lo = w.t.begin(u.tile);
+      s.hi = w.t.end(u.tile);
+      s.k0 = (s.lo >> LY::KS) + u.a;
+      s.tiles = u.e - u.a;
+      s.whole = u.a == 0 && u.e == u.k;
+      s.part = 2 * blockIdx.x + (u.begins ? 1 : 0);
+      if (!u.k) {  // nothing to attend
 #pragma unroll 1
-      for (int k = s.a; k < s.e && ok; k += nb) {
+        for (int i = lane; i < s.nt * s.heads * (D / 8); i += 32) {
+          const int r = i / (D / 8);
+          const long long row = static_cast<long long>(s.tok0 + r / s.heads) * a.nh + s.h0 + r % s.heads;
+          reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * D)[i % (D / 8)] = make_uint4(0, 0, 0, 0);
+          if (a.lse && i % (D / 8) == 0) a.lse[row] = -INFINITY;
+        }
+        continue;
+      }
+      if (!s.whole && u.begins && lane == 0) {
+        meta[0] = u.b;
+        meta[1] = u.sub;
+        meta[2] = u.tile;
+        meta[3] = static_cast<int>(u.last / w.per);
+      }
+      put_seg(s);
+#pragma unroll 1
+      for (int k = 0; k < s.tiles && ok; k += nb) {
         int page = -1;
         const int pos = ((s.k0 + k) << LY::KS) + (lane << rs);  // the tiles' boxes follow one another
-        if (lane < nb * ng && pos < s.hi) page = pg::phys_page(c, s.b, pos >> c.pshift);
+        if (lane < nb * ng && pos < s.hi) page = pg::phys_page(c, u.b, pos >> c.pshift);
 #pragma unroll 1
-        for (int j = 0; j < nb && k + j < s.e; ++j, ++tt) {
+        for (int j = 0; j < nb && k + j < s.tiles; ++j, ++tt) {
           // the load warp has begun tile tt - kAhead, so tile tt - kInfo is done with
           if (tt >= kAhead) {
             const long long t0 = clock64();
@@ -332,34 +426,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
           }
-          int* in = info + (tt % kInfo) * 16;
-          if (lane >> ngs == j) in[lane & (ng - 1)] = page;
+          if (lane >> ngs == j) info[slot * 16 + (lane & (ng - 1))] = page;
           __syncwarp();
-          if (lane == 0) mbar_arrive(ifull0 + 8 * (tt % kInfo));
+          if (lane == 0) mbar_arrive(ifull0 + 8 * slot);
+          if (++slot == kInfo) slot = 0;
         }
       }
     }
-  } else if (warp == 8) {
+    s.tiles = -1;
+    if (ok) put_seg(s);
+  } else if (warp == 4 * WG) {
     // ---------------- loads
     if (elect()) {
       const int rs = g.rshift, R = 1 << rs, ng = KT >> rs, P = 1 << c.pshift;
-      int pc = 0, slot = 0, tt = 0;  // slots so far, the next slot and the ring's phase there, tiles
-      unsigned phase = 0;
+      int pc = 0, slot = 0, tt = 0, is = 0;  // slots so far, the next slot and the ring's phase there; tiles, place of their pages
+      unsigned phase = 0, iphase = 0;
       bool ok = true;
-      while (ok && w.next(g, subs, s)) {
-        const int kvh = s.sub / g.hgs;
+      Seg s;
 #pragma unroll 1
-        for (int k = s.a; k < s.e && ok; ++k, ++tt) {
-          if (!wait_bar(ifull0 + 8 * (tt % kInfo), (tt / kInfo) & 1, dead, kSpin)) {
+      for (int i = 0; ok && get_seg(i, s); ++i) {
+#pragma unroll 1
+        for (int k = 0; k < s.tiles && ok; ++k, ++tt) {
+          if (!wait_in(ifull0 + 8 * is, iphase, dead, kSpin)) {
             ok = false;
             break;
           }
-          const int* in = info + (tt % kInfo) * 16;
+          const int* in = info + is * 16;
           const int off0 = ((s.k0 + k) << LY::KS) & (P - 1);  // 0 unless a page is longer than a tile
 #pragma unroll 1
           for (int j = 0; j < PT; ++j) {
             const unsigned bar = full0 + 8 * slot;
-            if (pc >= kRing && !wait_bar(empty0 + 8 * slot, phase ^ 1, dead, kSpin)) {
+            if (pc >= kRing && !wait_in(empty0 + 8 * slot, phase ^ 1, dead, kSpin)) {
               ok = false;
               break;
             }
@@ -371,14 +468,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int r = 0; r < ng; ++r, dst += R * 128) {
               const int page = in[r];  // -1: zeros
-              tma_4d(dst, map, x, off0, kvh, page, bar);
-              tma_4d(dst + LY::box, map, x + 64, off0, kvh, page, bar);
+              tma_4d(dst, map, x, off0, s.kvh, page, bar);
+              tma_4d(dst + LY::box, map, x + 64, off0, s.kvh, page, bar);
             }
             ++pc;
             if (++slot == kRing) {
               slot = 0;
               phase ^= 1;
             }
+          }
+          if (++is == kInfo) {
+            is = 0;
+            iphase ^= 1;
           }
         }
       }
@@ -391,7 +492,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == 4 * WG + 3) {
+    // ---------------- queries: boxes of 64 dims x the heads x the tokens (rows behind a unit's hold
+    // those of other tokens or zeros, for columns that nothing reads)
+    if (elect()) {
+      Seg s;
+      int n = 0;
+#pragma unroll 1
+      for (; get_seg(n, s); ++n) {
+        if (n && !wait_in(qused, (n - 1) & 1, dead, kSpin)) break;
+        mbar_expect_tx(qfull, g.qbytes * (D / 64));
+#pragma unroll 1
+        for (int j = 0; j < D / 64; ++j) tma_4d(base + LY::q + j * (N * 128), &mapQ, 64 * j, s.h0, s.tok0, 0, qfull);
+      }
+      const long long t0 = clock64();
+      while (n && !try_wait(qfull, (n - 1) & 1) && clock64() - t0 < kSpin) {
+      }
+    }
+    __syncwarp();
+  } else if (warp == 4 * WG + 1) {
     if (elect()) {
       // ---------------- MMA issue: the next sums or the next scores, whichever are ready.
       // fp32 += bf16 x bf16, N columns; scores: M = KT; sums: M = 128, A and B MN-major
@@ -400,28 +519,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       const unsigned tO = tmem, tS = tmem + NP * N;
       const unsigned kd = desc_lo(base, 16), vd = desc_lo(base, LY::box), qd = desc_lo(base + LY::q, 16),
                      pd = desc_lo(base + LY::p, KT * 128);
-      // tiles whose scores / sums are issued; tiles left of the scores' segment; segments begun by
-      // either; ring places
+      // tiles whose scores / sums are issued; tiles left of the scores' unit; units begun by either;
+      // ring places
       int tq = 0, tp = 0, left = 0, nseg = 0, pseg = 0, sq = 0, sp = own_v ? NP : 0;
-      unsigned fq = 0, fp = 0, starts = 0;  // starts bit i: tile tp + i is its segment's first
+      unsigned fq = 0, fp = 0, starts = 0;  // starts bit i: tile tp + i is its unit's first
       bool more = true, fresh = false;
       long long t0 = clock64();
+#pragma unroll 1
       while (more || tp < tq) {
         bool did = false;
-        if (more && left == 0) {
-          more = w.next(g, subs, s);
-          if (more) {
-            left = s.e - s.a;
-            if (left) ++nseg;
-            fresh = true;
+        if (more && left == 0 && test_wait(seg0 + 8 * (nseg % kSegs), (nseg / kSegs) & 1)) {
+          left = *reinterpret_cast<volatile int*>(&segs[nseg % kSegs].tiles);
+          if (left < 0) {
+            more = false;
+            left = 0;
           }
-          continue;
+          ++nseg;
+          fresh = true;
+          did = true;
         }
         if (tp < tq) {
           const bool first = starts & 1;
-          if (test_wait(pfull0 + 8 * (tp & 1), (tp >> 1) & 1) && (!first || pseg == 0 || test_wait(ofree, (pseg - 1) & 1))) {
+          if (test_wait(pfull0 + 8 * (tp & 1), (tp >> 1) & 1) &&
+              (!first || pseg == 0 || test_wait(ofree0 + 8 * ((pseg - 1) % kSegs), ((pseg - 1) / kSegs) & 1))) {
             if (own_v)
-              for (int i = 0; i < NP; ++i) wait_bar(full0 + 8 * (sp + i), fp, dead, kSpin);
+              for (int i = 0; i < NP; ++i) wait_in(full0 + 8 * (sp + i), fp, dead, kSpin);
             fence_after();
             const unsigned v0 = vd + sp * (LY::slot >> 4), p0 = pd + (PB == 1 ? 0 : (tp & 1) * (LY::PBY >> 4));
 #pragma unroll
@@ -442,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             did = true;
           }
         }
-        if (!did && more && tq < tp + 2) {
+        if (left > 0 && tq < tp + 2) {
           bool ready = (!fresh || test_wait(qfull, (nseg - 1) & 1)) &&
                        (tq < 2 || test_wait(sfree0 + 8 * (tq & 1), ((tq >> 1) - 1) & 1));
 #pragma unroll
@@ -462,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             starts = (starts & ~(1u << (tq - tp))) | (static_cast<unsigned>(fresh) << (tq - tp));
             fresh = false;
             ++tq;
-            --left;
+            if (--left == 0) commit(qused);
             if ((sq += PT) >= kRing) {
               sq -= kRing;
               fq ^= 1;
@@ -487,207 +609,187 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp < 8) {
-    // ---------------- softmax and outputs: a warpgroup per half of the columns, a thread per key of a
-    // tile, and per dim of each 128-dim block of the sums
+  } else {
+    // ---------------- softmax and outputs: a warpgroup per NC columns, a thread per key of a tile, and
+    // per dim of each 128-dim block of the sums
     const int wg = warp >> 2, wt = tid & 127, ww = warp & 3, col0 = wg * NC;
     const unsigned tw = tmem + (static_cast<unsigned>(32 * ww) << 16);
     const unsigned tO = tw + col0, tS = tw + NP * N + col0;
+    const f2 scale2 = two(a.scale_log2, a.scale_log2);
     float* const negm = reinterpret_cast<float*>(sm + LY::mref) + col0;
+    int* const top = reinterpret_cast<int*>(sm + LY::top) + col0;
+    float* const fac = reinterpret_cast<float*>(sm + LY::fac) + col0;
     unsigned* const bad = reinterpret_cast<unsigned*>(sm + LY::bad);
     // this thread's key of a tile: the accumulator row of its tensor-memory lane (M = 64 fills the
     // lower half of each warp's lanes)
     const int key = KT == 128 ? wt : 16 * ww + lane;
     const bool has = KT == 128 || lane < 16;
-    auto bar_wg = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); };
-    auto heads = [&](const Unit& u) { return min(N, G - (u.sub % g.hgs) * N); };
-    auto head0 = [&](const Unit& u) { return (u.sub / g.hgs) * G + (u.sub % g.hgs) * N; };
-    auto put_q = [&](const Unit& u) {
-      const int Gc = heads(u), nr = u.nt * Gc, h0 = head0(u);
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) +
-                               static_cast<long long>(u.s0 + u.tile * g.tpt) * a.q_stride + static_cast<long long>(h0) * D;
-#pragma unroll 4
-      for (int i = tid; i < N * (D / 8); i += 256) {
-        const int r = i / (D / 8), ch = i % (D / 8);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < nr) {
-          const int tok = r / Gc, h = r - tok * Gc;
-          v = *reinterpret_cast<const uint4*>(q + tok * a.q_stride + h * D + ch * 8);
-        }
-        *reinterpret_cast<uint4*>(sm + LY::q + (ch >> 3) * (N * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
-      }
-      fence_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(qfull);
-    };
-    auto scratch = [&](char* p) {
-      return reinterpret_cast<float*>(N == 128 ? p + wg * (KT * 128) : sm + LY::scratch + wg * (LY::scratch_bytes / 2));
-    };
-    auto wait_sums = [&](int t) { wait_bar(odone0 + 8 * (t & 1), (t >> 1) & 1, dead, kSpin); };
-    typename W::Seg sn;
-    // units without a key are answered here: they have no tile
-    auto next_unit = [&](typename W::Seg& u) {
-      while (w.next(g, subs, u)) {
-        if (u.n) return true;
-        const int Gc = heads(u), h0 = head0(u);
-        for (int i = tid; i < u.nt * Gc * (D / 8); i += 256) {
-          const int r = i / (D / 8), tok = u.s0 + u.tile * g.tpt + r / Gc;
-          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) +
-                                    (static_cast<long long>(tok) * a.nh + h0 + r % Gc) * D + i % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
-        }
-        if (a.lse)
-          for (int r = tid; r < u.nt * Gc; r += 256)
-            a.lse[static_cast<long long>(u.s0 + u.tile * g.tpt + r / Gc) * a.nh + h0 + r % Gc] = -INFINITY;
-      }
-      return false;
-    };
     const int rs = g.rshift;
-    bool have = next_unit(s);
-    if (have) put_q(s);
-    int tt = 0;  // tiles of the CTA before this segment
-    while (have) {
-      const int Gc = heads(s), nr = s.nt * Gc, nrw = min(max(nr - col0, 0), NC);  // rows; of this warpgroup
-      const int ntl = s.e - s.a;
-      // (columns behind the rows: scores of zero queries under a reference of 0)
+    auto bar_wg = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); };
+    auto wait_sums = [&](int t) { wait_in(odone0 + 8 * (t & 1), (t >> 1) & 1, dead, kSpin); };
+    // the bits i of 0..31 with lo <= i < hi
+    auto bits = [](int lo, int hi) {
+      lo = max(lo, 0);
+      hi = min(hi, 32);
+      return lo < hi ? 0xffffffffu >> (32 - hi + lo) << lo : 0u;
+    };
+    int at = 0, is = 0;  // tiles so far; the place of their pages
+    Seg s;
+#pragma unroll 1
+    for (int ns = 0; get_seg(ns, s); ++ns) {
+      const int nr = s.nt * s.heads, nrw = __shfl_sync(0xffffffffu, min(max(nr - col0, 0), NC), 0);  // rows; of this warpgroup
+      // (columns behind the rows: scores of anything under a reference of 0)
       if (wt < NC) negm[wt] = wt < nrw ? INFINITY : 0.f;
       if (wt < 4) bad[4 * wg + wt] = 0;
       bar_wg();
-      float l[NC];
+      f2 l[NC / 2];
 #pragma unroll
-      for (int i = 0; i < NC; ++i) l[i] = 0.f;
+      for (int i = 0; i < NC / 2; ++i) l[i] = two(0.f, 0.f);
 #pragma unroll 1
-      for (int t = 0; t < ntl; ++t) {
-        const int at = tt + t, buf = at & 1;
+      for (int t = 0; t < s.tiles; ++t, ++at) {
+        const int buf = at & 1;
         char* const pbuf = sm + LY::p + (PB == 1 ? 0 : buf * LY::PBY);
-        wait_bar(ifull0 + 8 * (at % kInfo), (at / kInfo) & 1, dead, kSpin);
-        // the rows [cmin, cmax) of this warpgroup attend this thread's key
-        const int pos = ((s.k0 + s.a + t) << LY::KS) + key, rel = pos - s.pos0;
-        const int page = has ? info[(at % kInfo) * 16 + (key >> rs)] : -1;
-        const bool valid = page >= 0 && pos >= s.lo && pos < s.hi;
-        const int cmin = (valid ? max(rel, 0) * Gc : N) - col0;
-        const int cmax = (a.window > 0 && a.window < s.nt - rel ? (rel + a.window) * Gc : nr) - col0;
-        const bool masked = !__all_sync(0xffffffffu, !has || (cmin <= 0 && cmax >= nrw));
-        wait_bar(sfull0 + 8 * buf, (at >> 1) & 1, dead, kSpin);
+        wait_in(sfull0 + 8 * buf, (at >> 1) & 1, dead, kSpin);
         __syncwarp();
         fence_after();
+        // x: the exponents under the references; a second time where these have moved
         float x[NC];
-#pragma unroll
-        for (int i = 0; i < NC; i += 16)
-          if (i < nrw) ld16(tS + buf * N + i, x + i);
-        ld_wait();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(sfree0 + 8 * buf);
-        bool up = t == 0;
-        if (!masked) {
-          float mx = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < NC; i += 4)
-            if (i < nrw) {
-              const float4 m4 = *reinterpret_cast<const float4*>(negm + i);
-              mx = fmaxf(fmaxf(mx, fmaf(x[i], a.scale_log2, m4.x)), fmaf(x[i + 1], a.scale_log2, m4.y));
-              mx = fmaxf(fmaxf(mx, fmaf(x[i + 2], a.scale_log2, m4.z)), fmaf(x[i + 3], a.scale_log2, m4.w));
-            }
-          up = up || (has && mx > 8.f);
-        } else {
-#pragma unroll
-          for (int i = 0; i < NC; ++i)
-            if (i < nrw && i >= cmin && i < cmax) up = up || (has && !(fmaf(x[i], a.scale_log2, negm[i]) <= 8.f));
-        }
-        int any;
-        asm volatile("{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n bar.red.or.pred q, %2, 128, p;\n selp.s32 %0, 1, 0, q;\n}"
-                     : "=r"(any)
-                     : "r"(up ? 1 : 0), "r"(1 + wg)
-                     : "memory");
-        if (any) {  // new references: the maxima so far
-          if (t > 0) wait_sums(at - 1);
-          __syncwarp();
-          fence_after();
-          float* const red = scratch(pbuf);
-#pragma unroll
-          for (int i = 0; i < NC; ++i)
-            if (i < nrw) {
-              const float v = has && i >= cmin && i < cmax ? pg::attended(x[i] * a.scale_log2) : -INFINITY;
-              const float m = warp_max_redux(v);
-              if (lane == (i & 31)) red[ww * NC + i] = m;
-            }
-          bar_wg();
-          if (wt < nrw) {
-            const float mo = -negm[wt], mn = fmaxf(fmaxf(fmaxf(red[wt], red[NC + wt]), fmaxf(red[2 * NC + wt], red[3 * NC + wt])), mo);
-            red[4 * NC + wt] = mo == -INFINITY ? 0.f : ex2(mo - mn);
-            negm[wt] = -mn;
-          }
-          bar_wg();
-#pragma unroll
-          for (int i = 0; i < NC; ++i)
-            if (i < nrw) l[i] *= red[4 * NC + i];
-          if (t > 0) {
+        // the rows [cmin, cmax) of this warpgroup attend this thread's key (its pages were found before
+        // they were loaded)
+        const int pos = ((s.k0 + t) << LY::KS) + key, rel = pos - s.pos0;
+        const int page = has ? info[is * 16 + (key >> rs)] : -1;
+        if (++is == kInfo) is = 0;
+        const bool valid = page >= 0 && pos >= s.lo && pos < s.hi;
+        const int cmin = (valid ? max(rel, 0) * s.heads : N) - col0;
+        const int cmax = (a.window > 0 && a.window < s.nt - rel ? (rel + a.window) * s.heads : nr) - col0;
+        const bool masked = !__all_sync(0xffffffffu, !has || (cmin <= 0 && cmax >= nrw));
+        if (nrw) {
 #pragma unroll 1
-            for (int b = 0; b < NP; ++b)
+          for (int pass = 0;; ++pass) {
 #pragma unroll
-              for (int i = 0; i < NC; i += 16)
-                if (i < nrw) {
+            for (int i = 0; i < NC; i += 16) ld16(tS + buf * N + i, x + i);
+            ld_wait();
+#pragma unroll
+            for (int i = 0; i < NC; i += 4) {
+              const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(negm + i);
+              split2(fma2(two(x[i], x[i + 1]), scale2, m.x), x[i], x[i + 1]);
+              split2(fma2(two(x[i + 2], x[i + 3]), scale2, m.y), x[i + 2], x[i + 3]);
+            }
+            if (masked) {
+              const unsigned on = bits(cmin, cmax);
+#pragma unroll
+              for (int i = 0; i < NC; ++i) x[i] = on >> i & 1 ? x[i] : -INFINITY;
+            }
+            if (pass) break;
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < NC; i += 8) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], fmaxf(x[i + 2 * e], x[i + 2 * e + 1]));
+            }
+            const bool up = t == 0 || (has && fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) > 8.f);
+            int any;
+            asm volatile("{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n bar.red.or.pred q, %2, 128, p;\n selp.s32 %0, 1, 0, q;\n}"
+                         : "=r"(any)
+                         : "r"(up ? 1 : 0), "r"(1 + wg)
+                         : "memory");
+            if (!any) break;
+            // new references: the maxima so far, 16 rows at a time from the scores once more (a short
+            // loop: a unit's first tile meets a cold instruction cache)
+            if (t > 0) wait_sums(at - 1);
+            __syncwarp();
+            fence_after();
+#pragma unroll 1
+            for (int i0 = 0; i0 < nrw; i0 += 16) {
+              float v[16];
+              int mine = kLowest;
+              ld16(tS + buf * N + i0, v);
+              ld_wait();
+              const unsigned on = has ? bits(cmin - i0, cmax - i0) : 0u;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const int m = __reduce_max_sync(0xffffffffu, on >> i & 1 ? ordered(pg::attended(v[i] * a.scale_log2)) : kLowest);
+                mine = lane == i ? m : mine;
+              }
+              if (lane < 16) atomicMax(top + i0 + lane, mine);
+            }
+            bar_wg();
+            if (wt < NC) {
+              const float mo = -negm[wt], mn = fmaxf(unordered(top[wt]), mo);
+              top[wt] = kLowest;
+              if (wt < nrw) {
+                fac[wt] = mo == -INFINITY ? 0.f : ex2(mo - mn);
+                negm[wt] = -mn;
+              } else {
+                fac[wt] = 0.f;
+              }
+            }
+            bar_wg();
+            if (t > 0) {
+#pragma unroll
+              for (int i = 0; i < NC; i += 4) {
+                const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(fac + i);
+                l[i / 2] = mul2(l[i / 2], f.x);
+                l[i / 2 + 1] = mul2(l[i / 2 + 1], f.y);
+              }
+#pragma unroll 1
+              for (int b = 0; b < NP; ++b)
+#pragma unroll 1
+                for (int i = 0; i < nrw; i += 16) {
                   float v[16];
                   ld16(tO + b * N + i, v);
                   ld_wait();
 #pragma unroll
-                  for (int e = 0; e < 16; ++e) v[e] *= i + e < nrw ? red[4 * NC + i + e] : 0.f;
+                  for (int e = 0; e < 16; ++e) v[e] *= fac[i + e];
                   st16(tO + b * N + i, v);
                 }
-            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-            fence_before();
-          }
-          bar_wg();  // the scratch is read
-        }
-        if (at >= PB) wait_sums(at - PB);  // the buffer's last probabilities are used
-        char* const prow = pbuf + key * 128;
-#pragma unroll
-        for (int i = 0; i < NC; i += 8)
-          if (i < nrw) {
-            float p[8];
-            const float4 m0 = *reinterpret_cast<const float4*>(negm + i), m1 = *reinterpret_cast<const float4*>(negm + i + 4);
-            const float mm[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) p[e] = ex2(fmaf(x[i + e], a.scale_log2, mm[e]));
-            if (masked) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) p[e] = i + e >= cmin && i + e < cmax ? p[e] : 0.f;
+              asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) l[i + e] += p[e];
-            const int col = col0 + i;
-            if (has)
-              *reinterpret_cast<uint4*>(prow + (col >> 6) * (KT * 128) + ((((col & 63) >> 3) ^ (key & 7)) << 4)) =
-                  make_uint4(pack2(p[0], p[1]), pack2(p[2], p[3]), pack2(p[4], p[5]), pack2(p[6], p[7]));
           }
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sfree0 + 8 * buf);
+        if (at >= PB) wait_sums(at - PB);  // the buffer's last probabilities are used
+        if (nrw) {
+          char* const prow = pbuf + (col0 >> 6) * (KT * 128) + key * 128;
+#pragma unroll
+          for (int i = 0; i < NC; i += 8) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[i + e] = ex2(x[i + e]);
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) l[(i + e) / 2] = add2(l[(i + e) / 2], two(x[i + e], x[i + e + 1]));
+            if (has)
+              *reinterpret_cast<uint4*>(prow + (((((col0 & 63) + i) >> 3) ^ (key & 7)) << 4)) =
+                  make_uint4(pack2(x[i], x[i + 1]), pack2(x[i + 2], x[i + 3]), pack2(x[i + 4], x[i + 5]), pack2(x[i + 6], x[i + 7]));
+          }
+        }
         // keys of the tile that no row of the unit attends, and values that are not finite in keys that
-        // only some do: this warpgroup's half of the dims
+        // only some do: this warpgroup's part of the dims
         const int amin = cmin + col0, amax = min(cmax + col0, nr);
         if (has && page >= 0 && (!valid || amin > 0 || amax < nr)) {
+          constexpr int V = D / 8 / WG;
 #pragma unroll 1
-          for (int j = wg * NP; j < (wg + 1) * NP; ++j) {  // blocks of 64 dims
-            const int pc = at * PT + (own_v ? NP : 0) + (j >> 1), slot = pc % kRing;
-            if (own_v && !wait_bar(full0 + 8 * slot, (pc / kRing) & 1, dead, kSpin)) break;
-            uint4* row = reinterpret_cast<uint4*>(sm + slot * LY::slot + (j & 1) * LY::box + key * 128);
-#pragma unroll 1
-            for (int e = 0; e < 8; ++e) {
-              if (!valid) {
-                row[e] = make_uint4(0, 0, 0, 0);
-                continue;
-              }
-              uint4 v = row[e];
-              unsigned* u = reinterpret_cast<unsigned*>(&v);
-              bool off = false;
+          for (int e = wg * V; e < (wg + 1) * V; ++e) {  // vectors of 8 dims
+            const int pc = at * PT + (own_v ? NP : 0) + (e >> 4), slot = pc % kRing;
+            if (own_v && !wait_in(full0 + 8 * slot, (pc / kRing) & 1, dead, kSpin)) break;
+            uint4* const at16 = reinterpret_cast<uint4*>(sm + slot * LY::slot + ((e >> 3) & 1) * LY::box + key * 128) + (e & 7);
+            if (!valid) {
+              *at16 = make_uint4(0, 0, 0, 0);
+              continue;
+            }
+            uint4 v = *at16;
+            unsigned* u = reinterpret_cast<unsigned*>(&v);
+            bool off = false;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if ((u[i] & 0x7f800000u) == 0x7f800000u) off = true, u[i] &= 0xffffu;
-                if ((u[i] & 0x7f80u) == 0x7f80u) off = true, u[i] &= 0xffff0000u;
-              }
-              if (off) {
-                row[e] = v;
+            for (int i = 0; i < 4; ++i) {
+              if ((u[i] & 0x7f800000u) == 0x7f800000u) off = true, u[i] &= 0xffffu;
+              if ((u[i] & 0x7f80u) == 0x7f80u) off = true, u[i] &= 0xffff0000u;
+            }
+            if (off) {
+              *at16 = v;
 #pragma unroll 1
-                for (int i = amin; i < amax; ++i) atomicOr(bad + 4 * wg + (i >> 5), 1u << (i & 31));
-              }
+              for (int i = amin; i < amax; ++i) atomicOr(bad + 4 * wg + (i >> 5), 1u << (i & 31));
             }
           }
         }
@@ -696,88 +798,109 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(pfull0 + 8 * buf);
       }
-      const bool more = next_unit(sn);
-      if (more) put_q(sn);  // every product with this unit's queries is done
-      // ---- the unit's sums
-      wait_sums(tt + ntl - 1);
+      // ---- the unit's sums. Every product is done: the probabilities' buffer serves as scratch
+      wait_sums(at - 1);
       __syncwarp();
       fence_after();
-      float* const red = scratch(sm + LY::p);
+      float* const red = reinterpret_cast<float*>(sm + LY::p) + wg * 5 * NC;  // [4][NC] parts of the exp-sums, [NC] their inverses
+      {
+        float v[NC];
 #pragma unroll
-      for (int i = 0; i < NC; ++i) l[i] = has ? l[i] : 0.f;
-      if constexpr (NC >= 32) {
-#pragma unroll
-        for (int i = 0; i < NC; i += 32) {
-          reduce_scatter<32, 16>(l + i, lane);
-          red[ww * NC + i + lane] = l[i];
-        }
-      } else {
-        reduce_scatter<NC, 16>(l, lane);
-        if (lane % (32 / NC) == 0) red[ww * NC + lane / (32 / NC)] = l[0];
+        for (int e = 0; e < NC; e += 2) split2(has ? l[e / 2] : two(0.f, 0.f), v[e], v[e + 1]);
+        reduce_scatter<NC, 16>(v, lane);
+        if (lane % (32 / NC) == 0) red[ww * NC + lane / (32 / NC)] = v[0];
       }
       bar_wg();
-      const bool whole = s.a == 0 && s.e == s.n;
-      const int h0 = head0(s);
-      const long long tok0 = s.s0 + static_cast<long long>(s.tile) * g.tpt;
-      const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + (s.begins ? 1 : 0)) * N;
+      const long long part = static_cast<long long>(s.part) * N;
       if (wt < nrw) {
         const int col = col0 + wt;
         float den = (red[wt] + red[NC + wt]) + (red[2 * NC + wt] + red[3 * NC + wt]);
         const float m = -negm[wt];
-        if (*dead || ((bad[col >> 5] | bad[4 + (col >> 5)]) >> (col & 31) & 1)) den = NAN;
-        if (whole) {
+        unsigned off = 0;
+#pragma unroll
+        for (int i = 0; i < WG; ++i) off |= bad[4 * i + (col >> 5)];
+        if (*dead || (off >> (col & 31) & 1)) den = NAN;
+        if (s.whole) {
           den = pg::row_sum(m, den);
           red[4 * NC + wt] = den == 0.f ? 0.f : 1.f / den;  // 0: nothing attended
           if (a.lse)
-            a.lse[(tok0 + col / Gc) * a.nh + h0 + col % Gc] = den == 0.f ? -INFINITY : (m + log2f(den)) * 0.6931471805599453f;
+            a.lse[static_cast<long long>(s.tok0 + col / s.heads) * a.nh + s.h0 + col % s.heads] =
+                den == 0.f ? -INFINITY : (m + log2f(den)) * 0.6931471805599453f;
         } else {
-          a.ws_ml[(part + col) * 2] = m;
-          a.ws_ml[(part + col) * 2 + 1] = den;
+          *reinterpret_cast<float2*>(a.ws_ml + (part + col) * 2) = make_float2(m, den);
         }
       }
       bar_wg();
+      const int tok = col0 / s.heads, skip = (a.nh - s.heads) * D;  // from a token's last head to the next one's first
+      __nv_bfloat16* out0 = static_cast<__nv_bfloat16*>(a.out) +
+                            (static_cast<long long>(s.tok0 + tok) * a.nh + s.h0 + col0 - tok * s.heads) * D + wt;
+      float* acc0 = a.ws_acc + (part + col0) * D + wt;
 #pragma unroll 1
       for (int b = 0; b < NP; ++b) {
+        __nv_bfloat16* out = out0 + b * 128;
+        int h = col0 - tok * s.heads;
 #pragma unroll 1
         for (int i = 0; i < nrw; i += 16) {
-          float v[16];
+          float v[16], f[16];
           ld16(tO + b * N + i, v);
-          ld_wait();
-          const int dim = b * 128 + wt;
-          int tok = (col0 + i) / Gc, h = (col0 + i) - tok * Gc;
+          if (s.whole) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            if (i + e < nrw) {
-              if (whole)
-                static_cast<__nv_bfloat16*>(a.out)[((tok0 + tok) * a.nh + h0 + h) * D + dim] =
-                    __float2bfloat16_rn(red[4 * NC + i + e] == 0.f ? 0.f : v[e] * red[4 * NC + i + e]);
-              else
-                a.ws_acc[(part + col0 + i + e) * D + dim] = v[e];
-              if (++h == Gc) {
+            for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(f + e) = *reinterpret_cast<const float4*>(red + 4 * NC + i + e);
+          }
+          ld_wait();
+          if (s.whole) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              if (i + e < nrw) *out = __float2bfloat16_rn(f[e] == 0.f ? 0.f : v[e] * f[e]);
+              out += D;
+              if (++h == s.heads) {
                 h = 0;
-                ++tok;
+                out += skip;
               }
             }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (i + e < nrw) acc0[b * 128 + (i + e) * D] = v[e];
           }
         }
       }
       fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(ofree);
-      if (!whole && s.begins && tid == 0) {
-        meta[0] = s.b;
-        meta[1] = s.sub;
-        meta[2] = s.tile;
-        meta[3] = static_cast<int>(s.last / w.per);
-      }
-      asm volatile("bar.sync 3, 256;" ::: "memory");  // both warpgroups have read the scratch, the marks and the references
-      tt += ntl;
-      s = sn;
-      have = more;
+      // every warpgroup has read the scratch, the marks and the references
+      asm volatile("bar.sync 5, %0;" ::"n"(128 * WG) : "memory");
+      if (lane == 0) mbar_arrive(ofree0 + 8 * (ns % kSegs));
     }
     fence_before();
   }
   __syncthreads();
+  if (*dead) {  // the rows of every unit of this CTA get NaN
+    const int G = a.nh / c.nkv;
+    Walk<LY::KS> w;
+    w.locate(g, c.nkv * g.hgs);
+    typename Walk<LY::KS>::Part u;
+    while (w.next(g, c.nkv * g.hgs, u)) {
+      const int kvh = u.sub / g.hgs, hg = u.sub % g.hgs, heads = min(N, G - hg * N), tok0 = w.s0 + (u.tile << g.ts);
+      const bool whole = u.a == 0 && u.e == u.k;
+      for (int r = tid; r < min(1 << g.ts, w.t.n - (u.tile << g.ts)) * heads; r += LY::threads) {
+        const long long row = static_cast<long long>(tok0 + r / heads) * a.nh + kvh * G + hg * N + r % heads;
+        if (!whole) {
+          float* ml = a.ws_ml + ((2LL * blockIdx.x + (u.begins ? 1 : 0)) * N + r) * 2;
+          ml[0] = 0.f;
+          ml[1] = NAN;
+          continue;
+        }
+        for (int i = 0; i < D; ++i) static_cast<__nv_bfloat16*>(a.out)[row * D + i] = __float2bfloat16_rn(NAN);
+        if (a.lse) a.lse[row] = NAN;
+      }
+      if (!whole && u.begins && tid == 0) {
+        int* meta = g.meta + 4 * blockIdx.x;
+        meta[0] = u.b;
+        meta[1] = u.sub;
+        meta[2] = u.tile;
+        meta[3] = static_cast<int>(u.last / w.per);
+      }
+    }
+  }
   if (warp == 0) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(LY::cols) : "memory");
@@ -796,10 +919,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_chunk_tc_join(const __grid_
   const ChunkArgs& a = g.a;
   int s0, n, first, L;
   pg::chunk_range(a, meta.x, s0, n, first, L);
-  const int G = a.nh / a.c.nkv, hg = meta.y % g.hgs, Gc = min(N, G - hg * N), nt = min(g.tpt, n - meta.z * g.tpt);
+  const int G = a.nh / a.c.nkv, hg = meta.y % g.hgs, Gc = min(N, G - hg * N), nt = min(1 << g.ts, n - (meta.z << g.ts));
   const int lane = threadIdx.x & 31, r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), c0 = blockIdx.x, np = meta.w - c0 + 1;
   if (r >= nt * Gc) return;
-  const long long row = (static_cast<long long>(s0) + meta.z * g.tpt + r / Gc) * a.nh + (meta.y / g.hgs) * G + hg * N + r % Gc;
+  const long long row = (static_cast<long long>(s0) + (meta.z << g.ts) + r / Gc) * a.nh + (meta.y / g.hgs) * G + hg * N + r % Gc;
   // part i: slot 1 of the first CTA, slot 0 of the next ones
   auto part = [&](int i) { return static_cast<size_t>((c0 + i) * 2 + (i == 0 ? 1 : 0)) * N + r; };
   constexpr int PW = (pg::kMaxSms + 31) / 32, V = D / 128;
@@ -851,19 +974,24 @@ int launch(const Args& g, cudaStream_t st) {
   static_assert(LY::total <= 232448, "shared memory of one CTA");
   static_assert(LY::ring >= 2 * LY::NP, "a tile of K and one of V, or two tiles");
   static_assert(LY::want <= 512, "tensor memory columns");
-  static_assert(N != 128 || 5 * LY::NC * 4 <= LY::KT * 128, "the softmax's scratch");
-  CUtensorMap mk, mv;
+  static_assert(5 * N * 4 <= LY::PBY && sizeof(Seg) == 48, "the scratch of a unit's end; the places of the units");
+  CUtensorMap mk, mv, mq;
   int rc = make_map(&mk, g.a.c, g.a.c.k, 1 << g.rshift);
   if (rc) return rc;
   mv = mk;
   if (g.a.c.v && (rc = make_map(&mv, g.a.c, g.a.c.v, 1 << g.rshift))) return rc;
+  const ChunkArgs& a = g.a;
+  const unsigned long long dim[4] = {D, static_cast<unsigned long long>(a.nh), static_cast<unsigned long long>(a.T), 1};
+  const unsigned long long stride[3] = {2 * D, 2ull * a.q_stride, 2ull * a.q_stride};
+  const unsigned box[4] = {64, static_cast<unsigned>(min(N, a.nh / a.c.nkv)), 1u << g.ts, 1};
+  if ((rc = encode_map(&mq, a.q, dim, stride, box, "the queries"))) return rc;
   const cudaError_t e = pg::allow_smem<k_chunk_tc<D, N>, LY::total>();
   if (e != cudaSuccess) {
     cudaGetLastError();
     set_error("chunk attention: %s", cudaGetErrorString(e));
     return MTP_ERR_CUDA;
   }
-  rc = pg::launch_pdl("chunk attention", k_chunk_tc<D, N>, dim3(g.grid), kThreads, LY::total, st, mk, mv, g);
+  rc = pg::launch_pdl("chunk attention", k_chunk_tc<D, N>, dim3(g.grid), LY::threads, LY::total, st, mk, mv, mq, g);
   return rc ? rc : pg::launch_pdl("chunk attention join", k_chunk_tc_join<D>, dim3(g.grid, N / kJoinWarps), kJoinWarps * 32, 0, st, g, N);
 }
 
@@ -888,9 +1016,9 @@ int run_chunk_tc(const pg::ChunkArgs& a, void* ws, int num_sms, cudaStream_t st)
   const int P = 1 << a.c.pshift, G = a.nh / a.c.nkv, N = chunk_tc_rows(a), KT = a.c.d == 512 ? 64 : 128;
   const int rows = P < KT ? P : KT;
   while ((1 << g.rshift) < rows) ++g.rshift;
-  g.tpt = 1;
-  while (g.tpt * 2 * G <= N) g.tpt *= 2;
+  while ((2 << g.ts) * G <= N) ++g.ts;
   g.hgs = (G + N - 1) / N;
+  g.qbytes = 128 * (G < N ? G : N) << g.ts;
   g.grid = num_sms;
   g.meta = static_cast<int*>(ws);
   g.a.ws_ml = reinterpret_cast<float*>(g.meta + 4 * pg::kMaxSms);

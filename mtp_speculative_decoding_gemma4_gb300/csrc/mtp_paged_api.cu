@@ -295,8 +295,8 @@ int mtp_paged_attention_chunk(const mtp_paged_kv* kv, const void* q, int64_t q_s
   }
   const int vec = a.c.f32 ? 4 : 8, size = a.c.f32 ? 4 : 2;
   const long long width = static_cast<long long>(n_head) * a.c.d;
-  if (T > 0 && (q_stride < width || q_stride % vec || q_stride > (1LL << 40))) {
-    set_error("q_stride=%lld must be n_head * head_dim = %lld to 2^40 elements, a multiple of %d",
+  if (T > 0 && (q_stride < width || q_stride % vec || q_stride > (1LL << 38))) {
+    set_error("q_stride=%lld must be n_head * head_dim = %lld to 2^38 elements, a multiple of %d",
               static_cast<long long>(q_stride), width, vec);
     return MTP_ERR_INVALID_ARG;
   }

@@ -114,6 +114,10 @@ __device__ __forceinline__ void st4(unsigned t, const float* v) {
 }
 __device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
+// A map of a bf16 tensor of four dimensions (the innermost first, strides in bytes from the second
+// on), 128-byte swizzle, zeros outside.
+int encode_map(CUtensorMap* map, const void* p, const unsigned long long* dims, const unsigned long long* strides,
+               const unsigned* box_dims, const char* what);
 // A map of the pages from `p` (k or v of the cache): boxes of `rows` tokens x 64 dims of one KV head
 // of one page, 128-byte swizzle; rows of no page read as zeros.
 int make_map(CUtensorMap* map, const pg::Cache& c, const void* p, int rows);

@@ -975,12 +975,16 @@ static PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
-int make_map(CUtensorMap* map, const Cache& c, const void* p, int rows) {
-  const cuuint64_t dim[4] = {static_cast<cuuint64_t>(c.d), 1ull << c.pshift, static_cast<cuuint64_t>(c.nkv),
-                             static_cast<cuuint64_t>(c.n_pages)};
-  const cuuint64_t str[3] = {static_cast<cuuint64_t>(c.st) * 2, static_cast<cuuint64_t>(c.sh) * 2,
-                             static_cast<cuuint64_t>(c.sp) * 2};
-  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows), 1, 1}, one[4] = {1, 1, 1, 1};
+int encode_map(CUtensorMap* map, const void* p, const unsigned long long* dims, const unsigned long long* strides,
+               const unsigned* box_dims, const char* what) {
+  cuuint64_t dim[4], str[3];
+  cuuint32_t box[4];
+  for (int i = 0; i < 4; ++i) {
+    dim[i] = dims[i];
+    box[i] = box_dims[i];
+    if (i < 3) str[i] = strides[i];
+  }
+  const cuuint32_t one[4] = {1, 1, 1, 1};
   const PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
   const auto encode = [&] {
     return enc ? enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p), dim, str, box, one,
@@ -995,10 +999,18 @@ int make_map(CUtensorMap* map, const Cache& c, const void* p, int rows) {
     if (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) r = encode();
   }
   if (r != CUDA_SUCCESS) {
-    set_error("cuTensorMapEncodeTiled failed (%d) for a paged cache", static_cast<int>(r));
+    set_error("cuTensorMapEncodeTiled failed (%d) for %s", static_cast<int>(r), what);
     return MTP_ERR_CUDA;
   }
   return MTP_OK;
+}
+
+int make_map(CUtensorMap* map, const Cache& c, const void* p, int rows) {
+  const unsigned long long dim[4] = {static_cast<unsigned long long>(c.d), 1ull << c.pshift,
+                                     static_cast<unsigned long long>(c.nkv), static_cast<unsigned long long>(c.n_pages)};
+  const unsigned long long str[3] = {2ull * c.st, 2ull * c.sh, 2ull * c.sp};
+  const unsigned box[4] = {64, static_cast<unsigned>(rows), 1, 1};
+  return encode_map(map, p, dim, str, box, "a paged cache");
 }
 
 // Clusters of the clustered form that the current device runs side by side (each CTA takes an SM, and
