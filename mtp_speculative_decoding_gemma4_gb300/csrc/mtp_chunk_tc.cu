@@ -86,9 +86,11 @@ struct Lay {
   static constexpr int fac = top + N * 4;                // [N] factors of the sums under a new reference
   static constexpr int segs = fac + N * 4;               // [kSegs][12] units (Seg below)
   static constexpr int info = segs + kSegs * 48;         // [kInfo][16] physical pages of a tile's boxes
-  static constexpr int bad = info + kInfo * 64;          // per warpgroup [4]: rows that attend values that are not finite
-  static constexpr int bars = bad + WG * 16;
-  static constexpr int nbars = 2 * ring + 2 * 4 + 3 + 2 * kSegs + kInfo;
+  static constexpr int holes = info + kInfo * 64;        // [kInfo] whether a tile lacks a page
+  static constexpr int bad = holes + kInfo * 4;          // per warpgroup [4]: rows that attend values that are not finite
+  static constexpr int over = bad + WG * 16;             // per warpgroup [2]: a score of a tile of this parity exceeds its reference by 2^8
+  static constexpr int bars = over + WG * 8;
+  static constexpr int nbars = 2 * ring + 2 * 4 + 3 + 2 * kSegs + kInfo + WG;
   static constexpr int misc = bars + nbars * 8;          // tensor-memory address, dead word, tiles begun
   static constexpr int total = misc + 16;
   static constexpr int want = (NP + 2) * N;              // tensor-memory columns: sums, two of scores
@@ -300,11 +302,12 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   // barriers: loaded slots, free slots; per score buffer: scores done, scores read; per parity of a
   // tile: probabilities written, sums done; queries loaded, queries used, drained; per place of a
-  // unit: its sums are read, it is found; pages of a tile found
+  // unit: its sums are read, it is found; pages of a tile found; per warpgroup: a tile's maxima compared
   const unsigned full0 = base + LY::bars, empty0 = full0 + 8 * kRing, sfull0 = empty0 + 8 * kRing, sfree0 = sfull0 + 16,
                  pfull0 = sfree0 + 16, odone0 = pfull0 + 16, qfull = odone0 + 16, qused = qfull + 8, drain = qused + 8,
-                 ofree0 = drain + 8, seg0 = ofree0 + 8 * kSegs, ifull0 = seg0 + 8 * kSegs;
+                 ofree0 = drain + 8, seg0 = ofree0 + 8 * kSegs, ifull0 = seg0 + 8 * kSegs, agree0 = ifull0 + 8 * kInfo;
   int* info = reinterpret_cast<int*>(sm + LY::info);
+  int* holes = reinterpret_cast<int*>(sm + LY::holes);
   Seg* segs = reinterpret_cast<Seg*>(sm + LY::segs);
   int* misc = reinterpret_cast<int*>(sm + LY::misc);  // 0: tensor memory, 1: dead, 2: begun
   volatile int *dead = misc + 1, *begun = misc + 2;   // begun: tiles that the load warp has begun
@@ -332,6 +335,8 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
       mbar_init(seg0 + 8 * i, 1);
     }
     for (int i = 0; i < kInfo; ++i) mbar_init(ifull0 + 8 * i, 1);
+    for (int i = 0; i < WG; ++i) mbar_init(agree0 + 8 * i, 4);
+    for (int i = 0; i < 2 * WG; ++i) reinterpret_cast<int*>(sm + LY::over)[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     misc[1] = (base & 1023u) != 0;  // (every wait then gives up)
     misc[2] = 0;
@@ -426,7 +431,9 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
           }
+          const unsigned none = __ballot_sync(0xffffffffu, lane >> ngs == j && page < 0);
           if (lane >> ngs == j) info[slot * 16 + (lane & (ng - 1))] = page;
+          if (lane == 0) holes[slot] = none != 0;
           __syncwarp();
           if (lane == 0) mbar_arrive(ifull0 + 8 * slot);
           if (++slot == kInfo) slot = 0;
@@ -511,39 +518,43 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
     }
     __syncwarp();
   } else if (warp == 4 * WG + 1) {
-    if (elect()) {
-      // ---------------- MMA issue: the next sums or the next scores, whichever are ready.
-      // fp32 += bf16 x bf16, N columns; scores: M = KT; sums: M = 128, A and B MN-major
-      const unsigned id = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<unsigned>(N >> 3) << 17);
-      const unsigned idS = id | (static_cast<unsigned>(KT >> 4) << 24), idO = id | (1u << 15) | (1u << 16) | (8u << 24);
-      const unsigned tO = tmem, tS = tmem + NP * N;
-      const unsigned kd = desc_lo(base, 16), vd = desc_lo(base, LY::box), qd = desc_lo(base + LY::q, 16),
-                     pd = desc_lo(base + LY::p, KT * 128);
-      // tiles whose scores / sums are issued; tiles left of the scores' unit; units begun by either;
-      // ring places
-      int tq = 0, tp = 0, left = 0, nseg = 0, pseg = 0, sq = 0, sp = own_v ? NP : 0;
-      unsigned fq = 0, fp = 0, starts = 0;  // starts bit i: tile tp + i is its unit's first
-      bool more = true, fresh = false;
-      long long t0 = clock64();
+    // ---------------- MMA issue: the next sums or the next scores, whichever are ready. The whole warp
+    // walks, on conditions that are votes, so that addresses and descriptors are uniform registers; one
+    // elected thread (always the same) issues.
+    // fp32 += bf16 x bf16, N columns; scores: M = KT; sums: M = 128, A and B MN-major
+    constexpr unsigned id = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<unsigned>(N >> 3) << 17);
+    constexpr unsigned idS = id | (static_cast<unsigned>(KT >> 4) << 24), idO = id | (1u << 15) | (1u << 16) | (8u << 24);
+    const unsigned tO = tmem, tS = tmem + NP * N;
+    const unsigned kd = desc_lo(base, 16), vd = desc_lo(base, LY::box), qd = desc_lo(base + LY::q, 16),
+                   pd = desc_lo(base + LY::p, KT * 128);
+    auto done = [](unsigned bar, unsigned parity) { return __all_sync(0xffffffffu, test_wait(bar, parity)) != 0; };
+    // tiles whose scores / sums are issued; tiles left of the scores' unit; units begun by either; ring
+    // places
+    int tq = 0, tp = 0, left = 0, nseg = 0, pseg = 0, sq = 0, sp = own_v ? NP : 0;
+    unsigned fq = 0, fp = 0, starts = 0;  // starts bit i: tile tp + i is its unit's first
+    bool more = true, fresh = false;
+    long long t0 = clock64();
 #pragma unroll 1
-      while (more || tp < tq) {
-        bool did = false;
-        if (more && left == 0 && test_wait(seg0 + 8 * (nseg % kSegs), (nseg / kSegs) & 1)) {
-          left = *reinterpret_cast<volatile int*>(&segs[nseg % kSegs].tiles);
-          if (left < 0) {
-            more = false;
-            left = 0;
-          }
-          ++nseg;
-          fresh = true;
-          did = true;
+    while (more || tp < tq) {
+      bool did = false;
+      if (more && left == 0 && done(seg0 + 8 * (nseg % kSegs), (nseg / kSegs) & 1)) {
+        left = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&segs[nseg % kSegs].tiles), 0);
+        if (left < 0) {
+          more = false;
+          left = 0;
         }
-        if (tp < tq) {
-          const bool first = starts & 1;
-          if (test_wait(pfull0 + 8 * (tp & 1), (tp >> 1) & 1) &&
-              (!first || pseg == 0 || test_wait(ofree0 + 8 * ((pseg - 1) % kSegs), ((pseg - 1) / kSegs) & 1))) {
-            if (own_v)
-              for (int i = 0; i < NP; ++i) wait_in(full0 + 8 * (sp + i), fp, dead, kSpin);
+        ++nseg;
+        fresh = true;
+        did = true;
+      }
+      if (tp < tq) {
+        const bool first = starts & 1;
+        bool ready = done(pfull0 + 8 * (tp & 1), (tp >> 1) & 1) &&
+                     (!first || pseg == 0 || done(ofree0 + 8 * ((pseg - 1) % kSegs), ((pseg - 1) / kSegs) & 1));
+        if (own_v)
+          for (int i = 0; i < NP; ++i) ready = ready && done(full0 + 8 * (sp + i), fp);
+        if (ready) {
+          if (elect()) {
             fence_after();
             const unsigned v0 = vd + sp * (LY::slot >> 4), p0 = pd + (PB == 1 ? 0 : (tp & 1) * (LY::PBY >> 4));
 #pragma unroll
@@ -554,22 +565,24 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
               commit(empty0 + 8 * (sp + i));
             }
             commit(odone0 + 8 * (tp & 1));
-            if (first) ++pseg;
-            starts >>= 1;
-            ++tp;
-            if ((sp += PT) >= kRing) {
-              sp -= kRing;
-              fp ^= 1;
-            }
-            did = true;
           }
+          __syncwarp();
+          if (first) ++pseg;
+          starts >>= 1;
+          ++tp;
+          if ((sp += PT) >= kRing) {
+            sp -= kRing;
+            fp ^= 1;
+          }
+          did = true;
         }
-        if (left > 0 && tq < tp + 2) {
-          bool ready = (!fresh || test_wait(qfull, (nseg - 1) & 1)) &&
-                       (tq < 2 || test_wait(sfree0 + 8 * (tq & 1), ((tq >> 1) - 1) & 1));
+      }
+      if (left > 0 && tq < tp + 2) {
+        bool ready = (!fresh || done(qfull, (nseg - 1) & 1)) && (tq < 2 || done(sfree0 + 8 * (tq & 1), ((tq >> 1) - 1) & 1));
 #pragma unroll
-          for (int i = 0; i < NP; ++i) ready = ready && test_wait(full0 + 8 * (sq + i), fq);
-          if (ready) {
+        for (int i = 0; i < NP; ++i) ready = ready && done(full0 + 8 * (sq + i), fq);
+        if (ready) {
+          if (elect()) {
             fence_after();
             const unsigned k0 = kd + sq * (LY::slot >> 4), d = tS + (tq & 1) * N;
 #pragma unroll
@@ -581,31 +594,32 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
               if (own_v) commit(empty0 + 8 * (sq + i));
             }
             commit(sfull0 + 8 * (tq & 1));
-            starts = (starts & ~(1u << (tq - tp))) | (static_cast<unsigned>(fresh) << (tq - tp));
-            fresh = false;
-            ++tq;
-            if (--left == 0) commit(qused);
-            if ((sq += PT) >= kRing) {
-              sq -= kRing;
-              fq ^= 1;
-            }
-            did = true;
+            if (left == 1) commit(qused);
           }
-        }
-        if (did) {
-          t0 = clock64();
-        } else if (*dead) {
-          break;
-        } else if (clock64() - t0 > kSpin) {
-          *dead = 1;
-          break;
+          __syncwarp();
+          starts = (starts & ~(1u << (tq - tp))) | (static_cast<unsigned>(fresh) << (tq - tp));
+          fresh = false;
+          ++tq;
+          --left;
+          if ((sq += PT) >= kRing) {
+            sq -= kRing;
+            fq ^= 1;
+          }
+          did = true;
         }
       }
-      if (*dead) {  // the products that were issued still run: wait for them
-        commit(drain);
+      if (did) {
         t0 = clock64();
-        while (!try_wait(drain, 0) && clock64() - t0 < kSpin) {
-        }
+      } else if (__any_sync(0xffffffffu, *dead || clock64() - t0 > kSpin)) {
+        *dead = 1;
+        break;
+      }
+    }
+    __syncwarp();
+    if (__any_sync(0xffffffffu, *dead) && elect()) {  // the products that were issued still run: wait for them
+      commit(drain);
+      t0 = clock64();
+      while (!try_wait(drain, 0) && clock64() - t0 < kSpin) {
       }
     }
     __syncwarp();
@@ -620,6 +634,8 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
     int* const top = reinterpret_cast<int*>(sm + LY::top) + col0;
     float* const fac = reinterpret_cast<float*>(sm + LY::fac) + col0;
     unsigned* const bad = reinterpret_cast<unsigned*>(sm + LY::bad);
+    volatile int* const over = reinterpret_cast<int*>(sm + LY::over) + 2 * wg;
+    unsigned agreed = 0;  // the phase of the warpgroup's agreement
     // this thread's key of a tile: the accumulator row of its tensor-memory lane (M = 64 fills the
     // lower half of each warp's lanes)
     const int key = KT == 128 ? wt : 16 * ww + lane;
@@ -645,6 +661,8 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
       f2 l[NC / 2];
 #pragma unroll
       for (int i = 0; i < NC / 2; ++i) l[i] = two(0.f, 0.f);
+      // keys that every row attends: [in_lo, in_hi)
+      const int in_lo = max(s.lo, a.window > 0 ? s.pos0 + s.nt - a.window : 0), in_hi = s.pos0 + 1;
 #pragma unroll 1
       for (int t = 0; t < s.tiles; ++t, ++at) {
         const int buf = at & 1;
@@ -657,12 +675,16 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
         // the rows [cmin, cmax) of this warpgroup attend this thread's key (its pages were found before
         // they were loaded)
         const int pos = ((s.k0 + t) << LY::KS) + key, rel = pos - s.pos0;
-        const int page = has ? info[is * 16 + (key >> rs)] : -1;
+        bool valid = true, edge = pos - key < in_lo || pos - key + KT > in_hi || holes[is] != 0;
+        int page = 0, cmin = -col0, cmax = nr - col0;
+        if (edge) {
+          page = has ? info[is * 16 + (key >> rs)] : -1;
+          valid = page >= 0 && pos >= s.lo && pos < s.hi;
+          if (!valid) cmin = NC;
+          else if (rel > 0) cmin += rel * s.heads;
+          if (a.window > 0 && a.window < s.nt - rel) cmax = (rel + a.window) * s.heads - col0;
+        }
         if (++is == kInfo) is = 0;
-        const bool valid = page >= 0 && pos >= s.lo && pos < s.hi;
-        const int cmin = (valid ? max(rel, 0) * s.heads : N) - col0;
-        const int cmax = (a.window > 0 && a.window < s.nt - rel ? (rel + a.window) * s.heads : nr) - col0;
-        const bool masked = !__all_sync(0xffffffffu, !has || (cmin <= 0 && cmax >= nrw));
         if (nrw) {
 #pragma unroll 1
           for (int pass = 0;; ++pass) {
@@ -675,25 +697,34 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
               split2(fma2(two(x[i], x[i + 1]), scale2, m.x), x[i], x[i + 1]);
               split2(fma2(two(x[i + 2], x[i + 3]), scale2, m.y), x[i + 2], x[i + 3]);
             }
-            if (masked) {
+            if (edge) {
               const unsigned on = bits(cmin, cmax);
 #pragma unroll
               for (int i = 0; i < NC; ++i) x[i] = on >> i & 1 ? x[i] : -INFINITY;
             }
-            if (pass) break;
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            if (!pass && t) {
+              float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < NC; i += 8) {
+              for (int i = 0; i < NC; i += 8) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], fmaxf(x[i + 2 * e], x[i + 2 * e + 1]));
+                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], fmaxf(x[i + 2 * e], x[i + 2 * e + 1]));
+              }
+              const bool up = has && fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) > 8.f;
+              const bool any = __any_sync(0xffffffffu, up);
+              if (lane == 0) {
+                if (any) over[buf] = 1;
+                mbar_arrive(agree0 + 8 * wg);
+              }
             }
-            const bool up = t == 0 || (has && fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) > 8.f);
-            int any;
-            asm volatile("{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n bar.red.or.pred q, %2, 128, p;\n selp.s32 %0, 1, 0, q;\n}"
-                         : "=r"(any)
-                         : "r"(up ? 1 : 0), "r"(1 + wg)
-                         : "memory");
-            if (!any) break;
+            // (while the warps agree that no reference has to move)
+#pragma unroll
+            for (int i = 0; i < NC; ++i) x[i] = ex2(x[i]);
+            if (pass) break;
+            if (t) {
+              wait_in(agree0 + 8 * wg, agreed, dead, kSpin);
+              agreed ^= 1;
+              if (!over[buf]) break;
+            }
             // new references: the maxima so far, 16 rows at a time from the scores once more (a short
             // loop: a unit's first tile meets a cold instruction cache)
             if (t > 0) wait_sums(at - 1);
@@ -714,6 +745,7 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
               if (lane < 16) atomicMax(top + i0 + lane, mine);
             }
             bar_wg();
+            if (wt == 0) over[buf] = 0;
             if (wt < NC) {
               const float mo = -negm[wt], mn = fmaxf(unordered(top[wt]), mo);
               top[wt] = kLowest;
@@ -750,13 +782,13 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(sfree0 + 8 * buf);
-        if (at >= PB) wait_sums(at - PB);  // the buffer's last probabilities are used
+        // the buffer's last probabilities are used: with two buffers the scores of this tile were issued
+        // behind the sums of the tile before the last
+        if (PB == 1 && at > 0) wait_sums(at - 1);
         if (nrw) {
           char* const prow = pbuf + (col0 >> 6) * (KT * 128) + key * 128;
 #pragma unroll
           for (int i = 0; i < NC; i += 8) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[i + e] = ex2(x[i + e]);
 #pragma unroll
             for (int e = 0; e < 8; e += 2) l[(i + e) / 2] = add2(l[(i + e) / 2], two(x[i + e], x[i + e + 1]));
             if (has)
@@ -767,7 +799,7 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
         // keys of the tile that no row of the unit attends, and values that are not finite in keys that
         // only some do: this warpgroup's part of the dims
         const int amin = cmin + col0, amax = min(cmax + col0, nr);
-        if (has && page >= 0 && (!valid || amin > 0 || amax < nr)) {
+        if (edge && has && page >= 0 && (!valid || amin > 0 || amax < nr)) {
           constexpr int V = D / 8 / WG;
 #pragma unroll 1
           for (int e = wg * V; e < (wg + 1) * V; ++e) {  // vectors of 8 dims
@@ -802,7 +834,7 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
       wait_sums(at - 1);
       __syncwarp();
       fence_after();
-      float* const red = reinterpret_cast<float*>(sm + LY::p) + wg * 5 * NC;  // [4][NC] parts of the exp-sums, [NC] their inverses
+      float* const red = reinterpret_cast<float*>(sm + LY::p) + wg * 4 * NC;  // [4][NC] parts of the exp-sums
       {
         float v[NC];
 #pragma unroll
@@ -822,7 +854,7 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
         if (*dead || (off >> (col & 31) & 1)) den = NAN;
         if (s.whole) {
           den = pg::row_sum(m, den);
-          red[4 * NC + wt] = den == 0.f ? 0.f : 1.f / den;  // 0: nothing attended
+          fac[wt] = den == 0.f ? 0.f : 1.f / den;  // 0: nothing attended
           if (a.lse)
             a.lse[static_cast<long long>(s.tok0 + col / s.heads) * a.nh + s.h0 + col % s.heads] =
                 den == 0.f ? -INFINITY : (m + log2f(den)) * 0.6931471805599453f;
@@ -831,37 +863,45 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
         }
       }
       bar_wg();
-      const int tok = col0 / s.heads, skip = (a.nh - s.heads) * D;  // from a token's last head to the next one's first
-      __nv_bfloat16* out0 = static_cast<__nv_bfloat16*>(a.out) +
-                            (static_cast<long long>(s.tok0 + tok) * a.nh + s.h0 + col0 - tok * s.heads) * D + wt;
-      float* acc0 = a.ws_acc + (part + col0) * D + wt;
+      if (s.whole) {
+        // by way of shared memory, 128 dims at a time: 16-byte stores of whole rows
+        __nv_bfloat16* const rows = reinterpret_cast<__nv_bfloat16*>(sm + LY::p) + col0 * 128;
+        const unsigned inv = (65536 + s.heads - 1) / s.heads;  // r / heads = r * inv >> 16 for r, heads <= 128
+        __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.out) + (static_cast<long long>(s.tok0) * a.nh + s.h0) * D;
+        asm volatile("bar.sync 5, %0;" ::"n"(128 * WG) : "memory");  // (every warpgroup's parts are read)
 #pragma unroll 1
-      for (int b = 0; b < NP; ++b) {
-        __nv_bfloat16* out = out0 + b * 128;
-        int h = col0 - tok * s.heads;
-#pragma unroll 1
-        for (int i = 0; i < nrw; i += 16) {
-          float v[16], f[16];
-          ld16(tO + b * N + i, v);
-          if (s.whole) {
+        for (int b = 0; b < NP; ++b) {
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(f + e) = *reinterpret_cast<const float4*>(red + 4 * NC + i + e);
+          for (int i = 0; i < NC; i += 16) {
+            float v[16], f[16];
+            ld16(tO + b * N + i, v);
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(f + e) = *reinterpret_cast<const float4*>(fac + i + e);
+            ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) rows[(i + e) * 128 + wt] = __float2bfloat16_rn(f[e] == 0.f ? 0.f : v[e] * f[e]);
           }
-          ld_wait();
-          if (s.whole) {
+          bar_wg();
+#pragma unroll 1
+          for (int i = wt; i < nrw * 16; i += 128) {
+            const int r = col0 + (i >> 4), tok = static_cast<int>(r * inv >> 16);
+            *reinterpret_cast<uint4*>(out + (static_cast<long long>(tok) * a.nh + r - tok * s.heads) * D + b * 128 + (i & 15) * 8) =
+                *reinterpret_cast<const uint4*>(rows + (i >> 4) * 128 + (i & 15) * 8);
+          }
+          bar_wg();
+        }
+      } else {
+        float* acc = a.ws_acc + (part + col0) * D + wt;
+#pragma unroll 1
+        for (int b = 0; b < NP; ++b, acc += 128) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              if (i + e < nrw) *out = __float2bfloat16_rn(f[e] == 0.f ? 0.f : v[e] * f[e]);
-              out += D;
-              if (++h == s.heads) {
-                h = 0;
-                out += skip;
-              }
-            }
-          } else {
+          for (int i = 0; i < NC; i += 16) {
+            float v[16];
+            ld16(tO + b * N + i, v);
+            ld_wait();
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              if (i + e < nrw) acc0[b * 128 + (i + e) * D] = v[e];
+              if (i + e < nrw) acc[(i + e) * D] = v[e];
           }
         }
       }
@@ -974,7 +1014,7 @@ int launch(const Args& g, cudaStream_t st) {
   static_assert(LY::total <= 232448, "shared memory of one CTA");
   static_assert(LY::ring >= 2 * LY::NP, "a tile of K and one of V, or two tiles");
   static_assert(LY::want <= 512, "tensor memory columns");
-  static_assert(5 * N * 4 <= LY::PBY && sizeof(Seg) == 48, "the scratch of a unit's end; the places of the units");
+  static_assert(N * 256 <= LY::PB * LY::PBY && sizeof(Seg) == 48, "128 dims of the rows; the places of the units");
   CUtensorMap mk, mv, mq;
   int rc = make_map(&mk, g.a.c, g.a.c.k, 1 << g.rshift);
   if (rc) return rc;
