@@ -50,7 +50,7 @@ using pg::Tiles;
 constexpr int kAhead = 4;       // tiles that the find warp runs ahead of the load warp
 constexpr int kInfo = 12;       // tiles whose pages are kept: kAhead and those between load and softmax
 constexpr int kSegs = 4;        // units whose descriptions are kept
-constexpr int kExtra = 2;       // what beginning a unit costs, in key tiles
+constexpr int kExtra = 4;       // what beginning a unit costs, in key tiles
 
 struct Args {
   ChunkArgs a;
@@ -532,6 +532,7 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
     // places
     int tq = 0, tp = 0, left = 0, nseg = 0, pseg = 0, sq = 0, sp = own_v ? NP : 0;
     unsigned fq = 0, fp = 0, starts = 0;  // starts bit i: tile tp + i is its unit's first
+    int got = 0;  // of the next scores' conditions (queries, buffer, slots), how many hold: each is polled until it does
     bool more = true, fresh = false;
     long long t0 = clock64();
 #pragma unroll 1
@@ -578,10 +579,13 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
         }
       }
       if (left > 0 && tq < tp + 2) {
-        bool ready = (!fresh || done(qfull, (nseg - 1) & 1)) && (tq < 2 || done(sfree0 + 8 * (tq & 1), ((tq >> 1) - 1) & 1));
+        if (got == 0 && (!fresh || done(qfull, (nseg - 1) & 1))) got = 1;
+        if (got == 1 && (tq < 2 || done(sfree0 + 8 * (tq & 1), ((tq >> 1) - 1) & 1))) got = 2;
 #pragma unroll
-        for (int i = 0; i < NP; ++i) ready = ready && done(full0 + 8 * (sq + i), fq);
-        if (ready) {
+        for (int i = 0; i < NP; ++i)
+          if (got == 2 + i && done(full0 + 8 * (sq + i), fq)) got = 3 + i;
+        if (got == 2 + NP) {
+          got = 0;
           if (elect()) {
             fence_after();
             const unsigned k0 = kd + sq * (LY::slot >> 4), d = tS + (tq & 1) * N;
