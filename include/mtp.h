@@ -260,6 +260,32 @@ MTP_API int mtp_verify_sample(const void *target_logits, const int32_t *draft, i
                               const float *u_sample, int32_t *accept_len, int32_t *out_tokens,
                               void *stream);
 
+/* Log probabilities of given tokens, with the rows' entropies and most probable tokens, in one pass
+ * over the logits (what a serving program answers with beside the tokens: rows of a prompt, or the
+ * target's rows of a verified draft block with the emitted tokens). The pages have no counterpart.
+ * With p = softmax(row / temperature): logprob = ln p[token], entropy = -sum_i p_i ln p_i (0 ln 0 = 0),
+ * top_ids the top_k tokens of the largest logits in descending order (ties: lower id first) and
+ * top_logprobs their ln p. fp32 arithmetic from the logits as they are. -inf is a logit of
+ * probability 0, also among the top_k where fewer are above it. A row without a softmax (a NaN, a
+ * +inf, or nothing above -inf) gets NaN for its values and -1 for its ids; a token outside [0, V)
+ * gets a logprob of NaN.
+ *   logits       device [rows][V], dtype (enum mtp_dtype), row_stride elements apart (>= V; any
+ *                alignment of the type)
+ *   token        device [rows] int32 (may be NULL when logprob is)
+ *   temperature  host float in [1e-30, 1e30]
+ *   logprob, entropy  device [rows] fp32, or NULL
+ *   top_ids, top_logprobs  device [rows][top_k] int32 and fp32 (may be NULL when top_k == 0)
+ *   workspace    16-byte aligned, of mtp_token_logprobs_workspace bytes (0 where rows are many), not
+ *                shared by calls that may overlap
+ * rows <= 2^24, V <= 2^30, top_k <= MTP_MAX_TOP_K. Outputs are buffers of their own. May be captured into
+ * CUDA graphs. Errors: INVALID_ARG, CUDA. */
+#define MTP_MAX_TOP_K 32
+MTP_API int mtp_token_logprobs(const void *logits, int32_t dtype, int64_t row_stride, const int32_t *token,
+                               int32_t rows, int32_t V, float temperature, int32_t top_k, float *logprob,
+                               float *entropy, int32_t *top_ids, float *top_logprobs, void *workspace,
+                               int64_t workspace_bytes, void *stream);
+MTP_API int mtp_token_logprobs_workspace(int32_t dtype, int32_t rows, int32_t V, int32_t top_k, int64_t *bytes);
+
 /* Size of the static device scratch of mtp_centroid_head_noalloc (1 MiB). */
 #define MTP_NOALLOC_SCRATCH_BYTES (1u << 20)
 

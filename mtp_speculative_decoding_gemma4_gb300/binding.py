@@ -22,7 +22,7 @@ EXPORTS = ("mtp_init_weights", "mtp_draft_block", "mtp_centroid_head", "mtp_veri
            "mtp_verify_sample", "mtp_set_sparse_head", "mtp_set_debug", "mtp_page_plan", "mtp_page_append",
            "mtp_page_select", "mtp_page_select_workspace", "mtp_paged_attention", "mtp_paged_attention_workspace",
            "mtp_draft_block_paged", "mtp_draft_block_paged_workspace", "mtp_paged_attention_chunk",
-           "mtp_paged_attention_chunk_workspace")
+           "mtp_paged_attention_chunk_workspace", "mtp_token_logprobs", "mtp_token_logprobs_workspace")
 MASK_NEG_1E30, MASK_MIN_MINUS_ONE = 0, 1  # enum mtp_logit_mask
 HEAD_AUTO, HEAD_PER_SEQUENCE, HEAD_CLUSTER_MAJOR = 0, 1, 2  # enum mtp_sparse_head
 
@@ -98,6 +98,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mtp_paged_attention_workspace.argtypes = [pkv, i32, i32, i32, ctypes.POINTER(i64)]
     lib.mtp_paged_attention_chunk.argtypes = [pkv, vp, i64, vp, i32, i32, i32, i32, f32, vp, vp, vp, i64, vp]
     lib.mtp_paged_attention_chunk_workspace.argtypes = [pkv, i32, i32, i32, ctypes.POINTER(i64)]
+    lib.mtp_token_logprobs.argtypes = [vp, i32, i64, vp, i32, i32, f32, i32, vp, vp, vp, vp, vp, i64, vp]
+    lib.mtp_token_logprobs_workspace.argtypes = [i32, i32, i32, i32, ctypes.POINTER(i64)]
     lib.mtp_page_select.argtypes = [pkv, vp, i32, i32, i32, i32, i32, vp, vp, i64, vp]
     lib.mtp_page_select_workspace.argtypes = [pkv, i32, ctypes.POINTER(i64)]
     lib.mtp_draft_block_paged.argtypes = [vp, vp, vp, pkv, pkv, vp, i32, i32, i32, i32, i32, vp, vp, vp, i64, vp]
@@ -111,7 +113,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                  "mtp_verify_sample", "mtp_set_sparse_head", "mtp_set_debug", "mtp_page_plan", "mtp_page_append",
                  "mtp_page_select", "mtp_page_select_workspace", "mtp_paged_attention",
                  "mtp_paged_attention_workspace", "mtp_draft_block_paged", "mtp_draft_block_paged_workspace",
-                 "mtp_paged_attention_chunk", "mtp_paged_attention_chunk_workspace"):
+                 "mtp_paged_attention_chunk", "mtp_paged_attention_chunk_workspace", "mtp_token_logprobs",
+                 "mtp_token_logprobs_workspace"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -159,6 +162,22 @@ def mtp_verify_sample(target_logits: int, draft: int, B: int, n: int, V: int, te
     _check(load_library().mtp_verify_sample(target_logits, draft or None, B, n, V, float(temperature),
                                             u_accept or None, u_sample, accept_len, out_tokens, stream or None),
            "mtp_verify_sample")
+
+
+def mtp_token_logprobs_workspace(dtype: int, rows: int, V: int, top_k: int) -> int:
+    n = ctypes.c_int64()
+    _check(load_library().mtp_token_logprobs_workspace(dtype, rows, V, top_k, ctypes.byref(n)),
+           "mtp_token_logprobs_workspace")
+    return n.value
+
+
+def mtp_token_logprobs(logits: int, dtype: int, row_stride: int, token: int, rows: int, V: int, temperature: float,
+                       top_k: int, logprob: int, entropy: int, top_ids: int, top_logprobs: int, workspace: int,
+                       workspace_bytes: int, stream: int = 0) -> None:
+    _check(load_library().mtp_token_logprobs(logits or None, dtype, row_stride, token or None, rows, V,
+                                             float(temperature), top_k, logprob or None, entropy or None,
+                                             top_ids or None, top_logprobs or None, workspace or None, workspace_bytes,
+                                             stream or None), "mtp_token_logprobs")
 
 
 def mtp_centroid_head_noalloc(y: int, centroids: int, token_ordering: int, token_embd: int, dtype: int, B: int,

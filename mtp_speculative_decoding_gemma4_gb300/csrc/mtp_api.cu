@@ -1218,6 +1218,68 @@ int mtp_verify_sample(const void* target_logits, const int32_t* draft, int32_t B
                                 st);
 }
 
+static int check_scores(int32_t dtype, int32_t rows, int32_t V, int32_t top_k) {
+  if (dtype != MTP_DTYPE_BF16 && dtype != MTP_DTYPE_F32) {
+    set_error("dtype=%d is neither BF16 nor F32", dtype);
+    return MTP_ERR_INVALID_ARG;
+  }
+  if (rows < 0 || rows > 1 << 24 || V < 1 || V > 1 << 30 || top_k < 0 || top_k > MTP_MAX_TOP_K || top_k > V) {
+    set_error("need 0 <= rows <= 2^24, 1 <= V <= 2^30 and 0 <= top_k <= %d and V (rows=%d V=%d top_k=%d)", MTP_MAX_TOP_K,
+              rows, V, top_k);
+    return MTP_ERR_INVALID_ARG;
+  }
+  return MTP_OK;
+}
+
+int mtp_token_logprobs_workspace(int32_t dtype, int32_t rows, int32_t V, int32_t top_k, int64_t* bytes) {
+  mtp::g_err[0] = 0;
+  const int rc = check_scores(dtype, rows, V, top_k);
+  if (rc) return rc;
+  if (!bytes) {
+    set_error("bytes must be non-NULL");
+    return MTP_ERR_INVALID_ARG;
+  }
+  *bytes = rows ? mtp::scores_workspace(rows, V, top_k) : 0;
+  return MTP_OK;
+}
+
+int mtp_token_logprobs(const void* logits, int32_t dtype, int64_t row_stride, const int32_t* token, int32_t rows,
+                       int32_t V, float temperature, int32_t top_k, float* logprob, float* entropy, int32_t* top_ids,
+                       float* top_logprobs, void* workspace, int64_t workspace_bytes, void* stream) {
+  mtp::g_err[0] = 0;
+  int rc = check_scores(dtype, rows, V, top_k);
+  if (rc) return rc;
+  const int size = dtype == MTP_DTYPE_F32 ? 4 : 2;
+  auto off = [](const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) % n) != 0; };
+  if (rows && (!logits || (logprob && !token) || (!logprob && !entropy && !top_k) || (top_k && (!top_ids || !top_logprobs)))) {
+    set_error("logits, token (with logprob), top_ids and top_logprobs (with top_k) must be non-NULL, and an output asked for");
+    return MTP_ERR_INVALID_ARG;
+  }
+  if (off(logits, size) || off(token, 4) || off(logprob, 4) || off(entropy, 4) || off(top_ids, 4) || off(top_logprobs, 4) ||
+      (rows > 1 && (row_stride < V || row_stride > (1LL << 40)))) {
+    set_error("pointers must be aligned to their type and row_stride=%lld be V=%d to 2^40", static_cast<long long>(row_stride), V);
+    return MTP_ERR_INVALID_ARG;
+  }
+  if (!(temperature >= 1e-30f && temperature <= 1e30f)) {
+    set_error("the temperature must be in [1e-30, 1e30] (%g)", static_cast<double>(temperature));
+    return MTP_ERR_INVALID_ARG;
+  }
+  if (!rows) return MTP_OK;
+  const long long need = mtp::scores_workspace(rows, V, top_k);
+  if (need > 0 && (!workspace || off(workspace, 16) || workspace_bytes < need)) {
+    set_error("the workspace must be 16-byte aligned and hold %lld bytes (%lld given)", need,
+              static_cast<long long>(workspace_bytes));
+    return MTP_ERR_INVALID_ARG;
+  }
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_fail("querying the device", e);
+  if (sms > 160) sms = 160;  // (what the workspace is sized for)
+  return mtp::run_scores(logits, dtype == MTP_DTYPE_F32, row_stride, token, rows, V, temperature, top_k,
+                         logprob, entropy, top_ids, top_logprobs, workspace, sms, static_cast<cudaStream_t>(stream));
+}
+
 int mtp_get_status(mtp_handle* h) {
   mtp::g_err[0] = 0;
   if (!h) {

@@ -97,4 +97,10 @@ int run_verify(const void* logits, const int* draft, int B, int n, int V, int* a
 int run_verify_sample(const void* logits, const int* draft, int B, int n, int V, float temperature,
                       const float* u_accept, const float* u_sample, int* accept_len, int* out_tokens, cudaStream_t st);
 
+// Log probabilities of given tokens, entropies and the k most probable tokens of rows of logits
+// at a temperature: workspace bytes and launch.
+long long scores_workspace(int rows, int V, int k);
+int run_scores(const void* logits, int f32, long long stride, const int* token, int rows, int V, float temperature,
+               int k, float* logprob, float* entropy, int* ids, float* best, void* ws, int num_sms, cudaStream_t st);
+
 }  // namespace mtp

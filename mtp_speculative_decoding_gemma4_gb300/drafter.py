@@ -204,3 +204,40 @@ def verify_greedy(target_logits: torch.Tensor, drafts: torch.Tensor, accept_len=
     B.mtp_verify_greedy(_ptr(_need_cuda(target_logits, "target_logits")), _ptr(drafts), Bn, n1 - 1, V,
                         _ptr(accept_len), _ptr(out_tokens), stream)
     return accept_len, out_tokens
+
+
+def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, temperature: float = 1.0, top_k: int = 0,
+                   stream: Optional[int] = None):
+    """Log probabilities of given tokens under softmax(logits / temperature), with the rows'
+    entropies and their top_k (<= 32) most probable tokens: logits bf16 or fp32 [..., V] (two
+    dimensions with any row stride, or contiguous), tokens int32 [...]. Returns (logprob, entropy) of
+    tokens' shape and, with top_k > 0, (logprob, entropy, top_ids, top_logprobs) with a last
+    dimension of top_k. Runs on `stream`, by default torch's current one."""
+    _need_cuda(tokens, "tokens")
+    if not (isinstance(logits, torch.Tensor) and logits.is_cuda and logits.dtype in _DTYPES and logits.dim() >= 1):
+        raise ValueError("logits must be a CUDA tensor [..., V] of bf16 or fp32")
+    shape, V, dev = logits.shape[:-1], logits.shape[-1], logits.device
+    rows = tokens.numel()
+    if logits.dim() != 2 and not logits.is_contiguous() or V > 1 and logits.stride(-1) != 1:
+        raise ValueError("logits must be [rows][V] with contiguous rows, or contiguous")
+    if tokens.shape != shape or tokens.dtype != torch.int32 or tokens.device != dev:
+        raise ValueError(f"tokens must be int32 of shape {list(shape)} on {dev}")
+    return call_on(dev, stream, _token_logprobs, logits, tokens, shape, rows, V, temperature, top_k)
+
+
+_DTYPES = {torch.bfloat16: B.MTP_DTYPE_BF16, torch.float32: B.MTP_DTYPE_F32}
+
+
+def _token_logprobs(st, logits, tokens, shape, rows, V, temperature, top_k):
+    dtype, dev = _DTYPES[logits.dtype], logits.device
+    n = B.mtp_token_logprobs_workspace(dtype, rows, V, top_k)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    out = torch.empty((2,) + tuple(shape), dtype=torch.float32, device=dev)
+    ids = best = None
+    if top_k:
+        ids = torch.empty(tuple(shape) + (top_k,), dtype=torch.int32, device=dev)
+        best = torch.empty(tuple(shape) + (top_k,), dtype=torch.float32, device=dev)
+    B.mtp_token_logprobs(logits.data_ptr(), dtype, logits.stride(0) if logits.dim() == 2 and rows > 1 else V,
+                         tokens.data_ptr(), rows, V, temperature, top_k, out[0].data_ptr(), out[1].data_ptr(), _ptr(ids),
+                         _ptr(best), _ptr(ws), n, st)
+    return (out[0], out[1], ids, best) if top_k else (out[0], out[1])
