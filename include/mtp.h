@@ -448,6 +448,51 @@ MTP_API int mtp_page_plan(const int32_t *old_len, const int32_t *new_len, int32_
 MTP_API int mtp_page_append(const mtp_paged_kv *kv, const void *k_new, const void *v_new, int64_t row_stride_k,
                             int64_t row_stride_v, const int32_t *slot_map, int32_t T, void *stream);
 
+/* Forks of sequences over shared pages (n samples of one prompt, the beams of a search). Fork i makes
+ * sequence dst[i] a copy of the first length[i] tokens of sequence src[i]: the entries of the complete
+ * pages are copied from block_table row src[i] to row dst[i] (from then on both sequences hold these
+ * pages), and where length[i] % P != 0 a page is taken from the head of the ring of free pages, gets the
+ * rows [0, length[i] % P) of src[i]'s page (k and v) and becomes the next entry. A sequence forked onto
+ * itself (src[i] == dst[i]) is cut to length[i] with a partial page of its own. Forks are granted in
+ * order while the pages taken fit ring_state's count; the first that does not fit and every later one
+ * are denied, as are forks whose src or dst is outside [0, B) or length outside [0, ctx_len[src]],
+ * those whose dst an earlier one has, and those whose src is the dst of another one. Denied sequences
+ * stay as they are. Pages that dst held before are not returned: mtp_page_collect does that.
+ * Sharing pages asks two things of a program: a sequence that holds shared pages returns pages with
+ * mtp_page_collect, not as a shrinker of mtp_page_plan; and rows are appended behind complete pages or
+ * into a partial page of the sequence's own, so after a cut inside a shared page the sequence is
+ * forked onto itself first.
+ *   kv           block_table is updated in place; k and v get the partial pages' rows
+ *   src, dst, length  device [n] int32;  free_ring device [n_pages] int32;  ring_state device [2] int32
+ *   len_out      device [B] int32: every sequence's length after the call
+ *   state_out    device [2] int32: the ring's head and count after the call
+ *   status       device [4] int32: forks granted, pages taken, pages shared, forks denied
+ * len_out and state_out are buffers of their own, so that the call can be repeated. B, n <= 8192.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, CUDA. */
+MTP_API int mtp_page_fork(const mtp_paged_kv *kv, int32_t B, const int32_t *src, const int32_t *dst,
+                          const int32_t *length, int32_t n, const int32_t *free_ring, const int32_t *ring_state,
+                          int32_t *len_out, int32_t *state_out, int32_t *status, void *stream);
+
+/* The free pages of a cache from its block tables alone: pages that are an entry of no sequence's
+ * first ceil(ctx_len / P) become the ring of free pages, in increasing order from its beginning (head
+ * 0; entries of free_ring behind them are left as they were). With table_out the held pages are also
+ * moved into the front of the pool: the held pages from the first `used` ones on, in increasing order,
+ * take the free places in front, in increasing order, with their rows (k and v) and summaries;
+ * table_out gets every sequence's entries under the new numbers (-1 for entries that are no page and
+ * behind a sequence's pages), and the ring the pages used .. n_pages - 1. Their old contents stay, so
+ * a call with a table_out of its own can be repeated; a program then reads the new table.
+ *   free_ring  device [n_pages] int32
+ *   table_out  device [B][table_out_stride] int32: NULL, block_table itself (of the same stride) or a
+ *              buffer of its own
+ *   state_out  device [2] int32: the ring's head and count
+ *   status     device [4] int32: pages held (`used`), pages free, pages moved, entries of held
+ *              positions that are no page
+ * B <= 2^20. Errors: INVALID_ARG (workspace too small included), UNSUPPORTED_SHAPE, CUDA. */
+MTP_API int mtp_page_collect(const mtp_paged_kv *kv, int32_t B, int32_t *free_ring, int32_t *table_out,
+                             int64_t table_out_stride, int32_t *state_out, int32_t *status, void *workspace,
+                             int64_t workspace_bytes, void *stream);
+MTP_API int mtp_page_collect_workspace(const mtp_paged_kv *kv, int32_t compact, int64_t *bytes);
+
 /* Attention of one new token per sequence over the paged cache, split over the cache's length
  * and joined: out[b][h] = sum_j p_j v_j, p = softmax(scale q[b][h] . k_j) over the attended
  * positions: [0, L), the last `window` of them when window > 0, and with `pages` only those in

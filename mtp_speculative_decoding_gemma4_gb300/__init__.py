@@ -11,7 +11,8 @@ def __getattr__(name):
     # a name is looked up once and then an attribute of the package.
     if name in ("Drafter", "verify_greedy", "verify_sample", "token_logprobs", "make_config", "make_kv"):
         from . import drafter as module
-    elif name in ("PagedKV", "page_plan", "page_append", "page_select", "paged_attention", "paged_attention_chunk"):
+    elif name in ("PagedKV", "page_plan", "page_append", "page_select", "paged_attention", "paged_attention_chunk", "page_fork",
+                  "page_collect"):
         from . import paged as module
     else:
         raise AttributeError(name)

@@ -22,7 +22,8 @@ EXPORTS = ("mtp_init_weights", "mtp_draft_block", "mtp_centroid_head", "mtp_veri
            "mtp_verify_sample", "mtp_set_sparse_head", "mtp_set_debug", "mtp_page_plan", "mtp_page_append",
            "mtp_page_select", "mtp_page_select_workspace", "mtp_paged_attention", "mtp_paged_attention_workspace",
            "mtp_draft_block_paged", "mtp_draft_block_paged_workspace", "mtp_paged_attention_chunk",
-           "mtp_paged_attention_chunk_workspace", "mtp_token_logprobs", "mtp_token_logprobs_workspace")
+           "mtp_paged_attention_chunk_workspace", "mtp_token_logprobs", "mtp_token_logprobs_workspace",
+           "mtp_page_fork", "mtp_page_collect", "mtp_page_collect_workspace")
 MASK_NEG_1E30, MASK_MIN_MINUS_ONE = 0, 1  # enum mtp_logit_mask
 HEAD_AUTO, HEAD_PER_SEQUENCE, HEAD_CLUSTER_MAJOR = 0, 1, 2  # enum mtp_sparse_head
 
@@ -100,6 +101,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mtp_paged_attention_chunk_workspace.argtypes = [pkv, i32, i32, i32, ctypes.POINTER(i64)]
     lib.mtp_token_logprobs.argtypes = [vp, i32, i64, vp, i32, i32, f32, i32, vp, vp, vp, vp, vp, i64, vp]
     lib.mtp_token_logprobs_workspace.argtypes = [i32, i32, i32, i32, ctypes.POINTER(i64)]
+    lib.mtp_page_fork.argtypes = [pkv, i32, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp]
+    lib.mtp_page_collect.argtypes = [pkv, i32, vp, vp, i64, vp, vp, vp, i64, vp]
+    lib.mtp_page_collect_workspace.argtypes = [pkv, i32, ctypes.POINTER(i64)]
     lib.mtp_page_select.argtypes = [pkv, vp, i32, i32, i32, i32, i32, vp, vp, i64, vp]
     lib.mtp_page_select_workspace.argtypes = [pkv, i32, ctypes.POINTER(i64)]
     lib.mtp_draft_block_paged.argtypes = [vp, vp, vp, pkv, pkv, vp, i32, i32, i32, i32, i32, vp, vp, vp, i64, vp]
@@ -114,7 +118,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                  "mtp_page_select", "mtp_page_select_workspace", "mtp_paged_attention",
                  "mtp_paged_attention_workspace", "mtp_draft_block_paged", "mtp_draft_block_paged_workspace",
                  "mtp_paged_attention_chunk", "mtp_paged_attention_chunk_workspace", "mtp_token_logprobs",
-                 "mtp_token_logprobs_workspace"):
+                 "mtp_token_logprobs_workspace", "mtp_page_fork", "mtp_page_collect", "mtp_page_collect_workspace"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -227,6 +231,28 @@ def mtp_page_append(kv: mtp_paged_kv, k_new: int, v_new: int, row_stride_k: int,
                                                   slot_map or None, T, stream or None)
     if rc:
         _check(rc, "mtp_page_append")
+
+
+def mtp_page_fork(kv: mtp_paged_kv, B: int, src: int, dst: int, length: int, n: int, free_ring: int, ring_state: int,
+                  len_out: int, state_out: int, status: int, stream: int = 0) -> None:
+    rc = (_lib or load_library()).mtp_page_fork(kv, B, src or None, dst or None, length or None, n, free_ring, ring_state,
+                                                len_out, state_out, status, stream or None)
+    if rc:
+        _check(rc, "mtp_page_fork")
+
+
+def mtp_page_collect_workspace(kv: mtp_paged_kv, compact: int) -> int:
+    n = ctypes.c_int64()
+    _check(load_library().mtp_page_collect_workspace(kv, compact, ctypes.byref(n)), "mtp_page_collect_workspace")
+    return n.value
+
+
+def mtp_page_collect(kv: mtp_paged_kv, B: int, free_ring: int, table_out: int, table_out_stride: int, state_out: int,
+                     status: int, workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    rc = (_lib or load_library()).mtp_page_collect(kv, B, free_ring, table_out or None, table_out_stride, state_out,
+                                                   status, workspace or None, workspace_bytes, stream or None)
+    if rc:
+        _check(rc, "mtp_page_collect")
 
 
 def mtp_paged_attention_workspace(kv: mtp_paged_kv, B: int, n_head: int, n_list: int) -> int:

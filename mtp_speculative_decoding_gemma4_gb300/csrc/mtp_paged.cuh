@@ -155,6 +155,13 @@ int run_page_append(const pg::Cache& c, const void* k_new, const void* v_new, lo
 int run_page_select(const pg::Cache& c, const float* q, int B, int nh, int n_select, int keep_first, int keep_last,
                     int* sel, void* ws, int num_sms, cudaStream_t st);
 
+// Forks of sequences over shared pages; the pages that no sequence holds, and their compaction.
+int run_page_fork(const pg::Cache& c, int B, const int* src, const int* dst, const int* len, int n, const int* ring,
+                  const int* state, int* len_out, int* state_out, int* status, int num_sms, cudaStream_t st);
+long long page_collect_workspace(const pg::Cache& c, bool compact);
+int run_page_collect(const pg::Cache& c, int B, int* ring, int* table_out, long long out_stride, int* state_out,
+                     int* status, void* ws, int num_sms, cudaStream_t st);
+
 struct Params;
 // What a paged draft block adds to its Params: the caches by attention type, the selection of the
 // full layers (n_select 0: every page) and the caller's workspace, carved.

@@ -209,6 +209,81 @@ int mtp_page_append(const mtp_paged_kv* kv, const void* k_new, const void* v_new
                          static_cast<cudaStream_t>(stream));
 }
 
+int mtp_page_fork(const mtp_paged_kv* kv, int32_t B, const int32_t* src, const int32_t* dst, const int32_t* length,
+                  int32_t n, const int32_t* free_ring, const int32_t* ring_state, int32_t* len_out, int32_t* state_out,
+                  int32_t* status, void* stream) {
+  set_error("%s", "");
+  pg::Cache c;
+  int rc = pg::make_cache(kv, true, &c);
+  if (rc) return rc;
+  if (B < 1 || B > pg::kPlanMaxB || n < 0 || n > pg::kPlanMaxB) {
+    set_error("need 1 <= B <= %d and 0 <= n <= %d (B=%d n=%d)", pg::kPlanMaxB, pg::kPlanMaxB, B, n);
+    return MTP_ERR_INVALID_ARG;
+  }
+  if ((n > 0 && (!src || !dst || !length)) || !free_ring || !ring_state || !len_out || !state_out || !status) {
+    set_error("src, dst, length (n > 0), free_ring, ring_state, len_out, state_out and status must be non-NULL");
+    return MTP_ERR_INVALID_ARG;
+  }
+  if (!pg::aligned(src, 4) || !pg::aligned(dst, 4) || !pg::aligned(length, 4) || !pg::aligned(free_ring, 4) ||
+      !pg::aligned(ring_state, 4) || !pg::aligned(len_out, 4) || !pg::aligned(state_out, 4) || !pg::aligned(status, 4)) {
+    set_error("src, dst, length, free_ring, ring_state, len_out, state_out and status must be 4-byte aligned");
+    return MTP_ERR_INVALID_ARG;
+  }
+  if (pg::overlap(len_out, 4LL * B, c.ctx_len, 4LL * B) || pg::overlap(len_out, 4LL * B, length, 4LL * n) ||
+      pg::overlap(len_out, 4LL * B, src, 4LL * n) || pg::overlap(len_out, 4LL * B, dst, 4LL * n) ||
+      pg::overlap(state_out, 8, ring_state, 8)) {
+    set_error("len_out and state_out must be buffers of their own");
+    return MTP_ERR_INVALID_ARG;
+  }
+  int sms = 0;
+  if ((rc = pg::sm_count(&sms))) return rc;
+  return run_page_fork(c, B, src, dst, length, n, free_ring, ring_state, len_out, state_out, status, sms,
+                       static_cast<cudaStream_t>(stream));
+}
+
+int mtp_page_collect_workspace(const mtp_paged_kv* kv, int32_t compact, int64_t* bytes) {
+  set_error("%s", "");
+  pg::Cache c;
+  const int rc = pg::make_cache(kv, true, &c);
+  if (rc) return rc;
+  if (!bytes) {
+    set_error("bytes must be non-NULL");
+    return MTP_ERR_INVALID_ARG;
+  }
+  *bytes = page_collect_workspace(c, compact != 0);
+  return MTP_OK;
+}
+
+int mtp_page_collect(const mtp_paged_kv* kv, int32_t B, int32_t* free_ring, int32_t* table_out,
+                     int64_t table_out_stride, int32_t* state_out, int32_t* status, void* workspace,
+                     int64_t workspace_bytes, void* stream) {
+  set_error("%s", "");
+  pg::Cache c;
+  int rc = pg::make_cache(kv, true, &c);
+  if (rc) return rc;
+  if (B < 1 || B > 1 << 20 || !free_ring || !state_out || !status || !pg::aligned(free_ring, 4) ||
+      !pg::aligned(table_out, 4) || !pg::aligned(state_out, 4) || !pg::aligned(status, 4)) {
+    set_error("need 1 <= B <= 2^20 (B=%d) and 4-byte aligned, non-NULL free_ring, state_out and status", B);
+    return MTP_ERR_INVALID_ARG;
+  }
+  if (table_out && table_out_stride < c.max_pages) {
+    set_error("table_out_stride=%lld must be at least max_pages=%d", static_cast<long long>(table_out_stride), c.max_pages);
+    return MTP_ERR_INVALID_ARG;
+  }
+  const long long in_bytes = 4 * ((B - 1LL) * c.table_stride + c.max_pages),
+                  out_bytes = 4 * ((B - 1LL) * table_out_stride + c.max_pages);
+  if (table_out && pg::overlap(table_out, out_bytes, c.table, in_bytes) &&
+      (table_out != c.table || table_out_stride != c.table_stride)) {
+    set_error("table_out must be a buffer of its own, or block_table itself");
+    return MTP_ERR_INVALID_ARG;
+  }
+  if ((rc = pg::check_workspace(workspace, workspace_bytes, page_collect_workspace(c, table_out != nullptr)))) return rc;
+  int sms = 0;
+  if ((rc = pg::sm_count(&sms))) return rc;
+  return run_page_collect(c, B, free_ring, table_out, table_out_stride, state_out, status, workspace, sms,
+                          static_cast<cudaStream_t>(stream));
+}
+
 int mtp_paged_attention_workspace(const mtp_paged_kv* kv, int32_t B, int32_t n_head, int32_t n_list, int64_t* bytes) {
   set_error("%s", "");
   pg::Cache c;

@@ -210,6 +210,57 @@ def _append(st, kv, k_new, slot_map, v_new):
                       slot_map.data_ptr(), T, st)
 
 
+def page_fork(kv: PagedKV, src: torch.Tensor, dst: torch.Tensor, length: torch.Tensor, free_ring: torch.Tensor,
+              ring_state: torch.Tensor, stream: Optional[int] = None):
+    """Makes sequences dst[i] copies of the first length[i] tokens of sequences src[i] (int32 [n]):
+    complete pages are shared through kv's block_table (updated in place), a partial page's rows are
+    copied into a page from the ring of free pages free_ring [n_pages] (ring_state: head and count).
+    Returns (len_out [B], state_out [2], status [4]), as mtp_page_fork describes, with what sharing
+    pages asks of a program."""
+    if kv.block_table is None:
+        raise ValueError("the cache has no block_table")
+    dev = kv.device
+    _need_flat(src, "src", _i32, (None,), dev)
+    for t, name, shape in ((dst, "dst", src.shape), (length, "length", src.shape), (ring_state, "ring_state", (2,)),
+                           (free_ring, "free_ring", (kv.c.n_pages,))):
+        if not _flat_like(t, _i32, dev, shape):
+            _need_flat(t, name, _i32, shape, dev)
+    return call_on(dev, stream, _fork, kv, src, dst, length, free_ring, ring_state)
+
+
+def _fork(st, kv, src, dst, length, free_ring, ring_state):
+    out = torch.empty(kv.batch + 6, dtype=_i32, device=kv.device)
+    at = out.data_ptr()
+    B.mtp_page_fork(kv.p, kv.batch, src.data_ptr(), dst.data_ptr(), length.data_ptr(), src.shape[0],
+                    free_ring.data_ptr(), ring_state.data_ptr(), at + 24, at, at + 8, st)
+    return out[6:], out[:2], out[2:6]
+
+
+def page_collect(kv: PagedKV, free_ring: torch.Tensor, compact: bool = False, stream: Optional[int] = None):
+    """Makes the pages that no sequence of kv holds the ring of free pages (free_ring [n_pages], from
+    its beginning), whatever held them before; with compact, moves the held pages into the front of
+    the pool first. Returns (table_out, state_out [2], status [4]), as mtp_page_collect describes:
+    table_out [B][max_pages] under the pages' new numbers with compact, else None."""
+    if kv.block_table is None:
+        raise ValueError("the cache has no block_table")
+    if not _flat_like(free_ring, _i32, kv.device, (kv.c.n_pages,)):
+        _need_flat(free_ring, "free_ring", _i32, (kv.c.n_pages,), kv.device)
+    return call_on(kv.device, stream, _collect, kv, free_ring, bool(compact))
+
+
+def _collect(st, kv, free_ring, compact):
+    n = kv._ws.get(("collect", compact))
+    if n is None:
+        n = kv._ws[("collect", compact)] = B.mtp_page_collect_workspace(kv.p, int(compact))
+    cols = kv.c.max_pages
+    table = torch.empty((kv.batch, cols), dtype=_i32, device=kv.device) if compact else None
+    out = torch.empty(6, dtype=_i32, device=kv.device)
+    at = out.data_ptr()
+    _with_workspace(kv, st, n, lambda ws, n: B.mtp_page_collect(
+        kv.p, kv.batch, free_ring.data_ptr(), table.data_ptr() if compact else 0, cols, at, at + 8, ws, n, st))
+    return table, out[:2], out[2:]
+
+
 def _queries(q, kv: PagedKV):
     """Checks the queries; their shape."""
     shape = q.shape if isinstance(q, torch.Tensor) else ()
