@@ -9,8 +9,11 @@
 // to the lowest index. A CTA keeps a list of candidates and a bar, the k-th best value so far; an
 // element of a later chunk has to exceed it. Where many do (the first chunk, or logits that rise), the
 // bar is raised first: the k-th largest of the chunk's 128 group maxima is a lower bound of its k-th
-// largest element, and at most k groups have elements at or above it, so the list is bounded whatever
-// the logits are. After the first chunk hardly any element passes, and a chunk costs one vote.
+// largest element. By value few more than k elements reach it; where many are equal the same is done by
+// key, and then at most k groups have elements at or above it, so the list is bounded whatever the
+// logits are. After the first chunk hardly any element passes, and the warps meet only after 1, 2, 4, 8,
+// .. chunks to raise the bar (as many elements as the list is long pass in between). Logits that rise
+// with their index can overfill the list so; they are gone over again, with a meeting at every chunk.
 //
 // A CTA takes a row, or a slice of it where rows are few (k_scores_join then joins the slices). What
 // bounds it is reading the logits once.
@@ -26,11 +29,11 @@ namespace mtp {
 namespace sc {
 
 constexpr int kT = 256;             // threads
-constexpr int kU = 8;               // 16-byte vectors of a thread and chunk
+constexpr int kU = 4;               // 16-byte vectors of a thread and chunk; the next chunk's are in flight meanwhile
 constexpr int kMaxK = 32;
 constexpr int kGroups = 128;        // of a chunk's elements
 constexpr int kMaxSplits = 64;
-constexpr int kCap = 4096 + 2 * kMaxK;  // candidates: kMaxK groups of at most 128 elements, and what was there
+constexpr int kCap = kMaxK * (kT * kU * 8 / kGroups) + 2 * kMaxK;  // candidates: kMaxK groups of elements, and what was there
 
 using key_t = unsigned long long;
 
@@ -58,9 +61,13 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
   return y;
 }
+// fp32 values as unsigned numbers of the same order (-0 as 0).
+__device__ __forceinline__ unsigned order(float v) {
+  const unsigned u = __float_as_uint(v + 0.f);
+  return u ^ (static_cast<int>(u) < 0 ? 0xffffffffu : 0x80000000u);
+}
 __device__ __forceinline__ key_t make_key(float v, int i) {
-  const unsigned u = __float_as_uint(v), o = u ^ (static_cast<int>(u) < 0 ? 0xffffffffu : 0x80000000u);
-  return static_cast<key_t>(o) << 32 | (0xffffffffu - static_cast<unsigned>(i));
+  return static_cast<key_t>(order(v)) << 32 | (0xffffffffu - static_cast<unsigned>(i));
 }
 __device__ __forceinline__ float key_value(key_t k) {
   const unsigned o = static_cast<unsigned>(k >> 32);
@@ -127,6 +134,8 @@ struct Shared {
   key_t group[kGroups];
   key_t best[kMaxK];
   key_t bar;        // the k-th largest of the group maxima
+  alignas(16) float top[kGroups];  // the same by value
+  float level;
   int n, n2;        // candidates
   float sum[kT / 32][3];
 };
@@ -136,13 +145,13 @@ __device__ void find_bar(Shared& sh, int k) {
   const int tid = threadIdx.x;
   if (tid == 0) sh.bar = 0;
   __syncthreads();
-  if (tid < kGroups) {
-    const key_t mine = sh.group[tid];
-    int above = 0;
+  static_assert(kT == 2 * kGroups, "two threads per group");
+  const key_t mine = sh.group[tid / 2];
+  int above = 0;
 #pragma unroll 8
-    for (int i = 0; i < kGroups; ++i) above += sh.group[i] > mine ? 1 : 0;
-    if (above == k - 1 && mine) sh.bar = mine;  // (keys are different but for those of empty groups)
-  }
+  for (int i = tid & 1; i < kGroups; i += 2) above += sh.group[i] > mine ? 1 : 0;
+  above += __shfl_xor_sync(0xffffffffu, above, 1);
+  if (above == k - 1 && mine) sh.bar = mine;  // (keys are different but for those of empty groups)
   __syncthreads();
 }
 
@@ -174,11 +183,16 @@ __device__ void select(Shared& sh, int k) {
   const int n2 = sh.n;
   if (tid < kMaxK) sh.best[tid] = 0;
   __syncthreads();
-  for (int i = tid; i < n2; i += kT) {
-    const key_t x = sh.list[i];
+  // four threads count what is above a key
+  for (int i0 = 0; i0 + (tid & ~31) / 4 < n2; i0 += kT / 4) {  // (whole warps)
+    const int i = i0 + tid / 4;
+    const key_t x = i < n2 ? sh.list[i] : 0;
     int above = 0;
-    for (int j = 0; j < n2; ++j) above += sh.list[j] > x ? 1 : 0;
-    if (above < k) sh.best[above] = x;
+#pragma unroll 4
+    for (int j = tid & 3; j < n2; j += 4) above += sh.list[j] > x ? 1 : 0;
+    above += __shfl_xor_sync(0xffffffffu, above, 1);
+    above += __shfl_xor_sync(0xffffffffu, above, 2);
+    if (x && above < k) sh.best[above] = x;
   }
   __syncthreads();
   if (tid < kMaxK) sh.list[tid] = sh.best[tid];
@@ -255,9 +269,7 @@ __global__ void __launch_bounds__(kT, 4) k_scores(const __grid_constant__ Args a
   Sum z = {-INFINITY, 0.f, 0.f};
   float bar = -INFINITY;  // what an element of a later chunk has to exceed
   bool first = true;
-#pragma unroll 1
-  for (int c0 = split * a.slice; c0 < hi; c0 += kChunk) {
-    uint4 u[kU];
+  auto load = [&](uint4* u, int c0) {
 #pragma unroll
     for (int j = 0; j < kU; ++j) {
       const int i = c0 + (j * kT + tid) * VE;
@@ -275,10 +287,45 @@ __global__ void __launch_bounds__(kT, 4) k_scores(const __grid_constant__ Args a
         }
       }
     }
+  };
+  // this thread's elements of a chunk that reach `lim` and exceed the bar, into the list while it has room
+  auto push = [&](const uint4* u, int c0, float lim) {
+    unsigned vecs = 0;
+#pragma unroll
+    for (int j = 0; j < kU; ++j) vecs |= (Elem2<T>::top(u[j]) >= lim ? 1u : 0u) << j;
+#pragma unroll 1
+    for (; vecs; vecs &= vecs - 1) {
+      const int j = __ffs(vecs) - 1;
+      uint4 y = u[0];
+#pragma unroll
+      for (int q = 1; q < kU; ++q)
+        if (q == j) y = u[q];
+      float v[VE];
+      Elem2<T>::unpack(y, v);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        const int i = c0 + (j * kT + tid) * VE + e;
+        if (i >= lo && i < hi && v[e] >= lim && (first || v[e] > bar)) {
+          const int at = atomicAdd(&sh.n, 1);
+          if (at < kCap) sh.list[at] = make_key(v[e], i - skew);
+        }
+      }
+    }
+  };
+  uint4 next[kU];
+  bool careful = false;  // the second time over
+again:
+  if (split * a.slice < hi) load(next, split * a.slice);
+#pragma unroll 1
+  for (int c0 = split * a.slice, ci = 0; c0 < hi; c0 += kChunk, ++ci) {
+    uint4 u[kU];
+#pragma unroll
+    for (int j = 0; j < kU; ++j) u[j] = next[j];
+    if (c0 + kChunk < hi) load(next, c0 + kChunk);
     float cm = -INFINITY;
 #pragma unroll
     for (int j = 0; j < kU; ++j) cm = fmaxf(cm, Elem2<T>::top(u[j]));
-    if (cm > z.m) {
+    if (!careful && cm > z.m) {
       if (z.m > -INFINITY) {
         const float f = max_nan((z.m - cm) * a.c, kLow), e = ex2(f);
         z.w = e * fmaf(f, z.s, z.w);
@@ -286,36 +333,74 @@ __global__ void __launch_bounds__(kT, 4) k_scores(const __grid_constant__ Args a
       }
       z.m = cm;
     }
-    // (a difference first: scores of the type's lowest value have one, but no product with c)
-    const float m = z.m == -INFINITY ? 0.f : -z.m;
-    const f2 m2 = two(m, m), c2 = two(a.c, a.c);
-    f2 s = two(0.f, 0.f), w = s;
+    if (!careful) {
+      // (a difference first: scores of the type's lowest value have one, but no product with c)
+      const float m = z.m == -INFINITY ? 0.f : -z.m;
+      const f2 m2 = two(m, m), c2 = two(a.c, a.c);
+      f2 s = two(0.f, 0.f), w = s;
 #pragma unroll
-    for (int j = 0; j < kU; ++j) {
-      float v[VE];
-      Elem2<T>::unpack(u[j], v);
+      for (int j = 0; j < kU; ++j) {
+        float v[VE];
+        Elem2<T>::unpack(u[j], v);
 #pragma unroll
-      for (int e = 0; e < VE; e += 2) {
-        float d0, d1;
-        split2(mul2(add2(two(v[e], v[e + 1]), m2), c2), d0, d1);
-        d0 = max_nan(d0, kLow);
-        d1 = max_nan(d1, kLow);
-        const f2 p = two(ex2(d0), ex2(d1));
-        s = add2(s, p);
-        w = fma2(p, two(d0, d1), w);
+        for (int e = 0; e < VE; e += 2) {
+          float d0, d1;
+          split2(mul2(add2(two(v[e], v[e + 1]), m2), c2), d0, d1);
+          d0 = max_nan(d0, kLow);
+          d1 = max_nan(d1, kLow);
+          const f2 p = two(ex2(d0), ex2(d1));
+          s = add2(s, p);
+          w = fma2(p, two(d0, d1), w);
+        }
       }
+      float s0, s1, w0, w1;
+      split2(s, s0, s1);
+      split2(w, w0, w1);
+      z.s += s0 + s1;
+      z.w += w0 + w1;
     }
-    float s0, s1, w0, w1;
-    split2(s, s0, s1);
-    split2(w, w0, w1);
-    z.s += s0 + s1;
-    z.w += w0 + w1;
-    if (k) {
+    if (k && !careful && (ci & (ci - 1))) {
+      if (cm > bar) push(u, c0, bar);
+    } else if (k) {
+      __syncthreads();
       const int had = sh.n, over = __syncthreads_count(first || cm > bar);  // (pushes begin behind the barrier)
+      if (had > kCap) break;
       if (over) {
-        key_t least = 0;  // where the bar is raised first
-        if (over * kU * VE + had > kCap) {
+        // at least `most` candidates may come: the bar is raised first, to the k-th largest of 128 pairs'
+        // maxima, which at least k elements reach, and few more unless many are equal
+        const int most = over * kU * VE;
+        float level = -INFINITY;
+        if (first || had + most > kCap) {
           if (had > k) select(sh, k);
+          const float other = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 1));
+          if (!(tid & 1)) sh.top[tid / 2] = other;
+          __syncthreads();
+          if (tid < 32) {
+            // the 16 leading bits of the k-th largest, one by one: a value that it reaches (comparing each
+            // group with all others took most of a meeting)
+            unsigned o[kGroups / 32], r = 0;
+#pragma unroll
+            for (int i = 0; i < kGroups / 32; ++i) o[i] = order(sh.top[32 * i + tid]);
+#pragma unroll 1
+            for (unsigned bit = 0x80000000u; bit > 0x8000u; bit >>= 1) {
+              int n = 0;
+#pragma unroll
+              for (int i = 0; i < kGroups / 32; ++i) n += __popc(__ballot_sync(0xffffffffu, o[i] >= (r | bit)));
+              if (n >= k) r |= bit;
+            }
+            // (below the lowest finite value there are -inf and, as prefixes, none)
+            if (tid == 0) sh.level = r < order(-FLT_MAX) ? -INFINITY : key_value(static_cast<key_t>(r) << 32);
+          }
+          __syncthreads();
+          level = sh.level;
+        }
+        const int n0 = had > k && (first || had + most > kCap) ? k : had;
+        const float lim = fmaxf(level, bar);  // (elements equal to the bar itself are left out below)
+        if (level > -INFINITY || !first) push(u, c0, lim);
+        __syncthreads();
+        if (sh.n > kCap || (first && !(level > -INFINITY))) {
+          // Too many are equal (or nothing is above -inf): once more by keys, of which no two are equal, so
+          // that at most k groups have elements that reach the k-th largest of the groups' maxima
           key_t mine = 0;
 #pragma unroll
           for (int j = 0; j < kU; ++j) {
@@ -324,37 +409,36 @@ __global__ void __launch_bounds__(kT, 4) k_scores(const __grid_constant__ Args a
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
               const int i = c0 + (j * kT + tid) * VE + e;
-              const key_t x1 = i >= lo && i < hi ? make_key(v[e], i - skew) : 0;
+              const key_t x1 = i >= lo && i < hi && (first || v[e] > bar) ? make_key(v[e], i - skew) : 0;
               mine = x1 > mine ? x1 : mine;
             }
           }
           const key_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
           if (!(tid & 1)) sh.group[tid / 2] = mine > other ? mine : other;
           __syncthreads();
+          if (tid == 0) sh.n = n0;
           find_bar(sh, k);
-          least = sh.bar;
-        }
-        if (first || cm > bar) {
+          const key_t least = sh.bar;
+          if (mine && mine >= least) {
 #pragma unroll 1
-          for (int j = 0; j < kU; ++j) {
-            uint4 y = u[0];
+            for (int j = 0; j < kU; ++j) {
+              uint4 y = u[0];
 #pragma unroll
-            for (int q = 1; q < kU; ++q)
-              if (q == j) y = u[q];
-            float v[VE];
-            Elem2<T>::unpack(y, v);
+              for (int q = 1; q < kU; ++q)
+                if (q == j) y = u[q];
+              float v[VE];
+              Elem2<T>::unpack(y, v);
 #pragma unroll
-            for (int e = 0; e < VE; ++e) {
-              const int i = c0 + (j * kT + tid) * VE + e;
-              if (i >= lo && i < hi && (first || v[e] > bar)) {
-                const key_t x1 = make_key(v[e], i - skew);
-                if (x1 >= least) sh.list[atomicAdd(&sh.n, 1)] = x1;
+              for (int e = 0; e < VE; ++e) {
+                const int i = c0 + (j * kT + tid) * VE + e;
+                const key_t x1 = i >= lo && i < hi && (first || v[e] > bar) ? make_key(v[e], i - skew) : 0;
+                if (x1 && x1 >= least) sh.list[atomicAdd(&sh.n, 1)] = x1;
               }
             }
           }
+          __syncthreads();
         }
-        __syncthreads();
-        if (first || sh.n > 4 * kMaxK) {
+        if (first || sh.n > k + kMaxK / 2) {
           select(sh, k);
           bar = sh.n < k ? -INFINITY : key_value(sh.best[k - 1]);
         }
@@ -362,7 +446,19 @@ __global__ void __launch_bounds__(kT, 4) k_scores(const __grid_constant__ Args a
       first = false;
     }
   }
-  if (k) select(sh, k);
+  if (k) {
+    __syncthreads();
+    const bool full = sh.n > kCap;
+    __syncthreads();
+    if (full) {
+      if (tid == 0) sh.n = 0;
+      careful = first = true;
+      bar = -INFINITY;
+      __syncthreads();
+      goto again;
+    }
+    select(sh, k);
+  }
   z = block_join(sh, z, a.c);
   if (a.splits == 1) {
     answer<T>(a, sh, row, z);
@@ -397,10 +493,11 @@ __global__ void __launch_bounds__(kT) k_scores_join(const __grid_constant__ Args
   answer<T>(a, sh, row, z);
 }
 
-// Slices of a row: two rounds of the GPU's CTAs over the call, at least 4096 elements each.
+// Slices of a row: as many CTAs as the GPU holds at once, at least 16384 elements each (5 rows of 262144:
+// 11.3 us, 14.6 with slices of 4096, whose lists cost more to join).
 int splits_of(int rows, int V, int num_sms) {
-  long long n = 2LL * num_sms / rows;
-  if (n > V / 4096) n = V / 4096;
+  long long n = 4LL * num_sms / rows;
+  if (n > V / 16384) n = V / 16384;
   if (n > kMaxSplits) n = kMaxSplits;
   return n < 1 ? 1 : static_cast<int>(n);
 }

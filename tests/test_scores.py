@@ -133,7 +133,7 @@ def test_temperatures_and_counts(k, temperature):
 @gpu
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("rows,V", [(2, 40000), (400, 20000)])
-@pytest.mark.parametrize("kind", ["equal", "few", "rising", "falling", "one thread", "lowest", "masked", "mostly masked", "all but 3"])
+@pytest.mark.parametrize("kind", ["equal", "few", "zeros", "rising", "falling", "one thread", "lowest", "masked", "mostly masked", "all but 3"])
 def test_ties_orders_and_masks(kind, rows, V, dtype):
     g = torch.Generator().manual_seed(3)
     x = torch.randn((rows, V), generator=g) * 3
@@ -143,6 +143,8 @@ def test_ties_orders_and_masks(kind, rows, V, dtype):
         x = torch.full_like(x, -2.5)
     elif kind == "few":  # hundreds of equal values at the top
         x = torch.randint(-2, 3, (rows, V), generator=g).float()
+    elif kind == "zeros":  # of both signs, which are equal
+        x = torch.where(x > 0, 0.0, torch.where(x > -3, -0.0, x))
     elif kind == "rising":
         x = (i * (60.0 / V) - 30).expand(rows, V).clone()
     elif kind == "falling":
