@@ -178,10 +178,12 @@ def mtp_token_logprobs_workspace(dtype: int, rows: int, V: int, top_k: int) -> i
 def mtp_token_logprobs(logits: int, dtype: int, row_stride: int, token: int, rows: int, V: int, temperature: float,
                        top_k: int, logprob: int, entropy: int, top_ids: int, top_logprobs: int, workspace: int,
                        workspace_bytes: int, stream: int = 0) -> None:
-    _check(load_library().mtp_token_logprobs(logits or None, dtype, row_stride, token or None, rows, V,
-                                             float(temperature), top_k, logprob or None, entropy or None,
-                                             top_ids or None, top_logprobs or None, workspace or None, workspace_bytes,
-                                             stream or None), "mtp_token_logprobs")
+    rc = (_lib or load_library()).mtp_token_logprobs(logits or None, dtype, row_stride, token or None, rows, V,
+                                                     temperature, top_k, logprob or None, entropy or None,
+                                                     top_ids or None, top_logprobs or None, workspace or None,
+                                                     workspace_bytes, stream or None)
+    if rc:
+        _check(rc, "mtp_token_logprobs")
 
 
 def mtp_centroid_head_noalloc(y: int, centroids: int, token_ordering: int, token_embd: int, dtype: int, B: int,

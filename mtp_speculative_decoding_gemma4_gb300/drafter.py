@@ -9,7 +9,7 @@ from typing import Optional
 import torch
 
 from . import binding as B
-from .paged import _need_flat, call_on
+from .paged import _flat_like, _need_flat, call_on
 
 _DT = {"bf16": (B.MTP_DTYPE_BF16, torch.bfloat16), "f32": (B.MTP_DTYPE_F32, torch.float32)}
 
@@ -213,31 +213,37 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, temperature: floa
     dimensions with any row stride, or contiguous), tokens int32 [...]. Returns (logprob, entropy) of
     tokens' shape and, with top_k > 0, (logprob, entropy, top_ids, top_logprobs) with a last
     dimension of top_k. Runs on `stream`, by default torch's current one."""
-    _need_cuda(tokens, "tokens")
     if not (isinstance(logits, torch.Tensor) and logits.is_cuda and logits.dtype in _DTYPES and logits.dim() >= 1):
         raise ValueError("logits must be a CUDA tensor [..., V] of bf16 or fp32")
-    shape, V, dev = logits.shape[:-1], logits.shape[-1], logits.device
-    rows = tokens.numel()
-    if logits.dim() != 2 and not logits.is_contiguous() or V > 1 and logits.stride(-1) != 1:
+    whole, strides, dev = logits.shape, logits.stride(), logits.device
+    shape, V = whole[:-1], whole[-1]
+    if not _flat_like(tokens, torch.int32, dev, shape):
+        raise ValueError(f"tokens must be int32, contiguous, of shape {list(shape)} on {dev}")
+    if len(whole) != 2 and not logits.is_contiguous() or V > 1 and strides[-1] != 1:
         raise ValueError("logits must be [rows][V] with contiguous rows, or contiguous")
-    if tokens.shape != shape or tokens.dtype != torch.int32 or tokens.device != dev:
-        raise ValueError(f"tokens must be int32 of shape {list(shape)} on {dev}")
-    return call_on(dev, stream, _token_logprobs, logits, tokens, shape, rows, V, temperature, top_k)
+    return call_on(dev, stream, _token_logprobs, logits, tokens, shape, strides[0] if len(whole) == 2 else V, V,
+                   temperature, top_k)
 
 
 _DTYPES = {torch.bfloat16: B.MTP_DTYPE_BF16, torch.float32: B.MTP_DTYPE_F32}
+_scores_workspace = {}  # bytes, by (dtype, rows, V, top_k)
 
 
-def _token_logprobs(st, logits, tokens, shape, rows, V, temperature, top_k):
-    dtype, dev = _DTYPES[logits.dtype], logits.device
-    n = B.mtp_token_logprobs_workspace(dtype, rows, V, top_k)
+def _token_logprobs(st, logits, tokens, shape, stride, V, temperature, top_k):
+    dtype, dev, f32, rows = _DTYPES[logits.dtype], logits.device, torch.float32, tokens.numel()
+    key = (dtype, rows, V, top_k)
+    n = _scores_workspace.get(key)
+    if n is None:
+        if len(_scores_workspace) >= 1024:
+            _scores_workspace.clear()
+        n = _scores_workspace[key] = B.mtp_token_logprobs_workspace(*key)
     ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-    out = torch.empty((2,) + tuple(shape), dtype=torch.float32, device=dev)
+    logprob, entropy = torch.empty(shape, dtype=f32, device=dev), torch.empty(shape, dtype=f32, device=dev)
     ids = best = None
     if top_k:
-        ids = torch.empty(tuple(shape) + (top_k,), dtype=torch.int32, device=dev)
-        best = torch.empty(tuple(shape) + (top_k,), dtype=torch.float32, device=dev)
-    B.mtp_token_logprobs(logits.data_ptr(), dtype, logits.stride(0) if logits.dim() == 2 and rows > 1 else V,
-                         tokens.data_ptr(), rows, V, temperature, top_k, out[0].data_ptr(), out[1].data_ptr(), _ptr(ids),
-                         _ptr(best), _ptr(ws), n, st)
-    return (out[0], out[1], ids, best) if top_k else (out[0], out[1])
+        ids = torch.empty((*shape, top_k), dtype=torch.int32, device=dev)
+        best = torch.empty((*shape, top_k), dtype=f32, device=dev)
+    B.mtp_token_logprobs(logits.data_ptr(), dtype, stride if rows > 1 else V, tokens.data_ptr(), rows, V, temperature,
+                         top_k, logprob.data_ptr(), entropy.data_ptr(), ids.data_ptr() if top_k else 0,
+                         best.data_ptr() if top_k else 0, ws.data_ptr() if n else 0, n, st)
+    return (logprob, entropy, ids, best) if top_k else (logprob, entropy)

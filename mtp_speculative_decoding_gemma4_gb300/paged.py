@@ -229,11 +229,12 @@ def page_fork(kv: PagedKV, src: torch.Tensor, dst: torch.Tensor, length: torch.T
 
 
 def _fork(st, kv, src, dst, length, free_ring, ring_state):
-    out = torch.empty(kv.batch + 6, dtype=_i32, device=kv.device)
+    n = kv.batch
+    out = torch.empty(n + 6, dtype=_i32, device=kv.device)
     at = out.data_ptr()
-    B.mtp_page_fork(kv.p, kv.batch, src.data_ptr(), dst.data_ptr(), length.data_ptr(), src.shape[0],
-                    free_ring.data_ptr(), ring_state.data_ptr(), at + 24, at, at + 8, st)
-    return out[6:], out[:2], out[2:6]
+    B.mtp_page_fork(kv.p, n, src.data_ptr(), dst.data_ptr(), length.data_ptr(), src.shape[0], free_ring.data_ptr(),
+                    ring_state.data_ptr(), at, at + 4 * n, at + 4 * n + 8, st)
+    return out.split((n, 2, 4))
 
 
 def page_collect(kv: PagedKV, free_ring: torch.Tensor, compact: bool = False, stream: Optional[int] = None):
@@ -258,7 +259,7 @@ def _collect(st, kv, free_ring, compact):
     at = out.data_ptr()
     _with_workspace(kv, st, n, lambda ws, n: B.mtp_page_collect(
         kv.p, kv.batch, free_ring.data_ptr(), table.data_ptr() if compact else 0, cols, at, at + 8, ws, n, st))
-    return table, out[:2], out[2:]
+    return (table, *out.split((2, 4)))
 
 
 def _queries(q, kv: PagedKV):
