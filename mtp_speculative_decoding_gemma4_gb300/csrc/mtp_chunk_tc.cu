@@ -78,8 +78,7 @@ struct Lay {
   static constexpr int PB = D == 256 && N == 128 ? 1 : 2;  // probability buffers
   static constexpr int misc_bytes = 3072;
   static constexpr int room = 232448 - misc_bytes - QBY - PB * PBY;
-  static constexpr int ring0 = room / slot > 16 ? 16 : room / slot;
-  static constexpr int ring = ring0 / NP * NP;           // a tile's slots of one operand are neighbours
+  static constexpr int ring = room / slot > 12 ? 12 : room / slot;  // (a tile's slots may wrap)
   static constexpr int q = ring * slot;
   static constexpr int p = q + QBY;
   static constexpr int mref = p + PB * PBY;              // [N] minus the rows' references
@@ -410,65 +409,75 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(ifull0 + 8 * slot);
           if (++slot == kInfo) slot = 0;
+          if (N == 32 && lane >> ngs == j && page >= 0) {
+            // with few rows keys come from memory once, and the ring alone holds too few of them in flight
+            const int t0 = pos & ((1 << c.pshift) - 1);
+#pragma unroll 1
+            for (int x = 0; x < D; x += 64) {
+              prefetch_4d(&mapK, x, t0, s.kvh, page);
+              if (own_v) prefetch_4d(&mapV, x, t0, s.kvh, page);
+            }
+          }
         }
       }
     }
     s.tiles = -1;
     if (ok) put_seg(s);
   } else if (warp == 4 * WG) {
-    // ---------------- loads
-    if (elect()) {
-      const int rs = g.rshift, R = 1 << rs, ng = KT >> rs, P = 1 << c.pshift;
-      int pc = 0, slot = 0, tt = 0, is = 0;  // slots so far, the next slot and the ring's phase there; tiles, place of their pages
-      unsigned phase = 0, iphase = 0;
-      bool ok = true;
-      Seg s;
+    // ---------------- loads. The whole warp walks, with everything that a copy takes in uniform
+    // registers; one elected thread issues (a tile of 64 KB took 1800 cycles to issue from one thread's
+    // own registers, as long as its keys take from memory).
+    const int rs = g.rshift, R = 1 << rs, ng = KT >> rs, P = 1 << c.pshift;
+    int pc = 0, slot = 0, tt = 0, is = 0;  // slots so far, the next slot and the ring's phase there; tiles, place of their pages
+    unsigned phase = 0, iphase = 0;
+    bool ok = true;
+    Seg s;
+    auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
 #pragma unroll 1
-      for (int i = 0; ok && get_seg(i, s); ++i) {
+    for (int i = 0; ok && all(get_seg(i, s)); ++i) {
+      const int tiles = __shfl_sync(0xffffffffu, s.tiles, 0), kvh = __shfl_sync(0xffffffffu, s.kvh, 0), k0 = __shfl_sync(0xffffffffu, s.k0, 0);
 #pragma unroll 1
-        for (int k = 0; k < s.tiles && ok; ++k, ++tt) {
-          if (!wait_in(ifull0 + 8 * is, iphase, dead, kSpin)) {
-            ok = false;
-            break;
-          }
-          const int* in = info + is * 16;
-          const int off0 = ((s.k0 + k) << LY::KS) & (P - 1);  // 0 unless a page is longer than a tile
+      for (int k = 0; k < tiles; ++k, ++tt) {
+        ok = all(wait_in(ifull0 + 8 * is, iphase, dead, kSpin));
+        if (!ok) break;
+        const int mine = info[is * 16 + (lane & 15)];  // -1: zeros
+        const int off0 = ((k0 + k) << LY::KS) & (P - 1);  // 0 unless a page is longer than a tile
+#pragma unroll
+        for (int j = 0; j < 2 * NP; ++j) {
+          if (j >= PT) break;
+          const unsigned bar = full0 + 8 * slot;
+          if (pc >= kRing) ok = all(wait_in(empty0 + 8 * slot, phase ^ 1, dead, kSpin));
+          if (!ok) break;
+          if (j == 0 && lane == 0) *begun = tt + 1;
+          const unsigned dst = base + slot * LY::slot;
+          if (elect()) mbar_expect_tx(bar, LY::slot);
+          __syncwarp();
 #pragma unroll 1
-          for (int j = 0; j < PT; ++j) {
-            const unsigned bar = full0 + 8 * slot;
-            if (pc >= kRing && !wait_in(empty0 + 8 * slot, phase ^ 1, dead, kSpin)) {
-              ok = false;
-              break;
-            }
-            if (j == 0) *begun = tt + 1;
-            mbar_expect_tx(bar, LY::slot);
-            const int x = (j < NP ? j : j - NP) * 128;
-            const CUtensorMap* map = j < NP ? &mapK : &mapV;
-            unsigned dst = base + slot * LY::slot;
-#pragma unroll 1
-            for (int r = 0; r < ng; ++r, dst += R * 128) {
-              const int page = in[r];  // -1: zeros
-              tma_4d(dst, map, x, off0, s.kvh, page, bar);
-              tma_4d(dst + LY::box, map, x + 64, off0, s.kvh, page, bar);
-            }
-            ++pc;
-            if (++slot == kRing) {
-              slot = 0;
-              phase ^= 1;
+          for (int r = 0; r < ng; ++r) {
+            const int page = __shfl_sync(0xffffffffu, mine, r);
+            if (elect()) {
+              tma_4d(dst + r * R * 128, j < NP ? &mapK : &mapV, (j < NP ? j : j - NP) * 128, off0, kvh, page, bar);
+              tma_4d(dst + r * R * 128 + LY::box, j < NP ? &mapK : &mapV, (j < NP ? j : j - NP) * 128 + 64, off0, kvh, page, bar);
             }
           }
-          if (++is == kInfo) {
-            is = 0;
-            iphase ^= 1;
+          ++pc;
+          if (++slot == kRing) {
+            slot = 0;
+            phase ^= 1;
           }
+        }
+        if (!ok) break;
+        if (++is == kInfo) {
+          is = 0;
+          iphase ^= 1;
         }
       }
-      // no copy may be in flight when the CTA ends
+    }
+    // no copy may be in flight when the CTA ends
 #pragma unroll 1
-      for (int i = max(0, pc - kRing); i < pc; ++i) {
-        const long long t0 = clock64();
-        while (!try_wait(full0 + 8 * (i % kRing), (i / kRing) & 1) && clock64() - t0 < kSpin) {
-        }
+    for (int i = max(0, pc - kRing); i < pc; ++i) {
+      const long long t0 = clock64();
+      while (!all(try_wait(full0 + 8 * (i % kRing), (i / kRing) & 1)) && all(clock64() - t0 < kSpin)) {
       }
     }
     __syncwarp();
@@ -500,6 +509,7 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
     const unsigned tO = tmem, tS = tmem + NP * N;
     const unsigned kd = desc_lo(base, 16), vd = desc_lo(base, LY::box), qd = desc_lo(base + LY::q, 16),
                    pd = desc_lo(base + LY::p, KT * 128);
+    auto wrap = [](int slot) { return slot >= kRing ? slot - kRing : slot; };
     auto done = [](unsigned bar, unsigned parity) { return __all_sync(0xffffffffu, test_wait(bar, parity)) != 0; };
     // tiles whose scores / sums are issued; tiles left of the scores' unit; units begun by either; ring
     // places
@@ -526,17 +536,17 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
         bool ready = done(pfull0 + 8 * (tp & 1), (tp >> 1) & 1) &&
                      (!first || pseg == 0 || done(ofree0 + 8 * ((pseg - 1) % kSegs), ((pseg - 1) / kSegs) & 1));
         if (own_v)
-          for (int i = 0; i < NP; ++i) ready = ready && done(full0 + 8 * (sp + i), fp);
+          for (int i = 0; i < NP; ++i) ready = ready && done(full0 + 8 * wrap(sp + i), fp ^ (sp + i >= kRing));
         if (ready) {
           if (elect()) {
             fence_after();
-            const unsigned v0 = vd + sp * (LY::slot >> 4), p0 = pd + (PB == 1 ? 0 : (tp & 1) * (LY::PBY >> 4));
+            const unsigned p0 = pd + (PB == 1 ? 0 : (tp & 1) * (LY::PBY >> 4));
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
+              const unsigned v0 = vd + wrap(sp + i) * (LY::slot >> 4);
 #pragma unroll
-              for (int x = 0; x < KT / 16; ++x)
-                mma(tO + i * N, v0 + ((i * LY::slot + x * 2048) >> 4), p0 + (x * 2048 >> 4), idO, x > 0 || !first);
-              commit(empty0 + 8 * (sp + i));
+              for (int x = 0; x < KT / 16; ++x) mma(tO + i * N, v0 + (x * 2048 >> 4), p0 + (x * 2048 >> 4), idO, x > 0 || !first);
+              commit(empty0 + 8 * wrap(sp + i));
             }
             commit(odone0 + 8 * (tp & 1));
           }
@@ -556,19 +566,20 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
         if (got == 1 && (tq < 2 || done(sfree0 + 8 * (tq & 1), ((tq >> 1) - 1) & 1))) got = 2;
 #pragma unroll
         for (int i = 0; i < NP; ++i)
-          if (got == 2 + i && done(full0 + 8 * (sq + i), fq)) got = 3 + i;
+          if (got == 2 + i && done(full0 + 8 * wrap(sq + i), fq ^ (sq + i >= kRing))) got = 3 + i;
         if (got == 2 + NP) {
           got = 0;
           if (elect()) {
             fence_after();
-            const unsigned k0 = kd + sq * (LY::slot >> 4), d = tS + (tq & 1) * N;
+            const unsigned d = tS + (tq & 1) * N;
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
+              const unsigned k0 = kd + wrap(sq + i) * (LY::slot >> 4);
 #pragma unroll
               for (int x = 0; x < 8; ++x)
-                mma(d, k0 + ((i * LY::slot + (x >> 2) * LY::box + (x & 3) * 32) >> 4),
+                mma(d, k0 + (((x >> 2) * LY::box + (x & 3) * 32) >> 4),
                     qd + (((2 * i + (x >> 2)) * (N * 128) + (x & 3) * 32) >> 4), idS, i > 0 || x > 0);
-              if (own_v) commit(empty0 + 8 * (sq + i));
+              if (own_v) commit(empty0 + 8 * wrap(sq + i));
             }
             commit(sfull0 + 8 * (tq & 1));
             if (left == 1) commit(qused);
@@ -648,7 +659,7 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
         __syncwarp();
         fence_after();
         // x: the exponents under the references; a second time where these have moved
-        float x[NC];
+        float x[NC], first = 0.f;  // (first: the score with the warpgroup's first row)
         // the rows [cmin, cmax) of this warpgroup attend this thread's key (its pages were found before
         // they were loaded)
         const int pos = ((s.k0 + t) << LY::KS) + key, rel = pos - s.pos0;
@@ -668,6 +679,7 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
 #pragma unroll
             for (int i = 0; i < NC; i += 16) ld16(tS + buf * N + i, x + i);
             ld_wait();
+            first = x[0];
 #pragma unroll
             for (int i = 0; i < NC; i += 4) {
               const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(negm + i);
@@ -724,7 +736,8 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
             bar_wg();
             if (wt == 0) over[buf] = 0;
             if (wt < NC) {
-              const float mo = -negm[wt], mn = fmaxf(unordered(top[wt]), mo);
+              // (each reference by its own row's scores, so that a row's bits do not depend on other rows)
+              const float mo = -negm[wt], tm = unordered(top[wt]), mn = tm > mo + 8.f ? tm : mo;
               top[wt] = kLowest;
               if (wt < nrw) {
                 fac[wt] = mo == -INFINITY ? 0.f : ex2(mo - mn);
@@ -773,32 +786,41 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
                   make_uint4(pack2(x[i], x[i + 1]), pack2(x[i + 2], x[i + 3]), pack2(x[i + 4], x[i + 5]), pack2(x[i + 6], x[i + 7]));
           }
         }
-        // keys of the tile that no row of the unit attends, and values that are not finite in keys that
-        // only some do: this warpgroup's part of the dims
-        const int amin = cmin + col0, amax = min(cmax + col0, nr);
-        if (edge && has && page >= 0 && (!valid || amin > 0 || amax < nr)) {
-          constexpr int V = D / 8 / WG;
-#pragma unroll 1
-          for (int e = wg * V; e < (wg + 1) * V; ++e) {  // vectors of 8 dims
-            const int pc = at * PT + (own_v ? NP : 0) + (e >> 4), slot = pc % kRing;
-            if (own_v && !wait_in(full0 + 8 * slot, (pc / kRing) & 1, dead, kSpin)) break;
-            uint4* const at16 = reinterpret_cast<uint4*>(sm + slot * LY::slot + ((e >> 3) & 1) * LY::box + key * 128) + (e & 7);
-            if (!valid) {
-              *at16 = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            uint4 v = *at16;
-            unsigned* u = reinterpret_cast<unsigned*>(&v);
-            bool off = false;
+        // Keys of the tile that no row of the unit attends, and keys that only some do: what is not finite in
+        // their values becomes 0, and the rows that attend it get NaN. With V = K a key whose score with
+        // the first row is finite is finite itself, and is not looked at.
+        if (edge) {
+          const int amin = cmin + col0, amax = min(cmax + col0, nr);
+          bool look = has && page >= 0 && (!valid || amin > 0 || amax < nr);
+          if (!own_v) look = look && wg == 0 && !isfinite(first);
+          const unsigned todo = __ballot_sync(0xffffffffu, look);
+          if (todo) {
+            // the warp's keys, V vectors of 8 dims of each: all dims, or with a V this warpgroup's part
+            constexpr int kPart = D / 8 / WG;
+            const int V = own_v ? kPart : D / 8, v0 = own_v ? wg * kPart : 0;
+            if (own_v)
+              for (int i = 0; i < NP; ++i) wait_in(full0 + 8 * ((at * PT + NP + i) % kRing), ((at * PT + NP + i) / kRing) & 1, dead, kSpin);
+#pragma unroll 2
+            for (int it = 0; it < V; ++it) {
+              const int src = (it * 32 + lane) / V, e = (it * 32 + lane) % V + v0;
+              const int lo = __shfl_sync(0xffffffffu, valid ? amin : -1, src), hi = __shfl_sync(0xffffffffu, amax, src);
+              if (!(todo >> src & 1)) continue;
+              const int slot = (at * PT + (own_v ? NP : 0) + (e >> 4)) % kRing, row = KT == 128 ? 32 * ww + src : 16 * ww + src;
+              uint4* const at16 = reinterpret_cast<uint4*>(sm + slot * LY::slot + ((e >> 3) & 1) * LY::box + row * 128) + (e & 7);
+              uint4 v = *at16;
+              unsigned* u = reinterpret_cast<unsigned*>(&v);
+              bool off = false;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if ((u[i] & 0x7f800000u) == 0x7f800000u) off = true, u[i] &= 0xffffu;
-              if ((u[i] & 0x7f80u) == 0x7f80u) off = true, u[i] &= 0xffff0000u;
-            }
-            if (off) {
-              *at16 = v;
+              for (int i = 0; i < 4; ++i) {
+                if ((u[i] & 0x7f800000u) == 0x7f800000u) off = true, u[i] &= 0xffffu;
+                if ((u[i] & 0x7f80u) == 0x7f80u) off = true, u[i] &= 0xffff0000u;
+              }
+              if (off) {
+                *at16 = v;
+                if (lo >= 0)
 #pragma unroll 1
-              for (int i = amin; i < amax; ++i) atomicOr(bad + 4 * wg + (i >> 5), 1u << (i & 31));
+                  for (int i = lo; i < hi; ++i) atomicOr(bad + 4 * wg + (i >> 5), 1u << (i & 31));
+              }
             }
           }
         }
