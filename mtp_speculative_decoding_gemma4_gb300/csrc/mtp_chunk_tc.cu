@@ -139,6 +139,23 @@ __device__ __forceinline__ int ordered(float v) {
 __device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
 constexpr int kLowest = static_cast<int>(0xff800000u ^ 0x7fffffffu);  // ordered(-inf)
 
+// The maxima of N <= 32 values over the warp: lane i ends with that of value i * N / 32 in v[0] (O: 16).
+template <int N, int O>
+__device__ __forceinline__ void max_scatter(float* v, int lane) {
+  if constexpr (O > 0) {
+    if constexpr (N > 1) {
+      constexpr int h = N / 2;
+      const bool up = (lane & O) != 0;
+#pragma unroll
+      for (int i = 0; i < h; ++i) v[i] = fmaxf(up ? v[i + h] : v[i], __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + h], O));
+      max_scatter<h, O / 2>(v, lane);
+    } else {
+      v[0] = fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], O));
+      max_scatter<1, O / 2>(v, lane);
+    }
+  }
+}
+
 // Bounded wait; false when this CTA has given up (the word `dead`) or gives up here. (Inlined: a call
 // would keep the softmax from its registers.)
 __device__ __forceinline__ bool wait_in(unsigned bar, unsigned parity, volatile int* dead, long long limit) {
@@ -176,9 +193,11 @@ struct Walk {
   __device__ __forceinline__ void locate(const Args& g, int subs) {
     const int lane = threadIdx.x & 31, each = (g.a.B + 31) >> 5, b0 = min(g.a.B, lane * each), b1 = min(g.a.B, b0 + each);
     long long mine = 0;
+    Tiles x;  // of the lane's last sequence: its only one in small batches
+    int x0 = 0;
 #pragma unroll 1
     for (int i = b0; i < b1; ++i) {
-      const Tiles x = tiles_of(g, KS, i, s0);
+      x = tiles_of(g, KS, i, x0);
       mine += x.cost(x.count());
     }
     mine *= subs;
@@ -199,8 +218,9 @@ struct Walk {
       long long at = r - (incl - mine), c;
 #pragma unroll 1
       for (b = b0;; ++b) {
-        t = tiles_of(g, KS, b, s0);
-        c = t.cost(t.count());
+        t = x;
+        if (each > 1) t = tiles_of(g, KS, b, x0);
+        c = each > 1 ? t.cost(t.count()) : mine / subs;
         if (at < c * subs) break;
         at -= c * subs;
       }
@@ -218,7 +238,12 @@ struct Walk {
     sub = __shfl_sync(0xffffffffu, sub, f);
     tile = __shfl_sync(0xffffffffu, tile, f);
     off = __shfl_sync(0xffffffffu, off, f);
-    t = tiles_of(g, KS, b, s0);
+    t = x;
+    t.n = __shfl_sync(0xffffffffu, t.n, f);
+    t.first = __shfl_sync(0xffffffffu, t.first, f);
+    t.L = __shfl_sync(0xffffffffu, t.L, f);
+    s0 = __shfl_sync(0xffffffffu, x0, f);
+    if (each > 1) t = tiles_of(g, KS, b, s0);
   }
   struct Part {
     int b, sub, tile;  // sub: KV head * groups + group
@@ -722,16 +747,13 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
 #pragma unroll 1
             for (int i0 = 0; i0 < nrw; i0 += 16) {
               float v[16];
-              int mine = kLowest;
               ld16(tS + buf * N + i0, v);
               ld_wait();
               const unsigned on = has ? bits(cmin - i0, cmax - i0) : 0u;
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const int m = __reduce_max_sync(0xffffffffu, on >> i & 1 ? ordered(pg::attended(v[i] * a.scale_log2)) : kLowest);
-                mine = lane == i ? m : mine;
-              }
-              if (lane < 16) atomicMax(top + i0 + lane, mine);
+              for (int i = 0; i < 16; ++i) v[i] = on >> i & 1 ? pg::attended(v[i] * a.scale_log2) : -INFINITY;
+              max_scatter<16, 16>(v, lane);
+              if (!(lane & 1)) atomicMax(top + i0 + lane / 2, ordered(v[0]));
             }
             bar_wg();
             if (wt == 0) over[buf] = 0;
