@@ -123,6 +123,12 @@ __device__ __forceinline__ void ld16(unsigned t, float* v) {
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(t));
 }
+__device__ __forceinline__ void ld32(unsigned t, float* v) {
+  unsigned* r = reinterpret_cast<unsigned*>(v);
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+               : "r"(t));
+}
 __device__ __forceinline__ void st16(unsigned t, const float* v) {
   const unsigned* r = reinterpret_cast<const unsigned*>(v);
   asm volatile(
@@ -701,8 +707,8 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
         if (nrw) {
 #pragma unroll 1
           for (int pass = 0;; ++pass) {
-#pragma unroll
-            for (int i = 0; i < NC; i += 16) ld16(tS + buf * N + i, x + i);
+            if constexpr (NC == 32) ld32(tS + buf * N, x);
+            else ld16(tS + buf * N, x);
             ld_wait();
             first = x[0];
 #pragma unroll
