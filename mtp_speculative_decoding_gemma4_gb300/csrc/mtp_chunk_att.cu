@@ -6,9 +6,11 @@
 // This file: the CUDA-core kernel for every dtype and head dim, and the join of the splits. A tile
 // is R = 16 RI rows (the query heads of one KV head for R / G tokens), a CTA of 256 threads takes 64
 // keys at a time: scores by 4 RI values per thread from shared memory (dims in blocks of 64, the
-// next block's global loads in flight), then the sums, RI rows x 4 dims per block of 64 and thread.
+// next block's global loads in flight), then the sums, RI rows x 4 dims per block of 64 and thread; with
+// few rows (RI = 1) a warp takes two of them, so that a vector of shared memory serves more products.
 // What bounds it is the fp32 pipes where rows are many (RI = 4: 16 products per two shared-memory
-// vectors), the loads where they are few; a unit's keys are split over CTAs while the GPU has room.
+// vectors), shared memory and latency where they are few; a unit's keys are split over CTAs while the
+// GPU has room.
 #include "mtp_common.cuh"
 #include "mtp_launch.h"
 #include "mtp_paged.cuh"
@@ -78,10 +80,11 @@ template <typename T, int DC, int RI>
 __global__ void __launch_bounds__(kTokThreads) k_chunk(const __grid_constant__ ChunkArgs a) {
   pdl_enter();
   constexpr int R = 16 * RI, D = 64 * DC, QP = D + 4, VE = Vec<T>::n, LV = kKeys * 64 / VE / kTokThreads;
+  constexpr int KP = RI == 1 ? 80 : kPad;  // floats between keys
   extern __shared__ __align__(16) float sm[];
   float* sq = sm;                 // [R][QP]
-  float* sk = sq + R * QP;        // [64 keys][kPad]: 64 dims of keys or values
-  float* sp = sk + kKeys * kPad;  // [R][kPad] scores, probabilities
+  float* sk = sq + R * QP;        // [64 keys][KP]: 64 dims of keys or values
+  float* sp = sk + kKeys * KP;    // [R][kPad] scores, probabilities
   __shared__ long long s_at[kKeys];  // a key's row in the cache, -1: no row that any query may read
   __shared__ int s_bad[kKeys], s_any;
   const Cache& c = a.c;
@@ -116,17 +119,27 @@ __global__ void __launch_bounds__(kTokThreads) k_chunk(const __grid_constant__ C
 #pragma unroll
     for (int e = 0; e < VE; ++e) sq[r * QP + v + e] = x[e];
   }
-  float acc[RI][4 * DC], m[RI], l[RI];
+  // RI = 4: rows ty + 16 i, scores with keys tx + 16 j, sums of dims 4 tx ..
+  // RI = 1: a warp for two rows. Scores: both rows, keys kq + 8 j, every fourth vector of the dims, then
+  // added up so that a thread has 4 scores of row `mine`; sums: both rows, dims 4 tx .., every other key
+  constexpr int RA = RI == 1 ? 2 : RI;  // rows of a thread's sums
+  const int warp = tid >> 5, lane = tid & 31, dg = lane & 3, kq = lane >> 2, kh = lane >> 4;
+  const int mine = 2 * warp + (dg >> 1);
+  auto row_of = [&](int i) { return RI == 1 ? mine : ty + 16 * i; };                                  // of m, l and scores
+  auto key_of = [&](int j) { return RI == 1 ? kq + 8 * (4 * (dg & 1) + j) : tx + 16 * j; };
+  float acc[RA][4 * DC], m[RI], l[RI];
   int qpos[RI];
 #pragma unroll
   for (int i = 0; i < RI; ++i) {
     m[i] = -INFINITY;
     l[i] = 0.f;
-    const int r = ty + 16 * i;
+    const int r = row_of(i);
     qpos[i] = r < nr ? pos0 + r / Gc : -1;  // -1: a row of no token attends nothing
+  }
+#pragma unroll
+  for (int i = 0; i < RA; ++i)
 #pragma unroll
     for (int e = 0; e < 4 * DC; ++e) acc[i][e] = 0.f;
-  }
   // one block of 64 dims of 64 rows: into registers, then into shared memory
   float buf[LV][VE];
   auto fetch = [&](const void* from, int dim0) {
@@ -160,7 +173,7 @@ __global__ void __launch_bounds__(kTokThreads) k_chunk(const __grid_constant__ C
       }
 #pragma unroll
       for (int e = 0; e < VE; e += 4)
-        *reinterpret_cast<float4*>(sk + key * kPad + v + e) = make_float4(buf[j][e], buf[j][e + 1], buf[j][e + 2], buf[j][e + 3]);
+        *reinterpret_cast<float4*>(sk + key * KP + v + e) = make_float4(buf[j][e], buf[j][e + 1], buf[j][e + 2], buf[j][e + 3]);
     }
   };
   const void* vals = c.v ? c.v : c.k;
@@ -180,9 +193,9 @@ __global__ void __launch_bounds__(kTokThreads) k_chunk(const __grid_constant__ C
     }
     __syncthreads();
     fetch(c.k, 0);
-    float s[RI][4];
+    float s[RI == 1 ? 4 : RI][4];  // RI = 1: s[2 row + half of the keys][..]
 #pragma unroll
-    for (int i = 0; i < RI; ++i)
+    for (int i = 0; i < (RI == 1 ? 4 : RI); ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
 #pragma unroll 1
@@ -190,34 +203,60 @@ __global__ void __launch_bounds__(kTokThreads) k_chunk(const __grid_constant__ C
       stage(false);
       __syncthreads();
       if (x + 1 < DC) fetch(c.k, 64 * (x + 1));
+      if constexpr (RI == 1) {
+#pragma unroll
+        for (int e = 4 * dg, n = 0; n < 4; ++n, e += 16) {
+          const float4 q0 = *reinterpret_cast<const float4*>(sq + 2 * warp * QP + 64 * x + e),
+                       q1 = *reinterpret_cast<const float4*>(sq + (2 * warp + 1) * QP + 64 * x + e);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float4 kv = *reinterpret_cast<const float4*>(sk + (kq + 8 * j) * KP + e);
+            float &a0 = s[j >> 2][j & 3], &a1 = s[2 + (j >> 2)][j & 3];
+            a0 = fmaf(q0.x, kv.x, fmaf(q0.y, kv.y, fmaf(q0.z, kv.z, fmaf(q0.w, kv.w, a0))));
+            a1 = fmaf(q1.x, kv.x, fmaf(q1.y, kv.y, fmaf(q1.z, kv.z, fmaf(q1.w, kv.w, a1))));
+          }
+        }
+      } else {
 #pragma unroll 4
-      for (int e = 0; e < 64; e += 4) {
-        float4 kv[4], qv;
+        for (int e = 0; e < 64; e += 4) {
+          float4 kv[4], qv;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(sk + (tx + 16 * j) * kPad + e);
+          for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(sk + (tx + 16 * j) * KP + e);
 #pragma unroll
-        for (int i = 0; i < RI; ++i) {
-          qv = *reinterpret_cast<const float4*>(sq + (ty + 16 * i) * QP + 64 * x + e);
+          for (int i = 0; i < RI; ++i) {
+            qv = *reinterpret_cast<const float4*>(sq + (ty + 16 * i) * QP + 64 * x + e);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            s[i][j] = fmaf(qv.x, kv[j].x, fmaf(qv.y, kv[j].y, fmaf(qv.z, kv[j].z, fmaf(qv.w, kv[j].w, s[i][j]))));
+            for (int j = 0; j < 4; ++j)
+              s[i][j] = fmaf(qv.x, kv[j].x, fmaf(qv.y, kv[j].y, fmaf(qv.z, kv[j].z, fmaf(qv.w, kv[j].w, s[i][j]))));
+          }
         }
       }
       if (x + 1 < DC) __syncthreads();
     }
     fetch(vals, 0);
+    if constexpr (RI == 1) {  // over the four groups of dims: the row, then the half of the keys
+      const bool r1 = dg & 2, k1 = dg & 1;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          s[i][j] = (r1 ? s[2 + i][j] : s[i][j]) + __shfl_xor_sync(0xffffffffu, r1 ? s[i][j] : s[2 + i][j], 2);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[0][j] = (k1 ? s[1][j] : s[0][j]) + __shfl_xor_sync(0xffffffffu, k1 ? s[0][j] : s[1][j], 1);
+    }
 #pragma unroll
     for (int i = 0; i < RI; ++i) {
       float mx = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int key = tx + 16 * j, pos = k0 + key;
+        const int key = key_of(j), pos = k0 + key;
         const bool on = pos <= qpos[i] && s_at[key] >= 0 && (a.window <= 0 || pos > qpos[i] - a.window);
         s[i][j] = on ? attended(s[i][j] * a.scale_log2) : -INFINITY;
         mx = fmaxf(mx, s[i][j]);
       }
 #pragma unroll
-      for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      for (int o = 1; o < (RI == 1 ? 32 : 16); o <<= 1)
+        if (RI != 1 || o != 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       mx = fmaxf(m[i], mx);
       const float corr = pexp(m[i], mx);
       m[i] = mx;
@@ -226,9 +265,18 @@ __global__ void __launch_bounds__(kTokThreads) k_chunk(const __grid_constant__ C
       for (int j = 0; j < 4; ++j) {
         const float p = pexp(s[i][j], mx);
         l[i] += p;
-        sp[(ty + 16 * i) * kPad + tx + 16 * j] = p;
+        sp[row_of(i) * kPad + key_of(j)] = p;
       }
-      if (corr != 1.f) {
+      if constexpr (RI == 1) {
+        const float c0 = __shfl_sync(0xffffffffu, corr, 0), c1 = __shfl_sync(0xffffffffu, corr, 2);
+        if (c0 != 1.f || c1 != 1.f) {
+#pragma unroll
+          for (int e = 0; e < 4 * DC; ++e) {
+            acc[0][e] *= c0;
+            acc[RA - 1][e] *= c1;
+          }
+        }
+      } else if (corr != 1.f) {
 #pragma unroll
         for (int e = 0; e < 4 * DC; ++e) acc[i][e] *= corr;
       }
@@ -240,13 +288,13 @@ __global__ void __launch_bounds__(kTokThreads) k_chunk(const __grid_constant__ C
       __syncthreads();
       if (x + 1 < DC) fetch(vals, 64 * (x + 1));
 #pragma unroll 2
-      for (int key = 0; key < kKeys; key += 4) {
+      for (int key = RI == 1 ? 4 * kh : 0; key < kKeys; key += RI == 1 ? 8 : 4) {
         float4 v[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const float4*>(sk + (key + j) * kPad + 4 * tx);
+        for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const float4*>(sk + (key + j) * KP + 4 * tx);
 #pragma unroll
-        for (int i = 0; i < RI; ++i) {
-          const float4 p = *reinterpret_cast<const float4*>(sp + (ty + 16 * i) * kPad + key);
+        for (int i = 0; i < RA; ++i) {
+          const float4 p = *reinterpret_cast<const float4*>(sp + (RI == 1 ? 2 * warp + i : ty + 16 * i) * kPad + key);
           float* o = acc[i] + 4 * x;
           o[0] = fmaf(p.x, v[0].x, fmaf(p.y, v[1].x, fmaf(p.z, v[2].x, fmaf(p.w, v[3].x, o[0]))));
           o[1] = fmaf(p.x, v[0].y, fmaf(p.y, v[1].y, fmaf(p.z, v[2].y, fmaf(p.w, v[3].y, o[1]))));
@@ -262,15 +310,27 @@ __global__ void __launch_bounds__(kTokThreads) k_chunk(const __grid_constant__ C
         if (s_bad[key]) {
 #pragma unroll
           for (int i = 0; i < RI; ++i)
-            if (sp[(ty + 16 * i) * kPad + key] != 0.f) l[i] = NAN;
+            if (sp[row_of(i) * kPad + key] != 0.f) l[i] = NAN;
         }
     }
   }
+  if constexpr (RI == 1) {  // the halves of the keys; then a half of the warp keeps one row
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+      if (o != 2) l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
+    l[0] = __shfl_sync(0xffffffffu, l[0], 2 * kh);
+    m[0] = __shfl_sync(0xffffffffu, m[0], 2 * kh);
+#pragma unroll
+    for (int e = 0; e < 4 * DC; ++e)
+      acc[0][e] = (kh ? acc[RA - 1][e] : acc[0][e]) + __shfl_xor_sync(0xffffffffu, kh ? acc[0][e] : acc[RA - 1][e], 16);
+  }
 #pragma unroll
   for (int i = 0; i < RI; ++i) {
+    if constexpr (RI != 1) {
 #pragma unroll
-    for (int o = 1; o < 16; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
-    const int r = ty + 16 * i;
+      for (int o = 1; o < 16; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+    }
+    const int r = RI == 1 ? 2 * warp + kh : ty + 16 * i;
     if (r >= nr) continue;
     const size_t row = q_row(r) * a.nh + head(r);
     if (a.nsplit == 1) {
@@ -324,6 +384,7 @@ __global__ void __launch_bounds__(256) k_chunk_join(const __grid_constant__ Chun
   for (int v0 = 0; v0 < d; v0 += 128) {
     const int v = v0 + 4 * lane;
     float4 s = make_float4(0, 0, 0, 0);
+#pragma unroll 8
     for (int i = 0; i < n; ++i) {
       const float f = __shfl_sync(0xffffffffu, i < 32 ? w[0] : w[1], i & 31);
       if (v < d) {
@@ -349,21 +410,22 @@ long long slots_of(const ChunkArgs& a, int R) {
   return a.T / tpt + a.B;
 }
 
-// Splits of a tile's keys: about 4 CTAs per SM over the call, at least 128 keys each.
+// Splits of a tile's keys: about 8 CTAs per SM over the call (sequences are not equally long), at least
+// 64 keys each.
 int choose_chunk_splits(const ChunkArgs& a, int R, int window, int num_sms) {
   const int G = a.nh / a.c.nkv;
   const long long units = slots_of(a, R) * a.c.nkv * ((G + R - 1) / R);
   long long keys = static_cast<long long>(a.c.max_pages) << a.c.pshift;
   if (window > 0 && static_cast<long long>(window) + R < keys) keys = window + R;
-  long long n = 4LL * num_sms / units;
-  if (n > keys / 128) n = keys / 128;
+  long long n = 8LL * num_sms / units;
+  if (n > keys / 64) n = keys / 64;
   if (n > kMaxChunkSplits) n = kMaxChunkSplits;
   return n < 1 ? 1 : static_cast<int>(n);
 }
 
 template <typename T, int DC, int RI>
 int launch_chunk(const ChunkArgs& a, cudaStream_t st) {
-  constexpr int R = 16 * RI, smem = (R * (64 * DC + 4) + kKeys * kPad + R * kPad) * 4;
+  constexpr int R = 16 * RI, smem = (R * (64 * DC + 4) + kKeys * (RI == 1 ? 80 : kPad) + R * kPad) * 4;
   static_assert(smem <= 232448 - 1024, "shared memory of one CTA");
   const cudaError_t e = allow_smem<k_chunk<T, DC, RI>, smem>();
   if (e != cudaSuccess) {

@@ -60,7 +60,7 @@ struct Args {
   int ts;       // log2 of the tokens of a tile
   int hgs;      // groups of N query heads per KV head (1 unless it has more than N)
   int qbytes;   // of a box of queries: 64 dims x min(N, heads per KV head) x 2^ts tokens
-  int* meta;    // [grid][4]: sequence, KV head and group, tile, last CTA of the unit a CTA starts and does not end
+  int* meta;    // [grid][8]: last CTA (-1: none), first token, tokens, first head, heads of the unit a CTA starts and does not end
 };
 
 template <int D, int N_>
@@ -369,8 +369,8 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
     const int rs = g.rshift, ngs = LY::KS - rs, ng = 1 << ngs, nb = min(32 >> ngs, kAhead);
     Walk<LY::KS> w;
     w.locate(g, subs);
-    int* meta = g.meta + 4 * blockIdx.x;
-    if (lane == 0) meta[3] = -1;
+    int* meta = g.meta + 8 * blockIdx.x;
+    if (lane == 0) meta[0] = -1;
     int tt = 0, ns = 0, slot = 0;
     bool ok = true;
     typename Walk<LY::KS>::Part u;
@@ -409,10 +409,11 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
         continue;
       }
       if (!s.whole && u.begins && lane == 0) {
-        meta[0] = u.b;
-        meta[1] = u.sub;
-        meta[2] = u.tile;
-        meta[3] = static_cast<int>(u.last / w.per);
+        meta[0] = static_cast<int>(u.last / w.per);
+        meta[1] = s.tok0;
+        meta[2] = s.nt;
+        meta[3] = s.h0;
+        meta[4] = s.heads;
       }
       put_seg(s);
 #pragma unroll 1
@@ -948,7 +949,8 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
     while (w.next(g, c.nkv * g.hgs, u)) {
       const int kvh = u.sub / g.hgs, hg = u.sub % g.hgs, heads = min(N, G - hg * N), tok0 = w.s0 + (u.tile << g.ts);
       const bool whole = u.a == 0 && u.e == u.k;
-      for (int r = tid; r < min(1 << g.ts, w.t.n - (u.tile << g.ts)) * heads; r += LY::threads) {
+      const int nt = min(1 << g.ts, w.t.n - (u.tile << g.ts));
+      for (int r = tid; r < nt * heads; r += LY::threads) {
         const long long row = static_cast<long long>(tok0 + r / heads) * a.nh + kvh * G + hg * N + r % heads;
         if (!whole) {
           float* ml = a.ws_ml + ((2LL * blockIdx.x + (u.begins ? 1 : 0)) * N + r) * 2;
@@ -960,11 +962,12 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
         if (a.lse) a.lse[row] = NAN;
       }
       if (!whole && u.begins && tid == 0) {
-        int* meta = g.meta + 4 * blockIdx.x;
-        meta[0] = u.b;
-        meta[1] = u.sub;
-        meta[2] = u.tile;
-        meta[3] = static_cast<int>(u.last / w.per);
+        int* meta = g.meta + 8 * blockIdx.x;
+        meta[0] = static_cast<int>(u.last / w.per);
+        meta[1] = tok0;
+        meta[2] = nt;
+        meta[3] = kvh * G + hg * N;
+        meta[4] = heads;
       }
     }
   }
@@ -981,15 +984,13 @@ constexpr int kJoinWarps = 8;
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_chunk_tc_join(const __grid_constant__ Args g, int N) {
   pdl_enter();
-  const int4 meta = *reinterpret_cast<const int4*>(g.meta + 4 * blockIdx.x);  // sequence, KV head and group, tile, last CTA
-  if (meta.w < 0) return;
+  const int4 meta = *reinterpret_cast<const int4*>(g.meta + 8 * blockIdx.x);  // last CTA, first token, tokens, first head
+  const int heads = g.meta[8 * blockIdx.x + 4];
+  if (meta.x < 0) return;
   const ChunkArgs& a = g.a;
-  int s0, n, first, L;
-  pg::chunk_range(a, meta.x, s0, n, first, L);
-  const int G = a.nh / a.c.nkv, hg = meta.y % g.hgs, Gc = min(N, G - hg * N), nt = min(1 << g.ts, n - (meta.z << g.ts));
-  const int lane = threadIdx.x & 31, r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), c0 = blockIdx.x, np = meta.w - c0 + 1;
-  if (r >= nt * Gc) return;
-  const long long row = (static_cast<long long>(s0) + (meta.z << g.ts) + r / Gc) * a.nh + (meta.y / g.hgs) * G + hg * N + r % Gc;
+  const int lane = threadIdx.x & 31, r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), c0 = blockIdx.x, np = meta.x - c0 + 1;
+  if (r >= meta.z * heads) return;
+  const long long row = (static_cast<long long>(meta.y) + r / heads) * a.nh + meta.w + r % heads;
   // part i: slot 1 of the first CTA, slot 0 of the next ones
   auto part = [&](int i) { return static_cast<size_t>((c0 + i) * 2 + (i == 0 ? 1 : 0)) * N + r; };
   constexpr int PW = (pg::kMaxSms + 31) / 32, V = D / 128;
@@ -1072,7 +1073,7 @@ static int chunk_tc_rows(const pg::ChunkArgs& a) {
 }
 
 long long chunk_tc_workspace(const pg::ChunkArgs& a) {
-  return pg::kMaxSms * (16LL + 2LL * chunk_tc_rows(a) * (a.c.d + 2) * 4);
+  return pg::kMaxSms * (32LL + 2LL * chunk_tc_rows(a) * (a.c.d + 2) * 4);
 }
 
 int run_chunk_tc(const pg::ChunkArgs& a, void* ws, int num_sms, cudaStream_t st) {
@@ -1088,7 +1089,7 @@ int run_chunk_tc(const pg::ChunkArgs& a, void* ws, int num_sms, cudaStream_t st)
   g.qbytes = 128 * (G < N ? G : N) << g.ts;
   g.grid = num_sms;
   g.meta = static_cast<int*>(ws);
-  g.a.ws_ml = reinterpret_cast<float*>(g.meta + 4 * pg::kMaxSms);
+  g.a.ws_ml = reinterpret_cast<float*>(g.meta + 8 * pg::kMaxSms);
   g.a.ws_acc = g.a.ws_ml + pg::kMaxSms * 2 * N * 2;
   if (a.c.d == 512) return N == 32 ? launch<512, 32>(g, st) : launch<512, 64>(g, st);
   if (a.c.d == 256) return N == 32 ? launch<256, 32>(g, st) : launch<256, 128>(g, st);
