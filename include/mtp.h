@@ -521,20 +521,19 @@ MTP_API int mtp_paged_attention_workspace(const mtp_paged_kv *kv, int32_t B, int
  * rows cu_new[b] .. cu_new[b + 1] - 1 of q and out (mtp_page_plan's cu_new; slices of a prompt, or
  * the tokens of a draft block to verify). The row of position t attends the keys j <= t of its
  * sequence, with window > 0 those with j > t - window: out = sum_j p_j v_j, p = softmax(scale q . k_j).
- * q, out and the cache have the model dtype: an output is rounded to it once. fp32 models are
- * computed in fp32. For bf16 the products are exact and sums, maxima and exp-sums fp32; on tensor
- * cores (head_dim 128, 256 or 512, page_size >= 8) the probabilities enter the second product as
- * bf16 and their sum is of the rounded values, so that an output is a weighted mean of the values
- * with weights off by at most 2^-9 each.
+ * q, out and the cache have the model dtype; an output is rounded to it once. fp32 models are computed
+ * in fp32. For bf16 the products are exact, sums, maxima and exp-sums are fp32, and on tensor cores
+ * (head_dim 128, 256 or 512, page_size >= 8) the probabilities enter the second product as bf16, off by
+ * at most 2^-8 of themselves each; lse has their fp32 sum.
  * A row with nothing to attend (a sequence that holds fewer tokens than its new ones, pages that are
  * none) gets out 0 and lse -inf. What a row does not attend may hold anything and does not reach it;
  * where a row's query or an attended key or value is not finite, or a score leaves the range of
  * fp32, its outputs are NaN, infinite, or those without the keys of score -inf (a row whose every
  * attended key scores -inf gets NaN). A device wait that gives up after about 2 s leaves NaN.
  * cu_new must not decrease; its entries are clamped to [0, T] on the device. Rows of out and lse
- * outside [cu_new[0], cu_new[B]) are left as they were, and q is not read there.
+ * outside [cu_new[0], cu_new[B]) are left as they were.
  *   q         device, token t and head h at q + t * q_stride + h * head_dim, 16-byte aligned
- *   q_stride  elements between tokens (>= n_head * head_dim, a multiple of 16 bytes)
+ *   q_stride  elements between tokens (n_head * head_dim to 2^38, a multiple of 16 bytes)
  *   cu_new    device [B + 1] int32
  *   T         rows of out and lse; T <= 2^24 and T * n_head <= 2^26
  *   out       device [T][n_head][head_dim], not over q

@@ -395,7 +395,7 @@ int mtp_paged_attention_chunk(const mtp_paged_kv* kv, const void* q, int64_t q_s
   a.cu = cu_new;
   a.out = out;
   a.lse = lse;
-  a.window = window;
+  a.window = window < 1 << 30 ? window : 1 << 30;  // (more than any cache holds, and far from where sums overflow)
   int sms = 0;
   if ((rc = pg::sm_count(&sms))) return rc;
   return run_chunk_att(a, workspace, sms, static_cast<cudaStream_t>(stream));

@@ -65,10 +65,6 @@ __device__ __forceinline__ void tma_4d(unsigned dst, const CUtensorMap* map, int
       "l"(map), "r"(x), "r"(t), "r"(h), "r"(page), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void prefetch_4d(const CUtensorMap* map, int x, int t, int h, int page) {
-  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global [%0, {%1, %2, %3, %4}];" ::"l"(map), "r"(x), "r"(t), "r"(h), "r"(page)
-               : "memory");
-}
 // Shared-memory descriptors, 128-byte swizzle: 8-row groups are 1024 bytes apart; in the MN-major
 // form (rows = K index, 64 MN elements per row) `lead` is the distance of the next 64. The low
 // word holds the address, so a step is one 32-bit addition.

@@ -329,6 +329,8 @@ def _attend_chunk(st, q, kv, cu_new, window, scale, want_lse, out):
     T, nh, d = q.shape
     n = kv._ws.get(("chunk", T, nh))
     if n is None:
+        if len(kv._ws) >= 1024:  # (calls of many lengths)
+            kv._ws.clear()
         n = kv._ws[("chunk", T, nh)] = B.mtp_paged_attention_chunk_workspace(kv.p, kv.batch, T, nh)
     if out is None:
         out = torch.empty((T, nh, d), dtype=q.dtype, device=kv.device)

@@ -323,6 +323,34 @@ def test_pages_that_are_none_and_sequences_shorter_than_their_new_tokens(d, dtyp
 
 
 @gpu
+@pytest.mark.parametrize("d,dtype", [(64, "f32"), (128, "bf16"), (256, "bf16"), (512, "bf16")])
+def test_the_largest_window_and_sequences_shorter_than_their_new_tokens(d, dtype):
+    from mtp_speculative_decoding_gemma4_gb300 import PagedKV, paged_attention_chunk
+    c = Case(11, [40, 200], [17, 30], 16, 4, 1, d, dtype)
+    kv, cu = c.kv(), _dev(c.cu)
+    assert torch.equal(paged_attention_chunk(c.dq, kv, cu, window=2 ** 31 - 1), paged_attention_chunk(c.dq, kv, cu))
+    # 17 new tokens said of a sequence of 12: the first 5 attend nothing, the others what 12 of 12 do
+    short = PagedKV(c.dk, _dev(c.table), _dev(np.array([12, 200], np.int32)))
+    for w in (0, 2 ** 31 - 1, 4):
+        got = paged_attention_chunk(c.dq, short, cu, window=w)
+        want = paged_attention_chunk(c.dq[5:].contiguous(), short, cu - torch.tensor([0, 5, 5], dtype=torch.int32, device="cuda"), window=w)
+        assert (got[:5] == 0).all() and (got[5:].float() - want.float()).abs().max() <= 2 * HALF * want.abs().max()
+
+
+@gpu
+@pytest.mark.parametrize("d,dtype", [(64, "f32"), (64, "bf16"), (128, "bf16"), (512, "bf16")])
+def test_pages_farther_apart_than_32_bits(d, dtype):
+    from mtp_speculative_decoding_gemma4_gb300 import PagedKV, paged_attention_chunk
+    c = Case(12, [90, 50], [20, 3], 16, 4, 1, d, dtype)
+    want = c.run()[0]
+    step = (1 << 32) // (4 if c.bf16 else 8) // c.k.shape[0] * 3 // 8 * 8  # 6 GB in all
+    far = torch.empty(step * c.k.shape[0], dtype=c.k.dtype, device="cuda").as_strided(c.k.shape, (step, d, d, 1))
+    assert far.stride(0) * (far.shape[0] - 1) * far.element_size() > 1 << 32
+    far.copy_(c.dk)
+    assert torch.equal(paged_attention_chunk(c.dq, PagedKV(far, _dev(c.table), _dev(c.L)), _dev(c.cu)), want)
+
+
+@gpu
 def test_lengths_and_offsets_out_of_range_are_clamped():
     from mtp_speculative_decoding_gemma4_gb300 import PagedKV, paged_attention_chunk
     for d, dtype in ((64, "f32"), (128, "bf16")):

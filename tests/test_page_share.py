@@ -352,6 +352,25 @@ def test_a_compaction_into_the_table_itself(lib):
     assert moves
 
 
+@gpu
+def test_pages_farther_apart_than_32_bits():
+    from mtp_speculative_decoding_gemma4_gb300 import PagedKV, page_collect, page_fork
+    n, P, d = 12, 16, 64
+    step = (3 << 30) // n // 8 * 8
+    k = torch.empty(step * n, dtype=torch.bfloat16, device="cuda").as_strided((n, P, 1, d), (step, d, d, 1))
+    rows = torch.randn(n, P, 1, d).bfloat16()
+    k.copy_(rows)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    kv = PagedKV(k, i32([[11, 10], [0, 0]]), i32([20, 0]))
+    ring, state = i32([9] + [0] * 11), i32([0, 1])
+    page_fork(kv, i32([0]), i32([1]), i32([20]), ring, state)
+    assert kv.block_table.tolist() == [[11, 10], [11, 9]] and torch.equal(k[9, :4].cpu(), rows[10, :4])
+    kv.ctx_len.copy_(i32([20, 20]))
+    table, state, status = page_collect(kv, ring, compact=True)
+    assert table.tolist() == [[2, 1], [2, 0]] and status.tolist() == [3, 9, 3, 0]
+    assert torch.equal(k[2].cpu(), rows[11]) and torch.equal(k[1].cpu(), rows[10]) and torch.equal(k[0, :4].cpu(), rows[10, :4])
+
+
 # ---------------------------------------------------------------- together
 
 
