@@ -229,12 +229,11 @@ def page_fork(kv: PagedKV, src: torch.Tensor, dst: torch.Tensor, length: torch.T
 
 
 def _fork(st, kv, src, dst, length, free_ring, ring_state):
-    n = kv.batch
-    out = torch.empty(n + 6, dtype=_i32, device=kv.device)
-    at = out.data_ptr()
-    B.mtp_page_fork(kv.p, n, src.data_ptr(), dst.data_ptr(), length.data_ptr(), src.shape[0], free_ring.data_ptr(),
-                    ring_state.data_ptr(), at, at + 4 * n, at + 4 * n + 8, st)
-    return out.split((n, 2, 4))
+    len_out, state, dev = torch.empty_like(kv.ctx_len), torch.empty_like(ring_state), kv.device
+    status = torch.empty(4, dtype=_i32, device=dev)
+    B.mtp_page_fork(kv.p, kv.batch, src.data_ptr(), dst.data_ptr(), length.data_ptr(), src.shape[0], free_ring.data_ptr(),
+                    ring_state.data_ptr(), len_out.data_ptr(), state.data_ptr(), status.data_ptr(), st)
+    return len_out, state, status
 
 
 def page_collect(kv: PagedKV, free_ring: torch.Tensor, compact: bool = False, stream: Optional[int] = None):
@@ -255,11 +254,11 @@ def _collect(st, kv, free_ring, compact):
         n = kv._ws[("collect", compact)] = B.mtp_page_collect_workspace(kv.p, int(compact))
     cols = kv.c.max_pages
     table = torch.empty((kv.batch, cols), dtype=_i32, device=kv.device) if compact else None
-    out = torch.empty(6, dtype=_i32, device=kv.device)
-    at = out.data_ptr()
+    state, status = torch.empty(2, dtype=_i32, device=kv.device), torch.empty(4, dtype=_i32, device=kv.device)
     _with_workspace(kv, st, n, lambda ws, n: B.mtp_page_collect(
-        kv.p, kv.batch, free_ring.data_ptr(), table.data_ptr() if compact else 0, cols, at, at + 8, ws, n, st))
-    return (table, *out.split((2, 4)))
+        kv.p, kv.batch, free_ring.data_ptr(), table.data_ptr() if compact else 0, cols, state.data_ptr(),
+        status.data_ptr(), ws, n, st))
+    return table, state, status
 
 
 def _queries(q, kv: PagedKV):
