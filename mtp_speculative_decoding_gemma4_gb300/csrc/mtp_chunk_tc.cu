@@ -445,6 +445,7 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
                 *dead = 1;
                 ok = false;
               }
+              __nanosleep(200);  // (issue slots are the softmax's)
             }
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -638,6 +639,10 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
       } else if (__any_sync(0xffffffffu, *dead || clock64() - t0 > kSpin)) {
         *dead = 1;
         break;
+      } else if (tq == tp + 2) {
+        // scores are ahead as far as they may be: nothing but probabilities can come next, and a wait
+        // leaves the softmax its issue slots
+        try_wait(pfull0 + 8 * (tp & 1), (tp >> 1) & 1);
       }
     }
     __syncwarp();
