@@ -90,7 +90,7 @@ struct Lay {
   static constexpr int QBY = D * N * 2;                  // 64-dim blocks of [N][128 bytes]
   static constexpr int PBY = KT * 128 * ((N + 63) / 64); // 64-row blocks of [KT][128 bytes]
   static constexpr int PB = D == 256 && N == 128 ? 1 : 2;  // probability buffers
-  static constexpr int misc_bytes = 3072;
+  static constexpr int misc_bytes = 3 * 1024;
   static constexpr int room = 232448 - misc_bytes - QBY - PB * PBY;
   static constexpr int ring = room / slot > 12 ? 12 : room / slot;  // (a tile's slots may wrap)
   static constexpr int q = ring * slot;
