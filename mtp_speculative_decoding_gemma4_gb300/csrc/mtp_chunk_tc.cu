@@ -240,7 +240,7 @@ struct Walk {
       for (b = b0;; ++b) {
         t = x;
         if (each > 1) t = tiles_of(g, KS, b, x0);
-        c = each > 1 ? t.cost(t.count()) : mine / subs;
+        c = each > 1 ? t.cost(t.count()) : subs > 1 ? mine / subs : mine;
         if (at < c * subs) break;
         at -= c * subs;
       }
