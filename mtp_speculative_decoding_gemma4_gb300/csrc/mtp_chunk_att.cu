@@ -401,10 +401,12 @@ __global__ void __launch_bounds__(256) k_chunk_join(const __grid_constant__ Chun
   if (a.lse && lane == 0) a.lse[row] = den == 0.f ? -INFINITY : (M + log2f(den)) * 0.6931471805599453f;
 }
 
-// Rows of a tile: 16 where the sequences have few rows on average, else 64 (16 fp32 contexts, 9 tokens of
-// 2 heads per KV head on average: 46 us with 16, 65 with 64).
+// Rows of a tile: 16 where the sequences have at most 32 rows on average, else 64. 16 fp32 contexts of 2000
+// keys, with 16 and with 64 rows, us: 16 rows each, d = 64 26 and 34, d = 512 111 and 193; 32 rows each, d =
+// 64 33 and 36, 128 57 and 52, 256 81 and 107, 512 182 and 202; 48 rows each, 41 and 37, 78 and 54, 107 and
+// 111, 251 and 212.
 int rows_of(const ChunkArgs& a) {
-  return static_cast<long long>(a.T) * (a.nh / a.c.nkv) <= 24LL * a.B ? 16 : 64;
+  return static_cast<long long>(a.T) * (a.nh / a.c.nkv) <= 32LL * a.B ? 16 : 64;
 }
 
 long long slots_of(const ChunkArgs& a, int R) {
