@@ -402,8 +402,12 @@ again:
         const int n0 = had > k && (first || had + most > kCap) ? k : had;
         const float lim = fmaxf(level, bar);  // (elements equal to the bar itself are left out below)
         if (level > -INFINITY || !first) push(u, c0, lim);
+        // what the list holds decides on branches with barriers: every thread takes the same count, and none
+        // pushes elements of the next chunk before all have it
         __syncthreads();
-        if (sh.n > kCap || (first && !(level > -INFINITY))) {
+        int now = sh.n;
+        __syncthreads();
+        if (now > kCap || (first && !(level > -INFINITY))) {
           // Too many are equal (or nothing is above -inf): once more by keys, of which no two are equal, so
           // that at most k groups have elements that reach the k-th largest of the groups' maxima
           key_t mine = 0;
@@ -442,10 +446,12 @@ again:
             }
           }
           __syncthreads();
+          now = sh.n;
+          __syncthreads();
         }
-        if (first || sh.n > k + kMaxK / 2) {
-          select(sh, k);
-          bar = sh.n < k ? -INFINITY : key_value(sh.best[k - 1]);
+        if (first || now > k + kMaxK / 2) {
+          select(sh, k);  // (best[] stays as it is until a select behind further barriers)
+          bar = now < k ? -INFINITY : key_value(sh.best[k - 1]);
         }
       }
       first = false;

@@ -252,3 +252,17 @@ def test_after_a_verified_block():
         m = int(n[b])
         assert torch.equal(lp[b, :m + 1], top[b, :m + 1, 0]) and torch.isnan(lp[b, m + 1:]).all()
     assert torch.equal(ids[..., 0], best)
+
+
+@gpu
+@pytest.mark.parametrize("k", [5, 20, 32])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_lists_that_fill_between_meetings(dtype, k):
+    """Rows of many chunks, of which about 3 k elements enter the list between two meetings, so that what
+    it holds lies near the count from which on it is sorted: the same bits at every call, and the right ones."""
+    from mtp_speculative_decoding_gemma4_gb300 import token_logprobs
+    logits, tokens = _case(640, 150001, dtype)
+    want = _check(logits, tokens, k=k)
+    for _ in range(8):
+        got = token_logprobs(logits, tokens, top_k=k)
+        assert all(torch.equal(a.cpu(), b) for a, b in zip(got, want))
