@@ -266,3 +266,26 @@ def test_lists_that_fill_between_meetings(dtype, k):
     for _ in range(8):
         got = token_logprobs(logits, tokens, top_k=k)
         assert all(torch.equal(a.cpu(), b) for a, b in zip(got, want))
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,V", [(400, 60000), (96, 262144), (700, 50257)])
+@pytest.mark.parametrize("kind", ["first masked", "first lower", "rising", "two steps"])
+def test_lists_that_overfill_long_before_the_end(kind, rows, V, dtype):
+    """Logits of which more exceed the best of the first ids than the list holds, in slices that go on
+    for several chunks behind the meeting that finds it out: every chunk enters the sums all the same."""
+    g = torch.Generator().manual_seed(7)
+    x = torch.randn((rows, V), generator=g) * 2
+    i = torch.arange(V)
+    if kind == "first masked":
+        x[:, :8192] = -math.inf
+    elif kind == "first lower":
+        x[:, :8192] -= 10
+    elif kind == "rising":
+        x = (i * (60.0 / V) - 30).expand(rows, V).clone()
+    elif kind == "two steps":  # a second time behind a later meeting
+        x += 10 * ((i >= 8192).float() + (i >= 8192 * 5).float())
+    tokens = torch.randint(0, V, (rows,), generator=g, dtype=torch.int32)
+    tokens[:2] = torch.tensor([V - 1, 0])
+    _check(x.to(dtype).cuda(), tokens.cuda(), k=20)
