@@ -544,6 +544,12 @@ MTP_API int mtp_paged_attention_chunk(const mtp_paged_kv *kv, const void *q, int
                                       float *lse, void *workspace, int64_t workspace_bytes, void *stream);
 MTP_API int mtp_paged_attention_chunk_workspace(const mtp_paged_kv *kv, int32_t B, int32_t T, int32_t n_head,
                                                 int64_t *bytes);
+/* For tests of the device waits of mtp_paged_attention_chunk, as mtp_set_debug is for a handle's: in the
+ * calling host thread's later calls on tensor cores no page of sequence skip_sequence is looked up, so
+ * that the waits for it run out, and spin_limit_cycles > 0 replaces their bound. The sequence's rows,
+ * and those of others in the same CTAs, then get NaN; later calls are not affected. (-1, 0) restores the
+ * defaults. Errors: INVALID_ARG (skip_sequence < -1, spin_limit_cycles < 0). */
+MTP_API int mtp_set_chunk_debug(int32_t skip_sequence, int64_t spin_limit_cycles);
 
 /* Pages a query attends, by a cheap score of each page: per query head the step
  * s = fl32(max |q| * fl32(1 / 127)) and codes c = rint(fl32(q / s)) (all 0 when q is not

@@ -23,7 +23,7 @@ EXPORTS = ("mtp_init_weights", "mtp_draft_block", "mtp_centroid_head", "mtp_veri
            "mtp_page_select", "mtp_page_select_workspace", "mtp_paged_attention", "mtp_paged_attention_workspace",
            "mtp_draft_block_paged", "mtp_draft_block_paged_workspace", "mtp_paged_attention_chunk",
            "mtp_paged_attention_chunk_workspace", "mtp_token_logprobs", "mtp_token_logprobs_workspace",
-           "mtp_page_fork", "mtp_page_collect", "mtp_page_collect_workspace")
+           "mtp_page_fork", "mtp_page_collect", "mtp_page_collect_workspace", "mtp_set_chunk_debug")
 MASK_NEG_1E30, MASK_MIN_MINUS_ONE = 0, 1  # enum mtp_logit_mask
 HEAD_AUTO, HEAD_PER_SEQUENCE, HEAD_CLUSTER_MAJOR = 0, 1, 2  # enum mtp_sparse_head
 
@@ -99,6 +99,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mtp_paged_attention_workspace.argtypes = [pkv, i32, i32, i32, ctypes.POINTER(i64)]
     lib.mtp_paged_attention_chunk.argtypes = [pkv, vp, i64, vp, i32, i32, i32, i32, f32, vp, vp, vp, i64, vp]
     lib.mtp_paged_attention_chunk_workspace.argtypes = [pkv, i32, i32, i32, ctypes.POINTER(i64)]
+    lib.mtp_set_chunk_debug.argtypes = [i32, i64]
     lib.mtp_token_logprobs.argtypes = [vp, i32, i64, vp, i32, i32, f32, i32, vp, vp, vp, vp, vp, i64, vp]
     lib.mtp_token_logprobs_workspace.argtypes = [i32, i32, i32, i32, ctypes.POINTER(i64)]
     lib.mtp_page_fork.argtypes = [pkv, i32, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp]
@@ -118,7 +119,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                  "mtp_page_select", "mtp_page_select_workspace", "mtp_paged_attention",
                  "mtp_paged_attention_workspace", "mtp_draft_block_paged", "mtp_draft_block_paged_workspace",
                  "mtp_paged_attention_chunk", "mtp_paged_attention_chunk_workspace", "mtp_token_logprobs",
-                 "mtp_token_logprobs_workspace", "mtp_page_fork", "mtp_page_collect", "mtp_page_collect_workspace"):
+                 "mtp_token_logprobs_workspace", "mtp_page_fork", "mtp_page_collect", "mtp_page_collect_workspace",
+                 "mtp_set_chunk_debug"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -288,6 +290,12 @@ def mtp_paged_attention_chunk(kv: mtp_paged_kv, q: int, q_stride: int, cu_new: i
                                                             workspace_bytes, stream or None)
     if rc:
         _check(rc, "mtp_paged_attention_chunk")
+
+
+def mtp_set_chunk_debug(skip_sequence: int = -1, spin_limit_cycles: int = 0) -> None:
+    """For tests: a sequence whose pages the chunk attention does not look up, and the bound of its
+    device waits, in the calling thread's later calls; the defaults without arguments."""
+    _check(load_library().mtp_set_chunk_debug(skip_sequence, spin_limit_cycles), "mtp_set_chunk_debug")
 
 
 def mtp_page_select_workspace(kv: mtp_paged_kv, B: int) -> int:

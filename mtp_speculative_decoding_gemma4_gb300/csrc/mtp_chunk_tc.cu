@@ -27,8 +27,11 @@
 // which k_chunk_tc_join adds in CTA order.
 //
 // Values that are not finite in keys that only some rows of a unit attend, or none, are zeroed before
-// the sums (0 * NaN would not vanish), and the attending rows get NaN. Waits are bounded; a CTA that
-// gives up writes NaN.
+// the sums (0 * NaN would not vanish), and the attending rows get NaN.
+//
+// Waits are bounded; a CTA that gives up writes NaN. The softmax warps meet at hardware barriers, which
+// have no bound, so they all take the same units and agree on when references move, whatever waits
+// have run out: then every one reaches each of the barriers.
 //
 // What bounds it, and what it measured (with the join):
 //   d = 512, two slices of 2048 tokens of 8 heads over 24000 keys: 1.97 ms, 800 Tflop/s, the tensor pipe
@@ -107,7 +110,7 @@ struct Lay {
   static constexpr int over = bad + WG * 16;             // per warpgroup [2]: a score of a tile of this parity exceeds its reference by 2^8
   static constexpr int bars = over + WG * 8;
   static constexpr int nbars = 2 * ring + 2 * 4 + 3 + 2 * kSegs + kInfo + WG;
-  static constexpr int misc = bars + nbars * 8;          // tensor-memory address, dead word, tiles begun
+  static constexpr int misc = bars + nbars * 8;          // tensor-memory address, dead word, tiles begun, units
   static constexpr int total = misc + 16;
   static constexpr int want = (NP + 2) * N;              // tensor-memory columns: sums, two of scores
   static constexpr int cols = want <= 128 ? 128 : want <= 256 ? 256 : 512;
@@ -116,7 +119,7 @@ struct Lay {
 // A part of a unit (a tile of rows of one KV head, and group of its heads, of one sequence) as the
 // warps of a CTA take it.
 struct Seg {
-  int tiles;           // key tiles; -1: no more units
+  int tiles;           // key tiles
   int k0;              // the first one
   int kvh;
   int tok0, nt, pos0;  // first token of the rows in q and out, tokens, position of the first
@@ -192,6 +195,16 @@ __device__ __forceinline__ bool wait_in(unsigned bar, unsigned parity, volatile 
     }
   }
   return true;
+}
+
+// A wait for warps that arrive in any case, since all that they wait for is bounded: the word `dead`
+// does not cut it short, so that whoever waits returns behind the same arrivals.
+__device__ __forceinline__ void wait_sure(unsigned bar, unsigned parity) {
+  if (test_wait(bar, parity)) return;
+  const long long t0 = clock64();
+#pragma unroll 1
+  while (!try_wait(bar, parity) && clock64() - t0 < 4 * kSpin) {
+  }
 }
 
 __device__ __forceinline__ Tiles tiles_of(const Args& g, int ks, int b, int& s0) {
@@ -329,7 +342,8 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
   int* holes = reinterpret_cast<int*>(sm + LY::holes);
   Seg* segs = reinterpret_cast<Seg*>(sm + LY::segs);
   int* misc = reinterpret_cast<int*>(sm + LY::misc);  // 0: tensor memory, 1: dead, 2: begun
-  volatile int *dead = misc + 1, *begun = misc + 2;   // begun: tiles that the load warp has begun
+  // begun: tiles that the load warp has begun; units: how many units this CTA has, once all are found
+  volatile int *dead = misc + 1, *begun = misc + 2, *units = misc + 3;
   const ChunkArgs& a = g.a;
   const Cache& c = a.c;
   const bool own_v = c.v != nullptr;
@@ -359,6 +373,7 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     misc[1] = (base & 1023u) != 0;  // (every wait then gives up)
     misc[2] = 0;
+    misc[3] = INT_MAX;
   }
   for (int i = tid; i < N; i += LY::threads) reinterpret_cast<int*>(sm + LY::top)[i] = kLowest;
   if (warp == 0) {
@@ -373,9 +388,9 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
 
   // unit i of this CTA, once it is found; false behind the last
   auto get_seg = [&](int i, Seg& s) {
-    if (!wait_in(seg0 + 8 * (i % kSegs), (i / kSegs) & 1, dead, kSpin)) return false;
+    if (!wait_in(seg0 + 8 * (i % kSegs), (i / kSegs) & 1, dead, a.spin)) return false;
     s = segs[i % kSegs];
-    return s.tiles > 0;
+    return i < *units;
   };
 
   if (warp == 4 * WG + 2) {
@@ -391,8 +406,9 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
     bool ok = true;
     typename Walk<LY::KS>::Part u;
     auto put_seg = [&](const Seg& s) {  // its place is free once the unit kSegs before is answered
-      if (ns >= kSegs) ok = __all_sync(0xffffffffu, wait_in(ofree0 + 8 * (ns % kSegs), (ns / kSegs - 1) & 1, dead, kSpin));
-      if (ok && lane == 0) {
+      if (ns >= kSegs) ok = __all_sync(0xffffffffu, wait_in(ofree0 + 8 * (ns % kSegs), (ns / kSegs - 1) & 1, dead, a.spin));
+      if (!ok) return;
+      if (lane == 0) {
         segs[ns % kSegs] = s;
         mbar_arrive(seg0 + 8 * (ns % kSegs));
       }
@@ -432,6 +448,7 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
         meta[4] = s.heads;
       }
       put_seg(s);
+      if (u.b == a.skip) ok = false;  // testing: the other warps wait for these tiles until they give up
 #pragma unroll 1
       for (int k = 0; k < s.tiles && ok; k += nb) {
         int page = -1;
@@ -443,7 +460,7 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
           if (tt >= kAhead) {
             const long long t0 = clock64();
             while (*begun < tt - kAhead + 1 && ok) {
-              if (*dead || clock64() - t0 > kSpin) {
+              if (*dead || clock64() - t0 > a.spin) {
                 *dead = 1;
                 ok = false;
               }
@@ -461,8 +478,11 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
         }
       }
     }
-    s.tiles = -1;
-    if (ok) put_seg(s);
+    if (lane == 0) {  // (in any case: the softmax waits for it)
+      *units = ns;
+      mbar_arrive(seg0 + 8 * (ns % kSegs));
+    }
+    __syncwarp();
   } else if (warp == 4 * WG) {
     // ---------------- loads. The whole warp walks, with everything that a copy takes in uniform
     // registers; one elected thread issues (a tile of 64 KB took 1800 cycles to issue from one thread's
@@ -478,7 +498,7 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
       const int tiles = __shfl_sync(0xffffffffu, s.tiles, 0), kvh = __shfl_sync(0xffffffffu, s.kvh, 0), k0 = __shfl_sync(0xffffffffu, s.k0, 0);
 #pragma unroll 1
       for (int k = 0; k < tiles; ++k, ++tt) {
-        ok = all(wait_in(ifull0 + 8 * is, iphase, dead, kSpin));
+        ok = all(wait_in(ifull0 + 8 * is, iphase, dead, a.spin));
         if (!ok) break;
         const int mine = info[is * 16 + (lane & 15)];  // -1: zeros
         const int off0 = ((k0 + k) << LY::KS) & (P - 1);  // 0 unless a page is longer than a tile
@@ -486,7 +506,7 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
         for (int j = 0; j < 2 * NP; ++j) {
           if (j >= PT) break;
           const unsigned bar = full0 + 8 * slot;
-          if (pc >= kRing) ok = all(wait_in(empty0 + 8 * slot, phase ^ 1, dead, kSpin));
+          if (pc >= kRing) ok = all(wait_in(empty0 + 8 * slot, phase ^ 1, dead, a.spin));
           if (!ok) break;
           if (j == 0 && lane == 0) *begun = tt + 1;
           const unsigned dst = base + slot * LY::slot;
@@ -529,7 +549,7 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
       int n = 0;
 #pragma unroll 1
       for (; get_seg(n, s); ++n) {
-        if (n && !wait_in(qused, (n - 1) & 1, dead, kSpin)) break;
+        if (n && !wait_in(qused, (n - 1) & 1, dead, a.spin)) break;
         mbar_expect_tx(qfull, g.qbytes * (D / 64));
 #pragma unroll 1
         for (int j = 0; j < D / 64; ++j) tma_4d(base + LY::q + j * (N * 128), &mapQ, 64 * j, s.h0, s.tok0, 0, qfull);
@@ -562,11 +582,8 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
     while (more || tp < tq) {
       bool did = false;
       if (more && left == 0 && done(seg0 + 8 * (nseg % kSegs), (nseg / kSegs) & 1)) {
-        left = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&segs[nseg % kSegs].tiles), 0);
-        if (left < 0) {
-          more = false;
-          left = 0;
-        }
+        more = __shfl_sync(0xffffffffu, nseg < *units ? 1 : 0, 0) != 0;
+        left = more ? __shfl_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&segs[nseg % kSegs].tiles), 0) : 0;
         ++nseg;
         fresh = true;
         did = true;
@@ -638,7 +655,7 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
       }
       if (did) {
         t0 = clock64();
-      } else if (__any_sync(0xffffffffu, *dead || clock64() - t0 > kSpin)) {
+      } else if (__any_sync(0xffffffffu, *dead || clock64() - t0 > a.spin)) {
         *dead = 1;
         break;
       } else if (tq == tp + 2) {
@@ -648,7 +665,7 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
       }
     }
     __syncwarp();
-    if (__any_sync(0xffffffffu, *dead) && elect()) {  // the products that were issued still run: wait for them
+    if (elect()) {  // no product may run when the CTA ends, however the others' waits end
       commit(drain);
       t0 = clock64();
       while (!try_wait(drain, 0) && clock64() - t0 < kSpin) {
@@ -674,7 +691,17 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
     const bool has = KT == 128 || lane < 16;
     const int rs = g.rshift;
     auto bar_wg = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); };
-    auto wait_sums = [&](int t) { wait_in(odone0 + 8 * (t & 1), (t >> 1) & 1, dead, kSpin); };
+    // (under the fixed bound, as the other warps' waits end it sooner: with a.spin prompt slices take 1 % longer)
+    auto wait = [&](unsigned bar, unsigned parity) { wait_in(bar, parity, dead, kSpin); };
+    auto wait_sums = [&](int t) { wait(odone0 + 8 * (t & 1), (t >> 1) & 1); };
+    // unit i, whatever waits have run out; false behind the last (asked by way of its tiles: with the
+    // comparison itself the compiler spills twice as much, and prompts with a V take 216 us instead of 190)
+    auto take = [&](int i, Seg& s) {
+      wait_sure(seg0 + 8 * (i % kSegs), (i / kSegs) & 1);
+      s = segs[i % kSegs];
+      s.tiles = i < *units ? s.tiles : 0;
+      return s.tiles > 0;
+    };
     // the bits i of 0..31 with lo <= i < hi
     auto bits = [](int lo, int hi) {
       lo = max(lo, 0);
@@ -684,7 +711,7 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
     int at = 0, is = 0;  // tiles so far; the place of their pages
     Seg s;
 #pragma unroll 1
-    for (int ns = 0; get_seg(ns, s); ++ns) {
+    for (int ns = 0; take(ns, s); ++ns) {
       const int nr = s.nt * s.heads, nrw = __shfl_sync(0xffffffffu, min(max(nr - col0, 0), NC), 0);  // rows; of this warpgroup
       // (columns behind the rows: scores of anything under a reference of 0)
       if (wt < NC) negm[wt] = wt < nrw ? INFINITY : 0.f;
@@ -699,7 +726,7 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
       for (int t = 0; t < s.tiles; ++t, ++at) {
         const int buf = at & 1;
         char* const pbuf = sm + LY::p + (PB == 1 ? 0 : buf * LY::PBY);
-        wait_in(sfull0 + 8 * buf, (at >> 1) & 1, dead, kSpin);
+        wait(sfull0 + 8 * buf, (at >> 1) & 1);
         __syncwarp();
         fence_after();
         // x: the exponents under the references; a second time where these have moved
@@ -754,7 +781,7 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
             for (int i = 0; i < NC; ++i) x[i] = ex2(x[i]);
             if (pass) break;
             if (t) {
-              wait_in(agree0 + 8 * wg, agreed, dead, kSpin);
+              wait_sure(agree0 + 8 * wg, agreed);
               agreed ^= 1;
               if (!over[buf]) break;
             }
@@ -840,7 +867,7 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
             constexpr int kPart = D / 8 / WG;
             const int V = own_v ? kPart : D / 8, v0 = own_v ? wg * kPart : 0;
             if (own_v)
-              for (int i = 0; i < NP; ++i) wait_in(full0 + 8 * ((at * PT + NP + i) % kRing), ((at * PT + NP + i) / kRing) & 1, dead, kSpin);
+              for (int i = 0; i < NP; ++i) wait(full0 + 8 * ((at * PT + NP + i) % kRing), ((at * PT + NP + i) / kRing) & 1);
 #pragma unroll 2
             for (int it = 0; it < V; ++it) {
               const int src = (it * 32 + lane) / V, e = (it * 32 + lane) % V + v0;

@@ -115,7 +115,9 @@ struct ChunkArgs {
   float* ws_acc;            // partial sums of the splits
   float* ws_ml;             // their (max, exp-sum)
   long long q_stride;
+  long long spin;           // bound of the device waits, in clock64 cycles
   float scale_log2;         // softmax scale * log2(e)
+  int skip;                 // testing: the tensor-core kernel looks up no page of this sequence (-1: none)
   int B, T, nh, window, nsplit;
 };
 

@@ -110,6 +110,10 @@ static int check_batch(const Cache& c, int B, int n_head) {
   return MTP_OK;
 }
 
+// testing only (mtp_set_chunk_debug), of the calling host thread
+static thread_local int chunk_skip = -1;
+static thread_local long long chunk_spin = 0;
+
 // Whether a chunk's batch, tokens and heads are served; fills a's sizes.
 static int check_chunk(ChunkArgs* a, int B, int T, int n_head) {
   if (B < 1 || B > 1 << 20 || T < 0 || T > 1 << 24 || n_head < 1 || n_head % a->c.nkv || n_head / a->c.nkv > 1024 ||
@@ -341,6 +345,17 @@ int mtp_paged_attention(const mtp_paged_kv* kv, const float* q, int32_t B, int32
   return run_paged_att(a, workspace, sms, static_cast<cudaStream_t>(stream));
 }
 
+int mtp_set_chunk_debug(int32_t skip_sequence, int64_t spin_limit_cycles) {
+  set_error("%s", "");
+  if (skip_sequence < -1 || spin_limit_cycles < 0) {
+    set_error("need skip_sequence >= -1 and spin_limit_cycles >= 0");
+    return MTP_ERR_INVALID_ARG;
+  }
+  pg::chunk_skip = skip_sequence;
+  pg::chunk_spin = spin_limit_cycles;
+  return MTP_OK;
+}
+
 int mtp_paged_attention_chunk_workspace(const mtp_paged_kv* kv, int32_t B, int32_t T, int32_t n_head, int64_t* bytes) {
   set_error("%s", "");
   pg::ChunkArgs a;
@@ -396,6 +411,8 @@ int mtp_paged_attention_chunk(const mtp_paged_kv* kv, const void* q, int64_t q_s
   a.out = out;
   a.lse = lse;
   a.window = window < 1 << 30 ? window : 1 << 30;  // (more than any cache holds, and far from where sums overflow)
+  a.spin = pg::chunk_spin > 0 ? pg::chunk_spin : pg::kSpin;
+  a.skip = pg::chunk_skip;
   int sms = 0;
   if ((rc = pg::sm_count(&sms))) return rc;
   return run_chunk_att(a, workspace, sms, static_cast<cudaStream_t>(stream));

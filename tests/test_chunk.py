@@ -421,3 +421,54 @@ def test_python_checks():
         paged_attention_chunk(c.dq[:, :3].contiguous(), kv, cu)  # 3 heads on 2 KV heads
     empty = paged_attention_chunk(c.dq[:0], kv, torch.zeros_like(cu))
     assert empty.shape == (0, 4, 64)
+
+
+# ---------------------------------------------------------------- device waits that run out
+
+
+def test_the_limits_of_the_waits_are_checked(lib):
+    for bad in ((-2, 0), (-1, -1)):
+        assert lib.mtp_set_chunk_debug(*bad) == B.MTP_ERR_INVALID_ARG and B.mtp_last_error()
+    assert lib.mtp_set_chunk_debug(-1, 0) == B.MTP_OK
+
+
+def _given_up(c, skip, window=0):
+    """Outputs of a call whose waits for sequence `skip` run out after some 10 ms, against those of an
+    ordinary call: NaN in the rows of the sequence, and in no row or every element of another; the
+    rows that have NaN."""
+    clean = [x.clone() for x in c.run(window)]
+    B.mtp_set_chunk_debug(skip, 20_000_000)
+    try:
+        out, lse = c.run(window)
+        torch.cuda.synchronize()
+    finally:
+        B.mtp_set_chunk_debug()
+    mine = slice(int(c.cu[skip]), int(c.cu[skip + 1]))
+    assert torch.isnan(out[mine]).all() and torch.isnan(lse[mine]).all()
+    gone = torch.isnan(lse)
+    assert torch.equal(torch.isnan(out).any(-1), gone) and torch.equal(torch.isnan(out).all(-1), gone)
+    assert torch.equal(out[~gone], clean[0][~gone]) and torch.equal(lse[~gone], clean[1][~gone])
+    again = c.run(window)
+    assert all(torch.equal(a, b) for a, b in zip(again, clean))
+    return gone.any(-1)
+
+
+@gpu
+@pytest.mark.parametrize("skip", [0, 1, 3, 5])
+@pytest.mark.parametrize("d,n_head,own_v", [(128, 4, False), (128, 4, True), (256, 4, False), (512, 4, False), (512, 4, True)])
+def test_waits_that_run_out_leave_nan(d, n_head, own_v, skip):
+    """Few rows and many, in units of one CTA and in units that cross CTAs."""
+    L = [300, 5000, 40, 20000, 100, 64]
+    for new in ([5, 7, 1, 8, 3, 5], [200, 70, 40, 90, 33, 64]):
+        _given_up(Case(d, L, new, 64, n_head, 1, d, own_v=own_v), skip)
+
+
+@gpu
+@pytest.mark.parametrize("d", [128, 256, 512])
+def test_waits_that_run_out_reach_the_rows_of_their_own_ctas(d):
+    n = 700
+    rs = np.random.RandomState(d)
+    c = Case(d, rs.randint(20, 400, n), np.full(n, 6), 16, 4, 1, d)
+    gone = _given_up(c, 350, window=100).cpu().reshape(n, 6).any(1)
+    assert gone[350] and int(gone.sum()) <= 40
+    assert int(gone.nonzero().max() - gone.nonzero().min()) <= 40
