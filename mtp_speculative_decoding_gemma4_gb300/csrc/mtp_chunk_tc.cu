@@ -273,7 +273,10 @@ struct Walk {
     sub = __shfl_sync(0xffffffffu, sub, f);
     tile = __shfl_sync(0xffffffffu, tile, f);
     off = __shfl_sync(0xffffffffu, off, f);
-    t = x;
+    t.window = g.a.window;  // (x of a lane without a sequence holds nothing)
+    t.ts = g.ts;
+    t.ks = KS;
+    t.extra = kExtra;
     t.n = __shfl_sync(0xffffffffu, t.n, f);
     t.first = __shfl_sync(0xffffffffu, t.first, f);
     t.L = __shfl_sync(0xffffffffu, t.L, f);

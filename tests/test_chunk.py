@@ -472,3 +472,12 @@ def test_waits_that_run_out_reach_the_rows_of_their_own_ctas(d):
     gone = _given_up(c, 350, window=100).cpu().reshape(n, 6).any(1)
     assert gone[350] and int(gone.sum()) <= 40
     assert int(gone.nonzero().max() - gone.nonzero().min()) <= 40
+
+
+@gpu
+@pytest.mark.parametrize("Bn", [2, 31, 32, 33, 65])
+@pytest.mark.parametrize("d", [128, 256])
+def test_batches_around_a_warp_s_lanes(Bn, d):
+    rs = np.random.RandomState(Bn)
+    L = rs.randint(1, 500, Bn)
+    Case(Bn + d, L, np.minimum(rs.randint(0, 40, Bn), L), 16, 4, 1, d).check(window=90)
