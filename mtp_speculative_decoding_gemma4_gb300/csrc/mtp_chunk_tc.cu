@@ -716,8 +716,9 @@ __global__ void __launch_bounds__(Lay<D, N>::threads, 1)
 #pragma unroll 1
     for (int ns = 0; take(ns, s); ++ns) {
       const int nr = s.nt * s.heads, nrw = __shfl_sync(0xffffffffu, min(max(nr - col0, 0), NC), 0);  // rows; of this warpgroup
-      // (columns behind the rows: scores of anything under a reference of 0)
-      if (wt < NC) negm[wt] = wt < nrw ? INFINITY : 0.f;
+      // (columns behind the rows hold scores of anything, which no reference of a row may move for: under a
+      // reference of +inf none exceeds it)
+      if (wt < NC) negm[wt] = wt < nrw ? INFINITY : -INFINITY;
       if (wt < 4) bad[4 * wg + wt] = 0;
       bar_wg();
       f2 l[NC / 2];
