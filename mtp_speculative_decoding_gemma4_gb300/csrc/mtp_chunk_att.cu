@@ -77,8 +77,10 @@ __device__ __forceinline__ bool find_tile(const ChunkArgs& a, int slot, int tpt,
   return tile >= 0;
 }
 
+// (d <= 128: two CTAs per SM; without the bound 2048 fp32 rows of d = 128 take 110 us instead of 92, and with
+// it for all d the registers of the others grow until one CTA fits)
 template <typename T, int DC, int RI>
-__global__ void __launch_bounds__(kTokThreads) k_chunk(const __grid_constant__ ChunkArgs a) {
+__global__ void __launch_bounds__(kTokThreads, DC <= 2 ? 2 : 0) k_chunk(const __grid_constant__ ChunkArgs a) {
   pdl_enter();
   constexpr int R = 16 * RI, D = 64 * DC, QP = D + 4, VE = Vec<T>::n, LV = kKeys * 64 / VE / kTokThreads;
   constexpr int KP = RI == 1 ? 80 : kPad;  // floats between keys
@@ -305,13 +307,15 @@ __global__ void __launch_bounds__(kTokThreads) k_chunk(const __grid_constant__ C
       }
       if (x + 1 < DC) __syncthreads();
     }
-    if (s_any) {  // rows that attend a value that is not finite
+    if (s_any) {  // rows that attend a value that is not finite, whatever its weight (V = K: but for scores of -inf)
 #pragma unroll 1
       for (int key = 0; key < kKeys; ++key)
         if (s_bad[key]) {
+          const int pos = k0 + key;
 #pragma unroll
           for (int i = 0; i < RI; ++i)
-            if (sp[row_of(i) * kPad + key] != 0.f) l[i] = NAN;
+            if (c.v ? pos <= qpos[i] && (a.window <= 0 || pos > qpos[i] - a.window) : sp[row_of(i) * kPad + key] != 0.f)
+              l[i] = NAN;
         }
     }
   }

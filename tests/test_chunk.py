@@ -522,3 +522,27 @@ def test_other_tokens_queries_neither_move_a_row_nor_slow_it_down(d, own_v):
         if ratios[-1] < 1.06:
             return
     assert False, ratios
+
+
+@gpu
+@pytest.mark.parametrize("d,dtype", [(64, "f32"), (64, "bf16"), (200, "f32"), (128, "bf16"), (256, "bf16"), (512, "bf16")])
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+@pytest.mark.parametrize("n", [3, 150])
+def test_a_value_that_is_not_finite_reaches_rows_of_no_weight_for_it(d, dtype, what, n):
+    """Key 60 scores so low that its weight is 0 in fp32: its value is attended all the same, by the rows from
+    token 60 on (in a window of 100, up to token 159)."""
+    c = Case(5, [200], [n], 16, 4, 1, d, dtype, own_v=True)
+    c.q = torch.ones_like(c.q)
+    c.k = torch.where(torch.isnan(c.k), c.k, 0 * c.k)
+    c.k[c.table[0, 3], 12] = -300.0
+    c.dk, c.dq = c.k.cuda(), c.q.cuda()
+    clean = {w: c.run(w)[0] for w in (0, 100)}
+    c.dv[c.table[0, 3], 12, :, 3] = what
+    for w in (0, 100):
+        out = c.run(w)[0]
+        for i in range(n):
+            pos = 200 - n + i
+            if pos >= 60 and (not w or pos < 160):
+                assert not torch.isfinite(out[i]).all(-1).any()
+            else:
+                assert torch.equal(out[i], clean[w][i])
