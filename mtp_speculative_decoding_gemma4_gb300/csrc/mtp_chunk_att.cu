@@ -406,11 +406,13 @@ __global__ void __launch_bounds__(256) k_chunk_join(const __grid_constant__ Chun
 }
 
 // Rows of a tile: 16 where the sequences have at most 32 rows on average, else 64. 16 fp32 contexts of 2000
-// keys, with 16 and with 64 rows, us: 16 rows each, d = 64 26 and 34, d = 512 111 and 193; 32 rows each, d =
-// 64 33 and 36, 128 57 and 52, 256 81 and 107, 512 182 and 202; 48 rows each, 41 and 37, 78 and 54, 107 and
-// 111, 251 and 212.
+// keys, with 16 and with 64 rows, us: 16 rows each, d = 64 26 and 34, d = 512 111 and 192; 32 rows each, d =
+// 64 33 and 36, 128 47 and 52, 256 80 and 107, 512 183 and 202; 48 rows each, 41 and 38, 62 and 53, 107 and
+// 112, 251 and 212. 64 as well where a grid has fewer rows than there would be groups of 16 heads.
 int rows_of(const ChunkArgs& a) {
-  return static_cast<long long>(a.T) * (a.nh / a.c.nkv) <= 32LL * a.B ? 16 : 64;
+  const int G = a.nh / a.c.nkv;
+  if (a.c.nkv * ((G + 15) / 16) > 65535) return 64;
+  return static_cast<long long>(a.T) * G <= 32LL * a.B ? 16 : 64;
 }
 
 long long slots_of(const ChunkArgs& a, int R) {

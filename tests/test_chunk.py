@@ -546,3 +546,16 @@ def test_a_value_that_is_not_finite_reaches_rows_of_no_weight_for_it(d, dtype, w
                 assert not torch.isfinite(out[i]).all(-1).any()
             else:
                 assert torch.equal(out[i], clean[w][i])
+
+
+@gpu
+def test_the_most_heads():
+    """1024 KV heads of 1024 query heads each, which is more than a grid has rows of 16."""
+    from mtp_speculative_decoding_gemma4_gb300 import PagedKV, paged_attention_chunk
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k = torch.randn((2, 1, 1024, 8), generator=g, device="cuda").bfloat16()
+    table, lens = torch.ones((32, 1), dtype=torch.int32, device="cuda"), torch.ones(32, dtype=torch.int32, device="cuda")
+    q = torch.randn((1, 1 << 20, 8), generator=g, device="cuda").bfloat16()
+    cu = torch.tensor([0] * 8 + [1] * 25, dtype=torch.int32, device="cuda")
+    out = paged_attention_chunk(q, PagedKV(k, table, lens), cu)
+    assert torch.equal(out.view(1024, 1024, 8), k[1, 0][:, None].expand(1024, 1024, 8))
