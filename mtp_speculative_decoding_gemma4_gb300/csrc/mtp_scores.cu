@@ -237,8 +237,12 @@ __device__ __forceinline__ void answer(const Args& a, const Shared& sh, int row,
   const int tid = threadIdx.x;
   const bool good = z.s > 0.f && z.s < INFINITY && z.m < INFINITY;
   const float ls = log2f(z.s);
-  // (not by way of log2, where the type's lowest logits would become -inf)
-  auto lp = [&](float x) { return good ? (x - z.m) * a.inv_t - kLn2 * ls : NAN; };
+  // (not by way of log2, where the type's lowest logits would become -inf; and a difference that leaves the
+  // range at a temperature at which it does not is one of quotients)
+  auto lp = [&](float x) {
+    const float d = x - z.m, y = d < -FLT_MAX ? x * a.inv_t - z.m * a.inv_t : d * a.inv_t;
+    return good ? y - kLn2 * ls : NAN;
+  };
   if (tid == 0) {
     if (a.logprob) {
       const int t = a.token[row];

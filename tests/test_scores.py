@@ -289,3 +289,17 @@ def test_lists_that_overfill_long_before_the_end(kind, rows, V, dtype):
     tokens = torch.randint(0, V, (rows,), generator=g, dtype=torch.int32)
     tokens[:2] = torch.tensor([V - 1, 0])
     _check(x.to(dtype).cuda(), tokens.cuda(), k=20)
+
+
+@gpu
+@pytest.mark.parametrize("V", [40, 70000])
+@pytest.mark.parametrize("temperature", [2.0, 7.0, 1e30])
+def test_differences_beyond_the_type_s_range(V, temperature):
+    """Logits farther apart than fp32's largest value, whose log probabilities at the temperature are not."""
+    g = torch.Generator().manual_seed(V)
+    x = torch.randn((3, V), generator=g)
+    x[0, 3], x[0, 5] = 3e38, -3e38
+    x[1] = torch.finfo(torch.float32).min
+    x[1, :3] = torch.tensor([3e38, 3e38, -math.inf])
+    x[2, 7], x[2, 9] = 2e38, -2e38
+    _check(x.cuda(), torch.tensor([5, 30, 9], dtype=torch.int32).cuda(), temperature=temperature, k=20)
