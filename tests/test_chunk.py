@@ -559,3 +559,43 @@ def test_the_most_heads():
     cu = torch.tensor([0] * 8 + [1] * 25, dtype=torch.int32, device="cuda")
     out = paged_attention_chunk(q, PagedKV(k, table, lens), cu)
     assert torch.equal(out.view(1024, 1024, 8), k[1, 0][:, None].expand(1024, 1024, 8))
+
+
+@gpu
+@pytest.mark.parametrize("scale", [1.0, 0.03])
+@pytest.mark.parametrize("d,dtype", [(64, "f32"), (64, "bf16"), (512, "f32"), (128, "bf16"), (256, "bf16"), (512, "bf16")])
+@pytest.mark.parametrize("new", [[5, 1, 7], [200, 1, 90]])
+def test_a_scale_of_the_caller_s(new, d, dtype, scale):
+    """Scores of the size that the default scale gives N(0, 1) queries, or smaller, so that the errors are no
+    larger either."""
+    c = Case(d, [3000, 40, 700], new, 16, 4, 1, d, dtype, own_v=d == 128, q_by=d ** -0.5 if scale == 1.0 else 1.0)
+    c.check(scale=scale)
+    c.check(window=100, scale=scale)
+
+
+@gpu
+@pytest.mark.parametrize("d,dtype", [(64, "f32"), (128, "bf16"), (512, "bf16")])
+def test_tens_of_thousands_of_short_and_empty_sequences(d, dtype):
+    """40000 sequences of at most one page of 16 tokens, of which up to 3 are new and mostly none."""
+    from mtp_speculative_decoding_gemma4_gb300 import PagedKV, paged_attention_chunk
+    Bn, P, dt = 40000, 16, torch.bfloat16 if dtype == "bf16" else torch.float32
+    rs = np.random.RandomState(d)
+    L = rs.randint(0, P + 1, Bn).astype(np.int32)
+    new = np.minimum(np.where(rs.uniform(size=Bn) < 0.3, rs.randint(1, 4, Bn), 0), L)
+    new[:2000], new[-2000:] = 0, 0
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    g = torch.Generator(device="cuda").manual_seed(d)
+    k = torch.randn((Bn, P, 1, d), generator=g, device="cuda").to(dt)
+    table = torch.randperm(Bn, generator=g, device="cuda").int()[:, None]
+    q = torch.randn((int(cu[-1]), 2, d), generator=g, device="cuda").to(dt)
+    out, lse = paged_attention_chunk(q, PagedKV(k, table, _dev(L)), _dev(cu), want_lse=True)
+    seq = np.repeat(np.arange(Bn), new)
+    pos = L[seq] - new[seq] + np.arange(len(seq)) - cu[seq]
+    keys = k[table[_dev(seq).long(), 0].long(), :, 0].double()
+    x = torch.einsum("thd,tjd->thj", q.double(), keys) * d ** -0.5
+    x = x.masked_fill((torch.arange(P, device="cuda") > _dev(pos)[:, None])[:, None], float("-inf"))
+    p = torch.softmax(x, -1)
+    want, mean = torch.einsum("thj,tjd->thd", p, keys), torch.einsum("thj,tjd->thd", p, keys.abs())
+    most = TOL + (HALF * (want.abs() + mean * (1 + HALF)) if dtype == "bf16" else 0)
+    assert ((out.double() - want).abs() <= most).all()
+    assert ((lse.double() - torch.logsumexp(x, -1)).abs() <= TOL).all()
