@@ -266,7 +266,7 @@ MTP_API int mtp_verify_sample(const void *target_logits, const int32_t *draft, i
  * With p = softmax(row / temperature): logprob = ln p[token], entropy = -sum_i p_i ln p_i (0 ln 0 = 0),
  * top_ids the top_k tokens of the largest logits in descending order (ties: lower id first) and
  * top_logprobs their ln p. fp32 arithmetic from the logits as they are. -inf is a logit of
- * probability 0, also among the top_k where fewer are above it. A row without a softmax (a NaN, a
+ * probability 0, also among the top_k where fewer are above it; a log probability below fp32's range is -inf. A row without a softmax (a NaN, a
  * +inf, or nothing above -inf) gets NaN for its values and -1 for its ids; a token outside [0, V)
  * gets a logprob of NaN.
  *   logits       device [rows][V], dtype (enum mtp_dtype), row_stride elements apart (>= V; any

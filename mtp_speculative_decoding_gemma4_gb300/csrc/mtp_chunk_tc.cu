@@ -12,7 +12,8 @@
 // two of tokens.
 //
 // The sums stay in tensor memory over a unit's key tiles. A row's softmax reference is a maximum that
-// moves only when a score exceeds it by 2^8, so they are rarely rescaled. (The tensor-memory adder
+// moves only when a score exceeds it by 2^8, so they are rarely rescaled (a published variant of the
+// softmax in one pass). (The tensor-memory adder
 // truncates: over 32768 keys, 2048 additions, that is some 10^-4 of a sum, beside the 2^-9 of the
 // output's own rounding and that of the probabilities, which enter as bf16; their sum is fp32.)
 //
@@ -34,18 +35,19 @@
 // have run out: then every one reaches each of the barriers.
 //
 // What bounds it, and what it measured (with the join):
-//   d = 512, two slices of 2048 tokens of 8 heads over 24000 keys: 1.97 ms, 800 Tflop/s, the tensor pipe
-//   45 % active. A tile of 64 KB stays in the ring from its load to its sums, 5000 cycles (load 1700,
+//   d = 512, two slices of 2048 tokens of 8 heads over 21800 keys on average: 1.96 ms, 710 Tflop/s, the
+//   tensor pipe 46 % active. A tile of 64 KB stays in the ring from its load to its sums, 5000 cycles (load 1700,
 //   scores 900, softmax 1650, sums 600), and the ring holds 2.25 of them beside 64 rows' queries: 2800
 //   cycles a tile. The products themselves (N = 64) would take 1500.
-//   d = 128 with a V, 8 ragged prompts to 4096 of 8 heads on 2: 190 us; d = 256, four slices in a window
-//   of 512: 81 us. 128 rows' softmax takes 3000 to 3600 cycles a tile, the products 1000 to 1500. It is a
-//   chain without a single bound: without the exponentials the two take 185 and 79 us, without the scores'
-//   load 171 and 73, without the agreement 174 and 71, with an eighth of the products 175 and 66; half of
-//   the warps starting a unit half a tile later changes nothing.
-//   Few rows (8 x 7 tokens of 4 heads over ragged long contexts, d = 512): 51.5 us for 151 MB, 22 at the
-//   copy rate: keys come in at 4.9 TB/s; 7 us pass before the first scores, 5 with the end and the join.
-//   (With the tiles prefetched into the L2 as their pages are found, 54.)
+//   d = 128 with a V, 8 ragged prompts to 4096 of 8 heads on 2: 181 us; d = 256, four slices in a window
+//   of 512: 77 us. 128 rows' softmax takes 3000 to 3600 cycles a tile, the products 1000 to 1500. It is a
+//   chain without a single bound: of 190 and 81 us (before columns without a row were kept out of the
+//   agreement) the two kept 185 and 79 without the exponentials, 171 and 73 without the scores' load, 174
+//   and 71 without the agreement, 175 and 66 with an eighth of the products; half of the warps starting a
+//   unit half a tile later changed nothing.
+//   Few rows (8 x 7 tokens of 4 heads over ragged long contexts, d = 512): 46.8 us for 135 MB, 20 at the
+//   copy rate, of which 38 before the join; 7 us pass before the first scores. (With the tiles prefetched
+//   into the L2 as their pages are found 54, when it was 51.5 without.)
 #include <cstring>
 
 #include "mtp_chunk.cuh"
@@ -68,8 +70,8 @@ using pg::Tiles;
 constexpr int kAhead = 4;       // tiles that the find warp runs ahead of the load warp
 constexpr int kInfo = 12;       // tiles whose pages are kept: kAhead and those between load and softmax
 constexpr int kSegs = 4;        // units whose descriptions are kept
-// What beginning a unit costs, in key tiles: 8 ragged prompts of d = 128 take 225 us with 2, 190 with 4, 196
-// with 6; four slices in a window of 512 77, 81 and 81 us; long contexts are indifferent.
+// What beginning a unit costs, in key tiles: 8 ragged prompts of d = 128 take 223 us with 2, 181 with 4, 182
+// with 6; four slices in a window of 512 73, 77 and 77 us; long contexts are indifferent.
 constexpr int kExtra = 4;
 
 struct Args {
@@ -1109,8 +1111,8 @@ int launch(const Args& g, cudaStream_t st) {
 }  // namespace pgc
 
 // Rows of a tile: 64 at d = 512, 128 below, and 32 where the sequences have at most 32 rows each on
-// average (8 x 7 tokens of 4 heads at d = 512: 51.5 us, 57 with 64 rows; one window of 512 keys at d = 256:
-// 12.3 us, 14.7 with 128).
+// average (8 x 7 tokens of 4 heads at d = 512: 46.8 us, 52.4 with 64 rows; one window of 512 keys at d = 256:
+// 12.4 us, 14.8 with 128).
 static int chunk_tc_rows(const pg::ChunkArgs& a) {
   if (static_cast<long long>(a.T) * (a.nh / a.c.nkv) <= 32LL * a.B) return 32;
   return a.c.d == 512 ? 64 : 128;

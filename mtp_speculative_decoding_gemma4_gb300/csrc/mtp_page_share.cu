@@ -3,7 +3,7 @@
 // the held ones moved into the front of the pool where that is asked for. No page carries a count of
 // its holders: the block tables say who holds it.
 // What bounds them is the chain of dependent reads and launches: 64 samples of a prompt take 6.2 us, 256
-// beams 6.7, the collection of a pool of 131072 pages 11.7 (three launches). A compaction is bound by
+// beams 6.7, the collection of a pool of 131072 pages 11.8 (three launches). A compaction is bound by
 // its copy: 33 us for 135 MB read and written in pages of 16 KB, 20 at the copy rate.
 #include "mtp_common.cuh"
 #include "mtp_launch.h"

@@ -20,8 +20,8 @@
 // 281 when rising, 83 otherwise (as called).
 //
 // A CTA takes a row, or a slice of it where rows are few (k_scores_join then joins the slices). What
-// bounds it is reading the logits once: 576 rows of 262144 bf16 logits take 57 us without alternatives
-// (5.3 TB/s), 69 with 5 and 77 with 20 of them; issue slots are 70 % busy (an element costs about six
+// bounds it is reading the logits once: 576 rows of 262144 bf16 logits take 59 us without alternatives
+// (5.1 TB/s), 70 with 5 and 78 with 20 of them; issue slots are 70 % busy (an element costs about six
 // instructions), and a meeting costs 1 to 2 us of a CTA's time, which other CTAs only partly cover. Five
 // rows take 6.7 us without and 10.8 with 5 alternatives, in two launches.
 #include <cfloat>
